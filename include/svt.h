@@ -315,6 +315,137 @@ int svt_rerank(const svt_index *ix, int32_t n_queries, const int8_t *queries, co
                int32_t n_cand, const int64_t *cand_ids, const svt_rerank_net *net, int32_t k_out,
                int64_t *out_ids, float *out_scores, int32_t *out_counts, void *hip_stream);
 
+/*
+ * Routed experts.  svt_rerank computes every expert of a small net for every candidate; the entry points
+ * below are the parts of a larger net that sends each token (a candidate, a request) to a few of many
+ * experts: the router's choice, tokens sorted by expert and back, and the experts' products with 4-bit
+ * weights ["Meta Andromeda" summary, model section: a router picks about 2 of 6 experts for each ad;
+ * "SilverTorch - Index as Model", recommendation-quality section: neural modules over an enlarged candidate
+ * set].  The pages give no formulas; each call states its own.
+ *   - All pointers are device pointers of the current HIP device, which is also hip_stream's; arrays are
+ *     row-major and dense, and need only their elements' alignment unless stated.
+ *   - Rows hold float32, float16 or bfloat16 (SVT_F32, SVT_F16, SVT_BF16).  Sums, softmax statistics and
+ *     weights are float32 and each result is rounded once.  No call uses atomics on floats: the same
+ *     inputs give the same bits.
+ *   - Every call is asynchronous on hip_stream, allocates nothing and can be captured into a graph.
+ *   - An output may not overlap an input or another output (SVT_EINVAL).
+ */
+enum { SVT_F32 = 0, SVT_F16 = 1, SVT_BF16 = 2 };   /* element types */
+enum { SVT_ACT_NONE = 0, SVT_ACT_RELU = 1 };       /* activations of svt_quant_linear */
+#define SVT_MAX_EXPERTS 512 /* experts of one net                                                     */
+#define SVT_MAX_TOP 16      /* experts per token                                                      */
+
+/*
+ * svt_route - the `top` best experts of each token and their weights.
+ *   logits       [n_tokens][n_experts] of dtype.  -inf or NaN shuts the expert for this token; +inf counts
+ *                as the largest finite float32
+ *   top          1 <= top <= min(SVT_MAX_TOP, n_experts <= SVT_MAX_EXPERTS)
+ *   renormalise  0: a weight is the softmax over all the token's open experts; 1: over the chosen ones
+ *   out_experts  [n_tokens][top] int32, by (logit desc, expert asc); -1 where fewer than top are open
+ *   out_weights  [n_tokens][top] float; 0 where the expert is -1
+ * n_tokens == 0 returns SVT_OK without enqueuing.  Errors: SVT_EINVAL (sizes or types out of range, NULL or
+ * misaligned pointers, overlap), SVT_EDEVICE (launch failure); on error nothing is enqueued.
+ */
+int svt_route(int32_t n_tokens, int32_t n_experts, int32_t top, int32_t dtype, const void *logits,
+              int32_t renormalise, int32_t *out_experts, float *out_weights, void *hip_stream);
+
+/*
+ * svt_route_backward - the gradient of svt_route's weights.
+ *   logits, renormalise  as given to svt_route; experts, weights: its outputs (an expert outside
+ *                        [0, n_experts) adds nothing)
+ *   d_weights            [n_tokens][top] float: the loss's gradient in the weights
+ *   d_logits             [n_tokens][n_experts] of dtype: the gradient in the logits, 0 for shut experts and,
+ *                        renormalised, for those not chosen
+ * The choice itself has no gradient.  Errors as svt_route.
+ */
+int svt_route_backward(int32_t n_tokens, int32_t n_experts, int32_t top, int32_t dtype, const void *logits,
+                       int32_t renormalise, const int32_t *experts, const float *weights, const float *d_weights,
+                       void *d_logits, void *hip_stream);
+
+/*
+ * svt_expert_sort - the (token, choice) entries grouped by expert, each expert's in their own order.
+ *   experts    [n_tokens][top] int32; entries outside [0, n_experts) are dropped
+ *   offsets    [n_experts + 1] int32: expert e's entries are sorted rows offsets[e] .. offsets[e + 1] - 1
+ *   order      [n_tokens * top] int32: the entry (token * top + choice) of each sorted row; -1 past
+ *              offsets[n_experts]
+ *   position   [n_tokens][top] int32: the sorted row of each entry; -1 for a dropped one
+ *   workspace  svt_expert_sort_workspace_size(n_tokens, top, n_experts) bytes, 4-byte aligned (NULL where
+ *              that is 0); contents on entry are ignored.  Calls in flight together need their own.
+ * n_tokens >= 0 (0 sets the offsets to 0), 1 <= top <= SVT_MAX_TOP, n_tokens * top <= 2^30.
+ * Errors: SVT_EINVAL, SVT_EDEVICE as svt_route.
+ */
+size_t svt_expert_sort_workspace_size(int32_t n_tokens, int32_t top, int32_t n_experts);
+int svt_expert_sort(int32_t n_tokens, int32_t top, int32_t n_experts, const int32_t *experts, int32_t *offsets,
+                    int32_t *order, int32_t *position, void *workspace, size_t workspace_bytes, void *hip_stream);
+
+/*
+ * The exchange of rows between tokens and sorted rows, and its gradients.  position is svt_expert_sort's:
+ * distinct rows of [0, n_tokens * top), or anything outside that range for dropped entries.
+ *   dispatch            rows[position[t][j]] = x[t]
+ *   dispatch_backward   dx[t] = sum_j d_rows[position[t][j]]
+ *   combine             y[t] = sum_j weights[t][j] rows[position[t][j]]  (weights NULL: every weight 1)
+ *   combine_backward    d_rows[position[t][j]] = weights[t][j] dy[t]
+ *                       d_weights[t][j] = dy[t] . rows[position[t][j]], 0 for a dropped entry
+ *   x, y, dx, dy   [n_tokens][width] of dtype; a token whose entries are all dropped gets a row of zeros
+ *   rows, d_rows   [n_tokens * top][width] of dtype; rows that no entry names are neither read nor written
+ *   weights, d_weights  [n_tokens][top] float
+ * n_tokens == 0 returns SVT_OK without enqueuing.  Errors: SVT_EINVAL, SVT_EDEVICE as svt_route.
+ */
+int svt_expert_dispatch(int32_t n_tokens, int32_t top, int32_t width, int32_t dtype, const void *x,
+                        const int32_t *position, void *rows, void *hip_stream);
+int svt_expert_dispatch_backward(int32_t n_tokens, int32_t top, int32_t width, int32_t dtype, const void *d_rows,
+                                 const int32_t *position, void *dx, void *hip_stream);
+int svt_expert_combine(int32_t n_tokens, int32_t top, int32_t width, int32_t dtype, const void *rows,
+                       const int32_t *position, const float *weights, void *y, void *hip_stream);
+int svt_expert_combine_backward(int32_t n_tokens, int32_t top, int32_t width, int32_t dtype, const void *dy,
+                                const void *rows, const int32_t *position, const float *weights, void *d_rows,
+                                float *d_weights, void *hip_stream);
+
+/*
+ * Weights in 4 bits with a scale for each group of inputs, in the layout svt_quant_linear reads:
+ *   W[n][k] = scale[n][k / group] * (q[n][k] - zero[n][k / group])
+ *   n_matrices   1 .. SVT_MAX_EXPERTS; n_out 1 .. 2^19; n_in 1 .. 2^20; group 32, 64 or 128 (the last group
+ *                of a row may be shorter)
+ *   scale_type   SVT_F32, SVT_F16 or SVT_BF16
+ *   has_zeros    1: a zero point per group; 0: every zero point is 8
+ *   packed       caller's device buffer, 256-byte aligned, of packed_bytes >= svt_quant_pack_size
+ */
+typedef struct {
+  int32_t n_matrices, n_out, n_in, group, scale_type, has_zeros;
+  void *packed;
+  size_t packed_bytes;
+} svt_quant_weights;
+
+/* svt_quant_pack_size - bytes of packed for these sizes; 0 if they are invalid (svt_last_error says why). */
+size_t svt_quant_pack_size(const svt_quant_weights *w);
+
+/*
+ * svt_quant_pack - lays weights out into w->packed.  The sources can be freed once the stream has passed.
+ *   nibbles  [n_matrices][n_out][(n_in + 1) / 2] bytes: q of input 2 i in the low half of byte i, of 2 i + 1
+ *            in the high half
+ *   scales   [n_matrices][n_out][ceil(n_in / group)] of scale_type
+ *   zeros    the same shape, one byte each; NULL exactly when has_zeros is 0
+ * Errors: SVT_EINVAL, SVT_EUNSUPPORTED (group), SVT_EDEVICE; on error nothing is enqueued.
+ */
+int svt_quant_pack(const svt_quant_weights *w, const uint8_t *nibbles, const void *scales, const uint8_t *zeros,
+                   void *hip_stream);
+
+/*
+ * svt_quant_linear - y[r] = act(W x[r] + bias), for few rows (a matrix-vector product) or many.
+ *   x           [n_rows][n_in] of dtype
+ *   offsets     NULL: w holds one matrix, which every row uses.  Else [n_matrices + 1] int32, ascending, e.g.
+ *               svt_expert_sort's: rows offsets[e] .. offsets[e + 1] - 1 use matrix e (an end is clamped to
+ *               [0, n_rows]); rows that no matrix names are neither read nor written
+ *   bias        [n_matrices][n_out] float or NULL
+ *   activation  SVT_ACT_NONE or SVT_ACT_RELU (NaN stays NaN)
+ *   y           [n_rows][n_out] of out_dtype: dtype or SVT_F32
+ * No weight or product is rounded: group sums of x q and of x are float32, and 256 times the sum of |x| over a
+ * group must stay finite.  A row that holds an infinity or NaN gets NaN outputs.  n_rows == 0 returns
+ * SVT_OK without enqueuing.  Errors: SVT_EINVAL, SVT_EUNSUPPORTED (group), SVT_EDEVICE as svt_quant_pack.
+ */
+int svt_quant_linear(int32_t n_rows, int32_t dtype, const void *x, const svt_quant_weights *w, const int32_t *offsets,
+                     const float *bias, int32_t activation, int32_t out_dtype, void *y, void *hip_stream);
+
 /* svt_last_error - message of the last failed call on this thread ("" if none). */
 const char *svt_last_error(void);
 

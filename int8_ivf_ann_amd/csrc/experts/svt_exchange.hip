@@ -1,0 +1,577 @@
+// svt_exchange.hip - tokens sorted by expert, their rows sent to the experts and brought back with weights,
+// and the gradients of both, on gfx950.
+//
+// Entries are the T x top (token, choice) pairs of a router; entry i = t * top + j is valid when its
+// expert lies in [0, E).  The sort is stable: position[i] = offsets[e] + (valid entries of e before i).
+//
+//   dispatch            rows[position[t][j]] = x[t]
+//   dispatch backward   dx[t] = sum_j d_rows[position[t][j]]
+//   combine             y[t] = sum_j w[t][j] rows[position[t][j]]
+//   combine backward    d_rows[position[t][j]] = w[t][j] dy[t],  dw[t][j] = dy[t] . rows[position[t][j]]
+//
+// Every exchange kernel walks tokens: a token's own row is read or written once, in order, and its `top`
+// rows on the experts' side are whole rows, so each byte moves once and the only gather is of rows.  Sums
+// run over j in order in float32 and no two threads write one address, so results never vary.
+
+#include <type_traits>
+
+#include "svt_experts.h"
+
+namespace svt {
+
+namespace {
+
+// ---- sort ----------------------------------------------------------------------------------------
+//
+// A counting sort.  Waves own contiguous pieces of the entries; within a piece, 64 entries at a time, an
+// entry's rank among the lanes of its expert comes from one ballot per bit of the expert's number (the
+// lanes that agree on every bit), so equal experts keep their order without atomics on the positions.
+//   one launch   (up to kOneEntries): a workgroup of 16 waves counts, scans and places.
+//   three        k_sort_count: a histogram per block; k_sort_scan: per expert, the exclusive sums over
+//                the blocks; k_sort_place: each block adds its experts' starts and places its entries.
+
+constexpr int kOneThreads = 1024, kOneWaves = kOneThreads / 64;
+constexpr int64_t kOneEntries = 16384;
+constexpr int kSortThreads = 256, kSortWaves = kSortThreads / 64;
+constexpr int64_t kBlockEntries = 2048;   // entries per block, until there are kMaxBlocks
+constexpr int64_t kMaxBlocks = 1024;
+constexpr int64_t kMaxEntries = int64_t(1) << 30;
+
+struct SortShape {
+  int64_t n;            // entries
+  int64_t per_block;    // entries per block, a multiple of 64 kSortWaves
+  int32_t blocks;
+};
+
+SortShape sort_shape(int64_t n) {
+  SortShape s{n, kBlockEntries, 1};
+  int64_t blocks = (n + kBlockEntries - 1) / kBlockEntries;
+  if (blocks > kMaxBlocks) {
+    const int64_t step = 64 * kSortWaves;
+    s.per_block = ((n + kMaxBlocks - 1) / kMaxBlocks + step - 1) / step * step;
+    blocks = (n + s.per_block - 1) / s.per_block;
+  }
+  s.blocks = (int32_t)(blocks < 1 ? 1 : blocks);
+  return s;
+}
+
+__device__ __forceinline__ int load_expert(const int32_t *experts, int64_t i, int64_t end, int E) {
+  if (i >= end) return -1;
+  const int e = experts[i];
+  return (uint32_t)e < (uint32_t)E ? e : -1;
+}
+
+// the lanes of this wave whose expert equals this lane's (0 for a lane without one)
+__device__ __forceinline__ uint64_t same_expert(int e, int bits) {
+  uint64_t same = __ballot(e >= 0);
+  for (int b = 0; b < bits; ++b) {
+    const uint64_t one = __ballot((e >> b) & 1);
+    same &= ((e >> b) & 1) ? one : ~one;
+  }
+  return e >= 0 ? same : 0ull;
+}
+
+// places the entries [i0, i1) of this wave: next[e] is the position of the wave's next entry of e
+__device__ __forceinline__ void place_entries(const int32_t *experts, int64_t i0, int64_t i1, int E, int bits,
+                                              volatile int32_t *next, int32_t *order, int32_t *position) {
+  const int l = lane_id();
+  for (int64_t i = i0 + l; i - l < i1; i += 64) {
+    const int e = load_expert(experts, i, i1, E);
+    const uint64_t same = same_expert(e, bits);
+    int32_t at = -1;
+    if (e >= 0) at = next[e] + mbcnt(same);
+    // the last lane of each expert moves next[e] on; a wave's LDS operations stay in order
+    if (e >= 0 && (same >> l) == 1ull) next[e] = at + 1;
+    if (i < i1) {
+      position[i] = at;
+      if (e >= 0) order[at] = (int32_t)i;
+    }
+  }
+}
+
+// exclusive scan of total[0 .. E) (LDS) into start[0 .. E], by the block's first SVT_MAX_EXPERTS / 2
+// threads or more; barriers inside
+template <int NT>
+__device__ __forceinline__ int scan_experts(const int32_t *total, int32_t *start, int E, int32_t *wave_tot) {
+  constexpr int kEach = SVT_MAX_EXPERTS / NT < 1 ? 1 : SVT_MAX_EXPERTS / NT;
+  int v[kEach], sum = 0, all;
+#pragma unroll
+  for (int q = 0; q < kEach; ++q) {
+    const int e = threadIdx.x * kEach + q;
+    v[q] = e < E ? total[e] : 0;
+    sum += v[q];
+  }
+  int at = block_excl_scan<NT>(sum, wave_tot, &all);
+#pragma unroll
+  for (int q = 0; q < kEach; ++q) {
+    const int e = threadIdx.x * kEach + q;
+    if (e < E) start[e] = at;
+    at += v[q];
+  }
+  if (threadIdx.x == 0) start[E] = all;
+  __syncthreads();
+  return all;
+}
+
+__global__ __launch_bounds__(kOneThreads) void k_sort_one(const int32_t *experts, int64_t n, int E, int bits,
+                                                          int32_t *offsets, int32_t *order, int32_t *position) {
+  __shared__ int32_t next[kOneWaves][SVT_MAX_EXPERTS];
+  __shared__ int32_t total[SVT_MAX_EXPERTS], start[SVT_MAX_EXPERTS + 1], wave_tot[kOneWaves + 1];
+  const int tid = threadIdx.x, wv = tid / 64;
+  const int64_t per = (n + 64 * kOneWaves - 1) / (64 * kOneWaves) * 64;
+  const int64_t i0 = wv * per < n ? wv * per : n, i1 = i0 + per < n ? i0 + per : n;
+  for (int i = tid; i < kOneWaves * E; i += kOneThreads) next[i / E][i % E] = 0;
+  __syncthreads();
+  for (int64_t i = i0 + tid % 64; i < i1; i += 64) {
+    const int e = load_expert(experts, i, i1, E);
+    if (e >= 0) atomicAdd(&next[wv][e], 1);
+  }
+  __syncthreads();
+  if (tid < E) {   // counts of the waves before, and the expert's total
+    int sum = 0;
+#pragma unroll
+    for (int w = 0; w < kOneWaves; ++w) {
+      const int c = next[w][tid];
+      next[w][tid] = sum;
+      sum += c;
+    }
+    total[tid] = sum;
+  }
+  __syncthreads();
+  const int all = scan_experts<kOneThreads>(total, start, E, wave_tot);
+  for (int i = tid; i < kOneWaves * E; i += kOneThreads) next[i / E][i % E] += start[i % E];
+  for (int e = tid; e <= E; e += kOneThreads) offsets[e] = start[e];
+  for (int64_t i = all + tid; i < n; i += kOneThreads) order[i] = -1;
+  __syncthreads();
+  place_entries(experts, i0, i1, E, bits, next[wv], order, position);
+}
+
+// counts[e * blocks + b]: block b's entries of expert e
+__global__ __launch_bounds__(kSortThreads) void k_sort_count(const int32_t *experts, SortShape s, int E,
+                                                             int32_t *counts) {
+  __shared__ int32_t hist[SVT_MAX_EXPERTS];
+  const int tid = threadIdx.x;
+  for (int e = tid; e < E; e += kSortThreads) hist[e] = 0;
+  __syncthreads();
+  const int64_t i0 = blockIdx.x * s.per_block, i1 = i0 + s.per_block < s.n ? i0 + s.per_block : s.n;
+  for (int64_t i = i0 + tid; i < i1; i += kSortThreads) {
+    const int e = load_expert(experts, i, i1, E);
+    if (e >= 0) atomicAdd(&hist[e], 1);
+  }
+  __syncthreads();
+  for (int e = tid; e < E; e += kSortThreads) counts[(int64_t)e * s.blocks + blockIdx.x] = hist[e];
+}
+
+// one block per expert: its counts become exclusive sums over the blocks; totals[e] = their sum
+__global__ __launch_bounds__(kSortThreads) void k_sort_scan(int32_t *counts, int blocks, int32_t *totals) {
+  constexpr int kEach = kMaxBlocks / kSortThreads;
+  __shared__ int32_t wave_tot[kSortWaves + 1];
+  int32_t *row = counts + (int64_t)blockIdx.x * blocks;
+  int v[kEach], sum = 0, all;
+#pragma unroll
+  for (int q = 0; q < kEach; ++q) {
+    const int b = threadIdx.x * kEach + q;
+    v[q] = b < blocks ? row[b] : 0;
+    sum += v[q];
+  }
+  int at = block_excl_scan<kSortThreads>(sum, wave_tot, &all);
+#pragma unroll
+  for (int q = 0; q < kEach; ++q) {
+    const int b = threadIdx.x * kEach + q;
+    if (b < blocks) row[b] = at;
+    at += v[q];
+  }
+  if (threadIdx.x == 0) totals[blockIdx.x] = all;
+}
+
+__global__ __launch_bounds__(kSortThreads) void k_sort_place(const int32_t *experts, SortShape s, int E, int bits,
+                                                             const int32_t *counts, const int32_t *totals,
+                                                             int32_t *offsets, int32_t *order, int32_t *position) {
+  __shared__ int32_t next[kSortWaves][SVT_MAX_EXPERTS];
+  __shared__ int32_t total[SVT_MAX_EXPERTS], start[SVT_MAX_EXPERTS + 1], wave_tot[kSortWaves + 1];
+  const int tid = threadIdx.x, wv = tid / 64, b = blockIdx.x;
+  for (int i = tid; i < kSortWaves * E; i += kSortThreads) next[i / E][i % E] = 0;
+  for (int e = tid; e < E; e += kSortThreads) total[e] = totals[e];
+  __syncthreads();
+  const int64_t b0 = b * s.per_block, b1 = b0 + s.per_block < s.n ? b0 + s.per_block : s.n;
+  const int64_t per = s.per_block / kSortWaves;
+  const int64_t i0 = b0 + wv * per < b1 ? b0 + wv * per : b1, i1 = i0 + per < b1 ? i0 + per : b1;
+  for (int64_t i = i0 + tid % 64; i < i1; i += 64) {
+    const int e = load_expert(experts, i, i1, E);
+    if (e >= 0) atomicAdd(&next[wv][e], 1);
+  }
+  const int all = scan_experts<kSortThreads>(total, start, E, wave_tot);   // barriers inside
+  for (int e = tid; e < E; e += kSortThreads) {
+    int at = start[e] + counts[(int64_t)e * s.blocks + b];
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+      const int c = next[w][e];
+      next[w][e] = at;
+      at += c;
+    }
+  }
+  if (b == 0)
+    for (int e = tid; e <= E; e += kSortThreads) offsets[e] = start[e];
+  for (int64_t i = b0 + tid; i < b1; i += kSortThreads)
+    if (i >= all) order[i] = -1;
+  __syncthreads();
+  place_entries(experts, i0, i1, E, bits, next[wv], order, position);
+}
+
+// ---- exchange ------------------------------------------------------------------------------------
+
+constexpr int kExThreads = 256;
+constexpr int64_t kExMaxBlocks = 1 << 20;
+
+// V bytes of a row, moved by one load or store
+template <int V> struct Bytes { typedef uint32_t type __attribute__((ext_vector_type(V / 4))); };
+template <> struct Bytes<4> { typedef uint32_t type; };
+template <> struct Bytes<2> { typedef uint16_t type; };
+
+template <class T, int V>
+struct Lanes {   // V bytes as float32 values
+  static constexpr int n = V / (int)sizeof(T);
+  float v[n];
+  __device__ __forceinline__ explicit Lanes(typename Bytes<V>::type raw) {
+    struct S { T t[n]; };
+    const S s = __builtin_bit_cast(S, raw);
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] = (float)s.t[i];
+  }
+  __device__ __forceinline__ Lanes() {
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] = 0.f;
+  }
+  // rounded once to T
+  __device__ __forceinline__ typename Bytes<V>::type raw() const {
+    struct S { T t[n]; } s;
+#pragma unroll
+    for (int i = 0; i < n; ++i) s.t[i] = (T)v[i];
+    return __builtin_bit_cast(typename Bytes<V>::type, s);
+  }
+};
+
+struct ExArgs {
+  int64_t n_tokens;
+  int64_t n_rows;          // n_tokens * top: positions outside [0, n_rows) are skipped
+  int32_t top;
+  int32_t chunks;          // V-byte pieces of a row
+  int32_t lanes;           // lanes that share a token: a power of two, at most 64
+  const int32_t *position;
+};
+
+__device__ __forceinline__ int64_t row_at(const ExArgs &a, int64_t t, int j) {
+  const int32_t p = j < a.top ? a.position[t * a.top + j] : -1;
+  return (uint32_t)p < (uint64_t)a.n_rows ? p : -1;
+}
+
+template <int V>
+__global__ __launch_bounds__(kExThreads) void k_dispatch(ExArgs a, const typename Bytes<V>::type *x,
+                                                         typename Bytes<V>::type *rows) {
+  const int in = threadIdx.x % a.lanes;
+  const int64_t per = kExThreads / a.lanes;
+  for (int64_t t = blockIdx.x * per + threadIdx.x / a.lanes; t < a.n_tokens; t += gridDim.x * per)
+    for (int c = in; c < a.chunks; c += a.lanes) {
+      const auto v = x[t * a.chunks + c];
+      for (int j = 0; j < a.top; ++j) {
+        const int64_t p = row_at(a, t, j);
+        if (p >= 0) rows[p * a.chunks + c] = v;
+      }
+    }
+}
+
+// y[t] = sum_j w[t][j] rows[position[t][j]] (weights NULL: every w is 1), J rows in flight together
+template <class T, int V, int J>
+__global__ __launch_bounds__(kExThreads) void k_combine(ExArgs a, const typename Bytes<V>::type *rows,
+                                                        const float *weights, typename Bytes<V>::type *y) {
+  using L = Lanes<T, V>;
+  const int in = threadIdx.x % a.lanes;
+  const int64_t per = kExThreads / a.lanes;
+  for (int64_t t = blockIdx.x * per + threadIdx.x / a.lanes; t < a.n_tokens; t += gridDim.x * per)
+    for (int c = in; c < a.chunks; c += a.lanes) {
+      L sum;
+      for (int j0 = 0; j0 < a.top; j0 += J) {
+        int64_t p[J];
+        float w[J];
+        typename Bytes<V>::type r[J];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          p[j] = row_at(a, t, j0 + j);
+          w[j] = weights && j0 + j < a.top ? weights[t * a.top + j0 + j] : 1.f;
+        }
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+          if (p[j] >= 0) r[j] = rows[p[j] * a.chunks + c];
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+          if (p[j] >= 0) {
+            const L v(r[j]);
+#pragma unroll
+            for (int i = 0; i < L::n; ++i) sum.v[i] = fmaf(w[j], v.v[i], sum.v[i]);
+          }
+      }
+      y[t * a.chunks + c] = sum.raw();
+    }
+}
+
+// d_rows[position[t][j]] = w[t][j] dy[t];  d_weights[t][j] = dy[t] . rows[position[t][j]] (0 for a dropped
+// entry).  The token's lanes sum their products over the row, then with each other.
+template <class T, int V, int J>
+__global__ __launch_bounds__(kExThreads) void k_combine_backward(ExArgs a, const typename Bytes<V>::type *dy,
+                                                                 const typename Bytes<V>::type *rows,
+                                                                 const float *weights,
+                                                                 typename Bytes<V>::type *d_rows, float *d_weights) {
+  using L = Lanes<T, V>;
+  const int in = threadIdx.x % a.lanes;
+  const int64_t per = kExThreads / a.lanes;
+  for (int64_t t0 = blockIdx.x * per; t0 < a.n_tokens; t0 += gridDim.x * per) {
+    const int64_t t = t0 + threadIdx.x / a.lanes;   // the group sums below need every lane
+    const bool live = t < a.n_tokens;
+    for (int j0 = 0; j0 < a.top; j0 += J) {
+      int64_t p[J];
+      float w[J], dot[J];
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        p[j] = live ? row_at(a, t, j0 + j) : -1;
+        w[j] = live && j0 + j < a.top ? weights[t * a.top + j0 + j] : 0.f;
+        dot[j] = 0.f;
+      }
+      if (live)
+        for (int c = in; c < a.chunks; c += a.lanes) {
+          const L g(dy[t * a.chunks + c]);
+          typename Bytes<V>::type r[J];
+#pragma unroll
+          for (int j = 0; j < J; ++j)
+            if (p[j] >= 0) r[j] = rows[p[j] * a.chunks + c];
+#pragma unroll
+          for (int j = 0; j < J; ++j)
+            if (p[j] >= 0) {
+              const L v(r[j]);
+              L d;
+#pragma unroll
+              for (int i = 0; i < L::n; ++i) {
+                dot[j] = fmaf(g.v[i], v.v[i], dot[j]);
+                d.v[i] = w[j] * g.v[i];
+              }
+              d_rows[p[j] * a.chunks + c] = d.raw();
+            }
+        }
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const float s = group_add(dot[j], a.lanes);
+        if (live && in == 0 && j0 + j < a.top) d_weights[t * a.top + j0 + j] = s;
+      }
+    }
+  }
+}
+
+// ---- host ----------------------------------------------------------------------------------------
+
+int check_shape(const char *who, int32_t n_tokens, int32_t top, int32_t width, int32_t dtype) {
+  if (n_tokens < 0) return report(SVT_EINVAL, "%s: n_tokens %d < 0", who, n_tokens);
+  if (top < 1 || top > SVT_MAX_TOP) return report(SVT_EINVAL, "%s: top %d out of [1, %d]", who, top, SVT_MAX_TOP);
+  if ((int64_t)n_tokens * top > kMaxEntries)
+    return report(SVT_EINVAL, "%s: %lld entries, more than 2^30", who, (long long)n_tokens * top);
+  if (width < 1) return report(SVT_EINVAL, "%s: width %d < 1", who, width);
+  if (!elem_size(dtype)) return report(SVT_EINVAL, "%s: unknown element type %d", who, dtype);
+  return SVT_OK;
+}
+
+// the widest piece (16, 8, 4 or 2 bytes) that divides a row and every pointer's address
+int piece(int32_t width, int b, std::initializer_list<const void *> ptrs) {
+  uintptr_t bits = (uintptr_t)width * b;
+  for (const void *p : ptrs) bits |= (uintptr_t)p;
+  return (bits & 15) == 0 ? 16 : (bits & 7) == 0 ? 8 : (bits & 3) == 0 ? 4 : 2;
+}
+
+ExArgs ex_args(int32_t n_tokens, int32_t top, int32_t width, int b, int v, const int32_t *position) {
+  ExArgs a{n_tokens, (int64_t)n_tokens * top, top, (int32_t)((int64_t)width * b / v), 1, position};
+  while (a.lanes < 64 && a.lanes < a.chunks) a.lanes *= 2;
+  return a;
+}
+
+unsigned ex_grid(const ExArgs &a) {
+  const int64_t per = kExThreads / a.lanes, n = (a.n_tokens + per - 1) / per;
+  return (unsigned)(n < kExMaxBlocks ? n : kExMaxBlocks);
+}
+
+// calls f with the piece size as a constant
+template <class F>
+void with_piece(int v, F f) {
+  switch (v) {
+    case 16: f(std::integral_constant<int, 16>{}); break;
+    case 8: f(std::integral_constant<int, 8>{}); break;
+    case 4: f(std::integral_constant<int, 4>{}); break;
+    default: f(std::integral_constant<int, 2>{}); break;
+  }
+}
+
+// calls f with the number of rows in flight for `top` as a constant
+template <class F>
+void with_batch(int top, F f) {
+  if (top == 1) f(std::integral_constant<int, 1>{});
+  else if (top == 2) f(std::integral_constant<int, 2>{});
+  else f(std::integral_constant<int, 4>{});
+}
+
+int combine(const char *who, int32_t n_tokens, int32_t top, int32_t width, int32_t dtype, const void *rows,
+            const int32_t *position, const float *weights, void *y, void *hip_stream) {
+  int rc = check_shape(who, n_tokens, top, width, dtype);
+  if (rc != SVT_OK || n_tokens == 0) return rc;
+  if (!rows || !position || !y) return report(SVT_EINVAL, "%s: NULL input or output", who);
+  const int b = elem_size(dtype);
+  if (misaligned(rows, b) || misaligned(y, b) || misaligned(position, 4) || misaligned(weights, 4))
+    return report(SVT_EINVAL, "%s: misaligned input or output", who);
+  const size_t nt = (size_t)n_tokens * width * b, nk = (size_t)n_tokens * top * 4;
+  if (overlap(y, nt, rows, nt * top) || overlap(y, nt, position, nk) || overlap(y, nt, weights, nk))
+    return report(SVT_EINVAL, "%s: the output overlaps an input", who);
+  const int v = piece(width, b, {rows, y});
+  const ExArgs a = ex_args(n_tokens, top, width, b, v, position);
+  with_type(dtype, [&](auto ty) {
+    using T = decltype(ty);
+    with_piece(v, [&](auto pv) {
+      constexpr int V = decltype(pv)::value;
+      if constexpr (V >= (int)sizeof(T))
+        with_batch(top, [&](auto batch) {
+          using B = typename Bytes<V>::type;
+          k_combine<T, V, decltype(batch)::value><<<ex_grid(a), kExThreads, 0, (hipStream_t)hip_stream>>>(
+              a, (const B *)rows, weights, (B *)y);
+        });
+    });
+  });
+  return launched(who);
+}
+
+}  // namespace
+
+}  // namespace svt
+
+using namespace svt;
+
+static int check_sort(const char *who, int32_t n_tokens, int32_t top, int32_t n_experts) {
+  const int rc = check_shape(who, n_tokens, top, 1, SVT_F32);
+  if (rc != SVT_OK) return rc;
+  if (n_experts < 1 || n_experts > SVT_MAX_EXPERTS)
+    return report(SVT_EINVAL, "%s: n_experts %d out of [1, %d]", who, n_experts, SVT_MAX_EXPERTS);
+  return SVT_OK;
+}
+
+static size_t sort_bytes(int64_t n, int32_t n_experts) {
+  return n <= kOneEntries ? 0 : ((size_t)sort_shape(n).blocks + 1) * n_experts * 4;
+}
+
+extern "C" size_t svt_expert_sort_workspace_size(int32_t n_tokens, int32_t top, int32_t n_experts) {
+  (void)report(SVT_OK, "%s", "");
+  if (check_sort("svt_expert_sort_workspace_size", n_tokens, top, n_experts) != SVT_OK) return 0;
+  return sort_bytes((int64_t)n_tokens * top, n_experts);
+}
+
+extern "C" int svt_expert_sort(int32_t n_tokens, int32_t top, int32_t n_experts, const int32_t *experts,
+                               int32_t *offsets, int32_t *order, int32_t *position, void *workspace,
+                               size_t workspace_bytes, void *hip_stream) {
+  const char *who = "svt_expert_sort";
+  (void)report(SVT_OK, "%s", "");
+  const int rc = check_sort(who, n_tokens, top, n_experts);
+  if (rc != SVT_OK) return rc;
+  const int64_t n = (int64_t)n_tokens * top;
+  if (!offsets || (n > 0 && (!experts || !order || !position)))
+    return report(SVT_EINVAL, "%s: NULL input or output", who);
+  if (misaligned(experts, 4) || misaligned(offsets, 4) || misaligned(order, 4) || misaligned(position, 4) ||
+      misaligned(workspace, 4))
+    return report(SVT_EINVAL, "%s: misaligned input, output or workspace", who);
+  const size_t need = sort_bytes(n, n_experts), ne = (size_t)n * 4, no = ((size_t)n_experts + 1) * 4;
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return report(SVT_EINVAL, "%s: workspace of %zu bytes, needs %zu", who, workspace ? workspace_bytes : (size_t)0, need);
+  const void *at[5] = {experts, offsets, order, position, workspace};
+  const size_t bytes[5] = {ne, no, ne, ne, need};
+  for (int i = 0; i < 5; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlap(at[i], bytes[i], at[j], bytes[j]))
+        return report(SVT_EINVAL, "%s: input, outputs and workspace overlap", who);
+  int bits = 0;
+  while ((1 << bits) < n_experts) ++bits;
+  hipStream_t s = (hipStream_t)hip_stream;
+  if (n <= kOneEntries) {
+    k_sort_one<<<1, kOneThreads, 0, s>>>(experts, n, n_experts, bits, offsets, order, position);
+    return launched(who);
+  }
+  const SortShape sh = sort_shape(n);
+  int32_t *counts = (int32_t *)workspace, *totals = counts + (size_t)sh.blocks * n_experts;
+  k_sort_count<<<sh.blocks, kSortThreads, 0, s>>>(experts, sh, n_experts, counts);
+  k_sort_scan<<<n_experts, kSortThreads, 0, s>>>(counts, sh.blocks, totals);
+  k_sort_place<<<sh.blocks, kSortThreads, 0, s>>>(experts, sh, n_experts, bits, counts, totals, offsets, order,
+                                                  position);
+  return launched(who);
+}
+
+extern "C" int svt_expert_dispatch(int32_t n_tokens, int32_t top, int32_t width, int32_t dtype, const void *x,
+                                   const int32_t *position, void *rows, void *hip_stream) {
+  const char *who = "svt_expert_dispatch";
+  (void)report(SVT_OK, "%s", "");
+  const int rc = check_shape(who, n_tokens, top, width, dtype);
+  if (rc != SVT_OK || n_tokens == 0) return rc;
+  if (!x || !position || !rows) return report(SVT_EINVAL, "%s: NULL input or output", who);
+  const int b = elem_size(dtype);
+  if (misaligned(x, b) || misaligned(rows, b) || misaligned(position, 4))
+    return report(SVT_EINVAL, "%s: misaligned input or output", who);
+  const size_t nt = (size_t)n_tokens * width * b, nk = (size_t)n_tokens * top * 4;
+  if (overlap(rows, nt * top, x, nt) || overlap(rows, nt * top, position, nk))
+    return report(SVT_EINVAL, "%s: the output overlaps an input", who);
+  const int v = piece(width, b, {x, rows});
+  const ExArgs a = ex_args(n_tokens, top, width, b, v, position);
+  with_piece(v, [&](auto pv) {
+    constexpr int V = decltype(pv)::value;
+    using B = typename Bytes<V>::type;
+    k_dispatch<V><<<ex_grid(a), kExThreads, 0, (hipStream_t)hip_stream>>>(a, (const B *)x, (B *)rows);
+  });
+  return launched(who);
+}
+
+extern "C" int svt_expert_dispatch_backward(int32_t n_tokens, int32_t top, int32_t width, int32_t dtype,
+                                            const void *d_rows, const int32_t *position, void *dx, void *hip_stream) {
+  (void)report(SVT_OK, "%s", "");
+  return combine("svt_expert_dispatch_backward", n_tokens, top, width, dtype, d_rows, position, nullptr, dx, hip_stream);
+}
+
+extern "C" int svt_expert_combine(int32_t n_tokens, int32_t top, int32_t width, int32_t dtype, const void *rows,
+                                  const int32_t *position, const float *weights, void *y, void *hip_stream) {
+  (void)report(SVT_OK, "%s", "");
+  return combine("svt_expert_combine", n_tokens, top, width, dtype, rows, position, weights, y, hip_stream);
+}
+
+extern "C" int svt_expert_combine_backward(int32_t n_tokens, int32_t top, int32_t width, int32_t dtype, const void *dy,
+                                           const void *rows, const int32_t *position, const float *weights,
+                                           void *d_rows, float *d_weights, void *hip_stream) {
+  const char *who = "svt_expert_combine_backward";
+  (void)report(SVT_OK, "%s", "");
+  const int rc = check_shape(who, n_tokens, top, width, dtype);
+  if (rc != SVT_OK || n_tokens == 0) return rc;
+  if (!dy || !rows || !position || !weights || !d_rows || !d_weights)
+    return report(SVT_EINVAL, "%s: NULL input or output", who);
+  const int b = elem_size(dtype);
+  if (misaligned(dy, b) || misaligned(rows, b) || misaligned(d_rows, b) || misaligned(position, 4) ||
+      misaligned(weights, 4) || misaligned(d_weights, 4))
+    return report(SVT_EINVAL, "%s: misaligned input or output", who);
+  const size_t nt = (size_t)n_tokens * width * b, nk = (size_t)n_tokens * top * 4;
+  const void *in[4] = {dy, rows, position, weights};
+  const size_t in_bytes[4] = {nt, nt * top, nk, nk};
+  for (int i = 0; i < 4; ++i)
+    if (overlap(d_rows, nt * top, in[i], in_bytes[i]) || overlap(d_weights, nk, in[i], in_bytes[i]))
+      return report(SVT_EINVAL, "%s: an output overlaps an input", who);
+  if (overlap(d_rows, nt * top, d_weights, nk)) return report(SVT_EINVAL, "%s: the outputs overlap", who);
+  const int v = piece(width, b, {dy, rows, d_rows});
+  const ExArgs a = ex_args(n_tokens, top, width, b, v, position);
+  with_type(dtype, [&](auto ty) {
+    using T = decltype(ty);
+    with_piece(v, [&](auto pv) {
+      constexpr int V = decltype(pv)::value;
+      if constexpr (V >= (int)sizeof(T))
+        with_batch(top, [&](auto batch) {
+          using B = typename Bytes<V>::type;
+          k_combine_backward<T, V, decltype(batch)::value><<<ex_grid(a), kExThreads, 0, (hipStream_t)hip_stream>>>(
+              a, (const B *)dy, (const B *)rows, weights, (B *)d_rows, d_weights);
+        });
+    });
+  });
+  return launched(who);
+}

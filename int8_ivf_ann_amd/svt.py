@@ -24,12 +24,18 @@ SVT_OPT_MERGE_FROM_SLOTS, SVT_OPT_FORCE_REDO = 1, 2
 SVT_MAX_MASK_GROUPS = 4
 SVT_NOALLOC_SCRATCH_BYTES = 256 << 20
 SVT_RERANK_MAX_EXPERTS, SVT_RERANK_MAX_UNITS, SVT_RERANK_MAX_CAND, SVT_RERANK_MAX_OUT = 8, 64, 4096, 2048
+SVT_F32, SVT_F16, SVT_BF16 = 0, 1, 2
+SVT_ACT_NONE, SVT_ACT_RELU = 0, 1
+SVT_MAX_EXPERTS, SVT_MAX_TOP = 512, 16
 _PATHS = {"auto": SVT_PATH_AUTO, "query": SVT_PATH_QUERY, "tile": SVT_PATH_TILE, "large_k": SVT_PATH_LARGE_K}
 
 #: every symbol include/svt.h declares
 EXPORTED = ("svt_index_upload", "svt_index_upload_updatable", "svt_index_insert", "svt_index_delete",
             "svt_index_resign", "svt_index_free", "svt_index_info", "svt_search_workspace_size", "svt_search_path",
-            "svt_search", "svt_search_noalloc", "svt_rerank", "svt_last_error", "svt_bloom_mask", "svt_bloom_sign", "svt_profile_enable", "svt_profile_read")
+            "svt_search", "svt_search_noalloc", "svt_rerank", "svt_route", "svt_route_backward",
+            "svt_expert_sort_workspace_size", "svt_expert_sort", "svt_expert_dispatch", "svt_expert_dispatch_backward",
+            "svt_expert_combine", "svt_expert_combine_backward", "svt_quant_pack_size", "svt_quant_pack",
+            "svt_quant_linear", "svt_last_error", "svt_bloom_mask", "svt_bloom_sign", "svt_profile_enable", "svt_profile_read")
 
 
 class SvtError(RuntimeError):
@@ -66,6 +72,14 @@ class svt_rerank_net(ctypes.Structure):
     _fields_ = [("n_experts", ctypes.c_int32), ("hidden", ctypes.c_int32), ("gate_w", ctypes.c_void_p),
                 ("gate_b", ctypes.c_void_p), ("w1", ctypes.c_void_p), ("b1", ctypes.c_void_p),
                 ("w2", ctypes.c_void_p), ("b2", ctypes.c_void_p)]
+
+
+class svt_quant_weights(ctypes.Structure):
+    """Weights in 4 bits (see svt_quant_pack); ``buffer`` keeps the packed tensor alive."""
+    _fields_ = [("n_matrices", ctypes.c_int32), ("n_out", ctypes.c_int32), ("n_in", ctypes.c_int32),
+                ("group", ctypes.c_int32), ("scale_type", ctypes.c_int32), ("has_zeros", ctypes.c_int32),
+                ("packed", ctypes.c_void_p), ("packed_bytes", ctypes.c_size_t)]
+    buffer = None
 
 
 def make_options(path="auto", pool_keys: int = 0, flags: int = 0, mask_groups: int = 0) -> svt_search_options:
@@ -115,13 +129,28 @@ def lib():
     L.svt_search.argtypes = [vp, i32, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     L.svt_search_noalloc.argtypes = [vp, i32, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp, vp, vp]
     L.svt_rerank.argtypes = [vp, i32, vp, vp, i32, vp, ctypes.POINTER(svt_rerank_net), i32, vp, vp, vp, vp]
+    qw = ctypes.POINTER(svt_quant_weights)
+    L.svt_route.argtypes = [i32, i32, i32, i32, vp, i32, vp, vp, vp]
+    L.svt_route_backward.argtypes = [i32, i32, i32, i32, vp, i32, vp, vp, vp, vp, vp]
+    L.svt_expert_sort_workspace_size.argtypes = [i32, i32, i32]
+    L.svt_expert_sort.argtypes = [i32, i32, i32, vp, vp, vp, vp, vp, sz, vp]
+    L.svt_expert_dispatch.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp]
+    L.svt_expert_dispatch_backward.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp]
+    L.svt_expert_combine.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp]
+    L.svt_expert_combine_backward.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp]
+    L.svt_quant_pack_size.argtypes = [qw]
+    L.svt_quant_pack.argtypes = [qw, vp, vp, vp, vp]
+    L.svt_quant_linear.argtypes = [i32, i32, vp, qw, vp, vp, i32, i32, vp, vp]
     L.svt_last_error.restype = ctypes.c_char_p
     L.svt_bloom_mask.argtypes = [vp, i32, i32, i32, vp]
     L.svt_bloom_sign.argtypes = [vp, i64, i32, i32, i32, vp, i32]
     L.svt_profile_enable.argtypes = [ctypes.c_int]
     L.svt_profile_read.argtypes = [vp, vp, i32, vp, vp]
+    sizes = ("svt_search_workspace_size", "svt_expert_sort_workspace_size", "svt_quant_pack_size")
     for name in EXPORTED:
-        if name not in ("svt_search_workspace_size", "svt_last_error"):
+        if name in sizes:
+            getattr(L, name).restype = sz
+        elif name != "svt_last_error":
             getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -395,6 +424,268 @@ def svt_rerank(handle, queries, cand_ids, net, k_out: int, query_scales=None, ou
                             ctypes.byref(cnet), k_out, _t_ptr(out_ids), _t_ptr(out_scores), _t_ptr(out_counts),
                             _stream_ptr(stream)))
     return out_ids, out_scores, out_counts
+
+
+# ------------------------------------------------------------------------------------------------
+# Routed experts: the calls of include/svt.h on torch tensors.  Inputs and outputs are dense tensors on one
+# device; outputs not passed in are allocated on the call's stream.  Gradients are calls of their own.
+_TYPES = None
+
+
+def _types():
+    global _TYPES
+    if _TYPES is None:
+        import torch
+        _TYPES = {torch.float32: SVT_F32, torch.float16: SVT_F16, torch.bfloat16: SVT_BF16}
+    return _TYPES
+
+
+class _Run:
+    """The device and stream of one call: inside, torch allocates on them; enters as the stream's handle.
+    Tensors on another device than the current one, and ``stream`` (default: the device's current one),
+    are made current for the call."""
+    __slots__ = ("ctx", "handle")
+
+    def __init__(self, dev, stream):
+        import torch
+        self.ctx = None
+        if stream is not None:
+            if stream.device != dev:
+                raise ValueError(f"stream: on {stream.device}, expected {dev}")
+            self.ctx = torch.cuda.stream(stream)   # also makes the stream's device current
+        elif torch.cuda.current_device() != dev.index:
+            self.ctx = torch.cuda.device(dev)
+        self.handle = (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _rows_of(name, t, dims=2):
+    """(shape, element type, device) of a dense float tensor of ``dims`` dimensions on a device."""
+    if not hasattr(t, "data_ptr") or t.dim() != dims:
+        raise ValueError(f"{name}: expected a {dims}-D tensor")
+    code = _types().get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name}: dtype {t.dtype} not in {[str(d) for d in _types()]}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: not a device tensor")
+    shape = tuple(t.shape)
+    if max(shape) >= 2 ** 31:
+        raise ValueError(f"{name}: shape {shape} beyond 2^31 - 1")
+    return shape, code, t.device
+
+
+def _check_dense(name, t, dtype, shape, dev):
+    """_check_tensor for one dtype, without its formatting on the way to success."""
+    if t is not None and getattr(t, "dtype", None) is dtype and t.shape == shape and t.is_contiguous() and \
+            t.device == dev:
+        return
+    _check_tensor(name, t, (dtype,), shape, dev)
+
+
+def _out(name, t, dtype, shape, dev):
+    import torch
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _check_dense(name, t, dtype, shape, dev)
+    return t
+
+
+def _entries(name, t, dev=None):
+    """(n_tokens, top, device) of an int32 tensor [n_tokens, top]."""
+    import torch
+    if not hasattr(t, "data_ptr") or t.dim() != 2:
+        raise ValueError(f"{name}: expected a 2-D tensor [n_tokens, top]")
+    T, K = t.shape
+    _check_dense(name, t, torch.int32, (T, K), t.device if dev is None else dev)
+    if T * K > 2 ** 30:
+        raise ValueError(f"{name}: {T * K} entries, more than 2^30")
+    return T, K, t.device
+
+
+def svt_route(logits, top: int, renormalise: bool = True, out_experts=None, out_weights=None, stream=None):
+    """The ``top`` best experts of each token: logits [T, E] (float32, float16, bfloat16) -> (experts int32
+    [T, top], weights float32 [T, top]), by (logit desc, expert asc).  Weights are the softmax over the chosen
+    experts (``renormalise``) or over all open ones; -inf and NaN shut an expert; -1 and 0 where fewer than
+    ``top`` are open."""
+    import torch
+    (T, E), code, dev = _rows_of("logits", logits)
+    with _Run(dev, stream) as s:
+        out_experts = _out("out_experts", out_experts, torch.int32, (T, top), dev)
+        out_weights = _out("out_weights", out_weights, torch.float32, (T, top), dev)
+        _check(lib().svt_route(T, E, top, code, logits.data_ptr(), int(renormalise), out_experts.data_ptr(),
+                               out_weights.data_ptr(), s))
+    return out_experts, out_weights
+
+
+def svt_route_backward(logits, experts, weights, d_weights, renormalise: bool = True, out=None, stream=None):
+    """The gradient in the logits of svt_route's weights: logits [T, E], svt_route's experts and weights and
+    the weights' gradient d_weights (float32 [T, top]) -> d_logits [T, E] of the logits' dtype."""
+    import torch
+    (T, E), code, dev = _rows_of("logits", logits)
+    _, K, _ = _entries("experts", experts, dev)
+    _check_dense("experts", experts, torch.int32, (T, K), dev)
+    _check_dense("weights", weights, torch.float32, (T, K), dev)
+    _check_dense("d_weights", d_weights, torch.float32, (T, K), dev)
+    with _Run(dev, stream) as s:
+        out = _out("out", out, logits.dtype, (T, E), dev)
+        _check(lib().svt_route_backward(T, E, K, code, logits.data_ptr(), int(renormalise), experts.data_ptr(),
+                                        weights.data_ptr(), d_weights.data_ptr(), out.data_ptr(), s))
+    return out
+
+
+def svt_expert_sort(experts, n_experts: int, offsets=None, order=None, position=None, workspace=None, stream=None):
+    """Entries grouped by expert, in their own order: experts int32 [T, top] (outside [0, n_experts): dropped)
+    -> (offsets int32 [n_experts + 1], order int32 [T * top], position int32 [T, top]).  ``order`` names the
+    entry of each sorted row (-1 past offsets[n_experts]), ``position`` the sorted row of each entry (-1:
+    dropped)."""
+    import torch
+    T, K, dev = _entries("experts", experts)
+    L = lib()
+    with _Run(dev, stream) as s:
+        offsets = _out("offsets", offsets, torch.int32, (n_experts + 1,), dev)
+        order = _out("order", order, torch.int32, (T * K,), dev)
+        position = _out("position", position, torch.int32, (T, K), dev)
+        need = L.svt_expert_sort_workspace_size(T, K, n_experts)
+        if workspace is not None:
+            _check_tensor("workspace", workspace, (torch.uint8,), (workspace.numel(),), dev)
+        elif need:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+        _check(L.svt_expert_sort(T, K, n_experts, experts.data_ptr(), offsets.data_ptr(), order.data_ptr(),
+                                 position.data_ptr(), None if workspace is None else workspace.data_ptr(),
+                                 0 if workspace is None else workspace.numel(), s))
+    return offsets, order, position
+
+
+def svt_expert_dispatch(x, position, out=None, stream=None):
+    """Each token's row to its sorted rows: x [T, D], position int32 [T, top] -> rows [T * top, D].  Rows that
+    no entry names (behind the last one) are left as they were."""
+    (T, D), code, dev = _rows_of("x", x)
+    _, K, _ = _entries("position", position, dev)
+    if position.shape[0] != T:
+        raise ValueError(f"position: shape {tuple(position.shape)} for {T} tokens")
+    with _Run(dev, stream) as s:
+        out = _out("out", out, x.dtype, (T * K, D), dev)
+        _check(lib().svt_expert_dispatch(T, K, D, code, x.data_ptr(), position.data_ptr(), out.data_ptr(), s))
+    return out
+
+
+def _gather_sum(fn, name, rows, position, weights, out, stream):
+    import torch
+    (R, D), code, dev = _rows_of(name, rows)
+    T, K, _ = _entries("position", position, dev)
+    if R != T * K:
+        raise ValueError(f"{name}: {R} rows for {T} tokens of {K} entries")
+    args = ()
+    if fn == "svt_expert_combine":
+        if weights is not None:
+            _check_dense("weights", weights, torch.float32, (T, K), dev)
+        args = (None if weights is None else weights.data_ptr(),)
+    with _Run(dev, stream) as s:
+        out = _out("out", out, rows.dtype, (T, D), dev)
+        _check(getattr(lib(), fn)(T, K, D, code, rows.data_ptr(), position.data_ptr(), *args, out.data_ptr(), s))
+    return out
+
+
+def svt_expert_dispatch_backward(d_rows, position, out=None, stream=None):
+    """The gradient of svt_expert_dispatch: d_rows [T * top, D], position [T, top] -> dx [T, D], the sum of a
+    token's rows."""
+    return _gather_sum("svt_expert_dispatch_backward", "d_rows", d_rows, position, None, out, stream)
+
+
+def svt_expert_combine(rows, position, weights=None, out=None, stream=None):
+    """The experts' rows back to their tokens: rows [T * top, D], position int32 [T, top], weights float32 [T,
+    top] (None: ones) -> y [T, D], the weighted sum of a token's rows."""
+    return _gather_sum("svt_expert_combine", "rows", rows, position, weights, out, stream)
+
+
+def svt_expert_combine_backward(dy, rows, position, weights, out_rows=None, out_weights=None, stream=None):
+    """The gradients of svt_expert_combine: dy [T, D], its rows [T * top, D], position and weights -> (d_rows
+    [T * top, D], d_weights float32 [T, top]).  Rows that no entry names are left as they were."""
+    import torch
+    (T, D), code, dev = _rows_of("dy", dy)
+    _, K, _ = _entries("position", position, dev)
+    _check_dense("position", position, torch.int32, (T, K), dev)
+    _check_dense("rows", rows, dy.dtype, (T * K, D), dev)
+    _check_dense("weights", weights, torch.float32, (T, K), dev)
+    with _Run(dev, stream) as s:
+        out_rows = _out("out_rows", out_rows, dy.dtype, (T * K, D), dev)
+        out_weights = _out("out_weights", out_weights, torch.float32, (T, K), dev)
+        _check(lib().svt_expert_combine_backward(T, K, D, code, dy.data_ptr(), rows.data_ptr(), position.data_ptr(),
+                                                 weights.data_ptr(), out_rows.data_ptr(), out_weights.data_ptr(), s))
+    return out_rows, out_weights
+
+
+def svt_quant_pack(nibbles, scales, zeros, n_in: int, group: int, packed=None, stream=None) -> svt_quant_weights:
+    """Weights W[n, k] = scales[n, k // group] * (q[n, k] - zeros[n, k // group]) in the layout svt_quant_linear
+    reads.  nibbles uint8 [M, N, (n_in + 1) // 2] (or [N, ..] for one matrix): q of input 2 i in the low half of
+    byte i; scales [M, N, ceil(n_in / group)] float32, float16 or bfloat16; zeros uint8 of the same shape, or
+    None (every zero point 8).  group: 32, 64 or 128."""
+    import torch
+    if hasattr(nibbles, "dim") and nibbles.dim() == 2:
+        nibbles = nibbles[None]
+        scales = scales[None] if hasattr(scales, "dim") else scales
+        zeros = zeros[None] if hasattr(zeros, "dim") else zeros
+    (M, N, _), code, dev = _rows_of("scales", scales, 3)
+    groups = -(-int(n_in) // int(group)) if group > 0 else 0
+    _check_tensor("nibbles", nibbles, (torch.uint8,), (M, N, (n_in + 1) // 2), dev)
+    _check_tensor("scales", scales, (scales.dtype,), (M, N, groups), dev)
+    _check_tensor("zeros", zeros, (torch.uint8,), (M, N, groups), dev, nullable=True)
+    w = svt_quant_weights(M, N, n_in, group, code, int(zeros is not None), None, 0)
+    need = lib().svt_quant_pack_size(ctypes.byref(w))
+    if need == 0:
+        raise SvtError(SVT_EUNSUPPORTED if group not in (32, 64, 128) else SVT_EINVAL, svt_last_error())
+    with _Run(dev, stream) as s:
+        packed = _out("packed", packed, torch.uint8, (need,), dev)
+        w.packed, w.packed_bytes, w.buffer = packed.data_ptr(), need, packed
+        _check(lib().svt_quant_pack(ctypes.byref(w), nibbles.data_ptr(), scales.data_ptr(),
+                                    None if zeros is None else zeros.data_ptr(), s))
+    return w
+
+
+_ACTIVATIONS = {"none": SVT_ACT_NONE, "relu": SVT_ACT_RELU}
+
+
+def svt_quant_linear(x, weights: svt_quant_weights, offsets=None, bias=None, activation: str = "none", out=None,
+                     out_dtype=None, stream=None):
+    """y = act(x W^T + bias) with svt_quant_pack's weights: x [R, n_in] -> y [R, n_out] of ``out_dtype`` (x's
+    dtype, the default, or float32).  Without ``offsets`` the one matrix serves every row; with offsets int32
+    [M + 1] (svt_expert_sort's) matrix e serves rows offsets[e] .. offsets[e + 1] - 1 and rows past the last
+    stay as they were.  bias: float32 [M, n_out], or None."""
+    import torch
+    (R, K), code, dev = _rows_of("x", x)
+    M, N = weights.n_matrices, weights.n_out
+    if K != weights.n_in:
+        raise ValueError(f"x: shape {tuple(x.shape)} for weights of {weights.n_in} inputs")
+    if weights.buffer is None or weights.buffer.device != dev:
+        raise ValueError(f"weights: not packed on {dev}")
+    if offsets is not None:
+        _check_dense("offsets", offsets, torch.int32, (M + 1,), dev)
+    if bias is not None:
+        if M == 1 and bias.dim() == 1:
+            bias = bias[None]
+        _check_dense("bias", bias, torch.float32, (M, N), dev)
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation: {activation!r} not in {sorted(_ACTIVATIONS)}")
+    out_dtype = out.dtype if out is not None else x.dtype if out_dtype is None else out_dtype
+    if out_dtype not in _types():
+        raise ValueError(f"out: dtype {out_dtype} not in {[str(d) for d in _types()]}")
+    with _Run(dev, stream) as s:
+        out = _out("out", out, out_dtype, (R, N), dev)
+        _check(lib().svt_quant_linear(R, code, x.data_ptr(), ctypes.byref(weights),
+                                      None if offsets is None else offsets.data_ptr(),
+                                      None if bias is None else bias.data_ptr(), _ACTIVATIONS[activation],
+                                      _types()[out_dtype], out.data_ptr(), s))
+    return out
 
 
 def svt_profile_enable(on) -> None:
