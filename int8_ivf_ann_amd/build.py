@@ -15,7 +15,9 @@ DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 # (source, holds device code); svt_api.cpp is host-only
 SOURCES = (("svt_kernels.hip", True), ("svt_tile.hip", True), ("svt_noalloc.hip", True), ("svt_rerank.hip", True),
            ("svt_largek.hip", True), ("svt_api.cpp", False), ("experts/svt_route.hip", True),
-           ("experts/svt_exchange.hip", True), ("experts/svt_quant.hip", True))
+           ("experts/svt_exchange.hip", True), ("experts/svt_quant.hip", True),
+           ("experts/svt_linear_f32.hip", True), ("experts/svt_linear_f16.hip", True),
+           ("experts/svt_linear_bf16.hip", True))
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-result", "-I", os.path.join(ROOT, "include"), "-I", CSRC]
 
 

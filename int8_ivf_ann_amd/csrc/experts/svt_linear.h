@@ -1,0 +1,564 @@
+// svt_linear.h - the kernel of products with 4-bit weights (svt_linear_*.hip instantiate it, one file per type
+// of the rows; svt_quant.hip packs the weights, checks arguments and calls).
+//
+//   W[n][k] = s[n][g] (q[n][k] - z[n][g]),  g = k / group,  q in 0 .. 15
+//   y[r][n] = act(bias[n] + sum_k x[r][k] W[n][k])
+//           = act(bias[n] + sum_g s[n][g] (sum_{k in g} x[r][k] q[n][k] - z[n][g] sum_{k in g} x[r][k]))
+//
+// The inner sums run on the matrix cores (v_mfma_f32_16x16x32, 16 outputs x 16 rows x 32 k) with q as bf16
+// or f16, which hold 0 .. 15 exactly, and float32 accumulation: no weight is rounded, and s and z are
+// applied to float32 group sums.  sum x comes from the same instruction with a matrix of ones, in the
+// lanes that need it.
+// q reaches bf16/f16 two at a time: the byte 0000qqqq read as an 8-bit float with 3 mantissa bits is
+// q * 2^-9 (its subnormals and its first binade share one spacing), and v_cvt_scalef32_pk_* turns two such
+// bytes into two exact numbers with the scale 2^9.
+// float32 rows are split into three bf16 parts of 8 bits each (24 bits: exact), one instruction per part.
+#pragma once
+
+#include <algorithm>
+#include <type_traits>
+
+#include "svt_experts.h"
+
+namespace svt {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef f16 f16x2 __attribute__((ext_vector_type(2)));
+typedef f16 f16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kTileN = 16;        // outputs of a tile
+constexpr int kBlockK = 128;      // k of a block: 4 instructions, 16 bytes of q per lane
+constexpr int kMaxWaves = 8;
+constexpr int kGroupsAt = 1024;   // of a record: its groups, after q
+constexpr int kMaxIn = 1 << 20, kMaxOut = 1 << 19;
+
+// Layout of the packed weights: per matrix (its stride a multiple of 256 bytes) a record for each block of
+// 128 k and tile of 16 outputs, [block][tile], holding
+//   q       [lane][16]: lane l holds output l % 16, k = 128 block + 32 s + 8 (l / 16) + i for s = 0..3 in dword
+//           s, whose byte i (0..3) holds i in its low and i + 4 in its high half
+//   groups  [h][g]: what lane (., h) of the instruction's result needs, together: the scales of outputs
+//           4 h .. 4 h + 3 for group g of the block, then, where there are any, their zero points (a byte each)
+// Outputs and groups past the end have scale 0.  A wave reads whole records, and workgroups that run
+// together read neighbouring ones.
+struct QuantShape {
+  int32_t n_out, n_in, group, has_zeros;
+  int32_t tiles, blocks;
+  int32_t four, record;   // bytes of one [h][g] entry, of a record
+  size_t stride;
+};
+
+inline QuantShape quant_shape(const svt_quant_weights &w) {
+  QuantShape s;
+  s.n_out = w.n_out;
+  s.n_in = w.n_in;
+  s.group = w.group;
+  s.has_zeros = w.has_zeros;
+  s.tiles = (w.n_out + kTileN - 1) / kTileN;
+  s.blocks = (w.n_in + kBlockK - 1) / kBlockK;
+  s.four = 4 * elem_size(w.scale_type) + (w.has_zeros ? 4 : 0);
+  s.record = kGroupsAt + 4 * (kBlockK / w.group) * s.four;
+  s.stride = ((size_t)s.tiles * s.blocks * s.record + 255) & ~(size_t)255;
+  return s;
+}
+
+struct LinearArgs {
+  QuantShape s;
+  int64_t n_rows, n_units;
+  int32_t n_matrices;
+  int32_t direct;              // with offsets: a unit is a matrix (all its rows), not a block of rows
+  int32_t lds_rows;            // rows that the launch has LDS for: min(16 MT, n_rows)
+  const uint8_t *packed;
+  const int32_t *offsets;      // NULL: one matrix, every row
+  const float *bias;
+  int32_t relu, out_f32;
+  int32_t wide_store;          // four neighbouring outputs lie in one aligned piece
+  const void *x;
+  void *y;
+};
+
+// one product with rows of type T (scale type and group are those of a.s); launches on stream
+template <class T>
+void linear_rows(LinearArgs a, int32_t scale_type, hipStream_t stream);
+
+// what a 16 x 16 x 32 instruction takes for rows of type T, and how many parts a row value has
+template <class T> struct Mma;
+template <> struct Mma<bf16> {
+  typedef bf16x8 frag;
+  static constexpr int parts = 1;
+  static __device__ __forceinline__ f32x4 mul(frag w, frag x, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ frag weights(uint32_t d) {
+    struct { bf16x2 p[4]; } u;
+    const uint32_t a = d & 0x0F0F0F0Fu, b = (d >> 4) & 0x0F0F0F0Fu;
+    u.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 512.f, false);
+    u.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 512.f, true);
+    u.p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 512.f, false);
+    u.p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 512.f, true);
+    return __builtin_bit_cast(frag, u);
+  }
+};
+template <> struct Mma<f16> {
+  typedef f16x8 frag;
+  static constexpr int parts = 1;
+  static __device__ __forceinline__ f32x4 mul(frag w, frag x, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(w, x, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ frag weights(uint32_t d) {
+    struct { f16x2 p[4]; } u;
+    const uint32_t a = d & 0x0F0F0F0Fu, b = (d >> 4) & 0x0F0F0F0Fu;
+    u.p[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 512.f, false);
+    u.p[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 512.f, true);
+    u.p[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 512.f, false);
+    u.p[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 512.f, true);
+    return __builtin_bit_cast(frag, u);
+  }
+};
+template <> struct Mma<float> : Mma<bf16> {
+  static constexpr int parts = 3;
+};
+
+template <class T> struct __attribute__((packed, aligned(sizeof(T)))) Eight { T v[8]; };
+
+// the parts of 8 row values, most significant first
+template <class T>
+__device__ __forceinline__ void row_parts(const Eight<T> &r, typename Mma<T>::frag (&f)[Mma<T>::parts]) {
+  if constexpr (sizeof(T) == 2) {
+    f[0] = __builtin_bit_cast(typename Mma<T>::frag, r);
+  } else {
+    struct { uint32_t d[4]; } hi, mid, lo;
+    float a[8], b[8], c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {   // by truncation, so that no part overflows: 8 + 8 + 8 bits
+      a[i] = __uint_as_float(__float_as_uint(r.v[i]) & 0xFFFF0000u);
+      const float rest = r.v[i] - a[i];
+      b[i] = __uint_as_float(__float_as_uint(rest) & 0xFFFF0000u);
+      c[i] = rest - b[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {   // the upper halves of two floats
+      hi.d[i] = __builtin_amdgcn_perm(__float_as_uint(a[2 * i + 1]), __float_as_uint(a[2 * i]), 0x07060302u);
+      mid.d[i] = __builtin_amdgcn_perm(__float_as_uint(b[2 * i + 1]), __float_as_uint(b[2 * i]), 0x07060302u);
+      lo.d[i] = __builtin_amdgcn_perm(__float_as_uint(c[2 * i + 1]), __float_as_uint(c[2 * i]), 0x07060302u);
+    }
+    f[0] = __builtin_bit_cast(bf16x8, hi);
+    f[1] = __builtin_bit_cast(bf16x8, mid);
+    f[2] = __builtin_bit_cast(bf16x8, lo);
+  }
+}
+
+__device__ __forceinline__ int64_t row_end(const LinearArgs &a, int e) {
+  const int64_t o = a.offsets[e];
+  return o < 0 ? 0 : o > a.n_rows ? a.n_rows : o;
+}
+
+// inclusive sums over the wave's lanes: shifts inside rows of 16 lanes, then each row's last lane to the next
+// row (1 and 3), then lane 31 to the upper half
+__device__ __forceinline__ int incl_sums(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);    // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast:15
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // row_bcast:31
+  return v;
+}
+
+// With offsets: the matrix and the rows [*r0, *r1) of a unit; false if there are none.  A unit is a block of
+// `most` rows of one matrix (every wave counts the matrices' blocks up), or all rows of a matrix (direct).
+// Every lane of the wave gets the same answer.
+__device__ __forceinline__ bool find_rows(const LinearArgs &a, int64_t unit, int most, int *matrix, int64_t *r0,
+                                          int64_t *r1) {
+  if (a.direct) {
+    *matrix = (int)unit;
+    *r0 = row_end(a, (int)unit);
+    *r1 = row_end(a, (int)unit + 1);
+    return *r0 < *r1;
+  }
+  const int l = lane_id();
+  int before = 0, owner = -1, rest = 0;
+#pragma unroll 1
+  for (int e0 = 0; e0 < a.n_matrices; e0 += 64) {   // 64 matrices at a time
+    const int e = e0 + l;
+    const int64_t n = e < a.n_matrices ? row_end(a, e + 1) - row_end(a, e) : 0;
+    const int mine = n > 0 ? (int)((n + most - 1) / most) : 0;
+    const int upto = before + incl_sums(mine);
+    const uint64_t above = __ballot(upto > unit);
+    if (above != 0ull) {
+      const int at = __ffsll((long long)above) - 1;
+      owner = e0 + at;
+      rest = (int)unit - __builtin_amdgcn_readlane(upto - mine, at);
+      break;
+    }
+    before = __builtin_amdgcn_readlane(upto, 63);
+  }
+  if (owner < 0) return false;
+  const int64_t end = row_end(a, owner + 1);
+  *matrix = owner;
+  *r0 = row_end(a, owner) + (int64_t)rest * most;
+  *r1 = *r0 + most < end ? *r0 + most : end;
+  return *r0 < *r1;
+}
+
+// the [h][g] entries of a record that one lane needs
+template <class S, int NG, bool Z>
+struct Groups {
+  struct __attribute__((packed, aligned(4))) Four {
+    S s[4];
+    uint32_t z[Z ? 1 : 0];
+  } g[NG];
+};
+
+// the first `left` of four values
+template <class O>
+__device__ __forceinline__ void store_four(O *p, f32x4 v, int left, int wide) {
+  if (wide) {
+    struct __attribute__((aligned(4 * sizeof(O)))) Four { O v[4]; } f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f.v[i] = (O)v[i];
+    *reinterpret_cast<Four *>(p) = f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < left) p[i] = (O)v[i];
+  }
+}
+
+// A workgroup of WK x WN waves computes 16 NT WN outputs of a block of 16 MT rows (at most).  k goes by in
+// chunks of WK U blocks: wave (ik, in) multiplies blocks ik U .. ik U + U - 1 of a chunk for its NT output
+// tiles, with the weights in registers, straight from memory, and the rows in LDS, where every wave needs
+// them: 0 past K, and float32 rows as their three parts, split once.  While a chunk is multiplied the next
+// one's rows and weights are on their way (rows first: waiting for them leaves the weights in flight).  At
+// the end the WK waves' sums meet in LDS, added in the waves' order.
+template <class T, int WK, int U>
+struct Stage {
+  static constexpr int kChunk = WK * U * kBlockK;      // k of a chunk
+  static constexpr int kRow = kChunk * 2 + 16;         // bytes of a row of one part: lanes of one h in 64 banks
+  static constexpr int kParts = Mma<T>::parts;
+  static size_t bytes(int rows, bool two) { return (size_t)(two ? 2 : 1) * kParts * rows * kRow; }
+};
+
+template <class T, class S, int G, bool Z, int MT, int NT, int U, int WK, int WN, bool PF, int OCC>
+__global__ __launch_bounds__(64 * WK * WN, OCC) void k_linear(LinearArgs a) {
+  using M = Mma<T>;
+  using St = Stage<T, WK, U>;
+  constexpr int P = M::parts, NG = kBlockK / G, kSteps = G / 32, MN = MT * NT, kThreads = 64 * WK * WN;
+  constexpr int kPieces = St::kChunk / 8;                            // 8 values each, of a row of a chunk
+  constexpr int kEach = (16 * MT * kPieces + kThreads - 1) / kThreads;   // pieces of a thread at most
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int64_t unit = (int64_t)blockIdx.z * gridDim.y + blockIdx.y;
+  int matrix = 0;
+  int64_t first, last;
+  if (unit >= a.n_units) return;   // the whole workgroup
+  if (a.offsets) {
+    if (!find_rows(a, unit, 16 * MT, &matrix, &first, &last)) return;   // the whole workgroup
+  } else {
+    first = unit * (16 * MT);
+    last = first + 16 * MT < a.n_rows ? first + 16 * MT : a.n_rows;
+  }
+  const int tid = threadIdx.x, l = tid % 64, wv = __builtin_amdgcn_readfirstlane(tid / 64);
+  const int ik = wv % WK, in = wv / WK;
+  const int j = l % 16, h = l / 16;
+  const QuantShape &s = a.s;
+  const int K = s.n_in, tile0 = (blockIdx.x * WN + in) * NT;
+  const int n_chunks = (s.blocks + WK * U - 1) / (WK * U);
+  const uint8_t *base = a.packed + (size_t)matrix * s.stride;
+  const uint8_t *record[NT];   // of the wave, at block 0; a lane adds its own offset
+  const size_t block_step = (size_t)s.tiles * s.record;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)   // tiles past the last one compute a copy of it, never stored
+    record[n] = base + (size_t)(tile0 + n < s.tiles ? tile0 + n : s.tiles - 1) * s.record;
+  struct Weights {
+    uint4 d[U][NT];
+    Groups<S, NG, Z> g[U][NT];
+  };
+  auto load_weights = [&](Weights &w, int chunk) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int b = chunk * (WK * U) + ik * U + u;   // past the last block: a copy of it, multiplied by 0
+      const size_t at = (size_t)(b < s.blocks ? b : s.blocks - 1) * block_step;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        w.d[u][n] = *reinterpret_cast<const uint4 *>(record[n] + at + (uint32_t)(l * 16));
+        w.g[u][n] = *reinterpret_cast<const Groups<S, NG, Z> *>(record[n] + at + kGroupsAt +
+                                                                (uint32_t)(h * (int)sizeof(Groups<S, NG, Z>)));
+      }
+    }
+  };
+  typename M::frag fixed;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) fixed[i] = Z ? 1.f : -8.f;
+  for (int64_t r0 = first; r0 < last; r0 += 16 * MT) {
+    const int n_rows = last - r0 < 16 * MT ? (int)(last - r0) : 16 * MT;
+    const T *rows = (const T *)a.x + r0 * K;
+    // pieces tid, tid + kThreads, ..: piece p is values 8 (p % kPieces) .. of row p / kPieces.  A piece that
+    // reaches past K is read further left (its value is not used), so that no load is conditional.
+    auto load_rows = [&](Eight<T> (&x)[kEach], int chunk) {
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) {
+        if (K < 8 || e * kThreads >= n_rows * kPieces) break;
+        const int p = e * kThreads + tid, r = p / kPieces, k = chunk * St::kChunk + 8 * (p % kPieces);
+        x[e] = *reinterpret_cast<const Eight<T> *>(rows + (int64_t)(r < n_rows ? r : 0) * K + (k + 8 <= K ? k : K - 8));
+      }
+    };
+    auto put_piece = [&](uint8_t *buf, int p, int r, const Eight<T> &e) {
+      typename M::frag f[P];
+      row_parts<T>(e, f);
+#pragma unroll
+      for (int q = 0; q < P; ++q)
+        *reinterpret_cast<typename M::frag *>(buf + (q * a.lds_rows + r) * St::kRow + 16 * (p % kPieces)) = f[q];
+    };
+    auto store_rows = [&](const Eight<T> (&x)[kEach], int chunk) {
+      uint8_t *buf = lds + (size_t)(PF ? chunk & 1 : 0) * (P * a.lds_rows * St::kRow);
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) {
+        if (e * kThreads >= n_rows * kPieces) break;
+        const int p = e * kThreads + tid, r = p / kPieces, k = chunk * St::kChunk + 8 * (p % kPieces);
+        if (r < n_rows && (k + 8 <= K || k >= K)) put_piece(buf, p, r, k < K ? x[e] : Eight<T>{});
+      }
+      if ((chunk + 1) * St::kChunk > K && K % 8) {   // the piece that K ends inside: a thread per row
+        for (int r = tid; r < n_rows; r += kThreads) {
+          const int k = K / 8 * 8;
+          Eight<T> e{};
+#pragma unroll
+          for (int i = 0; i < 7; ++i) {
+            const T v = rows[(int64_t)r * K + (k + i < K ? k + i : k)];
+            e.v[i] = k + i < K ? v : T(0.f);
+          }
+          put_piece(buf, (k - chunk * St::kChunk) / 8, r, e);
+        }
+      }
+    };
+    f32x4 acc[MT][NT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    int row_at[MT];   // lanes past the last row compute a copy of it, never stored
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int r = 16 * m + j;
+      row_at[m] = (r < n_rows ? r : n_rows - 1) * St::kRow + ik * (U * kBlockK * 2) + 16 * h;
+    }
+    auto multiply = [&](const Weights &k, int chunk) {
+      const uint8_t *buf = lds + (size_t)(PF ? chunk & 1 : 0) * (P * a.lds_rows * St::kRow);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        auto row_frag = [&](int p, int m, int st) {
+          return *reinterpret_cast<const typename M::frag *>(buf + p * a.lds_rows * St::kRow + row_at[m] +
+                                                             (u * kBlockK + 32 * st) * 2);
+        };
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          // xs = sum x over the group (or, without zero points, -8 sum x, which the products start from)
+          f32x4 part[MT][NT], xs[MT];
+#pragma unroll
+          for (int m = 0; m < MT; ++m) xs[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int st = g * kSteps; st < (g + 1) * kSteps; ++st)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+              for (int p = 0; p < P; ++p) xs[m] = M::mul(fixed, row_frag(p, m, st), xs[m]);
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) part[m][n] = Z ? f32x4{0.f, 0.f, 0.f, 0.f} : xs[m];
+#pragma unroll
+          for (int st = g * kSteps; st < (g + 1) * kSteps; ++st) {
+            typename M::frag w[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              w[n] = M::weights(st == 0 ? k.d[u][n].x : st == 1 ? k.d[u][n].y : st == 2 ? k.d[u][n].z : k.d[u][n].w);
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+              for (int p = 0; p < P; ++p) {
+                const typename M::frag x = row_frag(p, m, st);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) part[m][n] = M::mul(w[n], x, part[m][n]);
+              }
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float sv = (float)k.g[u][n].g[g].s[i];
+              if constexpr (Z) {
+                const float zv = (float)((k.g[u][n].g[g].z[0] >> (8 * i)) & 255u);
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                  acc[m][n][i] = fmaf(sv, fmaf(-zv, xs[m][i], part[m][n][i]), acc[m][n][i]);
+              } else {
+#pragma unroll
+                for (int m = 0; m < MT; ++m) acc[m][n][i] = fmaf(sv, part[m][n][i], acc[m][n][i]);
+              }
+            }
+        }
+      }
+    };
+    if (r0 != first) __syncthreads();   // the sums of the rows before have been read
+    f32x4 bias[NT];   // requested here; outputs past the end repeat the last one's, never stored
+#pragma unroll
+    for (int n = 0; n < NT; ++n) bias[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (a.bias && ik == 0) {
+      const float *row = a.bias + (size_t)matrix * s.n_out;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int o = (tile0 + n) * kTileN + 4 * h + i;
+          bias[n][i] = row[o < s.n_out ? o : s.n_out - 1];
+        }
+    }
+    Eight<T> x[kEach];
+    auto request = [&](int chunk) { load_rows(x, chunk); };
+    auto settle = [&](int chunk) {
+      store_rows(x, chunk);
+      __syncthreads();
+    };
+    if constexpr (PF) {
+      Weights now;
+      request(0);
+      load_weights(now, 0);
+      settle(0);
+#pragma unroll 1
+      for (int c = 0; c + 1 < n_chunks; ++c) {
+        Weights next;
+        request(c + 1);
+        load_weights(next, c + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(now, c);
+        settle(c + 1);   // the other buffer: its readers passed the last barrier
+        now = next;
+      }
+      multiply(now, n_chunks - 1);
+    } else {
+#pragma unroll 1
+      for (int c = 0; c < n_chunks; ++c) {
+        Weights now;
+        request(c);
+        load_weights(now, c);
+        if (c > 0) __syncthreads();   // the chunk before has been read
+        settle(c);
+        multiply(now, c);
+      }
+    }
+    f32x4 *sums = reinterpret_cast<f32x4 *>(lds);   // [in][ik - 1][MT * NT][64]
+    if constexpr (WK > 1) {
+      __syncthreads();   // the rows have been read
+      if (ik > 0) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) sums[((in * (WK - 1) + ik - 1) * MN + m * NT + n) * 64 + l] = acc[m][n];
+      }
+      __syncthreads();
+    }
+    if (ik == 0) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          f32x4 v = acc[m][n];
+#pragma unroll
+          for (int w = 0; w < WK - 1; ++w) {
+            const f32x4 u = sums[((in * (WK - 1) + w) * MN + m * NT + n) * 64 + l];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += u[i];
+          }
+          // lane (j, h) holds outputs 4 h .. 4 h + 3 of row j
+          const int64_t r = r0 + 16 * m + j;
+          const int o = (tile0 + n) * kTileN + 4 * h;
+          if (r < last && o < s.n_out) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              v[i] += bias[n][i];
+              if (a.relu) v[i] = v[i] < 0.f ? 0.f : v[i];   // NaN stays
+            }
+            if (a.out_f32) store_four((float *)a.y + r * s.n_out + o, v, s.n_out - o, a.wide_store);
+            else store_four((T *)a.y + r * s.n_out + o, v, s.n_out - o, a.wide_store);
+          }
+        }
+    }
+  }
+}
+
+template <class T, class S, int G, bool Z, int MT, int NT, int U, int WK, int WN, bool PF, int OCC>
+void launch_linear(LinearArgs a, hipStream_t stream) {
+  const int64_t blocks = (a.n_rows + 16 * MT - 1) / (16 * MT);
+  a.direct = a.offsets && blocks <= 4;
+  a.n_units = !a.offsets ? blocks : a.direct ? a.n_matrices : blocks + a.n_matrices;
+  a.lds_rows = (int32_t)std::min<int64_t>(a.n_rows, 16 * MT);
+  const int64_t y = a.n_units < 32768 ? a.n_units : 32768, z = (a.n_units + y - 1) / y;
+  const dim3 grid((unsigned)((a.s.tiles + NT * WN - 1) / (NT * WN)), (unsigned)y, (unsigned)z);
+  const size_t lds = std::max(Stage<T, WK, U>::bytes(a.lds_rows, PF), (size_t)WN * (WK - 1) * MT * NT * 1024);
+  k_linear<T, S, G, Z, MT, NT, U, WK, WN, PF, OCC><<<grid, 64 * WK * WN, lds, stream>>>(a);
+}
+
+template <class F>
+void with_group(int32_t group, F f) {
+  if (group == 32) f(std::integral_constant<int, 32>{});
+  else if (group == 64) f(std::integral_constant<int, 64>{});
+  else f(std::integral_constant<int, 128>{});
+}
+
+template <class F>
+void with_flag(int32_t on, F f) {
+  if (on) f(std::true_type{});
+  else f(std::false_type{});
+}
+
+
+// How a product is cut: rows x outputs of a workgroup and how its waves share them, by the number of
+// workgroups that each cut gives.  The largest cut that still gives 512 (two per compute unit, so that one
+// loads while the other multiplies) is taken; bfloat16, groups of 128, us, chosen cut
+// against its neighbour:
+//   1024 rows, 4096 x 1024:  64 x 256 cut 18.6,  32 x 128 22.0
+//   1024 rows, 1024 x 1024:  32 x  64 cut  9.4,  32 x 128 11.2
+//    256 rows, 1024 x 1024:  16 x  32 cut  5.7,  16 x  16  6.0
+//     16 rows, 4096 x 1024:  16 x  16 cut  4.3,  16 x  32  5.1
+// Up to 16 rows of a large matrix (a decoding step) are bound by the weights' bytes: two tiles per wave, four
+// waves along k and two blocks of each in flight: 1 row, 16384 x 4096: 10.7, 16 x 32 cut 12.7.
+// Rows by expert: a cut of 32 rows is mostly empty below 8 rows per expert on average (64 rows, 64 experts of
+// 2048 x 1024: 16 x 32 cut 11.0, 32 x 128 13.0; 1024 rows: 32 x 128 26.2, 16 x 32 more than 32), and one of 64
+// rows loses to 32 by the experts' uneven numbers of rows (4096 rows, 8 experts: 32.5 against 25.6).
+template <class T, class S, int G, bool Z>
+void linear_cut(LinearArgs a, hipStream_t stream) {
+  const int64_t rows = a.n_rows, tiles = a.s.tiles;
+  auto groups = [&](int64_t r, int64_t t) { return ((rows + r - 1) / r) * ((tiles + t - 1) / t); };
+  if (a.offsets) {
+    const int64_t some = std::min<int64_t>(a.n_matrices, rows) / 2;   // half-filled blocks, about
+    if (rows >= 8 * (int64_t)a.n_matrices && (rows / 32 + some) * ((tiles + 7) / 8) >= 256)
+      launch_linear<T, S, G, Z, 2, 2, 1, 1, 4, false, 2>(a, stream);
+    else
+      launch_linear<T, S, G, Z, 1, 1, 2, 2, 2, false, 2>(a, stream);
+  } else if (groups(64, 16) >= 256) {
+    launch_linear<T, S, G, Z, 4, 2, 1, 1, 8, true, 2>(a, stream);
+  } else if (groups(32, 8) >= 512) {
+    launch_linear<T, S, G, Z, 2, 2, 1, 1, 4, false, 2>(a, stream);
+  } else if (groups(32, 4) >= 512) {
+    launch_linear<T, S, G, Z, 2, 2, 1, 2, 2, false, 2>(a, stream);
+  } else if (rows <= 16 && groups(16, 2) >= 512 && a.s.blocks >= 8) {
+    launch_linear<T, S, G, Z, 1, 2, 2, 4, 1, false, 2>(a, stream);
+  } else if (groups(16, 2) >= 512 || a.s.blocks < 8) {
+    launch_linear<T, S, G, Z, 1, 1, 2, 2, 2, false, 2>(a, stream);
+  } else {
+    launch_linear<T, S, G, Z, 1, 1, 1, 8, 1, false, 2>(a, stream);
+  }
+}
+
+template <class T>
+void linear_rows(LinearArgs a, int32_t scale_type, hipStream_t stream) {
+  with_type(scale_type, [&](auto ts) {
+    with_group(a.s.group, [&](auto g) {
+      with_flag(a.s.has_zeros, [&](auto z) {
+        linear_cut<T, decltype(ts), decltype(g)::value, decltype(z)::value>(a, stream);
+      });
+    });
+  });
+}
+
+}  // namespace svt

@@ -274,6 +274,25 @@ def test_linear(svt, R, N, K, G, scale_kind, zeros, kind):
         near(host(y), ry, 4 * np.sqrt(n) * U * mag + HALF[out_kind] * np.abs(ry) + TINY[out_kind], f"{relu} {out_kind}")
 
 
+# sizes that reach every way the product is cut, each ending inside rows, outputs, blocks and groups
+CUTS = [(1030, 4100, 260, 128), (520, 4000, 150, 64), (300, 3300, 137, 32), (13, 16400, 1100, 128),
+        (100, 2400, 259, 64), (9, 700, 1500, 128), (40, 600, 385, 32)]
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("R, N, K, G", CUTS)
+def test_linear_every_cut(svt, R, N, K, G, kind):
+    say("cut", R, N, K, G, kind)
+    rng = np.random.default_rng(R + N + K)
+    packed, q, s, z = make_weights(svt, rng, 1, N, K, G, "bf16" if kind == "bf16" else "f32", R % 2 == 0)
+    x = dev(rng.normal(size=(R, K)), ty(kind))
+    bias = rng.normal(size=(1, N)).astype(np.float32)
+    y = svt.svt_quant_linear(x, packed, bias=dev(bias), activation="relu")
+    ry, mag = X.linear(host(x), q, s, z, G, None, bias, True, np.zeros((R, N)))
+    n = (3 if kind == "f32" else 1) * G + -(-K // G) + 12
+    near(host(y), ry, 4 * np.sqrt(n) * U * mag + HALF[kind] * np.abs(ry) + TINY[kind], "cut")
+
+
 @pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("G", [32, 64, 128])
 def test_linear_weights_are_exact(svt, kind, G):
@@ -290,7 +309,7 @@ def test_linear_weights_are_exact(svt, kind, G):
 EXPERTS = [  # rows per matrix, outputs, inputs, group
     ([1], 16, 64, 32), ([0, 3, 0, 1], 40, 130, 64), ([0, 0, 0], 16, 32, 32), ([17, 0, 40, 1, 16], 33, 256, 128),
     ([1] * 70, 16, 96, 32), ([0] * 63 + [5] + [0] * 100 + [2], 32, 64, 64), ([200, 7, 64], 100, 160, 32),
-    ([130, 0, 65, 300], 200, 257, 64)]
+    ([130, 0, 65, 300], 200, 257, 64), ([40, 3], 50, 300, 128), ([0, 33], 16, 7, 32)]
 
 
 @pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
