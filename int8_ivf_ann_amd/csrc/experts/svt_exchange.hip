@@ -25,197 +25,231 @@ namespace {
 //
 // A counting sort.  Waves own contiguous pieces of the entries; within a piece, 64 entries at a time, an
 // entry's rank among the lanes of its expert comes from one ballot per bit of the expert's number (the
-// lanes that agree on every bit), so equal experts keep their order without atomics on the positions.
-//   one launch   (up to kOneEntries): a workgroup of 16 waves counts, scans and places.
-//   three        k_sort_count: a histogram per block; k_sort_scan: per expert, the exclusive sums over
-//                the blocks; k_sort_place: each block adds its experts' starts and places its entries.
+// lanes that agree on every bit), added to the piece's count of that expert so far.  Ranks stay in
+// registers, so the entries are read once, and no position depends on the order of atomics.
+//   one launch   (up to kOneEntries): a workgroup of 16 waves ranks, scans and places.
+//   two          k_sort_count: a histogram per block; k_sort_place: each block sums the histograms (few blocks
+//                of many entries keep that table small), ranks its entries, orders them in LDS and writes
+//                each expert's run in one piece.
 
-constexpr int kOneThreads = 1024, kOneWaves = kOneThreads / 64;
-constexpr int64_t kOneEntries = 16384;
-constexpr int kSortThreads = 256, kSortWaves = kSortThreads / 64;
-constexpr int64_t kBlockEntries = 2048;   // entries per block, until there are kMaxBlocks
-constexpr int64_t kMaxBlocks = 1024;
+constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64, kSortSteps = 4;
+constexpr int kTileEntries = kSortThreads * kSortSteps;   // entries of a workgroup at a time
+constexpr int64_t kOneEntries = 8 * kSortThreads;
+constexpr int64_t kMaxBlocks = 512;                       // two per compute unit
 constexpr int64_t kMaxEntries = int64_t(1) << 30;
 
 struct SortShape {
   int64_t n;            // entries
-  int64_t per_block;    // entries per block, a multiple of 64 kSortWaves
+  int64_t per_block;    // entries per block, a multiple of kTileEntries
   int32_t blocks;
 };
 
-SortShape sort_shape(int64_t n) {
-  SortShape s{n, kBlockEntries, 1};
-  int64_t blocks = (n + kBlockEntries - 1) / kBlockEntries;
-  if (blocks > kMaxBlocks) {
-    const int64_t step = 64 * kSortWaves;
-    s.per_block = ((n + kMaxBlocks - 1) / kMaxBlocks + step - 1) / step * step;
-    blocks = (n + s.per_block - 1) / s.per_block;
-  }
-  s.blocks = (int32_t)(blocks < 1 ? 1 : blocks);
-  return s;
+// every block reads the whole table of histograms: at most 64 K counts
+SortShape sort_shape(int64_t n, int E) {
+  const int64_t tiles = (n + kTileEntries - 1) / kTileEntries;
+  const int64_t most = kMaxBlocks * E > 65536 ? 65536 / E : kMaxBlocks;
+  const int64_t each = (tiles + most - 1) / most;   // tiles per block
+  return SortShape{n, each * kTileEntries, (int32_t)((tiles + each - 1) / each)};
 }
 
 __device__ __forceinline__ int load_expert(const int32_t *experts, int64_t i, int64_t end, int E) {
-  if (i >= end) return -1;
-  const int e = experts[i];
-  return (uint32_t)e < (uint32_t)E ? e : -1;
+  const int e = experts[i < end ? i : end - 1];
+  return i < end && (uint32_t)e < (uint32_t)E ? e : -1;
 }
 
-// the lanes of this wave whose expert equals this lane's (0 for a lane without one)
-__device__ __forceinline__ uint64_t same_expert(int e, int bits) {
+// the lanes of this wave whose expert, below 2^BITS, equals this lane's (0 for a lane without one)
+template <int BITS>
+__device__ __forceinline__ uint64_t same_expert(int e) {
   uint64_t same = __ballot(e >= 0);
-  for (int b = 0; b < bits; ++b) {
+#pragma unroll
+  for (int b = 0; b < BITS; ++b) {
     const uint64_t one = __ballot((e >> b) & 1);
     same &= ((e >> b) & 1) ? one : ~one;
   }
   return e >= 0 ? same : 0ull;
 }
 
-// places the entries [i0, i1) of this wave: next[e] is the position of the wave's next entry of e
-__device__ __forceinline__ void place_entries(const int32_t *experts, int64_t i0, int64_t i1, int E, int bits,
-                                              volatile int32_t *next, int32_t *order, int32_t *position) {
+// ranks of a wave's entries, step by step: rank[q] = entries of the same expert before it in the wave's
+// piece; count[e] (the wave's own, cleared) becomes the piece's entries of e
+template <int STEPS, int BITS>
+__device__ __forceinline__ void rank_entries(const int (&e)[STEPS], int (&rank)[STEPS], volatile int32_t *count) {
   const int l = lane_id();
-  for (int64_t i = i0 + l; i - l < i1; i += 64) {
-    const int e = load_expert(experts, i, i1, E);
-    const uint64_t same = same_expert(e, bits);
-    int32_t at = -1;
-    if (e >= 0) at = next[e] + mbcnt(same);
-    // the last lane of each expert moves next[e] on; a wave's LDS operations stay in order
-    if (e >= 0 && (same >> l) == 1ull) next[e] = at + 1;
-    if (i < i1) {
-      position[i] = at;
-      if (e >= 0) order[at] = (int32_t)i;
+#pragma unroll
+  for (int q = 0; q < STEPS; ++q) {
+    const uint64_t same = same_expert<BITS>(e[q]);
+    rank[q] = 0;
+    if (e[q] >= 0) {
+      rank[q] = count[e[q]] + mbcnt(same);
+      // the last lane of each expert moves the count on; a wave's LDS operations stay in order
+      if ((same >> l) == 1ull) count[e[q]] = rank[q] + 1;
     }
   }
 }
 
-// exclusive scan of total[0 .. E) (LDS) into start[0 .. E], by the block's first SVT_MAX_EXPERTS / 2
-// threads or more; barriers inside
-template <int NT>
-__device__ __forceinline__ int scan_experts(const int32_t *total, int32_t *start, int E, int32_t *wave_tot) {
-  constexpr int kEach = SVT_MAX_EXPERTS / NT < 1 ? 1 : SVT_MAX_EXPERTS / NT;
-  int v[kEach], sum = 0, all;
-#pragma unroll
-  for (int q = 0; q < kEach; ++q) {
-    const int e = threadIdx.x * kEach + q;
-    v[q] = e < E ? total[e] : 0;
-    sum += v[q];
-  }
-  int at = block_excl_scan<NT>(sum, wave_tot, &all);
-#pragma unroll
-  for (int q = 0; q < kEach; ++q) {
-    const int e = threadIdx.x * kEach + q;
-    if (e < E) start[e] = at;
-    at += v[q];
-  }
-  if (threadIdx.x == 0) start[E] = all;
-  __syncthreads();
-  return all;
-}
-
-__global__ __launch_bounds__(kOneThreads) void k_sort_one(const int32_t *experts, int64_t n, int E, int bits,
-                                                          int32_t *offsets, int32_t *order, int32_t *position) {
-  __shared__ int32_t next[kOneWaves][SVT_MAX_EXPERTS];
-  __shared__ int32_t total[SVT_MAX_EXPERTS], start[SVT_MAX_EXPERTS + 1], wave_tot[kOneWaves + 1];
-  const int tid = threadIdx.x, wv = tid / 64;
-  const int64_t per = (n + 64 * kOneWaves - 1) / (64 * kOneWaves) * 64;
-  const int64_t i0 = wv * per < n ? wv * per : n, i1 = i0 + per < n ? i0 + per : n;
-  for (int i = tid; i < kOneWaves * E; i += kOneThreads) next[i / E][i % E] = 0;
-  __syncthreads();
-  for (int64_t i = i0 + tid % 64; i < i1; i += 64) {
-    const int e = load_expert(experts, i, i1, E);
-    if (e >= 0) atomicAdd(&next[wv][e], 1);
-  }
-  __syncthreads();
-  if (tid < E) {   // counts of the waves before, and the expert's total
+// count[w][e] become exclusive sums over the waves, total[e] their sum
+__device__ __forceinline__ void sum_waves(int32_t (*count)[SVT_MAX_EXPERTS], int32_t *total, int E) {
+  for (int e = threadIdx.x; e < E; e += kSortThreads) {
     int sum = 0;
 #pragma unroll
-    for (int w = 0; w < kOneWaves; ++w) {
-      const int c = next[w][tid];
-      next[w][tid] = sum;
+    for (int w = 0; w < kSortWaves; ++w) {
+      const int c = count[w][e];
+      count[w][e] = sum;
       sum += c;
     }
-    total[tid] = sum;
+    total[e] = sum;
   }
-  __syncthreads();
-  const int all = scan_experts<kOneThreads>(total, start, E, wave_tot);
-  for (int i = tid; i < kOneWaves * E; i += kOneThreads) next[i / E][i % E] += start[i % E];
-  for (int e = tid; e <= E; e += kOneThreads) offsets[e] = start[e];
-  for (int64_t i = all + tid; i < n; i += kOneThreads) order[i] = -1;
-  __syncthreads();
-  place_entries(experts, i0, i1, E, bits, next[wv], order, position);
 }
 
-// counts[e * blocks + b]: block b's entries of expert e
+// start[0 .. E] = exclusive sums of total[0 .. E), by the first wave; the caller's barriers around it
+__device__ __forceinline__ void scan_experts(const int32_t *total, int32_t *start, int E) {
+  if (threadIdx.x >= 64) return;
+  const int each = (E + 63) / 64;
+  int sum = 0;
+  for (int q = 0; q < each; ++q) {
+    const int e = threadIdx.x * each + q;
+    sum += e < E ? total[e] : 0;
+  }
+  const int upto = incl_sums(sum);
+  int at = upto - sum;
+  for (int q = 0; q < each; ++q) {
+    const int e = threadIdx.x * each + q;
+    if (e < E) {
+      start[e] = at;
+      at += total[e];
+    }
+  }
+  if (threadIdx.x == 63) start[E] = upto;
+}
+
+template <int STEPS, int BITS>
+__global__ __launch_bounds__(kSortThreads) void k_sort_one(const int32_t *experts, int64_t n, int E, int32_t *offsets,
+                                                           int32_t *order, int32_t *position) {
+  __shared__ int32_t count[kSortWaves][SVT_MAX_EXPERTS];
+  __shared__ int32_t total[SVT_MAX_EXPERTS], start[SVT_MAX_EXPERTS + 1];
+  const int tid = threadIdx.x, wv = tid / 64;
+  const int64_t i0 = (int64_t)wv * (64 * STEPS) + tid % 64;
+  int e[STEPS], rank[STEPS];
+#pragma unroll
+  for (int q = 0; q < STEPS; ++q) e[q] = n > 0 ? load_expert(experts, i0 + 64 * q, n, E) : -1;
+  for (int i = tid % 64; i < E; i += 64) count[wv][i] = 0;   // its own wave's: no barrier needed
+  rank_entries<STEPS, BITS>(e, rank, count[wv]);
+  __syncthreads();
+  sum_waves(count, total, E);
+  __syncthreads();
+  scan_experts(total, start, E);
+  __syncthreads();
+  for (int i = tid; i <= E; i += kSortThreads) offsets[i] = start[i];
+  for (int64_t i = start[E] + tid; i < n; i += kSortThreads) order[i] = -1;
+#pragma unroll
+  for (int q = 0; q < STEPS; ++q) {
+    const int64_t i = i0 + 64 * q;
+    const int at = e[q] >= 0 ? start[e[q]] + count[wv][e[q]] + rank[q] : -1;
+    if (i < n) position[i] = at;
+    if (e[q] >= 0) order[at] = (int32_t)i;
+  }
+}
+
+// counts[b * E + e]: block b's entries of expert e
 __global__ __launch_bounds__(kSortThreads) void k_sort_count(const int32_t *experts, SortShape s, int E,
                                                              int32_t *counts) {
   __shared__ int32_t hist[SVT_MAX_EXPERTS];
   const int tid = threadIdx.x;
+  const int64_t b0 = blockIdx.x * s.per_block, b1 = b0 + s.per_block < s.n ? b0 + s.per_block : s.n;
   for (int e = tid; e < E; e += kSortThreads) hist[e] = 0;
   __syncthreads();
-  const int64_t i0 = blockIdx.x * s.per_block, i1 = i0 + s.per_block < s.n ? i0 + s.per_block : s.n;
-  for (int64_t i = i0 + tid; i < i1; i += kSortThreads) {
-    const int e = load_expert(experts, i, i1, E);
-    if (e >= 0) atomicAdd(&hist[e], 1);
+  for (int64_t i0 = b0; i0 < b1; i0 += kTileEntries) {
+    int e[kSortSteps];
+#pragma unroll
+    for (int q = 0; q < kSortSteps; ++q) e[q] = load_expert(experts, i0 + q * kSortThreads + tid, b1, E);
+#pragma unroll
+    for (int q = 0; q < kSortSteps; ++q)
+      if (e[q] >= 0) atomicAdd(&hist[e[q]], 1);
   }
   __syncthreads();
-  for (int e = tid; e < E; e += kSortThreads) counts[(int64_t)e * s.blocks + blockIdx.x] = hist[e];
+  for (int e = tid; e < E; e += kSortThreads) counts[(int64_t)blockIdx.x * E + e] = hist[e];
 }
 
-// one block per expert: its counts become exclusive sums over the blocks; totals[e] = their sum
-__global__ __launch_bounds__(kSortThreads) void k_sort_scan(int32_t *counts, int blocks, int32_t *totals) {
-  constexpr int kEach = kMaxBlocks / kSortThreads;
-  __shared__ int32_t wave_tot[kSortWaves + 1];
-  int32_t *row = counts + (int64_t)blockIdx.x * blocks;
-  int v[kEach], sum = 0, all;
-#pragma unroll
-  for (int q = 0; q < kEach; ++q) {
-    const int b = threadIdx.x * kEach + q;
-    v[q] = b < blocks ? row[b] : 0;
-    sum += v[q];
-  }
-  int at = block_excl_scan<kSortThreads>(sum, wave_tot, &all);
-#pragma unroll
-  for (int q = 0; q < kEach; ++q) {
-    const int b = threadIdx.x * kEach + q;
-    if (b < blocks) row[b] = at;
-    at += v[q];
-  }
-  if (threadIdx.x == 0) totals[blockIdx.x] = all;
-}
-
-__global__ __launch_bounds__(kSortThreads) void k_sort_place(const int32_t *experts, SortShape s, int E, int bits,
-                                                             const int32_t *counts, const int32_t *totals,
-                                                             int32_t *offsets, int32_t *order, int32_t *position) {
-  __shared__ int32_t next[kSortWaves][SVT_MAX_EXPERTS];
-  __shared__ int32_t total[SVT_MAX_EXPERTS], start[SVT_MAX_EXPERTS + 1], wave_tot[kSortWaves + 1];
+template <int BITS>
+__global__ __launch_bounds__(kSortThreads) void k_sort_place(const int32_t *experts, SortShape s, int E,
+                                                             const int32_t *counts, int32_t *offsets, int32_t *order,
+                                                             int32_t *position) {
+  __shared__ int32_t count[kSortWaves][SVT_MAX_EXPERTS];
+  __shared__ int32_t total[SVT_MAX_EXPERTS], start[SVT_MAX_EXPERTS + 1];
+  __shared__ int32_t next[SVT_MAX_EXPERTS];   // the row of the block's next entry of each expert
+  __shared__ int32_t entry[kTileEntries];
+  __shared__ uint16_t owner[kTileEntries];
   const int tid = threadIdx.x, wv = tid / 64, b = blockIdx.x;
-  for (int i = tid; i < kSortWaves * E; i += kSortThreads) next[i / E][i % E] = 0;
-  for (int e = tid; e < E; e += kSortThreads) total[e] = totals[e];
-  __syncthreads();
   const int64_t b0 = b * s.per_block, b1 = b0 + s.per_block < s.n ? b0 + s.per_block : s.n;
-  const int64_t per = s.per_block / kSortWaves;
-  const int64_t i0 = b0 + wv * per < b1 ? b0 + wv * per : b1, i1 = i0 + per < b1 ? i0 + per : b1;
-  for (int64_t i = i0 + tid % 64; i < i1; i += 64) {
-    const int e = load_expert(experts, i, i1, E);
-    if (e >= 0) atomicAdd(&next[wv][e], 1);
-  }
-  const int all = scan_experts<kSortThreads>(total, start, E, wave_tot);   // barriers inside
-  for (int e = tid; e < E; e += kSortThreads) {
-    int at = start[e] + counts[(int64_t)e * s.blocks + b];
+  const int64_t in_tile = wv * (64 * kSortSteps) + tid % 64;
+  int e[kSortSteps], rank[kSortSteps];
 #pragma unroll
-    for (int w = 0; w < kSortWaves; ++w) {
-      const int c = next[w][e];
-      next[w][e] = at;
-      at += c;
+  for (int q = 0; q < kSortSteps; ++q) e[q] = load_expert(experts, b0 + in_tile + 64 * q, b1, E);
+  for (int i = tid; i < E; i += kSortThreads) total[i] = next[i] = 0;
+  __syncthreads();
+  {   // every expert's total and its entries in the blocks before, 2^k threads along the experts
+    int along = 64;
+    while (along < E) along *= 2;
+    const int i = tid % along;
+    int sum = 0, before = 0;
+    if (i < E)
+      for (int r = tid / along; r < s.blocks; r += kSortThreads / along) {
+        const int c = counts[(int64_t)r * E + i];
+        sum += c;
+        before += r < b ? c : 0;
+      }
+    if (i < E && sum) {
+      atomicAdd(&total[i], sum);
+      atomicAdd(&next[i], before);
     }
   }
-  if (b == 0)
-    for (int e = tid; e <= E; e += kSortThreads) offsets[e] = start[e];
-  for (int64_t i = b0 + tid; i < b1; i += kSortThreads)
-    if (i >= all) order[i] = -1;
   __syncthreads();
-  place_entries(experts, i0, i1, E, bits, next[wv], order, position);
+  scan_experts(total, start, E);
+  __syncthreads();
+  for (int i = tid; i < E; i += kSortThreads) next[i] += start[i];
+  if (b == 0)
+    for (int i = tid; i <= E; i += kSortThreads) offsets[i] = start[i];
+  for (int64_t i = b0 + tid; i < b1; i += kSortThreads)
+    if (i >= start[E]) order[i] = -1;
+  for (int64_t t0 = b0; t0 < b1; t0 += kTileEntries) {
+    if (t0 != b0) {
+#pragma unroll
+      for (int q = 0; q < kSortSteps; ++q) e[q] = load_expert(experts, t0 + in_tile + 64 * q, b1, E);
+    }
+    for (int i = tid % 64; i < E; i += 64) count[wv][i] = 0;
+    rank_entries<kSortSteps, BITS>(e, rank, count[wv]);
+    __syncthreads();   // also: start has been read
+    sum_waves(count, total, E);
+    __syncthreads();
+    scan_experts(total, start, E);
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kSortSteps; ++q) {
+      const int64_t i = t0 + in_tile + 64 * q;
+      int at = -1;
+      if (e[q] >= 0) {
+        const int in = count[wv][e[q]] + rank[q];   // among the tile's entries of the expert
+        at = next[e[q]] + in;
+        entry[start[e[q]] + in] = (int32_t)i;
+        owner[start[e[q]] + in] = (uint16_t)e[q];
+      }
+      if (i < b1) position[i] = at;
+    }
+    __syncthreads();
+    for (int p = tid; p < start[E]; p += kSortThreads) {
+      const int o = owner[p];
+      order[next[o] + p - start[o]] = entry[p];
+    }
+    __syncthreads();
+    for (int i = tid; i < E; i += kSortThreads) next[i] += total[i];   // read again behind a barrier
+  }
+}
+
+// calls f with enough bits for an expert's number as a constant
+template <class F>
+void with_bits(int E, F f) {
+  if (E <= 8) f(std::integral_constant<int, 3>{});
+  else if (E <= 64) f(std::integral_constant<int, 6>{});
+  else f(std::integral_constant<int, 9>{});
 }
 
 // ---- exchange ------------------------------------------------------------------------------------
@@ -265,17 +299,22 @@ __device__ __forceinline__ int64_t row_at(const ExArgs &a, int64_t t, int j) {
   return (uint32_t)p < (uint64_t)a.n_rows ? p : -1;
 }
 
+// a thread takes two pieces of a row at a time, `lanes` apart, so that twice the loads are in flight
 template <int V>
 __global__ __launch_bounds__(kExThreads) void k_dispatch(ExArgs a, const typename Bytes<V>::type *x,
                                                          typename Bytes<V>::type *rows) {
   const int in = threadIdx.x % a.lanes;
   const int64_t per = kExThreads / a.lanes;
   for (int64_t t = blockIdx.x * per + threadIdx.x / a.lanes; t < a.n_tokens; t += gridDim.x * per)
-    for (int c = in; c < a.chunks; c += a.lanes) {
-      const auto v = x[t * a.chunks + c];
+    for (int c = in; c < a.chunks; c += 2 * a.lanes) {
+      const bool two = c + a.lanes < a.chunks;
+      const auto v = x[t * a.chunks + c], w = x[t * a.chunks + (two ? c + a.lanes : c)];
       for (int j = 0; j < a.top; ++j) {
         const int64_t p = row_at(a, t, j);
-        if (p >= 0) rows[p * a.chunks + c] = v;
+        if (p >= 0) {
+          rows[p * a.chunks + c] = v;
+          if (two) rows[p * a.chunks + c + a.lanes] = w;
+        }
       }
     }
 }
@@ -288,12 +327,13 @@ __global__ __launch_bounds__(kExThreads) void k_combine(ExArgs a, const typename
   const int in = threadIdx.x % a.lanes;
   const int64_t per = kExThreads / a.lanes;
   for (int64_t t = blockIdx.x * per + threadIdx.x / a.lanes; t < a.n_tokens; t += gridDim.x * per)
-    for (int c = in; c < a.chunks; c += a.lanes) {
-      L sum;
+    for (int c = in; c < a.chunks; c += 2 * a.lanes) {
+      const bool two = c + a.lanes < a.chunks;
+      L sum[2];
       for (int j0 = 0; j0 < a.top; j0 += J) {
         int64_t p[J];
         float w[J];
-        typename Bytes<V>::type r[J];
+        typename Bytes<V>::type r[J][2];
 #pragma unroll
         for (int j = 0; j < J; ++j) {
           p[j] = row_at(a, t, j0 + j);
@@ -301,16 +341,23 @@ __global__ __launch_bounds__(kExThreads) void k_combine(ExArgs a, const typename
         }
 #pragma unroll
         for (int j = 0; j < J; ++j)
-          if (p[j] >= 0) r[j] = rows[p[j] * a.chunks + c];
+          if (p[j] >= 0) {
+            r[j][0] = rows[p[j] * a.chunks + c];
+            r[j][1] = rows[p[j] * a.chunks + (two ? c + a.lanes : c)];
+          }
 #pragma unroll
         for (int j = 0; j < J; ++j)
           if (p[j] >= 0) {
-            const L v(r[j]);
 #pragma unroll
-            for (int i = 0; i < L::n; ++i) sum.v[i] = fmaf(w[j], v.v[i], sum.v[i]);
+            for (int h = 0; h < 2; ++h) {
+              const L v(r[j][h]);
+#pragma unroll
+              for (int i = 0; i < L::n; ++i) sum[h].v[i] = fmaf(w[j], v.v[i], sum[h].v[i]);
+            }
           }
       }
-      y[t * a.chunks + c] = sum.raw();
+      y[t * a.chunks + c] = sum[0].raw();
+      if (two) y[t * a.chunks + c + a.lanes] = sum[1].raw();
     }
 }
 
@@ -337,23 +384,33 @@ __global__ __launch_bounds__(kExThreads) void k_combine_backward(ExArgs a, const
         dot[j] = 0.f;
       }
       if (live)
-        for (int c = in; c < a.chunks; c += a.lanes) {
-          const L g(dy[t * a.chunks + c]);
-          typename Bytes<V>::type r[J];
-#pragma unroll
-          for (int j = 0; j < J; ++j)
-            if (p[j] >= 0) r[j] = rows[p[j] * a.chunks + c];
+        for (int c = in; c < a.chunks; c += 2 * a.lanes) {
+          const bool two = c + a.lanes < a.chunks;
+          const int c2 = two ? c + a.lanes : c;
+          const L g0(dy[t * a.chunks + c]), g1(dy[t * a.chunks + c2]);
+          typename Bytes<V>::type r[J][2];
 #pragma unroll
           for (int j = 0; j < J; ++j)
             if (p[j] >= 0) {
-              const L v(r[j]);
-              L d;
+              r[j][0] = rows[p[j] * a.chunks + c];
+              r[j][1] = rows[p[j] * a.chunks + c2];
+            }
 #pragma unroll
-              for (int i = 0; i < L::n; ++i) {
-                dot[j] = fmaf(g.v[i], v.v[i], dot[j]);
-                d.v[i] = w[j] * g.v[i];
+          for (int j = 0; j < J; ++j)
+            if (p[j] >= 0) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                if (h == 1 && !two) break;
+                const L &g = h ? g1 : g0;
+                const L v(r[j][h]);
+                L d;
+#pragma unroll
+                for (int i = 0; i < L::n; ++i) {
+                  dot[j] = fmaf(g.v[i], v.v[i], dot[j]);
+                  d.v[i] = w[j] * g.v[i];
+                }
+                d_rows[p[j] * a.chunks + (h ? c2 : c)] = d.raw();
               }
-              d_rows[p[j] * a.chunks + c] = d.raw();
             }
         }
 #pragma unroll
@@ -457,7 +514,7 @@ static int check_sort(const char *who, int32_t n_tokens, int32_t top, int32_t n_
 }
 
 static size_t sort_bytes(int64_t n, int32_t n_experts) {
-  return n <= kOneEntries ? 0 : ((size_t)sort_shape(n).blocks + 1) * n_experts * 4;
+  return n <= kOneEntries ? 0 : (size_t)sort_shape(n, n_experts).blocks * n_experts * 4;
 }
 
 extern "C" size_t svt_expert_sort_workspace_size(int32_t n_tokens, int32_t top, int32_t n_experts) {
@@ -488,19 +545,22 @@ extern "C" int svt_expert_sort(int32_t n_tokens, int32_t top, int32_t n_experts,
     for (int j = 0; j < i; ++j)
       if (overlap(at[i], bytes[i], at[j], bytes[j]))
         return report(SVT_EINVAL, "%s: input, outputs and workspace overlap", who);
-  int bits = 0;
-  while ((1 << bits) < n_experts) ++bits;
   hipStream_t s = (hipStream_t)hip_stream;
-  if (n <= kOneEntries) {
-    k_sort_one<<<1, kOneThreads, 0, s>>>(experts, n, n_experts, bits, offsets, order, position);
-    return launched(who);
-  }
-  const SortShape sh = sort_shape(n);
-  int32_t *counts = (int32_t *)workspace, *totals = counts + (size_t)sh.blocks * n_experts;
-  k_sort_count<<<sh.blocks, kSortThreads, 0, s>>>(experts, sh, n_experts, counts);
-  k_sort_scan<<<n_experts, kSortThreads, 0, s>>>(counts, sh.blocks, totals);
-  k_sort_place<<<sh.blocks, kSortThreads, 0, s>>>(experts, sh, n_experts, bits, counts, totals, offsets, order,
-                                                  position);
+  with_bits(n_experts, [&](auto bits) {
+    constexpr int B = decltype(bits)::value;
+    auto one = [&](auto steps) {
+      k_sort_one<decltype(steps)::value, B><<<1, kSortThreads, 0, s>>>(experts, n, n_experts, offsets, order, position);
+    };
+    if (n <= kSortThreads) one(std::integral_constant<int, 1>{});
+    else if (n <= 4 * kSortThreads) one(std::integral_constant<int, 4>{});
+    else if (n <= kOneEntries) one(std::integral_constant<int, 8>{});
+    else {
+      const SortShape sh = sort_shape(n, n_experts);
+      k_sort_count<<<sh.blocks, kSortThreads, 0, s>>>(experts, sh, n_experts, (int32_t *)workspace);
+      k_sort_place<B><<<sh.blocks, kSortThreads, 0, s>>>(experts, sh, n_experts, (const int32_t *)workspace, offsets,
+                                                         order, position);
+    }
+  });
   return launched(who);
 }
 

@@ -154,18 +154,6 @@ __device__ __forceinline__ int64_t row_end(const LinearArgs &a, int e) {
   return o < 0 ? 0 : o > a.n_rows ? a.n_rows : o;
 }
 
-// inclusive sums over the wave's lanes: shifts inside rows of 16 lanes, then each row's last lane to the next
-// row (1 and 3), then lane 31 to the upper half
-__device__ __forceinline__ int incl_sums(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);    // row_shr:1
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast:15
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // row_bcast:31
-  return v;
-}
-
 // With offsets: the matrix and the rows [*r0, *r1) of a unit; false if there are none.  A unit is a block of
 // `most` rows of one matrix (every wave counts the matrices' blocks up), or all rows of a matrix (direct).
 // Every lane of the wave gets the same answer.

@@ -8,10 +8,10 @@
 //          experts and 0 elsewhere
 //
 // A token belongs to a group of L lanes (L = 1 .. 64, the least power of two with kPer logits a lane), so
-// a wave holds 64 / L tokens and a row of logits is read once into registers.  The choice takes `top`
-// rounds: each lane's best remaining logit as an ordered integer, the group's maximum by DPP moves, the
-// lowest lane that holds it (a ballot), which strikes it out.  Ordered integers compare exactly, so ties
-// go to the lowest expert in every type.  Logits, maximum and sums are float32.
+// a wave holds 64 / L tokens and a row of logits is read once into registers.  Each lane sorts its logits
+// (a network of 19 exchanges); then `top` rounds take the group's best head by DPP moves, and the lane that
+// held it moves up.  Logits become integers of the same order, so ties go to the lowest expert in every type;
+// with 16-bit logits one integer holds the logit and the expert.  Maximum, sums and weights are float32.
 
 #include <type_traits>
 
@@ -25,16 +25,70 @@ constexpr int kPer = 8;            // logits per lane
 constexpr int kRouteThreads = 256;
 static_assert(SVT_MAX_EXPERTS == 64 * kPer, "one wave holds the widest row");
 
-// float -> uint32 whose unsigned order is the float order; 0 for a shut expert (-inf or NaN).  +inf
-// counts as the largest finite value, so that its weight is a number.
+// float -> uint32 whose unsigned order is the float order (-0 as 0); 0 for a shut expert (-inf or NaN)
 __device__ __forceinline__ uint32_t logit_order(float f) {
-  if (!(f > -INFINITY)) return 0u;
-  const uint32_t b = __float_as_uint(fminf(f, FLT_MAX));
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  const uint32_t b = __float_as_uint(f + 0.f);
+  return f > -INFINITY ? ((b & 0x80000000u) ? ~b : (b | 0x80000000u)) : 0u;
 }
+// its inverse; +inf counts as the largest finite value, so that its weight is a number
 __device__ __forceinline__ float order_logit(uint32_t o) {
-  return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
+  return fminf(__uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o), FLT_MAX);
 }
+
+// exp(x) for x <= 0 (0 below -200, long past the smallest float): 2^y with y = x log2 e and the product's
+// rounding put back, so that the result is off by 3 u and not by |x| u.  Half the instructions of expf.
+__device__ __forceinline__ float exp_below(float x) {
+  constexpr float kLog2e = 1.44269502e+0f, kLog2eRest = 1.92596299e-8f, kLn2 = 6.93147182e-1f;
+  x = fmaxf(x, -200.f);
+  const float y = x * kLog2e;
+  const float rest = fmaf(x, kLog2eRest, fmaf(x, kLog2e, -y));
+  const float e = __builtin_amdgcn_exp2f(y);
+  return fmaf(e, rest * kLn2, e);
+}
+
+// A logit and its expert; greater: (logit desc, expert asc).
+// 16-bit logits: one integer, the logit's bits made ascending (0: shut) above 65535 - expert.
+template <class T>
+struct Choice {
+  uint32_t key;
+  __device__ __forceinline__ static Choice make(float f, int expert) {
+    const uint32_t b = __builtin_bit_cast(uint16_t, (T)(f + 0.f));   // exact; -0 as 0
+    const uint32_t o = (b & 0x8000u) ? ~b & 0xFFFFu : b | 0x8000u;
+    return {f > -INFINITY ? (o << 16) | (uint32_t)(65535 - expert) : 0u};
+  }
+  __device__ __forceinline__ bool open() const { return key != 0u; }
+  __device__ __forceinline__ float logit() const {
+    const uint32_t o = key >> 16;
+    return fminf((float)__builtin_bit_cast(T, (uint16_t)((o & 0x8000u) ? o & 0x7FFFu : ~o)), FLT_MAX);
+  }
+  __device__ __forceinline__ int expert() const { return 65535 - (int)(key & 0xFFFFu); }
+  __device__ __forceinline__ bool same(Choice c) const { return key == c.key; }
+  __device__ __forceinline__ static void order(Choice &a, Choice &b) {   // a the greater
+    const uint32_t x = a.key, y = b.key;
+    a.key = x > y ? x : y;
+    b.key = x > y ? y : x;
+  }
+  __device__ __forceinline__ static Choice best(Choice c, int L) { return {group_max(c.key, L)}; }
+};
+template <>
+struct Choice<float> {
+  uint32_t o, id;
+  __device__ __forceinline__ static Choice make(float f, int expert) { return {logit_order(f), (uint32_t)expert}; }
+  __device__ __forceinline__ bool open() const { return o != 0u; }
+  __device__ __forceinline__ float logit() const { return order_logit(o); }
+  __device__ __forceinline__ int expert() const { return (int)id; }
+  __device__ __forceinline__ bool same(Choice c) const { return id == c.id && o == c.o; }
+  __device__ __forceinline__ static void order(Choice &a, Choice &b) {
+    const bool swap = b.o > a.o || (b.o == a.o && b.id < a.id);
+    const Choice x = a, y = b;
+    a = swap ? y : x;
+    b = swap ? x : y;
+  }
+  __device__ __forceinline__ static Choice best(Choice c, int L) {
+    const uint32_t m = group_max(c.o, L);
+    return {m, ~group_max(c.o == m ? ~c.id : 0u, L)};
+  }
+};
 
 struct __attribute__((packed, aligned(2))) Eight16 { uint16_t v[8]; };
 struct __attribute__((packed, aligned(4))) Eight32 { float v[8]; };
@@ -58,13 +112,22 @@ __device__ __forceinline__ void load_logits(const T *row, int first, int E, floa
   }
 }
 
+// descending, by a network of 19 exchanges
+template <class C>
+__device__ __forceinline__ void sort_eight(C (&c)[kPer]) {
+  constexpr int pairs[19][2] = {{0, 1}, {2, 3}, {4, 5}, {6, 7}, {0, 2}, {1, 3}, {4, 6}, {5, 7}, {1, 2}, {5, 6},
+                                {0, 4}, {1, 5}, {2, 6}, {3, 7}, {2, 4}, {3, 5}, {1, 2}, {3, 4}, {5, 6}};
+#pragma unroll
+  for (int i = 0; i < 19; ++i) C::order(c[pairs[i][0]], c[pairs[i][1]]);
+}
+
 template <class T, int L>
 __global__ __launch_bounds__(kRouteThreads) void k_route(const T *logits, int64_t n_tokens, int E, int top,
                                                          int renormalise, int32_t *out_experts, float *out_weights) {
-  const int l = threadIdx.x % 64, in = l % L, first = in * kPer;
-  const uint64_t mine = (L == 64 ? ~0ull : ((1ull << (L & 63)) - 1)) << (l - in);   // this group's lanes
-  // entries a lane keeps: top <= 16, and top <= E <= kPer L
-  constexpr int kKept = ((SVT_MAX_TOP < kPer * L ? SVT_MAX_TOP : kPer * L) + L - 1) / L;
+  using C = Choice<T>;
+  const int in = threadIdx.x % L, first = in * kPer;
+  // entries a lane keeps (entry j with lane j % L): top <= 16, and top <= E <= kPer L
+  constexpr int kTop = SVT_MAX_TOP < kPer * L ? SVT_MAX_TOP : kPer * L, kKept = (kTop + L - 1) / L;
   const int64_t per_block = kRouteThreads / L;
   for (int64_t t0 = blockIdx.x * per_block; t0 < n_tokens; t0 += gridDim.x * per_block) {
     // every lane of the wave takes part in the group moves: a token past the end is a copy of the last
@@ -72,90 +135,86 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(const T *logits, int64_
     const int64_t tr = t < n_tokens ? t : n_tokens - 1;
     float v[kPer];
     load_logits(logits + tr * E, first, E, v);
-    uint32_t o[kPer];
+    C c[kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) o[i] = logit_order(v[i]);
-    float peak = 0.f, total = 0.f;
-    float kept_e[kKept];   // entry j stays with lane j % L until the sum is known
-    int32_t kept_id[kKept];
-    for (int j = 0; j < top; ++j) {
-      uint32_t best = o[0];
-      int at = 0;
+    for (int i = 0; i < kPer; ++i) c[i] = C::make(v[i], first + i);
+    sort_eight(c);
+    C kept[kKept];
+    C peak{};
 #pragma unroll
-      for (int i = 1; i < kPer; ++i)
-        if (o[i] > best) { best = o[i]; at = i; }
-      const uint32_t gbest = group_max(best, L);
-      const int winner = __ffsll((long long)(__ballot(best == gbest) & mine)) - 1;
-      const bool open = gbest != 0u;
-      const int picked = L == 1 ? first + at : __shfl(first + at, winner);
-      const int id = open ? picked : -1;
-      if (l == winner) {
+    for (int j = 0; j < kTop; ++j)
+      if (j < top) {
+        const C best = C::best(c[0], L);
+        if (j == 0) peak = best;
+        if (in == j % L) kept[j / L] = best;
+        const bool mine = c[0].same(best);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (i == at) o[i] = 0u;
+        for (int i = 0; i + 1 < kPer; ++i) c[i] = mine ? c[i + 1] : c[i];
+        if (mine) c[kPer - 1] = C{};
       }
-      const float x = order_logit(gbest);
-      if (j == 0) {
-        peak = open ? x : 0.f;
-        if (!renormalise) {
-          float s = 0.f;
+    const float high = peak.open() ? peak.logit() : 0.f;
+    float e[kKept], sum = 0.f;
 #pragma unroll
-          for (int i = 0; i < kPer; ++i) s += logit_order(v[i]) ? expf(fminf(v[i], FLT_MAX) - peak) : 0.f;
-          total = group_add(s, L);
-        }
-      }
-      const float e = open ? expf(x - peak) : 0.f;
-      if (renormalise) total += e;
-      if (in == j % L) {
-#pragma unroll
-        for (int q = 0; q < kKept; ++q)
-          if (q == j / L) {
-            kept_e[q] = e;
-            kept_id[q] = id;
-          }
-      }
+    for (int q = 0; q < kKept; ++q) {
+      const bool open = q * L + in < top && kept[q].open();
+      e[q] = open ? exp_below(kept[q].logit() - high) : 0.f;
+      sum += e[q];
     }
-    const float scale = total > 0.f ? total : 1.f;
+    if (!renormalise) {
+      sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) sum += logit_order(v[i]) ? exp_below(fminf(v[i], FLT_MAX) - high) : 0.f;
+    }
+    sum = group_add(sum, L);
+    const float scale = sum > 0.f ? sum : 1.f;
     if (t < n_tokens) {
 #pragma unroll
       for (int q = 0; q < kKept; ++q) {
         const int j = q * L + in;
         if (j < top) {
-          out_experts[t * top + j] = kept_id[q];
-          out_weights[t * top + j] = kept_e[q] / scale;
+          out_experts[t * top + j] = kept[q].open() ? kept[q].expert() : -1;
+          out_weights[t * top + j] = e[q] / scale;
         }
       }
     }
   }
 }
 
+// The weights' gradients reach their experts' lanes through LDS (added there: an expert named twice gets
+// both).
 template <class T, int L>
 __global__ __launch_bounds__(kRouteThreads) void k_route_backward(const T *logits, int64_t n_tokens, int E, int top,
                                                                   int renormalise, const int32_t *experts,
                                                                   const float *weights, const float *d_weights,
                                                                   T *d_logits) {
-  const int l = threadIdx.x % 64, in = l % L, first = in * kPer;
+  __shared__ __attribute__((aligned(16))) float spread[kRouteThreads][kPer];
+  const int in = threadIdx.x % L, first = in * kPer;
+  float *own = spread[threadIdx.x], *token = spread[threadIdx.x - in];
   const int64_t per_block = kRouteThreads / L;
   for (int64_t t0 = blockIdx.x * per_block; t0 < n_tokens; t0 += gridDim.x * per_block) {
     const int64_t t = t0 + threadIdx.x / L;
     const int64_t tr = t < n_tokens ? t : n_tokens - 1;
-    const int32_t *ids = experts + tr * top;
-    const float *w = weights + tr * top, *dw = d_weights + tr * top;
+    float v[kPer];
+    load_logits(logits + tr * E, first, E, v);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) own[i] = 0.f;
     float dot = 0.f;
-    for (int j = 0; j < top; ++j) dot += (uint32_t)ids[j] < (uint32_t)E ? dw[j] * w[j] : 0.f;
+    for (int j = in; j < top; j += L) {
+      const bool ok = (uint32_t)experts[tr * top + j] < (uint32_t)E;
+      dot += ok ? d_weights[tr * top + j] * weights[tr * top + j] : 0.f;
+    }
+    dot = group_add(dot, L);
+    __syncthreads();
+    for (int j = in; j < top; j += L) {
+      const int id = experts[tr * top + j];
+      const float d = d_weights[tr * top + j];
+      if ((uint32_t)id < (uint32_t)E) atomicAdd(&token[id], renormalise ? weights[tr * top + j] * (d - dot) : d);
+    }
+    __syncthreads();
     float g[kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) g[i] = 0.f;
-    if (renormalise) {
-      for (int j = 0; j < top; ++j) {
-        const int at = ids[j] - first;
-        const float d = w[j] * (dw[j] - dot);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) g[i] += at == i ? d : 0.f;
-      }
-    } else {
-      float v[kPer];
-      load_logits(logits + tr * E, first, E, v);
+    for (int i = 0; i < kPer; ++i) g[i] = own[i];
+    if (!renormalise) {
       uint32_t best = 0u;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
@@ -163,23 +222,17 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_backward(const T *logit
         best = o > best ? o : best;
       }
       best = group_max(best, L);
-      const float peak = best ? order_logit(best) : 0.f;
-      float s = 0.f;
+      const float high = best ? order_logit(best) : 0.f;
+      float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        v[i] = logit_order(v[i]) ? expf(fminf(v[i], FLT_MAX) - peak) : 0.f;
-        s += v[i];
+        v[i] = logit_order(v[i]) ? exp_below(fminf(v[i], FLT_MAX) - high) : 0.f;
+        sum += v[i];
       }
-      s = group_add(s, L);
-      const float scale = s > 0.f ? s : 1.f;
-      for (int j = 0; j < top; ++j) {
-        const int at = ids[j] - first;
-        const float d = dw[j];
+      sum = group_add(sum, L);
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) g[i] += at == i ? d : 0.f;
-      }
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) g[i] = v[i] / scale * (g[i] - dot);
+      for (int i = 0; i < kPer; ++i) g[i] = v[i] * inv * (g[i] - dot);
     }
     if (t >= n_tokens) continue;
     T *out = d_logits + t * E + first;

@@ -110,11 +110,26 @@ def test_route_infinite_logits(svt):
     assert host(w).tolist() == [[0.5, 0.5, 0.0], [1.0, 0.0, 0.0]]
 
 
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+def test_route_zeros_tie_and_neighbours_do_not(svt, kind):
+    """-0 ties with 0 (the lower expert first); logits one step of the type apart do not."""
+    step = 1.0 + 2 * HALF[kind]
+    l = np.array([[0.0, -0.0, 0.0, -0.0, -1.0, 0.0], [1.0, step, 1.0, -step, -1.0, step]])
+    ids, _ = svt.svt_route(dev(l, ty(kind)), 6)
+    assert host(ids).tolist() == [[0, 1, 2, 3, 5, 4], [1, 5, 0, 2, 4, 3]]
+    ids, _ = svt.svt_route(dev(l[:, ::-1].copy(), ty(kind)), 6)
+    assert host(ids).tolist() == [[0, 2, 3, 4, 5, 1], [0, 4, 3, 5, 1, 2]]
+
+
 def test_route_backward_ignores_foreign_experts(svt):
     l = dev(np.zeros((1, 4), np.float32))
     ids = dev(np.array([[-1, 9, 2, -2 ** 31]], np.int32))
     ones = dev(np.ones((1, 4), np.float32))
     assert host(svt.svt_route_backward(l, ids, ones, ones, renormalise=True)).tolist() == [[0, 0, 0, 0]]
+    twice = dev(np.array([[2, 2, 0, 2]], np.int32))   # an expert named more than once gets every part
+    half = dev(np.full((1, 4), 0.5, np.float32))
+    got = svt.svt_route_backward(l, twice, half, dev(np.array([[1.0, 2.0, 4.0, 8.0]], np.float32)), renormalise=True)
+    assert host(got).tolist() == [[0.5 * (4 - 7.5), 0, 0.5 * (11 - 3 * 7.5), 0]]
     w = dev(np.full((1, 4), 0.25, np.float32))
     assert host(svt.svt_route_backward(l, ids, w, ones, renormalise=False)).tolist() == [[-0.0625, -0.0625, 0.1875, -0.0625]]
 
