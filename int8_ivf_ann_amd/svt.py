@@ -508,10 +508,10 @@ def _check_dense(name, t, dtype, shape, dev):
     _check_tensor(name, t, (dtype,), shape, dev)
 
 
-def _out(name, t, dtype, shape, dev):
-    import torch
+def _out(name, t, dtype, shape, dev, like):
+    """t, checked; or a new tensor, made by ``like`` (a tensor on dev), the quickest way torch has."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
     _check_dense(name, t, dtype, shape, dev)
     return t
 
@@ -536,8 +536,8 @@ def svt_route(logits, top: int, renormalise: bool = True, out_experts=None, out_
     import torch
     (T, E), code, dev = _rows_of("logits", logits)
     with _Run(dev, stream) as s:
-        out_experts = _out("out_experts", out_experts, torch.int32, (T, top), dev)
-        out_weights = _out("out_weights", out_weights, torch.float32, (T, top), dev)
+        out_experts = _out("out_experts", out_experts, torch.int32, (T, top), dev, logits)
+        out_weights = _out("out_weights", out_weights, torch.float32, (T, top), dev, logits)
         _check(lib().svt_route(T, E, top, code, logits.data_ptr(), int(renormalise), out_experts.data_ptr(),
                                out_weights.data_ptr(), s))
     return out_experts, out_weights
@@ -553,7 +553,7 @@ def svt_route_backward(logits, experts, weights, d_weights, renormalise: bool = 
     _check_dense("weights", weights, torch.float32, (T, K), dev)
     _check_dense("d_weights", d_weights, torch.float32, (T, K), dev)
     with _Run(dev, stream) as s:
-        out = _out("out", out, logits.dtype, (T, E), dev)
+        out = _out("out", out, logits.dtype, (T, E), dev, logits)
         _check(lib().svt_route_backward(T, E, K, code, logits.data_ptr(), int(renormalise), experts.data_ptr(),
                                         weights.data_ptr(), d_weights.data_ptr(), out.data_ptr(), s))
     return out
@@ -568,9 +568,9 @@ def svt_expert_sort(experts, n_experts: int, offsets=None, order=None, position=
     T, K, dev = _entries("experts", experts)
     L = lib()
     with _Run(dev, stream) as s:
-        offsets = _out("offsets", offsets, torch.int32, (n_experts + 1,), dev)
-        order = _out("order", order, torch.int32, (T * K,), dev)
-        position = _out("position", position, torch.int32, (T, K), dev)
+        offsets = _out("offsets", offsets, torch.int32, (n_experts + 1,), dev, experts)
+        order = _out("order", order, torch.int32, (T * K,), dev, experts)
+        position = _out("position", position, torch.int32, (T, K), dev, experts)
         need = L.svt_expert_sort_workspace_size(T, K, n_experts)
         if workspace is not None:
             _check_tensor("workspace", workspace, (torch.uint8,), (workspace.numel(),), dev)
@@ -590,7 +590,7 @@ def svt_expert_dispatch(x, position, out=None, stream=None):
     if position.shape[0] != T:
         raise ValueError(f"position: shape {tuple(position.shape)} for {T} tokens")
     with _Run(dev, stream) as s:
-        out = _out("out", out, x.dtype, (T * K, D), dev)
+        out = _out("out", out, x.dtype, (T * K, D), dev, x)
         _check(lib().svt_expert_dispatch(T, K, D, code, x.data_ptr(), position.data_ptr(), out.data_ptr(), s))
     return out
 
@@ -607,7 +607,7 @@ def _gather_sum(fn, name, rows, position, weights, out, stream):
             _check_dense("weights", weights, torch.float32, (T, K), dev)
         args = (None if weights is None else weights.data_ptr(),)
     with _Run(dev, stream) as s:
-        out = _out("out", out, rows.dtype, (T, D), dev)
+        out = _out("out", out, rows.dtype, (T, D), dev, rows)
         _check(getattr(lib(), fn)(T, K, D, code, rows.data_ptr(), position.data_ptr(), *args, out.data_ptr(), s))
     return out
 
@@ -634,8 +634,8 @@ def svt_expert_combine_backward(dy, rows, position, weights, out_rows=None, out_
     _check_dense("rows", rows, dy.dtype, (T * K, D), dev)
     _check_dense("weights", weights, torch.float32, (T, K), dev)
     with _Run(dev, stream) as s:
-        out_rows = _out("out_rows", out_rows, dy.dtype, (T * K, D), dev)
-        out_weights = _out("out_weights", out_weights, torch.float32, (T, K), dev)
+        out_rows = _out("out_rows", out_rows, dy.dtype, (T * K, D), dev, dy)
+        out_weights = _out("out_weights", out_weights, torch.float32, (T, K), dev, dy)
         _check(lib().svt_expert_combine_backward(T, K, D, code, dy.data_ptr(), rows.data_ptr(), position.data_ptr(),
                                                  weights.data_ptr(), out_rows.data_ptr(), out_weights.data_ptr(), s))
     return out_rows, out_weights
@@ -661,7 +661,7 @@ def svt_quant_pack(nibbles, scales, zeros, n_in: int, group: int, packed=None, s
     if need == 0:
         raise SvtError(SVT_EUNSUPPORTED if group not in (32, 64, 128) else SVT_EINVAL, svt_last_error())
     with _Run(dev, stream) as s:
-        packed = _out("packed", packed, torch.uint8, (need,), dev)
+        packed = _out("packed", packed, torch.uint8, (need,), dev, nibbles)
         w.packed, w.packed_bytes, w.buffer = packed.data_ptr(), need, packed
         _check(lib().svt_quant_pack(ctypes.byref(w), nibbles.data_ptr(), scales.data_ptr(),
                                     None if zeros is None else zeros.data_ptr(), s))
@@ -696,7 +696,7 @@ def svt_quant_linear(x, weights: svt_quant_weights, offsets=None, bias=None, act
     if out_dtype not in _types():
         raise ValueError(f"out: dtype {out_dtype} not in {[str(d) for d in _types()]}")
     with _Run(dev, stream) as s:
-        out = _out("out", out, out_dtype, (R, N), dev)
+        out = _out("out", out, out_dtype, (R, N), dev, x)
         _check(lib().svt_quant_linear(R, code, x.data_ptr(), ctypes.byref(weights),
                                       None if offsets is None else offsets.data_ptr(),
                                       None if bias is None else bias.data_ptr(), _ACTIVATIONS[activation],
