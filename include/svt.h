@@ -386,7 +386,7 @@ int svt_expert_sort(int32_t n_tokens, int32_t top, int32_t n_experts, const int3
  *   combine             y[t] = sum_j weights[t][j] rows[position[t][j]]  (weights NULL: every weight 1)
  *   combine_backward    d_rows[position[t][j]] = weights[t][j] dy[t]
  *                       d_weights[t][j] = dy[t] . rows[position[t][j]], 0 for a dropped entry
- *   x, y, dx, dy   [n_tokens][width] of dtype; a token whose entries are all dropped gets a row of zeros
+ *   x, y, dx, dy   [n_tokens][width] of dtype, 1 <= width <= 2^24; a token whose entries are all dropped gets a row of zeros
  *   rows, d_rows   [n_tokens * top][width] of dtype; rows that no entry names are neither read nor written
  *   weights, d_weights  [n_tokens][top] float
  * n_tokens == 0 returns SVT_OK without enqueuing.  Errors: SVT_EINVAL, SVT_EDEVICE as svt_route.
@@ -440,7 +440,8 @@ int svt_quant_pack(const svt_quant_weights *w, const uint8_t *nibbles, const voi
  *   activation  SVT_ACT_NONE or SVT_ACT_RELU (NaN stays NaN)
  *   y           [n_rows][n_out] of out_dtype: dtype or SVT_F32
  * No weight or product is rounded: group sums of x q and of x are float32, and 256 times the sum of |x| over a
- * group must stay finite.  A row that holds an infinity or NaN gets NaN outputs.  n_rows == 0 returns
+ * group must stay finite, as must the scales.  A row that holds an infinity or NaN gets NaN outputs.  Of float32
+ * rows, digits below 2^-133 are not used.  n_rows == 0 returns
  * SVT_OK without enqueuing.  Errors: SVT_EINVAL, SVT_EUNSUPPORTED (group), SVT_EDEVICE as svt_quant_pack.
  */
 int svt_quant_linear(int32_t n_rows, int32_t dtype, const void *x, const svt_quant_weights *w, const int32_t *offsets,

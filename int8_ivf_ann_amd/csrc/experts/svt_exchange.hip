@@ -256,6 +256,7 @@ void with_bits(int E, F f) {
 
 constexpr int kExThreads = 256;
 constexpr int64_t kExMaxBlocks = 1 << 20;
+constexpr int32_t kMaxWidth = 1 << 24;
 
 // V bytes of a row, moved by one load or store
 template <int V> struct Bytes { typedef uint32_t type __attribute__((ext_vector_type(V / 4))); };
@@ -431,7 +432,7 @@ int check_shape(const char *who, int32_t n_tokens, int32_t top, int32_t width, i
   if (top < 1 || top > SVT_MAX_TOP) return report(SVT_EINVAL, "%s: top %d out of [1, %d]", who, top, SVT_MAX_TOP);
   if ((int64_t)n_tokens * top > kMaxEntries)
     return report(SVT_EINVAL, "%s: %lld entries, more than 2^30", who, (long long)n_tokens * top);
-  if (width < 1) return report(SVT_EINVAL, "%s: width %d < 1", who, width);
+  if (width < 1 || width > kMaxWidth) return report(SVT_EINVAL, "%s: width %d out of [1, %d]", who, width, kMaxWidth);
   if (!elem_size(dtype)) return report(SVT_EINVAL, "%s: unknown element type %d", who, dtype);
   return SVT_OK;
 }

@@ -182,7 +182,7 @@ __device__ __forceinline__ bool find_rows(const LinearArgs &a, int64_t unit, int
     }
     before = __builtin_amdgcn_readlane(upto, 63);
   }
-  if (owner < 0) return false;
+  if (owner < 0 || rest < 0) return false;   // rest < 0: offsets that do not ascend, their counts past 2^31
   const int64_t end = row_end(a, owner + 1);
   *matrix = owner;
   *r0 = row_end(a, owner) + (int64_t)rest * most;

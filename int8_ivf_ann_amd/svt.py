@@ -503,7 +503,7 @@ def _rows_of(name, t, dims=2):
 def _check_dense(name, t, dtype, shape, dev):
     """_check_tensor for one dtype, without its formatting on the way to success."""
     if t is not None and getattr(t, "dtype", None) is dtype and t.shape == shape and t.is_contiguous() and \
-            t.device == dev:
+            t.is_cuda and t.device == dev:
         return
     _check_tensor(name, t, (dtype,), shape, dev)
 
@@ -535,6 +535,8 @@ def svt_route(logits, top: int, renormalise: bool = True, out_experts=None, out_
     ``top`` are open."""
     import torch
     (T, E), code, dev = _rows_of("logits", logits)
+    if not 1 <= top <= min(SVT_MAX_TOP, E):
+        raise ValueError(f"top: {top} out of [1, min({SVT_MAX_TOP}, {E} experts)]")
     with _Run(dev, stream) as s:
         out_experts = _out("out_experts", out_experts, torch.int32, (T, top), dev, logits)
         out_weights = _out("out_weights", out_weights, torch.float32, (T, top), dev, logits)
@@ -548,8 +550,9 @@ def svt_route_backward(logits, experts, weights, d_weights, renormalise: bool = 
     the weights' gradient d_weights (float32 [T, top]) -> d_logits [T, E] of the logits' dtype."""
     import torch
     (T, E), code, dev = _rows_of("logits", logits)
-    _, K, _ = _entries("experts", experts, dev)
-    _check_dense("experts", experts, torch.int32, (T, K), dev)
+    n, K, _ = _entries("experts", experts, dev)
+    if n != T:
+        raise ValueError(f"experts: shape {tuple(experts.shape)} for {T} tokens")
     _check_dense("weights", weights, torch.float32, (T, K), dev)
     _check_dense("d_weights", d_weights, torch.float32, (T, K), dev)
     with _Run(dev, stream) as s:
@@ -566,6 +569,8 @@ def svt_expert_sort(experts, n_experts: int, offsets=None, order=None, position=
     dropped)."""
     import torch
     T, K, dev = _entries("experts", experts)
+    if not 1 <= n_experts <= SVT_MAX_EXPERTS:
+        raise ValueError(f"n_experts: {n_experts} out of [1, {SVT_MAX_EXPERTS}]")
     L = lib()
     with _Run(dev, stream) as s:
         offsets = _out("offsets", offsets, torch.int32, (n_experts + 1,), dev, experts)
@@ -586,8 +591,8 @@ def svt_expert_dispatch(x, position, out=None, stream=None):
     """Each token's row to its sorted rows: x [T, D], position int32 [T, top] -> rows [T * top, D].  Rows that
     no entry names (behind the last one) are left as they were."""
     (T, D), code, dev = _rows_of("x", x)
-    _, K, _ = _entries("position", position, dev)
-    if position.shape[0] != T:
+    n, K, _ = _entries("position", position, dev)
+    if n != T:
         raise ValueError(f"position: shape {tuple(position.shape)} for {T} tokens")
     with _Run(dev, stream) as s:
         out = _out("out", out, x.dtype, (T * K, D), dev, x)
@@ -629,8 +634,9 @@ def svt_expert_combine_backward(dy, rows, position, weights, out_rows=None, out_
     [T * top, D], d_weights float32 [T, top]).  Rows that no entry names are left as they were."""
     import torch
     (T, D), code, dev = _rows_of("dy", dy)
-    _, K, _ = _entries("position", position, dev)
-    _check_dense("position", position, torch.int32, (T, K), dev)
+    n, K, _ = _entries("position", position, dev)
+    if n != T:
+        raise ValueError(f"position: shape {tuple(position.shape)} for {T} tokens")
     _check_dense("rows", rows, dy.dtype, (T * K, D), dev)
     _check_dense("weights", weights, torch.float32, (T, K), dev)
     with _Run(dev, stream) as s:

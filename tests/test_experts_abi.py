@@ -81,7 +81,7 @@ def test_sort_workspace_size(L):
 
 
 COMMON = [(dict(T=-1), "n_tokens"), (dict(top=0), "top"), (dict(top=17), "top"), (dict(T=2 ** 27, top=16), "2^30"),
-          (dict(D=0), "width"), (dict(dtype=3), "type")]
+          (dict(D=0), "width"), (dict(D=2 ** 24 + 1), "width"), (dict(dtype=3), "type")]
 
 
 @pytest.mark.parametrize("kw, text", COMMON + [
@@ -191,6 +191,7 @@ def test_binding_refusals():
         (lambda: svt.svt_route(None, 2), "2-D"),
         (lambda: svt.svt_route_backward(f, i, f, f), "device tensor"),
         (lambda: svt.svt_expert_sort(i.long(), 4), "dtype"),
+        (lambda: svt.svt_expert_sort(i, 4), "device tensor"),
         (lambda: svt.svt_expert_sort(i[0], 4), "2-D"),
         (lambda: svt.svt_expert_sort(i.t(), 4), "contiguous"),
         (lambda: svt.svt_expert_dispatch(f, i), "device tensor"),

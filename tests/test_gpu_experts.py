@@ -347,6 +347,71 @@ def test_linear_by_expert(svt, counts, N, K, G, kind):
     assert np.all(host(y)[off[-1]:] == 7.0)
 
 
+@pytest.mark.parametrize("kind, unit", [("f16", 2.0 ** -24), ("bf16", 2.0 ** -120), ("f32", 2.0 ** -105)])
+def test_linear_small_values_are_exact(svt, kind, unit):
+    """Rows of the identity times a small unit (float16: its smallest subnormal; float32: with 24 significant
+    bits): scales of 1, so every output is the unit times q - z, exactly."""
+    K, N = 40, 48
+    q = np.random.default_rng(3).integers(0, 16, (1, N, K)).astype(np.uint8)
+    nib = dev((q[..., 0::2] | (q[..., 1::2] << 4)).astype(np.uint8))
+    packed = svt.svt_quant_pack(nib, dev(np.ones((1, N, 2), np.float32)), None, K, 32)
+    value = unit * ((2 ** 24 - 1) / 2 ** 23 if kind == "f32" else 1.0)
+    y = svt.svt_quant_linear(dev(np.eye(K) * value, ty(kind)), packed, out_dtype=ty("f32"))
+    if kind == "f32":   # 24 bits times 4 bits: rounded once more, and the start value 8 x once
+        near(host(y), value * (q[0].astype(np.float64) - 8).T, 3 * U * 16 * value, "small")
+    else:
+        assert np.array_equal(host(y), value * (q[0].astype(np.float64) - 8).T)
+
+
+def test_nothing_to_do(svt):
+    """No tokens: empty outputs, offsets of 0; no rows: an empty product."""
+    import torch
+    e = torch.empty(0, 8, device="cuda", dtype=torch.float16)
+    ids, w = svt.svt_route(e, 2)
+    assert ids.shape == (0, 2) and w.shape == (0, 2)
+    assert svt.svt_route_backward(e, ids, w, w).shape == (0, 8)
+    off, order, pos = svt.svt_expert_sort(ids, 5)
+    assert host(off).tolist() == [0] * 6 and order.shape == (0,) and pos.shape == (0, 2)
+    rows = svt.svt_expert_dispatch(e, pos)
+    assert rows.shape == (0, 8) and svt.svt_expert_combine(rows, pos, w).shape == (0, 8)
+    assert svt.svt_expert_dispatch_backward(rows, pos).shape == (0, 8)
+    assert [t.shape for t in svt.svt_expert_combine_backward(e, rows, pos, w)] == [(0, 8), (0, 2)]
+    packed, *_ = make_weights(svt, np.random.default_rng(0), 5, 16, 8, 32, "f16", False)
+    assert svt.svt_quant_linear(rows, packed, offsets=off).shape == (0, 16)
+
+
+def test_refusals_leave_outputs(svt):
+    """Calls that are refused on the device tensors themselves: errors, and outputs as they were."""
+    import torch
+    f = torch.ones(4, 8, device="cuda")
+    i = torch.zeros(4, 2, dtype=torch.int32, device="cuda")
+    rows, w = torch.ones(8, 8, device="cuda"), torch.ones(4, 2, device="cuda")
+    out = torch.full((8, 8), 7.0, device="cuda")
+    packed, *_ = make_weights(svt, np.random.default_rng(0), 2, 16, 8, 32, "f16", False)
+    for call in [
+        lambda: svt.svt_route(f, 9), lambda: svt.svt_route(f, 0), lambda: svt.svt_route(f, -1),
+        lambda: svt.svt_route_backward(f, i[:3], w, w), lambda: svt.svt_route_backward(f, i, w.half(), w),
+        lambda: svt.svt_expert_sort(i, 0), lambda: svt.svt_expert_sort(i, 513), lambda: svt.svt_expert_sort(i, -4),
+        lambda: svt.svt_expert_dispatch(f, i[:2], out=out), lambda: svt.svt_expert_dispatch(f, i, out=out[:4]),
+        lambda: svt.svt_expert_dispatch(out[:4], i, out=out),
+        lambda: svt.svt_expert_combine(rows[:6], i, w), lambda: svt.svt_expert_combine(out, i, w, out=out[:4]),
+        lambda: svt.svt_expert_combine_backward(f, rows.half(), i, w, out_rows=out),
+        lambda: svt.svt_expert_combine_backward(f, rows, i, w, out_rows=rows),
+        lambda: svt.svt_quant_linear(f, packed, out=out), lambda: svt.svt_quant_linear(f[:, :4], packed),
+        lambda: svt.svt_quant_linear(f, packed, offsets=torch.zeros(2, dtype=torch.int32, device="cuda")),
+        lambda: svt.svt_quant_linear(f, packed, offsets=torch.zeros(3, dtype=torch.int32, device="cuda"),
+                                     activation="gelu"),
+        lambda: svt.svt_quant_linear(f, packed, offsets=torch.zeros(3, dtype=torch.int32, device="cuda"),
+                                     out_dtype=torch.float16),
+        lambda: svt.svt_quant_pack(torch.zeros(16, 3, dtype=torch.uint8, device="cuda"), rows[:, :1], None, 8, 32),
+        lambda: svt.svt_quant_pack(torch.zeros(8, 4, dtype=torch.uint8, device="cuda"), rows[:, :1].contiguous(), None, 8, 16),
+    ]:
+        with pytest.raises((ValueError, svt.SvtError)):
+            call()
+    torch.cuda.synchronize()
+    assert bool((out == 7.0).all()) and bool((rows == 1.0).all())
+
+
 def test_linear_offsets_are_clamped(svt):
     """Ends past the rows are cut, ends that do not ascend give no rows; nothing else is touched."""
     rng = np.random.default_rng(8)
