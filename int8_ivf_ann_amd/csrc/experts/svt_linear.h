@@ -502,17 +502,20 @@ void with_flag(int32_t on, F f) {
 
 // How a product is cut: rows x outputs of a workgroup and how its waves share them, by the number of
 // workgroups that each cut gives.  The largest cut that still gives 512 (two per compute unit, so that one
-// loads while the other multiplies) is taken; bfloat16, groups of 128, us, chosen cut
-// against its neighbour:
+// loads while the other multiplies; the 8 waves of the 64 x 256 cut do with 256) is taken.  bfloat16, groups
+// of 128, us, the chosen cut against its neighbour:
 //   1024 rows, 4096 x 1024:  64 x 256 cut 18.6,  32 x 128 22.0
 //   1024 rows, 1024 x 1024:  32 x  64 cut  9.4,  32 x 128 11.2
 //    256 rows, 1024 x 1024:  16 x  32 cut  5.7,  16 x  16  6.0
 //     16 rows, 4096 x 1024:  16 x  16 cut  4.3,  16 x  32  5.1
-// Up to 16 rows of a large matrix (a decoding step) are bound by the weights' bytes: two tiles per wave, four
-// waves along k and two blocks of each in flight: 1 row, 16384 x 4096: 10.7, 16 x 32 cut 12.7.
+// Up to 16 rows of a large matrix (a decoding step) are bound by the weights' bytes and want about 8 waves on
+// every compute unit, each with two tiles and two blocks in flight: four or eight along k.  1 row, 16384 x
+// 4096: 10.7, as 16 x 16 cut 13.1; 8192 x 8192: 10.6 against 12.3.
 // Rows by expert: a cut of 32 rows is mostly empty below 8 rows per expert on average (64 rows, 64 experts of
 // 2048 x 1024: 16 x 32 cut 11.0, 32 x 128 13.0; 1024 rows: 32 x 128 26.2, 16 x 32 more than 32), and one of 64
 // rows loses to 32 by the experts' uneven numbers of rows (4096 rows, 8 experts: 32.5 against 25.6).
+// The last constant is waves per SIMD to leave registers for: 4096 rows of float16, groups of 32 with float32
+// scales: 3 waves 13.7, 2 waves 16.7; 64 rows of 64 experts: 4 waves 11.5, 2 waves 12.7.
 template <class T, class S, int G, bool Z>
 void linear_cut(LinearArgs a, hipStream_t stream) {
   const int64_t rows = a.n_rows, tiles = a.s.tiles;
@@ -520,19 +523,21 @@ void linear_cut(LinearArgs a, hipStream_t stream) {
   if (a.offsets) {
     const int64_t some = std::min<int64_t>(a.n_matrices, rows) / 2;   // half-filled blocks, about
     if (rows >= 8 * (int64_t)a.n_matrices && (rows / 32 + some) * ((tiles + 7) / 8) >= 256)
-      launch_linear<T, S, G, Z, 2, 2, 1, 1, 4, false, 2>(a, stream);
+      launch_linear<T, S, G, Z, 2, 2, 1, 1, 4, false, 3>(a, stream);
     else
-      launch_linear<T, S, G, Z, 1, 1, 2, 2, 2, false, 2>(a, stream);
+      launch_linear<T, S, G, Z, 1, 1, 2, 2, 2, false, 4>(a, stream);
   } else if (groups(64, 16) >= 256) {
     launch_linear<T, S, G, Z, 4, 2, 1, 1, 8, true, 2>(a, stream);
   } else if (groups(32, 8) >= 512) {
-    launch_linear<T, S, G, Z, 2, 2, 1, 1, 4, false, 2>(a, stream);
+    launch_linear<T, S, G, Z, 2, 2, 1, 1, 4, false, 3>(a, stream);
   } else if (groups(32, 4) >= 512) {
     launch_linear<T, S, G, Z, 2, 2, 1, 2, 2, false, 2>(a, stream);
   } else if (rows <= 16 && groups(16, 2) >= 512 && a.s.blocks >= 8) {
     launch_linear<T, S, G, Z, 1, 2, 2, 4, 1, false, 2>(a, stream);
+  } else if (rows <= 16 && groups(16, 2) >= 256 && a.s.blocks >= 16) {
+    launch_linear<T, S, G, Z, 1, 2, 2, 8, 1, false, 2>(a, stream);
   } else if (groups(16, 2) >= 512 || a.s.blocks < 8) {
-    launch_linear<T, S, G, Z, 1, 1, 2, 2, 2, false, 2>(a, stream);
+    launch_linear<T, S, G, Z, 1, 1, 2, 2, 2, false, 4>(a, stream);
   } else {
     launch_linear<T, S, G, Z, 1, 1, 1, 8, 1, false, 2>(a, stream);
   }

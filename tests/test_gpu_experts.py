@@ -290,7 +290,7 @@ def test_linear(svt, R, N, K, G, scale_kind, zeros, kind):
 
 
 # sizes that reach every way the product is cut, each ending inside rows, outputs, blocks and groups
-CUTS = [(1030, 4100, 260, 128), (520, 4000, 150, 64), (300, 3300, 137, 32), (13, 16400, 1100, 128),
+CUTS = [(1030, 4100, 260, 128), (520, 4000, 150, 64), (300, 3300, 137, 32), (13, 16400, 1100, 128), (5, 8200, 2050, 64),
         (100, 2400, 259, 64), (9, 700, 1500, 128), (40, 600, 385, 32)]
 
 
