@@ -514,22 +514,28 @@ void with_flag(int32_t on, F f) {
 // Rows by expert: a cut of 32 rows is mostly empty below 8 rows per expert on average (64 rows, 64 experts of
 // 2048 x 1024: 16 x 32 cut 11.0, 32 x 128 13.0; 1024 rows: 32 x 128 26.2, 16 x 32 more than 32), and one of 64
 // rows loses to 32 by the experts' uneven numbers of rows (4096 rows, 8 experts: 32.5 against 25.6).
-// The last constant is waves per SIMD to leave registers for: 4096 rows of float16, groups of 32 with float32
-// scales: 3 waves 13.7, 2 waves 16.7; 64 rows of 64 experts: 4 waves 11.5, 2 waves 12.7.
+// The last constant is waves per SIMD to leave registers for; more than a kind's registers allow spill.  Two-byte
+// rows: 4096 rows by 8 experts, 32 x 128 cut: 3 waves 13.7, 2 waves 16.7; 64 rows by 64 experts, 16 x 32 cut: 4
+// waves 11.5, 2 waves 12.7; but groups of 32, 64 rows, 4096 x 1024: 4 waves 7.4, 2 waves 5.9.  float32 rows
+// need two: 32 x 128 cut 20.8, with three 28.3.  The second chunk's buffers of the 64 x 256 cut fit groups of 128
+// without zero points (18.8 against 21.0); elsewhere they spill (groups of 32: 22.1, with them more than 27).
 template <class T, class S, int G, bool Z>
 void linear_cut(LinearArgs a, hipStream_t stream) {
+  constexpr bool kShort = sizeof(T) == 2;
+  constexpr int kWaves32 = kShort ? 3 : 2, kWaves16 = kShort && G >= 64 ? 4 : 2;
+  constexpr bool kAhead = kShort && G == 128 && !Z;
   const int64_t rows = a.n_rows, tiles = a.s.tiles;
   auto groups = [&](int64_t r, int64_t t) { return ((rows + r - 1) / r) * ((tiles + t - 1) / t); };
   if (a.offsets) {
     const int64_t some = std::min<int64_t>(a.n_matrices, rows) / 2;   // half-filled blocks, about
     if (rows >= 8 * (int64_t)a.n_matrices && (rows / 32 + some) * ((tiles + 7) / 8) >= 256)
-      launch_linear<T, S, G, Z, 2, 2, 1, 1, 4, false, 3>(a, stream);
+      launch_linear<T, S, G, Z, 2, 2, 1, 1, 4, false, kWaves32>(a, stream);
     else
-      launch_linear<T, S, G, Z, 1, 1, 2, 2, 2, false, 4>(a, stream);
-  } else if (groups(64, 16) >= 256) {
-    launch_linear<T, S, G, Z, 4, 2, 1, 1, 8, true, 2>(a, stream);
+      launch_linear<T, S, G, Z, 1, 1, 2, 2, 2, false, kWaves16>(a, stream);
+  } else if ((kShort || G < 128) && groups(64, 16) >= 256) {   // float32, groups of 128: 32 x 128 is quicker
+    launch_linear<T, S, G, Z, 4, 2, 1, 1, 8, kAhead, 2>(a, stream);
   } else if (groups(32, 8) >= 512) {
-    launch_linear<T, S, G, Z, 2, 2, 1, 1, 4, false, 3>(a, stream);
+    launch_linear<T, S, G, Z, 2, 2, 1, 1, 4, false, kWaves32>(a, stream);
   } else if (groups(32, 4) >= 512) {
     launch_linear<T, S, G, Z, 2, 2, 1, 2, 2, false, 2>(a, stream);
   } else if (rows <= 16 && groups(16, 2) >= 512 && a.s.blocks >= 8) {
@@ -537,7 +543,7 @@ void linear_cut(LinearArgs a, hipStream_t stream) {
   } else if (rows <= 16 && groups(16, 2) >= 256 && a.s.blocks >= 16) {
     launch_linear<T, S, G, Z, 1, 2, 2, 8, 1, false, 2>(a, stream);
   } else if (groups(16, 2) >= 512 || a.s.blocks < 8) {
-    launch_linear<T, S, G, Z, 1, 1, 2, 2, 2, false, 4>(a, stream);
+    launch_linear<T, S, G, Z, 1, 1, 2, 2, 2, false, kWaves16>(a, stream);
   } else {
     launch_linear<T, S, G, Z, 1, 1, 1, 8, 1, false, 2>(a, stream);
   }
