@@ -191,11 +191,21 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_place(const int32_t *expe
     while (along < E) along *= 2;
     const int i = tid % along;
     int sum = 0, before = 0;
+    const int step = kSortThreads / along;
     if (i < E)
-      for (int r = tid / along; r < s.blocks; r += kSortThreads / along) {
-        const int c = counts[(int64_t)r * E + i];
-        sum += c;
-        before += r < b ? c : 0;
+      for (int r0 = tid / along; r0 < s.blocks; r0 += 8 * step) {   // 8 loads in flight
+        int c[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int r = r0 + q * step;
+          c[q] = counts[(int64_t)(r < s.blocks ? r : r0) * E + i];
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int r = r0 + q * step;
+          sum += r < s.blocks ? c[q] : 0;
+          before += r < b ? c[q] : 0;
+        }
       }
     if (i < E && sum) {
       atomicAdd(&total[i], sum);
