@@ -325,8 +325,8 @@ int svt_rerank(const svt_index *ix, int32_t n_queries, const int8_t *queries, co
  *   - All pointers are device pointers of the current HIP device, which is also hip_stream's; arrays are
  *     row-major and dense, and need only their elements' alignment unless stated.
  *   - Rows hold float32, float16 or bfloat16 (SVT_F32, SVT_F16, SVT_BF16).  Sums, softmax statistics and
- *     weights are float32 and each result is rounded once.  No call uses atomics on floats: the same
- *     inputs give the same bits.
+ *     weights are float32 and each result is rounded once.  Sums run in a fixed order: the same inputs
+ *     give the same bits.
  *   - Every call is asynchronous on hip_stream, allocates nothing and can be captured into a graph.
  *   - An output may not overlap an input or another output (SVT_EINVAL).
  */

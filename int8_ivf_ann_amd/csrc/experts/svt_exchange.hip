@@ -31,6 +31,8 @@ namespace {
 //   two          k_sort_count: a histogram per block; k_sort_place: each block sums the histograms (few blocks
 //                of many entries keep that table small), ranks its entries, orders them in LDS and writes
 //                each expert's run in one piece.
+// Measured: 256 entries 2.3 us, 4096 4.6, 8192 9.0 (two launches 9.2), 1 M entries of 64 experts 13.4 (12.6
+// MB).  All are chains of short steps between barriers; bytes would take 2.5 us at 1 M.
 
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64, kSortSteps = 4;
 constexpr int kTileEntries = kSortThreads * kSortSteps;   // entries of a workgroup at a time
@@ -263,6 +265,9 @@ void with_bits(int E, F f) {
 }
 
 // ---- exchange ------------------------------------------------------------------------------------
+
+// Bound by memory.  65536 x 1024 bfloat16 rows, top 2: dispatch 64 us (6.3 TB/s), combine 90 us (4.5 TB/s);
+// 32768 tokens, top 4: combine's gradient 105 us (5.8 TB/s), dispatch's 76 us (4.4 TB/s).  A copy runs at 5.1.
 
 constexpr int kExThreads = 256;
 constexpr int64_t kExMaxBlocks = 1 << 20;
