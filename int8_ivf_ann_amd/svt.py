@@ -7,6 +7,7 @@ fallback: if libsvt.so is missing or fails to load, every entry point raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence, Tuple
 
@@ -562,6 +563,15 @@ def svt_route_backward(logits, experts, weights, d_weights, renormalise: bool = 
     return out
 
 
+@functools.lru_cache(maxsize=256)
+def svt_expert_sort_workspace_size(n_tokens: int, top: int, n_experts: int) -> int:
+    """Bytes of workspace that svt_expert_sort needs for these sizes (0: none)."""
+    need = lib().svt_expert_sort_workspace_size(n_tokens, top, n_experts)
+    if need == 0 and svt_last_error():
+        raise SvtError(SVT_EINVAL, svt_last_error())
+    return int(need)
+
+
 def svt_expert_sort(experts, n_experts: int, offsets=None, order=None, position=None, workspace=None, stream=None):
     """Entries grouped by expert, in their own order: experts int32 [T, top] (outside [0, n_experts): dropped)
     -> (offsets int32 [n_experts + 1], order int32 [T * top], position int32 [T, top]).  ``order`` names the
@@ -571,17 +581,16 @@ def svt_expert_sort(experts, n_experts: int, offsets=None, order=None, position=
     T, K, dev = _entries("experts", experts)
     if not 1 <= n_experts <= SVT_MAX_EXPERTS:
         raise ValueError(f"n_experts: {n_experts} out of [1, {SVT_MAX_EXPERTS}]")
-    L = lib()
+    need = svt_expert_sort_workspace_size(T, K, n_experts)
     with _Run(dev, stream) as s:
         offsets = _out("offsets", offsets, torch.int32, (n_experts + 1,), dev, experts)
         order = _out("order", order, torch.int32, (T * K,), dev, experts)
         position = _out("position", position, torch.int32, (T, K), dev, experts)
-        need = L.svt_expert_sort_workspace_size(T, K, n_experts)
         if workspace is not None:
             _check_tensor("workspace", workspace, (torch.uint8,), (workspace.numel(),), dev)
         elif need:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
-        _check(L.svt_expert_sort(T, K, n_experts, experts.data_ptr(), offsets.data_ptr(), order.data_ptr(),
+            workspace = experts.new_empty((need,), dtype=torch.uint8)
+        _check(lib().svt_expert_sort(T, K, n_experts, experts.data_ptr(), offsets.data_ptr(), order.data_ptr(),
                                  position.data_ptr(), None if workspace is None else workspace.data_ptr(),
                                  0 if workspace is None else workspace.numel(), s))
     return offsets, order, position

@@ -78,6 +78,9 @@ def test_sort_workspace_size(L):
     assert L.svt_expert_sort_workspace_size(1 << 26, 16, 512) < 1 << 24
     for bad in ((-1, 2, 8), (8, 0, 8), (8, 17, 8), (8, 2, 0), (8, 2, 513), (2 ** 27, 16, 8)):
         assert L.svt_expert_sort_workspace_size(*bad) == 0 and svt.svt_last_error()
+        with pytest.raises(svt.SvtError):
+            svt.svt_expert_sort_workspace_size(*bad)
+    assert svt.svt_expert_sort_workspace_size(8, 2, 8) == 0
 
 
 COMMON = [(dict(T=-1), "n_tokens"), (dict(top=0), "top"), (dict(top=17), "top"), (dict(T=2 ** 27, top=16), "2^30"),

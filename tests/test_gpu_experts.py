@@ -169,7 +169,7 @@ def test_sort(svt, T, K, E, mode):
 def test_sort_dirty_workspace_and_small_one(svt):
     import torch
     e = dev(np.random.default_rng(5).integers(0, 9, (30000, 2)).astype(np.int32))
-    need = svt.lib().svt_expert_sort_workspace_size(30000, 2, 9)
+    need = svt.svt_expert_sort_workspace_size(30000, 2, 9)
     a = svt.svt_expert_sort(e, 9)
     b = svt.svt_expert_sort(e, 9, workspace=torch.full((need,), 0xAB, dtype=torch.uint8, device="cuda"))
     for x, y in zip(a, b):
