@@ -266,8 +266,8 @@ void with_bits(int E, F f) {
 
 // ---- exchange ------------------------------------------------------------------------------------
 
-// Bound by memory.  65536 x 1024 bfloat16 rows, top 2: dispatch 64 us (6.3 TB/s), combine 90 us (4.5 TB/s);
-// 32768 tokens, top 4: combine's gradient 105 us (5.8 TB/s), dispatch's 76 us (4.4 TB/s).  A copy runs at 5.1.
+// Bound by memory (a copy runs at 5.1 TB/s).  65536 x 1024 bfloat16 rows, top 2: dispatch and combine together
+// 154 us (5.2 TB/s); 32768 tokens, top 4: both gradients 184 us (5.1 TB/s).
 
 constexpr int kExThreads = 256;
 constexpr int64_t kExMaxBlocks = 1 << 20;

@@ -8,7 +8,7 @@
 // The inner sums run on the matrix cores (v_mfma_f32_16x16x32, 16 outputs x 16 rows x 32 k) with q as bf16
 // or f16, which hold 0 .. 15 exactly, and float32 accumulation: no weight is rounded, and s and z are
 // applied to float32 group sums.  sum x comes from the same instruction with a matrix of ones, in the
-// lanes that need it.
+// lanes that need it; where every zero point is 8, a matrix of -8 gives what the products then start from.
 // q reaches bf16/f16 two at a time: the byte 0000qqqq read as an 8-bit float with 3 mantissa bits is
 // q * 2^-9 (its subnormals and its first binade share one spacing), and v_cvt_scalef32_pk_* turns two such
 // bytes into two exact numbers with the scale 2^9.
@@ -30,7 +30,6 @@ typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kTileN = 16;        // outputs of a tile
 constexpr int kBlockK = 128;      // k of a block: 4 instructions, 16 bytes of q per lane
-constexpr int kMaxWaves = 8;
 constexpr int kGroupsAt = 1024;   // of a record: its groups, after q
 constexpr int kMaxIn = 1 << 20, kMaxOut = 1 << 19;
 
@@ -217,15 +216,16 @@ __device__ __forceinline__ void store_four(O *p, f32x4 v, int left, int wide) {
 // A workgroup of WK x WN waves computes 16 NT WN outputs of a block of 16 MT rows (at most).  k goes by in
 // chunks of WK U blocks: wave (ik, in) multiplies blocks ik U .. ik U + U - 1 of a chunk for its NT output
 // tiles, with the weights in registers, straight from memory, and the rows in LDS, where every wave needs
-// them: 0 past K, and float32 rows as their three parts, split once.  While a chunk is multiplied the next
-// one's rows and weights are on their way (rows first: waiting for them leaves the weights in flight).  At
-// the end the WK waves' sums meet in LDS, added in the waves' order.
+// them: 0 past K, and float32 rows as their three parts, split once.  Rows are requested before weights:
+// waiting for them leaves the weights in flight.  With PF there are two buffers, and the next chunk's loads
+// are on their way while one is multiplied; without, other workgroups' loads are.  At the end the WK waves'
+// sums meet in LDS, added in the waves' order.  OCC: waves per SIMD to leave registers for.
 template <class T, int WK, int U>
 struct Stage {
   static constexpr int kChunk = WK * U * kBlockK;      // k of a chunk
   static constexpr int kRow = kChunk * 2 + 16;         // bytes of a row of one part: lanes of one h in 64 banks
   static constexpr int kParts = Mma<T>::parts;
-  static size_t bytes(int rows, bool two) { return (size_t)(two ? 2 : 1) * kParts * rows * kRow; }
+  static constexpr size_t bytes(int rows, bool two) { return (size_t)(two ? 2 : 1) * kParts * rows * kRow; }
 };
 
 template <class T, class S, int G, bool Z, int MT, int NT, int U, int WK, int WN, bool PF, int OCC>
@@ -476,6 +476,7 @@ __global__ __launch_bounds__(64 * WK * WN, OCC) void k_linear(LinearArgs a) {
 
 template <class T, class S, int G, bool Z, int MT, int NT, int U, int WK, int WN, bool PF, int OCC>
 void launch_linear(LinearArgs a, hipStream_t stream) {
+  static_assert(Stage<T, WK, U>::bytes(16 * MT, PF) <= 160 * 1024, "the rows of a chunk fit a compute unit's LDS");
   const int64_t blocks = (a.n_rows + 16 * MT - 1) / (16 * MT);
   a.direct = a.offsets && blocks <= 4;
   a.n_units = !a.offsets ? blocks : a.direct ? a.n_matrices : blocks + a.n_matrices;
@@ -514,7 +515,7 @@ void with_flag(int32_t on, F f) {
 // Rows by expert: a cut of 32 rows is mostly empty below 8 rows per expert on average (64 rows, 64 experts of
 // 2048 x 1024: 16 x 32 cut 11.0, 32 x 128 13.0; 1024 rows: 32 x 128 26.2, 16 x 32 more than 32), and one of 64
 // rows loses to 32 by the experts' uneven numbers of rows (4096 rows, 8 experts: 32.5 against 25.6).
-// The last constant is waves per SIMD to leave registers for; more than a kind's registers allow spill.  Two-byte
+// OCC: more waves than a kind's registers allow spill.  Two-byte
 // rows: 4096 rows by 8 experts, 32 x 128 cut: 3 waves 13.7, 2 waves 16.7; 64 rows by 64 experts, 16 x 32 cut: 4
 // waves 11.5, 2 waves 12.7; but groups of 32, 64 rows, 4096 x 1024: 4 waves 7.4, 2 waves 5.9.  float32 rows
 // need two: 32 x 128 cut 20.8, with three 28.3.  The second chunk's buffers of the 64 x 256 cut fit groups of 128
@@ -540,8 +541,8 @@ void linear_cut(LinearArgs a, hipStream_t stream) {
     launch_linear<T, S, G, Z, 2, 2, 1, 2, 2, false, 2>(a, stream);
   } else if (rows <= 16 && groups(16, 2) >= 512 && a.s.blocks >= 8) {
     launch_linear<T, S, G, Z, 1, 2, 2, 4, 1, false, 2>(a, stream);
-  } else if (rows <= 16 && groups(16, 2) >= 256 && a.s.blocks >= 16) {
-    launch_linear<T, S, G, Z, 1, 2, 2, 8, 1, false, 2>(a, stream);
+  } else if (kShort && rows <= 16 && groups(16, 2) >= 256 && a.s.blocks >= 16) {   // float32: not in LDS
+    if constexpr (kShort) launch_linear<T, S, G, Z, 1, 2, 2, 8, 1, false, 2>(a, stream);
   } else if (groups(16, 2) >= 512 || a.s.blocks < 8) {
     launch_linear<T, S, G, Z, 1, 1, 2, 2, 2, false, kWaves16>(a, stream);
   } else {

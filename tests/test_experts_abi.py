@@ -206,3 +206,38 @@ def test_binding_refusals():
     ]:
         with pytest.raises(ValueError, match=text):
             call()
+
+
+def test_calls_run_on_the_tensors_device(monkeypatch):
+    """Tensors of another device than the current one: the call makes that device current and takes its stream;
+    a stream of another device is refused.  (Without devices: torch's functions are stood in for.)"""
+    import torch
+    entered = []
+
+    class Guard:
+        def __init__(self, what):
+            self.what = what
+
+        def __enter__(self):
+            entered.append(self.what)
+
+        def __exit__(self, *exc):
+            entered.append(("left", self.what))
+
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 1), 77
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: Guard(("device", d.index)))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: Guard(("stream", s.cuda_stream)))
+    monkeypatch.setattr(svt, "_raw_stream", lambda index: 1000 + index)
+    with svt._Run(torch.device("cuda", 1), None) as handle:
+        assert handle == 1001 and entered == [("device", 1)]
+    assert entered == [("device", 1), ("left", ("device", 1))]
+    del entered[:]
+    with svt._Run(torch.device("cuda", 0), None) as handle:
+        assert handle == 1000 and entered == []
+    with svt._Run(torch.device("cuda", 1), Stream) as handle:
+        assert handle == 77 and entered == [("stream", 77)]
+    with pytest.raises(ValueError, match="stream"):
+        svt._Run(torch.device("cuda", 0), Stream)

@@ -76,7 +76,8 @@ def near(got, want, tol, what):
 # ---- router ------------------------------------------------------------------------------------------
 
 ROUTES = [(1, 1, 1), (1, 8, 2), (3, 7, 7), (65, 9, 4), (64, 16, 16), (33, 31, 5), (130, 64, 8), (17, 100, 3),
-          (9, 128, 8), (40, 255, 16), (12, 256, 1), (5, 511, 16), (6, 512, 16)]
+          (9, 128, 8), (40, 255, 16), (12, 256, 1), (5, 511, 16), (6, 512, 16),
+          (7, 512, 8), (3, 257, 7), (21, 250, 8), (5, 12, 12), (9, 30, 10), (33, 60, 9), (4, 120, 13), (600, 16, 8)]
 
 
 @pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
@@ -290,7 +291,7 @@ def test_linear(svt, R, N, K, G, scale_kind, zeros, kind):
 
 
 # sizes that reach every way the product is cut, each ending inside rows, outputs, blocks and groups
-CUTS = [(1030, 4100, 260, 128), (520, 4000, 150, 64), (300, 3300, 137, 32), (13, 16400, 1100, 128), (5, 8200, 2050, 64),
+CUTS = [(1030, 4100, 260, 128), (520, 4000, 150, 64), (300, 3300, 137, 32), (13, 16400, 1100, 128), (5, 8200, 2050, 64), (16, 8200, 2050, 32), (16, 16400, 1100, 128), (16, 300, 4099, 64),
         (100, 2400, 259, 64), (9, 700, 1500, 128), (40, 600, 385, 32)]
 
 
