@@ -514,7 +514,9 @@ void with_flag(int32_t on, F f) {
 // 4096: 10.7, as 16 x 16 cut 13.1; 8192 x 8192: 10.6 against 12.3.
 // Rows by expert: a cut of 32 rows is mostly empty below 8 rows per expert on average (64 rows, 64 experts of
 // 2048 x 1024: 16 x 32 cut 11.0, 32 x 128 13.0; 1024 rows: 32 x 128 26.2, 16 x 32 more than 32), and one of 64
-// rows loses to 32 by the experts' uneven numbers of rows (4096 rows, 8 experts: 32.5 against 25.6).
+// rows loses to 32 by the experts' uneven numbers of rows (4096 rows, 8 experts: 32.5 against 25.6).  Below 8
+// rows per expert, 16 x 64 wins over 16 x 32 where that still gives every compute unit a workgroup (64 rows,
+// 64 experts of 2048 x 1024: 10.1 against 10.8; 8 experts of 2048 x 512: 6.9 against 6.4).
 // OCC: more waves than a kind's registers allow spill.  Two-byte
 // rows: 4096 rows by 8 experts, 32 x 128 cut: 3 waves 13.7, 2 waves 16.7; 64 rows by 64 experts, 16 x 32 cut: 4
 // waves 11.5, 2 waves 12.7; but groups of 32, 64 rows, 4096 x 1024: 4 waves 7.4, 2 waves 5.9.  float32 rows
@@ -531,6 +533,8 @@ void linear_cut(LinearArgs a, hipStream_t stream) {
     const int64_t some = std::min<int64_t>(a.n_matrices, rows) / 2;   // half-filled blocks, about
     if (rows >= 8 * (int64_t)a.n_matrices && (rows / 32 + some) * ((tiles + 7) / 8) >= 256)
       launch_linear<T, S, G, Z, 2, 2, 1, 1, 4, false, kWaves32>(a, stream);
+    else if ((rows / 16 + some) * ((tiles + 3) / 4) >= 288)
+      launch_linear<T, S, G, Z, 1, 2, 2, 2, 2, false, kWaves32>(a, stream);
     else
       launch_linear<T, S, G, Z, 1, 1, 2, 2, 2, false, kWaves16>(a, stream);
   } else if ((kShort || G < 128) && groups(64, 16) >= 256) {   // float32, groups of 128: 32 x 128 is quicker

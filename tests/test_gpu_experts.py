@@ -325,7 +325,8 @@ def test_linear_weights_are_exact(svt, kind, G):
 EXPERTS = [  # rows per matrix, outputs, inputs, group
     ([1], 16, 64, 32), ([0, 3, 0, 1], 40, 130, 64), ([0, 0, 0], 16, 32, 32), ([17, 0, 40, 1, 16], 33, 256, 128),
     ([1] * 70, 16, 96, 32), ([0] * 63 + [5] + [0] * 100 + [2], 32, 64, 64), ([200, 7, 64], 100, 160, 32),
-    ([130, 0, 65, 300], 200, 257, 64), ([40, 3], 50, 300, 128), ([0, 33], 16, 7, 32)]
+    ([130, 0, 65, 300], 200, 257, 64), ([40, 3], 50, 300, 128), ([0, 33], 16, 7, 32),
+    ([1, 0, 2, 17] * 16, 2050, 300, 64), ([3] * 30 + [0, 50], 1500, 1030, 128), ([90, 33, 0, 250], 1030, 260, 128)]
 
 
 @pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
