@@ -104,6 +104,24 @@ def test_route_and_backward(svt, T, E, K, renorm, kind):
     near(host(d), rd, U * mag * (bsens + 31 + 20) + HALF[kind] * np.abs(rd) + TINY[kind] + 2.0 ** -126, "d_logits")
 
 
+def test_route_more_tokens_than_one_grid(svt):
+    """270,000 tokens of 512 experts: workgroups go round more than once; tokens of every part are compared."""
+    import torch
+    T, E, K = 270000, 512, 8
+    g = torch.Generator(device="cuda").manual_seed(5)
+    l = torch.randn((T, E), generator=g, device="cuda").bfloat16()
+    ids, w = svt.svt_route(l, K)
+    dw = torch.randn((T, K), generator=g, device="cuda")
+    d = svt.svt_route_backward(l, ids, w, dw)
+    pick = [0, 1, 3, 4, 131071, 262139, 262143, 262144, 262145, 269998, 269999]
+    rl = host(l[pick])
+    rid, rw, sens = X.route(rl, K, True)
+    assert np.array_equal(host(ids[pick]), rid)
+    near(host(w[pick]), rw, U * rw * (sens + 31) + 2.0 ** -126, "weights")
+    rd, mag, bs = X.route_backward(rl, rid, host(w[pick]), host(dw[pick]), True)
+    near(host(d[pick]), rd, U * mag * (bs + 51) + HALF["bf16"] * np.abs(rd) + TINY["bf16"], "d_logits")
+
+
 def test_route_infinite_logits(svt):
     l = np.array([[np.inf, 0.0, np.inf, -1.0], [3e38, -3e38, np.inf, 1.0]], np.float32)
     ids, w = svt.svt_route(dev(l), 3)
@@ -414,6 +432,24 @@ def test_refusals_leave_outputs(svt):
     assert bool((out == 7.0).all()) and bool((rows == 1.0).all())
 
 
+def test_linear_more_units_than_one_grid(svt):
+    """1,100,000 rows by 3 experts: more blocks of rows than one grid dimension takes; rows around its end and
+    the experts' are compared."""
+    import torch
+    R, N, K = 1100000, 16, 32
+    rng = np.random.default_rng(2)
+    packed, q, s, z = make_weights(svt, rng, 3, N, K, 32, "f16", True)
+    x = torch.randn(R, K, device="cuda").half()
+    off = np.array([0, 5, 1048570, R], np.int32)
+    y = svt.svt_quant_linear(x, packed, offsets=dev(off))
+    pick = np.array([0, 4, 5, 6, 1000, 524287, 524288, 1048560, 1048569, 1048570, 1048580, 1048608, R - 1])
+    hx, hy = host(x[pick]), host(y[pick])
+    for i, r in enumerate(pick):
+        e = int(np.searchsorted(off, r, side="right")) - 1
+        ry, mag = X.linear(hx[i:i + 1], q[e:e + 1], s[e:e + 1], z[e:e + 1], 32, None, None, False, np.zeros((1, N)))
+        near(hy[i:i + 1], ry, 4 * np.sqrt(45) * U * mag + HALF["f16"] * np.abs(ry) + TINY["f16"], f"row {r}")
+
+
 def test_linear_offsets_are_clamped(svt):
     """Ends past the rows are cut, ends that do not ascend give no rows; nothing else is touched."""
     rng = np.random.default_rng(8)
@@ -580,6 +616,45 @@ def test_captured_layer_replays(svt):
         torch.cuda.synchronize()
         for (g, x, l, y), want in zip(graphs, wants):
             assert torch.equal(y, want), f"replay {step}"
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_captured_gradients_and_products_replay(svt, kind):
+    """Every gradient call and a large product captured into one graph: each replay, on inputs changed in place
+    and with the same calls run eagerly between, gives the eager bits."""
+    import torch
+    T, E, K, D, N = 1100, 20, 3, 200, 2100
+    rng = np.random.default_rng(13)
+    packed, *_ = make_weights(svt, rng, 1, N, D, 32, "f32", True)
+    logits, dy = torch.zeros(T, E, device="cuda", dtype=ty(kind)), torch.zeros(T, D, device="cuda", dtype=ty(kind))
+    rows = torch.zeros(T * K, D, device="cuda", dtype=ty(kind))
+
+    def step():
+        ids, w = svt.svt_route(logits, K, renormalise=False)
+        off, order, pos = svt.svt_expert_sort(ids, E)
+        dr, dw = svt.svt_expert_combine_backward(dy, rows, pos, w)
+        dx = svt.svt_expert_dispatch_backward(dr, pos)
+        dl = svt.svt_route_backward(logits, ids, w, dw, renormalise=False)
+        return ids, w, off, order, pos, dr, dw, dx, dl, svt.svt_quant_linear(dy, packed)
+
+    def change():
+        for t in (logits, dy, rows):
+            t.copy_(torch.randn(t.shape, device="cuda"))
+
+    change()
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for i in range(4):
+        change()
+        want = step()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), f"replay {i}"
 
 
 def test_layer_on_another_stream(svt):
