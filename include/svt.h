@@ -356,7 +356,8 @@ int svt_route(int32_t n_tokens, int32_t n_experts, int32_t top, int32_t dtype, c
  *   d_weights            [n_tokens][top] float: the loss's gradient in the weights
  *   d_logits             [n_tokens][n_experts] of dtype: the gradient in the logits, 0 for shut experts and,
  *                        renormalised, for those not chosen
- * The choice itself has no gradient.  Errors as svt_route.
+ * The choice itself has no gradient.  A token whose d_weights at a named expert hold an infinity or NaN may get
+ * NaN at every expert.  Errors as svt_route.
  */
 int svt_route_backward(int32_t n_tokens, int32_t n_experts, int32_t top, int32_t dtype, const void *logits,
                        int32_t renormalise, const int32_t *experts, const float *weights, const float *d_weights,

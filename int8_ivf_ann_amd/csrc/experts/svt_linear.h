@@ -9,6 +9,7 @@
 // or f16, which hold 0 .. 15 exactly, and float32 accumulation: no weight is rounded, and s and z are
 // applied to float32 group sums.  sum x comes from the same instruction with a matrix of ones, in the
 // lanes that need it; where every zero point is 8, a matrix of -8 gives what the products then start from.
+// (Of float32 rows, products of many rows add x up in float32 while they store the rows.)
 // q reaches bf16/f16 two at a time: the byte 0000qqqq read as an 8-bit float with 3 mantissa bits is
 // q * 2^-9 (its subnormals and its first binade share one spacing), and v_cvt_scalef32_pk_* turns two such
 // bytes into two exact numbers with the scale 2^9.
@@ -217,24 +218,40 @@ __device__ __forceinline__ void store_four(O *p, f32x4 v, int left, int wide) {
 // chunks of WK U blocks: wave (ik, in) multiplies blocks ik U .. ik U + U - 1 of a chunk for its NT output
 // tiles, with the weights in registers, straight from memory, and the rows in LDS, where every wave needs
 // them: 0 past K, and float32 rows as their three parts, split once.  Rows are requested before weights:
-// waiting for them leaves the weights in flight.  With PF there are two buffers, and the next chunk's loads
-// are on their way while one is multiplied; without, other workgroups' loads are.  At the end the WK waves'
+// waiting for them leaves the weights in flight; other workgroups multiply meanwhile.  At the end the WK waves'
 // sums meet in LDS, added in the waves' order.  OCC: waves per SIMD to leave registers for.
 template <class T, int WK, int U>
 struct Stage {
   static constexpr int kChunk = WK * U * kBlockK;      // k of a chunk
   static constexpr int kRow = kChunk * 2 + 16;         // bytes of a row of one part: lanes of one h in 64 banks
   static constexpr int kParts = Mma<T>::parts;
-  static constexpr size_t bytes(int rows, bool two) { return (size_t)(two ? 2 : 1) * kParts * rows * kRow; }
+  static constexpr size_t bytes(int rows) { return (size_t)kParts * rows * kRow; }
+  // Whether sum x over a group is made once, where the rows are stored, for all waves (else: each wave's own
+  // instructions with a matrix of ones).  For float32 rows those would be three per product of a part: 1024
+  // rows by 32 experts of 2048 x 1024 35 us, else 41.  For two-byte rows they hide better than the sums'
+  // additions: 512 rows, 4096 x 1024: 11.7 us, with sums stored 13.6.
+  template <int MT>
+  static constexpr bool sums = sizeof(T) == 4 && MT >= 2 && WK == 1;
 };
 
-template <class T, class S, int G, bool Z, int MT, int NT, int U, int WK, int WN, bool PF, int OCC>
+// the row values' sum
+template <class T>
+__device__ __forceinline__ float sum_eight(const Eight<T> &r) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = (float)r.v[i];
+  return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+}
+
+template <class T, class S, int G, bool Z, int MT, int NT, int U, int WK, int WN, int OCC>
 __global__ __launch_bounds__(64 * WK * WN, OCC) void k_linear(LinearArgs a) {
   using M = Mma<T>;
   using St = Stage<T, WK, U>;
   constexpr int P = M::parts, NG = kBlockK / G, kSteps = G / 32, MN = MT * NT, kThreads = 64 * WK * WN;
   constexpr int kPieces = St::kChunk / 8;                            // 8 values each, of a row of a chunk
   constexpr int kEach = (16 * MT * kPieces + kThreads - 1) / kThreads;   // pieces of a thread at most
+  constexpr bool kSums = St::template sums<MT>;
+  constexpr int kGroups = St::kChunk / G;                            // of a row of a chunk
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int64_t unit = (int64_t)blockIdx.z * gridDim.y + blockIdx.y;
   int matrix = 0;
@@ -291,22 +308,28 @@ __global__ __launch_bounds__(64 * WK * WN, OCC) void k_linear(LinearArgs a) {
         x[e] = *reinterpret_cast<const Eight<T> *>(rows + (int64_t)(r < n_rows ? r : 0) * K + (k + 8 <= K ? k : K - 8));
       }
     };
-    auto put_piece = [&](uint8_t *buf, int p, int r, const Eight<T> &e) {
+    auto put_piece = [&](int p, int r, const Eight<T> &e) {
       typename M::frag f[P];
       row_parts<T>(e, f);
 #pragma unroll
       for (int q = 0; q < P; ++q)
-        *reinterpret_cast<typename M::frag *>(buf + (q * a.lds_rows + r) * St::kRow + 16 * (p % kPieces)) = f[q];
+        *reinterpret_cast<typename M::frag *>(lds + (q * a.lds_rows + r) * St::kRow + 16 * (p % kPieces)) = f[q];
     };
+    float *xsum = reinterpret_cast<float *>(lds + P * a.lds_rows * St::kRow);   // behind the rows
     auto store_rows = [&](const Eight<T> (&x)[kEach], int chunk) {
-      uint8_t *buf = lds + (size_t)(PF ? chunk & 1 : 0) * (P * a.lds_rows * St::kRow);
 #pragma unroll
       for (int e = 0; e < kEach; ++e) {
         if (e * kThreads >= n_rows * kPieces) break;
         const int p = e * kThreads + tid, r = p / kPieces, k = chunk * St::kChunk + 8 * (p % kPieces);
-        if (r < n_rows && (k + 8 <= K || k >= K)) put_piece(buf, p, r, k < K ? x[e] : Eight<T>{});
+        if (r < n_rows && (k + 8 <= K || k >= K)) put_piece(p, r, k < K ? x[e] : Eight<T>{});
+        if constexpr (kSums) {
+          static_assert(kPieces % (G / 8) == 0 && kThreads % kPieces == 0, "a group's pieces lie in neighbouring lanes");
+          const float sum = group_add(r < n_rows && k + 8 <= K ? sum_eight(x[e]) : 0.f, G / 8);
+          if (r < n_rows && p % (G / 8) == 0) xsum[p / (G / 8)] = Z ? sum : -8.f * sum;   // p / (G / 8) = r kGroups + ..
+        }
       }
       if ((chunk + 1) * St::kChunk > K && K % 8) {   // the piece that K ends inside: a thread per row
+        if constexpr (kSums) __syncthreads();
         for (int r = tid; r < n_rows; r += kThreads) {
           const int k = K / 8 * 8;
           Eight<T> e{};
@@ -315,7 +338,9 @@ __global__ __launch_bounds__(64 * WK * WN, OCC) void k_linear(LinearArgs a) {
             const T v = rows[(int64_t)r * K + (k + i < K ? k + i : k)];
             e.v[i] = k + i < K ? v : T(0.f);
           }
-          put_piece(buf, (k - chunk * St::kChunk) / 8, r, e);
+          const int p = (k - chunk * St::kChunk) / 8;
+          put_piece(p, r, e);
+          if constexpr (kSums) xsum[r * kGroups + p / (G / 8)] += (Z ? 1.f : -8.f) * sum_eight(e);
         }
       }
     };
@@ -324,18 +349,18 @@ __global__ __launch_bounds__(64 * WK * WN, OCC) void k_linear(LinearArgs a) {
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int n = 0; n < NT; ++n) acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-    int row_at[MT];   // lanes past the last row compute a copy of it, never stored
+    int row_at[MT], sum_at[MT];   // lanes past the last row compute a copy of it, never stored
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const int r = 16 * m + j;
       row_at[m] = (r < n_rows ? r : n_rows - 1) * St::kRow + ik * (U * kBlockK * 2) + 16 * h;
+      sum_at[m] = (r < n_rows ? r : n_rows - 1) * kGroups;
     }
-    auto multiply = [&](const Weights &k, int chunk) {
-      const uint8_t *buf = lds + (size_t)(PF ? chunk & 1 : 0) * (P * a.lds_rows * St::kRow);
+    auto multiply = [&](const Weights &k) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         auto row_frag = [&](int p, int m, int st) {
-          return *reinterpret_cast<const typename M::frag *>(buf + p * a.lds_rows * St::kRow + row_at[m] +
+          return *reinterpret_cast<const typename M::frag *>(lds + p * a.lds_rows * St::kRow + row_at[m] +
                                                              (u * kBlockK + 32 * st) * 2);
         };
 #pragma unroll
@@ -343,13 +368,18 @@ __global__ __launch_bounds__(64 * WK * WN, OCC) void k_linear(LinearArgs a) {
           // xs = sum x over the group (or, without zero points, -8 sum x, which the products start from)
           f32x4 part[MT][NT], xs[MT];
 #pragma unroll
-          for (int m = 0; m < MT; ++m) xs[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+          for (int m = 0; m < MT; ++m) {
+            const float v = kSums ? xsum[sum_at[m] + (ik * U + u) * NG + g] : 0.f;
+            xs[m] = f32x4{v, v, v, v};
+          }
+          if constexpr (!kSums) {
 #pragma unroll
-          for (int st = g * kSteps; st < (g + 1) * kSteps; ++st)
+            for (int st = g * kSteps; st < (g + 1) * kSteps; ++st)
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+              for (int m = 0; m < MT; ++m)
 #pragma unroll
-              for (int p = 0; p < P; ++p) xs[m] = M::mul(fixed, row_frag(p, m, st), xs[m]);
+                for (int p = 0; p < P; ++p) xs[m] = M::mul(fixed, row_frag(p, m, st), xs[m]);
+          }
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -402,37 +432,15 @@ __global__ __launch_bounds__(64 * WK * WN, OCC) void k_linear(LinearArgs a) {
         }
     }
     Eight<T> x[kEach];
-    auto request = [&](int chunk) { load_rows(x, chunk); };
-    auto settle = [&](int chunk) {
-      store_rows(x, chunk);
-      __syncthreads();
-    };
-    if constexpr (PF) {
+#pragma unroll 1
+    for (int c = 0; c < n_chunks; ++c) {
       Weights now;
-      request(0);
-      load_weights(now, 0);
-      settle(0);
-#pragma unroll 1
-      for (int c = 0; c + 1 < n_chunks; ++c) {
-        Weights next;
-        request(c + 1);
-        load_weights(next, c + 1);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(now, c);
-        settle(c + 1);   // the other buffer: its readers passed the last barrier
-        now = next;
-      }
-      multiply(now, n_chunks - 1);
-    } else {
-#pragma unroll 1
-      for (int c = 0; c < n_chunks; ++c) {
-        Weights now;
-        request(c);
-        load_weights(now, c);
-        if (c > 0) __syncthreads();   // the chunk before has been read
-        settle(c);
-        multiply(now, c);
-      }
+      load_rows(x, c);
+      load_weights(now, c);
+      if (c > 0) __syncthreads();   // the chunk before has been read
+      store_rows(x, c);
+      __syncthreads();
+      multiply(now);
     }
     f32x4 *sums = reinterpret_cast<f32x4 *>(lds);   // [in][ik - 1][MT * NT][64]
     if constexpr (WK > 1) {
@@ -474,17 +482,19 @@ __global__ __launch_bounds__(64 * WK * WN, OCC) void k_linear(LinearArgs a) {
   }
 }
 
-template <class T, class S, int G, bool Z, int MT, int NT, int U, int WK, int WN, bool PF, int OCC>
+template <class T, class S, int G, bool Z, int MT, int NT, int U, int WK, int WN, int OCC>
 void launch_linear(LinearArgs a, hipStream_t stream) {
-  static_assert(Stage<T, WK, U>::bytes(16 * MT, PF) <= 160 * 1024, "the rows of a chunk fit a compute unit's LDS");
+  using St = Stage<T, WK, U>;
+  constexpr size_t kSumBytes = St::template sums<MT> ? (size_t)16 * MT * (St::kChunk / G) * 4 : 0;
+  static_assert(St::bytes(16 * MT) + kSumBytes <= 160 * 1024, "the rows of a chunk fit a compute unit's LDS");
   const int64_t blocks = (a.n_rows + 16 * MT - 1) / (16 * MT);
   a.direct = a.offsets && blocks <= 4;
   a.n_units = !a.offsets ? blocks : a.direct ? a.n_matrices : blocks + a.n_matrices;
   a.lds_rows = (int32_t)std::min<int64_t>(a.n_rows, 16 * MT);
   const int64_t y = a.n_units < 32768 ? a.n_units : 32768, z = (a.n_units + y - 1) / y;
   const dim3 grid((unsigned)((a.s.tiles + NT * WN - 1) / (NT * WN)), (unsigned)y, (unsigned)z);
-  const size_t lds = std::max(Stage<T, WK, U>::bytes(a.lds_rows, PF), (size_t)WN * (WK - 1) * MT * NT * 1024);
-  k_linear<T, S, G, Z, MT, NT, U, WK, WN, PF, OCC><<<grid, 64 * WK * WN, lds, stream>>>(a);
+  const size_t lds = std::max(St::bytes(a.lds_rows) + kSumBytes, (size_t)WN * (WK - 1) * MT * NT * 1024);
+  k_linear<T, S, G, Z, MT, NT, U, WK, WN, OCC><<<grid, 64 * WK * WN, lds, stream>>>(a);
 }
 
 template <class F>
@@ -505,52 +515,80 @@ void with_flag(int32_t on, F f) {
 // workgroups that each cut gives.  The largest cut that still gives 512 (two per compute unit, so that one
 // loads while the other multiplies; the 8 waves of the 64 x 256 cut do with 256) is taken.  bfloat16, groups
 // of 128, us, the chosen cut against its neighbour:
-//   1024 rows, 4096 x 1024:  64 x 256 cut 18.6,  32 x 128 22.0
+//   4096 rows, 4096 x 4096:  32 x 256 cut 213,  64 x 256  266,  32 x 128 241
+//   1024 rows, 4096 x 1024:  32 x 256 cut 18.8, 64 x 256 21.0,  32 x 128 22.8
+//    512 rows, 4096 x 1024:  32 x 128 cut 11.8, 32 x 256 13.8
 //   1024 rows, 1024 x 1024:  32 x  64 cut  9.4,  32 x 128 11.2
 //    256 rows, 1024 x 1024:  16 x  32 cut  5.7,  16 x  16  6.0
 //     16 rows, 4096 x 1024:  16 x  16 cut  4.3,  16 x  32  5.1
+// The 32 x 256 cut keeps four tiles' scales and weights: with groups of 64 it loses to 64 x 256 (1024 rows, 4096 x
+// 1024: 23.6 against 22.4; float32 rows, whose sums of x are stored, win: 41.5 against 43.5), with groups of 32
+// for every type (float32 55.5 against 44.6).
 // Up to 16 rows of a large matrix (a decoding step) are bound by the weights' bytes and want about 8 waves on
-// every compute unit, each with two tiles and two blocks in flight: four or eight along k.  1 row, 16384 x
-// 4096: 10.7, as 16 x 16 cut 13.1; 8192 x 8192: 10.6 against 12.3.
+// every compute unit, each with two tiles in flight, of two blocks where they stay in registers: four or eight along
+// k.  1 row, 16384 x 4096: 10.9, as 16 x 16 cut 13.1; float32 rows 14.6, with two blocks more than 16.
+// 17 to 64 rows: 16 x 64 while that gives 512 (64 rows, 8192 x 2048: 9.8, 16 x 32 10.7; float32 rows 16.7, 16 x 32
+// more than 22).  Fewer: 8 waves along k for as many workgroups as compute units, 16 x 32 (64 rows, 2048 x 4096:
+// 8.9, 16 x 16 9.7) or, up to 128 of those, 16 x 16; each wave with two blocks of a long k (1 row, 4096 x 4096:
+// 5.3, one block 5.6; 8 rows, 2048 x 8192: 8.7 against 10.1).
 // Rows by expert: a cut of 32 rows is mostly empty below 8 rows per expert on average (64 rows, 64 experts of
 // 2048 x 1024: 16 x 32 cut 11.0, 32 x 128 13.0; 1024 rows: 32 x 128 26.2, 16 x 32 more than 32), and one of 64
-// rows loses to 32 by the experts' uneven numbers of rows (4096 rows, 8 experts: 32.5 against 25.6).  Below 8
+// rows loses to 32 by the experts' uneven numbers of rows (4096 rows, 8 experts: 32.5 against 25.6).  32 x 256 wins
+// over 32 x 128 for two-byte rows, groups of 128, from 384 workgroups (8192 rows, 8 experts of 4096 x 4096: 445
+// against 474; 1024 rows, 32 experts of 2048 x 1024: 19.6 against 21.2; 8 experts, 288 workgroups: 17.8 against
+// 16.1; float32 rows, 4096 rows, 8 experts: 86 against 83).  Below 8
 // rows per expert, 16 x 64 wins over 16 x 32 where that still gives every compute unit a workgroup (64 rows,
-// 64 experts of 2048 x 1024: 10.1 against 10.8; 8 experts of 2048 x 512: 6.9 against 6.4).
+// 64 experts of 2048 x 1024: 10.1 against 10.8; 8 experts of 2048 x 512: 6.9 against 6.4).  With groups of 32 two
+// tiles of two blocks do not stay in registers (400 rows, 64 experts: one block 25.3, two 28.3).
 // OCC: more waves than a kind's registers allow spill.  Two-byte
 // rows: 4096 rows by 8 experts, 32 x 128 cut: 3 waves 13.7, 2 waves 16.7; 64 rows by 64 experts, 16 x 32 cut: 4
-// waves 11.5, 2 waves 12.7; but groups of 32, 64 rows, 4096 x 1024: 4 waves 7.4, 2 waves 5.9.  float32 rows
-// need two: 32 x 128 cut 20.8, with three 28.3.  The second chunk's buffers of the 64 x 256 cut fit groups of 128
-// without zero points (18.8 against 21.0); elsewhere they spill (groups of 32: 22.1, with them more than 27).
+// waves 11.5, 2 waves 12.7; but groups of 32, 64 rows, 4096 x 1024: 4 waves 7.4, 2 waves 5.9.  float32 rows, 32 x
+// 128 cut, 4096 rows by 8 experts of 2048 x 1024: groups of 64, 3 waves 86, 2 waves 109; groups of 128 84 and 83.
 template <class T, class S, int G, bool Z>
 void linear_cut(LinearArgs a, hipStream_t stream) {
   constexpr bool kShort = sizeof(T) == 2;
-  constexpr int kWaves32 = kShort ? 3 : 2, kWaves16 = kShort && G >= 64 ? 4 : 2;
-  constexpr bool kAhead = kShort && G == 128 && !Z;
-  const int64_t rows = a.n_rows, tiles = a.s.tiles;
+  constexpr int kWaves32 = kShort || G <= 64 ? 3 : 2, kWaves16 = kShort && G >= 64 ? 4 : 2;
+  constexpr bool kFew = kShort && G >= 64;                   // two tiles of two blocks stay in registers
+  constexpr bool kWide = G == 128 || (!kShort && G == 64);   // 32 x 256 rather than 64 x 256
+  const int64_t rows = a.n_rows, tiles = a.s.tiles, blocks = a.s.blocks;
   auto groups = [&](int64_t r, int64_t t) { return ((rows + r - 1) / r) * ((tiles + t - 1) / t); };
+  auto cut_16_64 = [&] { launch_linear<T, S, G, Z, 1, 2, kFew || G == 128 ? 2 : 1, 2, 2, kFew ? 3 : 2>(a, stream); };
+  auto cut_16_32 = [&] { launch_linear<T, S, G, Z, 1, 1, 2, 2, 2, kWaves16>(a, stream); };
   if (a.offsets) {
     const int64_t some = std::min<int64_t>(a.n_matrices, rows) / 2;   // half-filled blocks, about
-    if (rows >= 8 * (int64_t)a.n_matrices && (rows / 32 + some) * ((tiles + 7) / 8) >= 256)
-      launch_linear<T, S, G, Z, 2, 2, 1, 1, 4, false, kWaves32>(a, stream);
-    else if ((rows / 16 + some) * ((tiles + 3) / 4) >= 288)
-      launch_linear<T, S, G, Z, 1, 2, 2, 2, 2, false, kWaves32>(a, stream);
-    else
-      launch_linear<T, S, G, Z, 1, 1, 2, 2, 2, false, kWaves16>(a, stream);
-  } else if ((kShort || G < 128) && groups(64, 16) >= 256) {   // float32, groups of 128: 32 x 128 is quicker
-    launch_linear<T, S, G, Z, 4, 2, 1, 1, 8, kAhead, 2>(a, stream);
+    const bool full = rows >= 8 * (int64_t)a.n_matrices;
+    if (kShort && G == 128 && full && (rows / 32 + some) * ((tiles + 15) / 16) >= 384) {
+      if constexpr (kShort && G == 128) launch_linear<T, S, G, Z, 2, 4, 1, 1, 4, 2>(a, stream);
+    } else if (full && (rows / 32 + some) * ((tiles + 7) / 8) >= 256) {
+      launch_linear<T, S, G, Z, 2, 2, 1, 1, 4, kWaves32>(a, stream);
+    } else if ((rows / 16 + some) * ((tiles + 3) / 4) >= 288) {
+      cut_16_64();
+    } else {
+      cut_16_32();
+    }
+  } else if (kWide ? groups(32, 16) >= 512 : groups(64, 16) >= 256) {
+    if constexpr (kWide) launch_linear<T, S, G, Z, 2, 4, 1, 1, 4, 2>(a, stream);
+    else launch_linear<T, S, G, Z, 4, 2, 1, 1, 8, 2>(a, stream);
   } else if (groups(32, 8) >= 512) {
-    launch_linear<T, S, G, Z, 2, 2, 1, 1, 4, false, kWaves32>(a, stream);
+    launch_linear<T, S, G, Z, 2, 2, 1, 1, 4, kWaves32>(a, stream);
   } else if (groups(32, 4) >= 512) {
-    launch_linear<T, S, G, Z, 2, 2, 1, 2, 2, false, 2>(a, stream);
-  } else if (rows <= 16 && groups(16, 2) >= 512 && a.s.blocks >= 8) {
-    launch_linear<T, S, G, Z, 1, 2, 2, 4, 1, false, 2>(a, stream);
-  } else if (kShort && rows <= 16 && groups(16, 2) >= 256 && a.s.blocks >= 16) {   // float32: not in LDS
-    if constexpr (kShort) launch_linear<T, S, G, Z, 1, 2, 2, 8, 1, false, 2>(a, stream);
-  } else if (groups(16, 2) >= 512 || a.s.blocks < 8) {
-    launch_linear<T, S, G, Z, 1, 1, 2, 2, 2, false, kWaves16>(a, stream);
+    launch_linear<T, S, G, Z, 2, 2, 1, 2, 2, 2>(a, stream);
+  } else if (rows <= 16 && groups(16, 2) >= 512 && blocks >= 8) {
+    launch_linear<T, S, G, Z, 1, 2, kFew ? 2 : 1, 4, 1, 2>(a, stream);
+  } else if (groups(16, 4) >= 512) {
+    cut_16_64();
+  } else if (blocks < 8 || groups(16, 2) > (rows <= 16 ? 511 : 256)) {
+    cut_16_32();
+  } else if (groups(16, 2) > 128) {
+    if (kShort && blocks >= 16) {   // float32 rows of two blocks: not in LDS
+      if constexpr (kShort) launch_linear<T, S, G, Z, 1, 2, 2, 8, 1, 2>(a, stream);
+    } else {
+      launch_linear<T, S, G, Z, 1, 2, 1, 8, 1, 2>(a, stream);
+    }
+  } else if (kShort && blocks >= 16) {
+    if constexpr (kShort) launch_linear<T, S, G, Z, 1, 1, 2, 8, 1, 2>(a, stream);
   } else {
-    launch_linear<T, S, G, Z, 1, 1, 1, 8, 1, false, 2>(a, stream);
+    launch_linear<T, S, G, Z, 1, 1, 1, 8, 1, 2>(a, stream);
   }
 }
 

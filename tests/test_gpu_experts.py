@@ -327,6 +327,43 @@ def test_linear_every_cut(svt, R, N, K, G, kind):
     near(host(y), ry, 4 * np.sqrt(n) * U * mag + HALF[kind] * np.abs(ry) + TINY[kind], "cut")
 
 
+# sizes between the cuts' bounds: rows, outputs, inputs
+BETWEEN = [(1031, 4100, 261), (1030, 4100, 7), (600, 4100, 33), (40, 11000, 261), (40, 2100, 1030), (40, 2100, 2101),
+           (9, 700, 2101), (9, 5000, 1501), (3, 300, 1100)]
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("G", [32, 64, 128])
+@pytest.mark.parametrize("R, N, K", BETWEEN)
+def test_linear_between_cuts(svt, R, N, K, G, kind):
+    say("between", R, N, K, G, kind)
+    rng = np.random.default_rng(R + N + K + G)
+    packed, q, s, z = make_weights(svt, rng, 1, N, K, G, "f16" if kind == "f16" else "f32", (R + G // 32) % 2 == 0)
+    x = dev(rng.normal(size=(R, K)) + 0.5, ty(kind))
+    y = svt.svt_quant_linear(x, packed)
+    ry, mag = X.linear(host(x), q, s, z, G, None, None, False, np.zeros((R, N)))
+    n = (3 if kind == "f32" else 1) * G + -(-K // G) + 12
+    near(host(y), ry, 4 * np.sqrt(n) * U * mag + HALF[kind] * np.abs(ry) + TINY[kind], "between")
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("G", [32, 64, 128])
+@pytest.mark.parametrize("counts, N, K", [([200, 90, 33, 0, 250, 1, 140, 61], 4100, 261), ([90, 33, 0, 250], 4100, 130),
+                                          ([3] * 30 + [0, 50], 1500, 389), ([1, 0, 2, 5], 40, 1030)])
+def test_linear_by_expert_between_cuts(svt, counts, N, K, G, kind):
+    say("experts between", counts[:5], N, K, G, kind)
+    rng = np.random.default_rng(len(counts) + N + G)
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    R = int(off[-1]) + 2
+    packed, q, s, z = make_weights(svt, rng, len(counts), N, K, G, "f32", len(counts) % 8 == 0)
+    xd = dev(rng.normal(size=(R, K)), ty(kind))
+    y = svt.svt_quant_linear(xd, packed, offsets=dev(off), out=dev(np.full((R, N), 7.0), ty(kind)))
+    ry, mag = X.linear(host(xd), q, s, z, G, off, None, False, np.full((R, N), 7.0))
+    n = (3 if kind == "f32" else 1) * G + -(-K // G) + 12
+    near(host(y), ry, 4 * np.sqrt(n) * U * mag + HALF[kind] * np.abs(ry) + TINY[kind], "experts between")
+    assert np.all(host(y)[off[-1]:] == 7.0)
+
+
 @pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("G", [32, 64, 128])
 def test_linear_weights_are_exact(svt, kind, G):
