@@ -329,6 +329,8 @@ int svt_rerank(const svt_index *ix, int32_t n_queries, const int8_t *queries, co
  *     give the same bits.
  *   - Every call is asynchronous on hip_stream, allocates nothing and can be captured into a graph.
  *   - An output may not overlap an input or another output (SVT_EINVAL).
+ *   - A refused call enqueues nothing.  svt_expert_sort and svt_quant_pack may make several launches: the
+ *     first that fails ends the call (SVT_EDEVICE), and the outputs of the launches before it are undefined.
  */
 enum { SVT_F32 = 0, SVT_F16 = 1, SVT_BF16 = 2 };   /* element types */
 enum { SVT_ACT_NONE = 0, SVT_ACT_RELU = 1 };       /* activations of svt_quant_linear */
@@ -426,7 +428,7 @@ size_t svt_quant_pack_size(const svt_quant_weights *w);
  *            in the high half
  *   scales   [n_matrices][n_out][ceil(n_in / group)] of scale_type
  *   zeros    the same shape, one byte each; NULL exactly when has_zeros is 0
- * Errors: SVT_EINVAL, SVT_EUNSUPPORTED (group), SVT_EDEVICE; on error nothing is enqueued.
+ * Errors: SVT_EINVAL, SVT_EUNSUPPORTED (group), SVT_EDEVICE.
  */
 int svt_quant_pack(const svt_quant_weights *w, const uint8_t *nibbles, const void *scales, const uint8_t *zeros,
                    void *hip_stream);

@@ -256,12 +256,12 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_place(const int32_t *expe
   }
 }
 
-// calls f with enough bits for an expert's number as a constant
+// f of enough bits for an expert's number as a constant
 template <class F>
-void with_bits(int E, F f) {
-  if (E <= 8) f(std::integral_constant<int, 3>{});
-  else if (E <= 64) f(std::integral_constant<int, 6>{});
-  else f(std::integral_constant<int, 9>{});
+int with_bits(int E, F f) {
+  if (E <= 8) return f(std::integral_constant<int, 3>{});
+  if (E <= 64) return f(std::integral_constant<int, 6>{});
+  return f(std::integral_constant<int, 9>{});
 }
 
 // ---- exchange ------------------------------------------------------------------------------------
@@ -470,23 +470,22 @@ unsigned ex_grid(const ExArgs &a) {
   return (unsigned)(n < kExMaxBlocks ? n : kExMaxBlocks);
 }
 
-// calls f with the piece size as a constant
-template <class F>
-void with_piece(int v, F f) {
-  switch (v) {
-    case 16: f(std::integral_constant<int, 16>{}); break;
-    case 8: f(std::integral_constant<int, 8>{}); break;
-    case 4: f(std::integral_constant<int, 4>{}); break;
-    default: f(std::integral_constant<int, 2>{}); break;
-  }
+// f of the piece size as a constant; T's own size is the least
+template <class T, class F>
+int with_piece(int v, F f) {
+  if (v == 16) return f(std::integral_constant<int, 16>{});
+  if (v == 8) return f(std::integral_constant<int, 8>{});
+  if constexpr (sizeof(T) <= 2)
+    if (v == 2) return f(std::integral_constant<int, 2>{});
+  return f(std::integral_constant<int, 4>{});
 }
 
-// calls f with the number of rows in flight for `top` as a constant
+// f of the number of rows in flight for `top` as a constant
 template <class F>
-void with_batch(int top, F f) {
-  if (top == 1) f(std::integral_constant<int, 1>{});
-  else if (top == 2) f(std::integral_constant<int, 2>{});
-  else f(std::integral_constant<int, 4>{});
+int with_batch(int top, F f) {
+  if (top == 1) return f(std::integral_constant<int, 1>{});
+  if (top == 2) return f(std::integral_constant<int, 2>{});
+  return f(std::integral_constant<int, 4>{});
 }
 
 int combine(const char *who, int32_t n_tokens, int32_t top, int32_t width, int32_t dtype, const void *rows,
@@ -502,19 +501,17 @@ int combine(const char *who, int32_t n_tokens, int32_t top, int32_t width, int32
     return report(SVT_EINVAL, "%s: the output overlaps an input", who);
   const int v = piece(width, b, {rows, y});
   const ExArgs a = ex_args(n_tokens, top, width, b, v, position);
-  with_type(dtype, [&](auto ty) {
+  return with_type(dtype, [&](auto ty) {
     using T = decltype(ty);
-    with_piece(v, [&](auto pv) {
-      constexpr int V = decltype(pv)::value;
-      if constexpr (V >= (int)sizeof(T))
-        with_batch(top, [&](auto batch) {
-          using B = typename Bytes<V>::type;
-          k_combine<T, V, decltype(batch)::value><<<ex_grid(a), kExThreads, 0, (hipStream_t)hip_stream>>>(
-              a, (const B *)rows, weights, (B *)y);
-        });
+    return with_piece<T>(v, [&](auto pv) {
+      return with_batch(top, [&](auto batch) {
+        constexpr int V = decltype(pv)::value;
+        using B = typename Bytes<V>::type;
+        return launch(who, k_combine<T, V, decltype(batch)::value>, ex_grid(a), kExThreads, 0, hip_stream, a,
+                      (const B *)rows, weights, (B *)y);
+      });
     });
   });
-  return launched(who);
 }
 
 }  // namespace
@@ -563,23 +560,22 @@ extern "C" int svt_expert_sort(int32_t n_tokens, int32_t top, int32_t n_experts,
     for (int j = 0; j < i; ++j)
       if (overlap(at[i], bytes[i], at[j], bytes[j]))
         return report(SVT_EINVAL, "%s: input, outputs and workspace overlap", who);
-  hipStream_t s = (hipStream_t)hip_stream;
-  with_bits(n_experts, [&](auto bits) {
+  return with_bits(n_experts, [&](auto bits) {
     constexpr int B = decltype(bits)::value;
     auto one = [&](auto steps) {
-      k_sort_one<decltype(steps)::value, B><<<1, kSortThreads, 0, s>>>(experts, n, n_experts, offsets, order, position);
+      return launch(who, k_sort_one<decltype(steps)::value, B>, 1, kSortThreads, 0, hip_stream, experts, n, n_experts,
+                    offsets, order, position);
     };
-    if (n <= kSortThreads) one(std::integral_constant<int, 1>{});
-    else if (n <= 4 * kSortThreads) one(std::integral_constant<int, 4>{});
-    else if (n <= kOneEntries) one(std::integral_constant<int, 8>{});
-    else {
-      const SortShape sh = sort_shape(n, n_experts);
-      k_sort_count<<<sh.blocks, kSortThreads, 0, s>>>(experts, sh, n_experts, (int32_t *)workspace);
-      k_sort_place<B><<<sh.blocks, kSortThreads, 0, s>>>(experts, sh, n_experts, (const int32_t *)workspace, offsets,
-                                                         order, position);
-    }
+    if (n <= kSortThreads) return one(std::integral_constant<int, 1>{});
+    if (n <= 4 * kSortThreads) return one(std::integral_constant<int, 4>{});
+    if (n <= kOneEntries) return one(std::integral_constant<int, 8>{});
+    const SortShape sh = sort_shape(n, n_experts);
+    const int counted = launch(who, k_sort_count, sh.blocks, kSortThreads, 0, hip_stream, experts, sh, n_experts,
+                               (int32_t *)workspace);
+    if (counted != SVT_OK) return counted;   // the second kernel writes where the counts say
+    return launch(who, k_sort_place<B>, sh.blocks, kSortThreads, 0, hip_stream, experts, sh, n_experts,
+                  (const int32_t *)workspace, offsets, order, position);
   });
-  return launched(who);
 }
 
 extern "C" int svt_expert_dispatch(int32_t n_tokens, int32_t top, int32_t width, int32_t dtype, const void *x,
@@ -597,12 +593,11 @@ extern "C" int svt_expert_dispatch(int32_t n_tokens, int32_t top, int32_t width,
     return report(SVT_EINVAL, "%s: the output overlaps an input", who);
   const int v = piece(width, b, {x, rows});
   const ExArgs a = ex_args(n_tokens, top, width, b, v, position);
-  with_piece(v, [&](auto pv) {
+  return with_piece<uint16_t>(v, [&](auto pv) {
     constexpr int V = decltype(pv)::value;
     using B = typename Bytes<V>::type;
-    k_dispatch<V><<<ex_grid(a), kExThreads, 0, (hipStream_t)hip_stream>>>(a, (const B *)x, (B *)rows);
+    return launch(who, k_dispatch<V>, ex_grid(a), kExThreads, 0, hip_stream, a, (const B *)x, (B *)rows);
   });
-  return launched(who);
 }
 
 extern "C" int svt_expert_dispatch_backward(int32_t n_tokens, int32_t top, int32_t width, int32_t dtype,
@@ -639,17 +634,15 @@ extern "C" int svt_expert_combine_backward(int32_t n_tokens, int32_t top, int32_
   if (overlap(d_rows, nt * top, d_weights, nk)) return report(SVT_EINVAL, "%s: the outputs overlap", who);
   const int v = piece(width, b, {dy, rows, d_rows});
   const ExArgs a = ex_args(n_tokens, top, width, b, v, position);
-  with_type(dtype, [&](auto ty) {
+  return with_type(dtype, [&](auto ty) {
     using T = decltype(ty);
-    with_piece(v, [&](auto pv) {
-      constexpr int V = decltype(pv)::value;
-      if constexpr (V >= (int)sizeof(T))
-        with_batch(top, [&](auto batch) {
-          using B = typename Bytes<V>::type;
-          k_combine_backward<T, V, decltype(batch)::value><<<ex_grid(a), kExThreads, 0, (hipStream_t)hip_stream>>>(
-              a, (const B *)dy, (const B *)rows, weights, (B *)d_rows, d_weights);
-        });
+    return with_piece<T>(v, [&](auto pv) {
+      return with_batch(top, [&](auto batch) {
+        constexpr int V = decltype(pv)::value;
+        using B = typename Bytes<V>::type;
+        return launch(who, k_combine_backward<T, V, decltype(batch)::value>, ex_grid(a), kExThreads, 0, hip_stream, a,
+                      (const B *)dy, (const B *)rows, weights, (B *)d_rows, d_weights);
+      });
     });
   });
-  return launched(who);
 }

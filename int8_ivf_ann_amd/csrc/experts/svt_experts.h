@@ -27,21 +27,28 @@ inline bool overlap(const void *a, size_t na, const void *b, size_t nb) {
   return a && b && na && nb && x < y + nb && y < x + na;
 }
 
-// calls f with a value of the element type that dtype names (dtype was checked)
+// f of a value of the element type that dtype names (dtype was checked)
 template <class F>
-void with_type(int32_t dtype, F f) {
+int with_type(int32_t dtype, F f) {
   switch (dtype) {
-    case SVT_F32: f(float{}); break;
-    case SVT_F16: f(f16{}); break;
-    default: f(bf16{}); break;
+    case SVT_F32: return f(float{});
+    case SVT_F16: return f(f16{});
+    default: return f(bf16{});
   }
 }
 
-// the launch just made: SVT_OK, or its error reported
-inline int launched(const char *who) {
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return report(SVT_EDEVICE, "%s: launch: %s", who, hipGetErrorString(e));
-  return SVT_OK;
+// Launches a kernel: SVT_OK, or its failure reported.  The status is this launch's own (an error that an earlier call
+// left unread is its caller's, and stays), so that a call of several launches can end at the one that failed.
+template <class... P, class... A>
+int launch(const char *who, void (*kernel)(P...), dim3 grid, unsigned threads, size_t lds, void *stream, A... args) {
+  static_assert(sizeof...(P) == sizeof...(A), "one argument per parameter");
+  return [&](P... values) {   // converted to the kernel's types
+    void *ptrs[] = {(void *)&values...};
+    const hipError_t e = hipLaunchKernel((const void *)kernel, grid, dim3(threads), ptrs, lds, (hipStream_t)stream);
+    if (e == hipSuccess) return (int)SVT_OK;
+    (void)hipGetLastError();   // reported here
+    return report(SVT_EDEVICE, "%s: launch: %s", who, hipGetErrorString(e));
+  }(args...);
 }
 
 // ---- device --------------------------------------------------------------------------------------

@@ -80,7 +80,7 @@ struct LinearArgs {
 
 // one product with rows of type T (scale type and group are those of a.s); launches on stream
 template <class T>
-void linear_rows(LinearArgs a, int32_t scale_type, hipStream_t stream);
+int linear_rows(const char *who, LinearArgs a, int32_t scale_type, void *stream);
 
 // what a 16 x 16 x 32 instruction takes for rows of type T, and how many parts a row value has
 template <class T> struct Mma;
@@ -483,7 +483,7 @@ __global__ __launch_bounds__(64 * WK * WN, OCC) void k_linear(LinearArgs a) {
 }
 
 template <class T, class S, int G, bool Z, int MT, int NT, int U, int WK, int WN, int OCC>
-void launch_linear(LinearArgs a, hipStream_t stream) {
+int launch_linear(const char *who, LinearArgs a, void *stream) {
   using St = Stage<T, WK, U>;
   constexpr size_t kSumBytes = St::template sums<MT> ? (size_t)16 * MT * (St::kChunk / G) * 4 : 0;
   static_assert(St::bytes(16 * MT) + kSumBytes <= 160 * 1024, "the rows of a chunk fit a compute unit's LDS");
@@ -494,20 +494,19 @@ void launch_linear(LinearArgs a, hipStream_t stream) {
   const int64_t y = a.n_units < 32768 ? a.n_units : 32768, z = (a.n_units + y - 1) / y;
   const dim3 grid((unsigned)((a.s.tiles + NT * WN - 1) / (NT * WN)), (unsigned)y, (unsigned)z);
   const size_t lds = std::max(St::bytes(a.lds_rows) + kSumBytes, (size_t)WN * (WK - 1) * MT * NT * 1024);
-  k_linear<T, S, G, Z, MT, NT, U, WK, WN, OCC><<<grid, 64 * WK * WN, lds, stream>>>(a);
+  return launch(who, k_linear<T, S, G, Z, MT, NT, U, WK, WN, OCC>, grid, 64 * WK * WN, lds, stream, a);
 }
 
 template <class F>
-void with_group(int32_t group, F f) {
-  if (group == 32) f(std::integral_constant<int, 32>{});
-  else if (group == 64) f(std::integral_constant<int, 64>{});
-  else f(std::integral_constant<int, 128>{});
+int with_group(int32_t group, F f) {
+  if (group == 32) return f(std::integral_constant<int, 32>{});
+  if (group == 64) return f(std::integral_constant<int, 64>{});
+  return f(std::integral_constant<int, 128>{});
 }
 
 template <class F>
-void with_flag(int32_t on, F f) {
-  if (on) f(std::true_type{});
-  else f(std::false_type{});
+int with_flag(int32_t on, F f) {
+  return on ? f(std::true_type{}) : f(std::false_type{});
 }
 
 
@@ -545,59 +544,53 @@ void with_flag(int32_t on, F f) {
 // waves 11.5, 2 waves 12.7; but groups of 32, 64 rows, 4096 x 1024: 4 waves 7.4, 2 waves 5.9.  float32 rows, 32 x
 // 128 cut, 4096 rows by 8 experts of 2048 x 1024: groups of 64, 3 waves 86, 2 waves 109; groups of 128 84 and 83.
 template <class T, class S, int G, bool Z>
-void linear_cut(LinearArgs a, hipStream_t stream) {
+int linear_cut(const char *who, LinearArgs a, void *stream) {
   constexpr bool kShort = sizeof(T) == 2;
   constexpr int kWaves32 = kShort || G <= 64 ? 3 : 2, kWaves16 = kShort && G >= 64 ? 4 : 2;
   constexpr bool kFew = kShort && G >= 64;                   // two tiles of two blocks stay in registers
   constexpr bool kWide = G == 128 || (!kShort && G == 64);   // 32 x 256 rather than 64 x 256
   const int64_t rows = a.n_rows, tiles = a.s.tiles, blocks = a.s.blocks;
   auto groups = [&](int64_t r, int64_t t) { return ((rows + r - 1) / r) * ((tiles + t - 1) / t); };
-  auto cut_16_64 = [&] { launch_linear<T, S, G, Z, 1, 2, kFew || G == 128 ? 2 : 1, 2, 2, kFew ? 3 : 2>(a, stream); };
-  auto cut_16_32 = [&] { launch_linear<T, S, G, Z, 1, 1, 2, 2, 2, kWaves16>(a, stream); };
+  auto cut_16_64 = [&] { return launch_linear<T, S, G, Z, 1, 2, kFew || G == 128 ? 2 : 1, 2, 2, kFew ? 3 : 2>(who, a, stream); };
+  auto cut_16_32 = [&] { return launch_linear<T, S, G, Z, 1, 1, 2, 2, 2, kWaves16>(who, a, stream); };
   if (a.offsets) {
     const int64_t some = std::min<int64_t>(a.n_matrices, rows) / 2;   // half-filled blocks, about
     const bool full = rows >= 8 * (int64_t)a.n_matrices;
-    if (kShort && G == 128 && full && (rows / 32 + some) * ((tiles + 15) / 16) >= 384) {
-      if constexpr (kShort && G == 128) launch_linear<T, S, G, Z, 2, 4, 1, 1, 4, 2>(a, stream);
-    } else if (full && (rows / 32 + some) * ((tiles + 7) / 8) >= 256) {
-      launch_linear<T, S, G, Z, 2, 2, 1, 1, 4, kWaves32>(a, stream);
-    } else if ((rows / 16 + some) * ((tiles + 3) / 4) >= 288) {
-      cut_16_64();
-    } else {
-      cut_16_32();
-    }
-  } else if (kWide ? groups(32, 16) >= 512 : groups(64, 16) >= 256) {
-    if constexpr (kWide) launch_linear<T, S, G, Z, 2, 4, 1, 1, 4, 2>(a, stream);
-    else launch_linear<T, S, G, Z, 4, 2, 1, 1, 8, 2>(a, stream);
-  } else if (groups(32, 8) >= 512) {
-    launch_linear<T, S, G, Z, 2, 2, 1, 1, 4, kWaves32>(a, stream);
-  } else if (groups(32, 4) >= 512) {
-    launch_linear<T, S, G, Z, 2, 2, 1, 2, 2, 2>(a, stream);
-  } else if (rows <= 16 && groups(16, 2) >= 512 && blocks >= 8) {
-    launch_linear<T, S, G, Z, 1, 2, kFew ? 2 : 1, 4, 1, 2>(a, stream);
-  } else if (groups(16, 4) >= 512) {
-    cut_16_64();
-  } else if (blocks < 8 || groups(16, 2) > (rows <= 16 ? 511 : 256)) {
-    cut_16_32();
-  } else if (groups(16, 2) > 128) {
-    if (kShort && blocks >= 16) {   // float32 rows of two blocks: not in LDS
-      if constexpr (kShort) launch_linear<T, S, G, Z, 1, 2, 2, 8, 1, 2>(a, stream);
-    } else {
-      launch_linear<T, S, G, Z, 1, 2, 1, 8, 1, 2>(a, stream);
-    }
-  } else if (kShort && blocks >= 16) {
-    if constexpr (kShort) launch_linear<T, S, G, Z, 1, 1, 2, 8, 1, 2>(a, stream);
-  } else {
-    launch_linear<T, S, G, Z, 1, 1, 1, 8, 1, 2>(a, stream);
+    if constexpr (kShort && G == 128)
+      if (full && (rows / 32 + some) * ((tiles + 15) / 16) >= 384)
+        return launch_linear<T, S, G, Z, 2, 4, 1, 1, 4, 2>(who, a, stream);
+    if (full && (rows / 32 + some) * ((tiles + 7) / 8) >= 256)
+      return launch_linear<T, S, G, Z, 2, 2, 1, 1, 4, kWaves32>(who, a, stream);
+    if ((rows / 16 + some) * ((tiles + 3) / 4) >= 288) return cut_16_64();
+    return cut_16_32();
   }
+  if constexpr (kWide) {
+    if (groups(32, 16) >= 512) return launch_linear<T, S, G, Z, 2, 4, 1, 1, 4, 2>(who, a, stream);
+  } else {
+    if (groups(64, 16) >= 256) return launch_linear<T, S, G, Z, 4, 2, 1, 1, 8, 2>(who, a, stream);
+  }
+  if (groups(32, 8) >= 512) return launch_linear<T, S, G, Z, 2, 2, 1, 1, 4, kWaves32>(who, a, stream);
+  if (groups(32, 4) >= 512) return launch_linear<T, S, G, Z, 2, 2, 1, 2, 2, 2>(who, a, stream);
+  if (rows <= 16 && groups(16, 2) >= 512 && blocks >= 8)
+    return launch_linear<T, S, G, Z, 1, 2, kFew ? 2 : 1, 4, 1, 2>(who, a, stream);
+  if (groups(16, 4) >= 512) return cut_16_64();
+  if (blocks < 8 || groups(16, 2) > (rows <= 16 ? 511 : 256)) return cut_16_32();
+  if (groups(16, 2) > 128) {
+    if constexpr (kShort)   // float32 rows of two blocks: not in LDS
+      if (blocks >= 16) return launch_linear<T, S, G, Z, 1, 2, 2, 8, 1, 2>(who, a, stream);
+    return launch_linear<T, S, G, Z, 1, 2, 1, 8, 1, 2>(who, a, stream);
+  }
+  if constexpr (kShort)
+    if (blocks >= 16) return launch_linear<T, S, G, Z, 1, 1, 2, 8, 1, 2>(who, a, stream);
+  return launch_linear<T, S, G, Z, 1, 1, 1, 8, 1, 2>(who, a, stream);
 }
 
 template <class T>
-void linear_rows(LinearArgs a, int32_t scale_type, hipStream_t stream) {
-  with_type(scale_type, [&](auto ts) {
-    with_group(a.s.group, [&](auto g) {
-      with_flag(a.s.has_zeros, [&](auto z) {
-        linear_cut<T, decltype(ts), decltype(g)::value, decltype(z)::value>(a, stream);
+int linear_rows(const char *who, LinearArgs a, int32_t scale_type, void *stream) {
+  return with_type(scale_type, [&](auto ts) {
+    return with_group(a.s.group, [&](auto g) {
+      return with_flag(a.s.has_zeros, [&](auto z) {
+        return linear_cut<T, decltype(ts), decltype(g)::value, decltype(z)::value>(who, a, stream);
       });
     });
   });

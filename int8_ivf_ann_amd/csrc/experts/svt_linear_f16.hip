@@ -4,6 +4,6 @@
 
 namespace svt {
 
-template void linear_rows<f16>(LinearArgs, int32_t, hipStream_t);
+template int linear_rows<f16>(const char *, LinearArgs, int32_t, void *);
 
 }  // namespace svt

@@ -4,6 +4,6 @@
 
 namespace svt {
 
-template void linear_rows<float>(LinearArgs, int32_t, hipStream_t);
+template int linear_rows<float>(const char *, LinearArgs, int32_t, void *);
 
 }  // namespace svt

@@ -5,9 +5,9 @@
 
 namespace svt {
 
-extern template void linear_rows<float>(LinearArgs, int32_t, hipStream_t);
-extern template void linear_rows<f16>(LinearArgs, int32_t, hipStream_t);
-extern template void linear_rows<bf16>(LinearArgs, int32_t, hipStream_t);
+extern template int linear_rows<float>(const char *, LinearArgs, int32_t, void *);
+extern template int linear_rows<f16>(const char *, LinearArgs, int32_t, void *);
+extern template int linear_rows<bf16>(const char *, LinearArgs, int32_t, void *);
 
 namespace {
 
@@ -101,24 +101,20 @@ extern "C" int svt_quant_pack(const svt_quant_weights *w, const uint8_t *nibbles
   if (overlap(w->packed, need, nibbles, rows * ((w->n_in + 1) / 2)) ||
       overlap(w->packed, need, scales, rows * src_groups * b) || overlap(w->packed, need, zeros, rows * src_groups))
     return report(SVT_EINVAL, "%s: the packed buffer overlaps an input", who);
-  hipStream_t st = (hipStream_t)hip_stream;
   auto grid = [](int64_t n) {
     const int64_t g = (n + kPackThreads - 1) / kPackThreads;
     return (unsigned)(g < 65536 ? g : 65536);
   };
   const int64_t pieces = (int64_t)w->n_matrices * s.tiles * s.blocks * 64;
-  k_pack_q<<<grid(pieces), kPackThreads, 0, st>>>(s, pieces, nibbles, (uint8_t *)w->packed);
+  int done = launch(who, k_pack_q, grid(pieces), kPackThreads, 0, hip_stream, s, pieces, nibbles, (uint8_t *)w->packed);
   const int64_t values = (int64_t)w->n_matrices * s.tiles * s.blocks * kTileN * (kBlockK / s.group);
-  if (b == 4)
-    k_pack_groups<uint32_t><<<grid(values), kPackThreads, 0, st>>>(s, values, src_groups, 0,
-                                                                  (const uint32_t *)scales, (uint8_t *)w->packed);
-  else
-    k_pack_groups<uint16_t><<<grid(values), kPackThreads, 0, st>>>(s, values, src_groups, 0,
-                                                                  (const uint16_t *)scales, (uint8_t *)w->packed);
-  if (w->has_zeros)
-    k_pack_groups<uint8_t><<<grid(values), kPackThreads, 0, st>>>(s, values, src_groups, 4 * b, zeros,
-                                                                 (uint8_t *)w->packed);
-  return launched(who);
+  auto groups = [&](auto *src, int at) {
+    return launch(who, k_pack_groups<std::remove_const_t<std::remove_pointer_t<decltype(src)>>>, grid(values),
+                  kPackThreads, 0, hip_stream, s, values, src_groups, at, src, (uint8_t *)w->packed);
+  };
+  if (done == SVT_OK) done = b == 4 ? groups((const uint32_t *)scales, 0) : groups((const uint16_t *)scales, 0);
+  if (done == SVT_OK && w->has_zeros) done = groups(zeros, 4 * b);
+  return done;
 }
 
 extern "C" int svt_quant_linear(int32_t n_rows, int32_t dtype, const void *x, const svt_quant_weights *w,
@@ -162,6 +158,5 @@ extern "C" int svt_quant_linear(int32_t n_rows, int32_t dtype, const void *x, co
   a.wide_store = w->n_out % 4 == 0 && !misaligned(y, 4 * by);
   a.x = x;
   a.y = y;
-  with_type(dtype, [&](auto tx) { linear_rows<decltype(tx)>(a, w->scale_type, (hipStream_t)hip_stream); });
-  return launched(who);
+  return with_type(dtype, [&](auto tx) { return linear_rows<decltype(tx)>(who, a, w->scale_type, hip_stream); });
 }

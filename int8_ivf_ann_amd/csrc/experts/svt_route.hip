@@ -316,17 +316,17 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_backward(const T *logit
   }
 }
 
-// calls f with the group width for E experts as a constant
+// f of the group width for E experts as a constant
 template <class F>
-void with_lanes(int E, F f) {
+int with_lanes(int E, F f) {
   const int need = (E + kPer - 1) / kPer;
-  if (need <= 1) f(std::integral_constant<int, 1>{});
-  else if (need <= 2) f(std::integral_constant<int, 2>{});
-  else if (need <= 4) f(std::integral_constant<int, 4>{});
-  else if (need <= 8) f(std::integral_constant<int, 8>{});
-  else if (need <= 16) f(std::integral_constant<int, 16>{});
-  else if (need <= 32) f(std::integral_constant<int, 32>{});
-  else f(std::integral_constant<int, 64>{});
+  if (need <= 1) return f(std::integral_constant<int, 1>{});
+  if (need <= 2) return f(std::integral_constant<int, 2>{});
+  if (need <= 4) return f(std::integral_constant<int, 4>{});
+  if (need <= 8) return f(std::integral_constant<int, 8>{});
+  if (need <= 16) return f(std::integral_constant<int, 16>{});
+  if (need <= 32) return f(std::integral_constant<int, 32>{});
+  return f(std::integral_constant<int, 64>{});
 }
 
 unsigned route_grid(int64_t n_tokens, int lanes) {
@@ -365,19 +365,19 @@ extern "C" int svt_route(int32_t n_tokens, int32_t n_experts, int32_t top, int32
   if (overlap(logits, nl, out_experts, no) || overlap(logits, nl, out_weights, no) ||
       overlap(out_experts, no, out_weights, no))
     return report(SVT_EINVAL, "%s: an output overlaps the logits or the other output", who);
-  with_type(dtype, [&](auto ty) {
+  return with_type(dtype, [&](auto ty) {
     using T = decltype(ty);
-    with_lanes(n_experts, [&](auto lanes) {
+    return with_lanes(n_experts, [&](auto lanes) {
       constexpr int L = decltype(lanes)::value;
-      auto launch = [&](auto rounds) {
-        k_route<T, L, decltype(rounds)::value><<<route_grid(n_tokens, L), kRouteThreads, 0, (hipStream_t)hip_stream>>>(
-            (const T *)logits, n_tokens, n_experts, top, renormalise, out_experts, out_weights);
+      auto go = [&](auto rounds) {
+        return launch(who, k_route<T, L, decltype(rounds)::value>, route_grid(n_tokens, L), kRouteThreads, 0, hip_stream,
+                      (const T *)logits, n_tokens, n_experts, top, renormalise, out_experts, out_weights);
       };
-      if (top <= kPer) launch(std::false_type{});
-      else if constexpr (L > 1) launch(std::true_type{});   // one lane holds at most kPer experts
+      if constexpr (L > 1)   // one lane holds at most kPer experts
+        if (top > kPer) return go(std::true_type{});
+      return go(std::false_type{});
     });
   });
-  return launched(who);
 }
 
 extern "C" int svt_route_backward(int32_t n_tokens, int32_t n_experts, int32_t top, int32_t dtype, const void *logits,
@@ -397,13 +397,12 @@ extern "C" int svt_route_backward(int32_t n_tokens, int32_t n_experts, int32_t t
   if (overlap(d_logits, nl, logits, nl) || overlap(d_logits, nl, experts, nk) || overlap(d_logits, nl, weights, nk) ||
       overlap(d_logits, nl, d_weights, nk))
     return report(SVT_EINVAL, "%s: d_logits overlaps an input", who);
-  with_type(dtype, [&](auto ty) {
+  return with_type(dtype, [&](auto ty) {
     using T = decltype(ty);
-    with_lanes(n_experts, [&](auto lanes) {
+    return with_lanes(n_experts, [&](auto lanes) {
       constexpr int L = decltype(lanes)::value;
-      k_route_backward<T, L><<<route_grid(n_tokens, L), kRouteThreads, 0, (hipStream_t)hip_stream>>>(
-          (const T *)logits, n_tokens, n_experts, top, renormalise, experts, weights, d_weights, (T *)d_logits);
+      return launch(who, k_route_backward<T, L>, route_grid(n_tokens, L), kRouteThreads, 0, hip_stream,
+                    (const T *)logits, n_tokens, n_experts, top, renormalise, experts, weights, d_weights, (T *)d_logits);
     });
   });
-  return launched(who);
 }
