@@ -31,14 +31,15 @@ constexpr int kPer = 8;            // logits per lane
 constexpr int kRouteThreads = 256;
 static_assert(SVT_MAX_EXPERTS == 64 * kPer, "one wave holds the widest row");
 
-// float -> uint32 whose unsigned order is the float order (-0 as 0); 0 for a shut expert (-inf or NaN)
+// float -> uint32 whose unsigned order is the float order (-0 as 0, +inf as the largest finite value, so that they tie
+// and its weight is a number); 0 for a shut expert (-inf or NaN)
 __device__ __forceinline__ uint32_t logit_order(float f) {
-  const uint32_t b = __float_as_uint(f + 0.f);
+  const uint32_t b = __float_as_uint(fminf(f, FLT_MAX) + 0.f);
   return f > -INFINITY ? ((b & 0x80000000u) ? ~b : (b | 0x80000000u)) : 0u;
 }
-// its inverse; +inf counts as the largest finite value, so that its weight is a number
+// its inverse
 __device__ __forceinline__ float order_logit(uint32_t o) {
-  return fminf(__uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o), FLT_MAX);
+  return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
 }
 
 // v of a lane in the neighbouring aligned group of STEP lanes (any of them: they agree)
