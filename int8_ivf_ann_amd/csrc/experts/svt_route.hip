@@ -53,15 +53,15 @@ __device__ __forceinline__ uint32_t half_other(uint32_t v) {
 }
 
 // exp(x) for x <= 0, and for NaN 0 (which stands for a shut expert), for +inf 1 (+inf counts as the peak).
-// 2^y with y = x log2 e and the product's rounding put back, so that the result is off by 3 u and not by
-// |x| u; 0 below -200, long past the smallest float.  No branch, half the instructions of expf.
+// x log2 e = n + f with n a whole number and |f| <= 1/2 (to the last bit: the product is subtracted unrounded, and its
+// constant's rest added), exp = 2^f 2^n.  f is off by u, the hardware's 2^f by 1 ulp, so the result by 3 u; below
+// 2^-126, which the hardware's 2^x would flush, 2^n rounds it to a subnormal.  0 below -200.
 __device__ __forceinline__ float exp_below(float x) {
-  constexpr float kLog2e = 1.44269502e+0f, kLog2eRest = 1.92596299e-8f, kLn2 = 6.93147182e-1f;
+  constexpr float kLog2e = 1.44269502e+0f, kLog2eRest = 1.92596299e-8f;
   x = fminf(fmaxf(x, -200.f), 0.f);
-  const float y = x * kLog2e;
-  const float rest = fmaf(x, kLog2eRest, fmaf(x, kLog2e, -y));
-  const float e = __builtin_amdgcn_exp2f(y);
-  return fmaf(e, rest * kLn2, e);
+  const float n = __builtin_rintf(x * kLog2e);
+  const float f = fmaf(x, kLog2eRest, fmaf(x, kLog2e, -n));
+  return ldexpf(__builtin_amdgcn_exp2f(f), (int)n);
 }
 
 // A logit and its expert; greater: (logit desc, expert asc).

@@ -37,3 +37,31 @@ def test_route_plus_infinity_ties_with_the_largest_float(svt, E, K, renorm):
     rid, rw, _ = X.route(l, K, renorm)
     assert np.array_equal(host(ids), rid)
     near(host(w), rw, 32 * U * rw, "weights")   # differences of 0 or past every exponential: 31 u, as everywhere
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("E", [11, 64, 300])
+def test_route_weights_below_the_smallest_normal_float(svt, E, renorm, kind):
+    """Experts 80 to 110 below the best: weights down to the smallest subnormal, and their gradients.  The exponential
+    and the division each round a subnormal by at most 2^-150; the gradient's two products by as much, and pass the
+    first on by |dw| + |dot|."""
+    say("subnormal", E, renorm, kind)
+    rng = np.random.default_rng(E)
+    gaps = np.array([0, 80, 87, 87.4, 88, 92, 95, 100, 103, 103.9, 110])
+    l = np.full((6, E), -np.inf)
+    for t in range(6):
+        l[t, rng.permutation(E)[:11]] = rng.normal() - gaps - 0.1 * rng.random(11)
+    lt = dev(l, ty(kind))
+    l = host(lt)
+    for K in (8, 11):
+        ids, w = svt.svt_route(lt, K, renormalise=renorm)
+        rid, rw, sens = X.route(l, K, renorm)
+        assert np.array_equal(host(ids), rid)
+        near(host(w), rw, U * rw * (sens + 31) + 2.0 ** -149, "weights")
+        dw = rng.normal(size=(6, K)).astype(np.float32)
+        d = svt.svt_route_backward(lt, ids, w, dev(dw), renormalise=renorm, out=dev(np.zeros((6, E)), ty(kind)))
+        rd, mag, bs = X.route_backward(l, rid, host(w), dw.astype(np.float64), renorm)
+        most = np.abs(dw).max(1, keepdims=True).astype(np.float64)
+        near(host(d), rd, U * mag * (bs + 51) + HALF[kind] * np.abs(rd) + TINY[kind] + 2.0 ** -149 * (2 * most + 1),
+             "d_logits")
