@@ -236,8 +236,17 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(const T *logits, int64_
   }
 }
 
-// The weights' gradients reach their experts' lanes through LDS (added there: an expert named twice gets
-// both).
+// between LDS operations of one wave that reach the same addresses: the hardware keeps them in order, so that only the
+// compiler has to
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// The weights' gradients reach their experts' lanes through LDS.  An expert named more than once gets every part, in
+// the order of the choices: each choice's additions are an instruction of their own, and a wave's LDS operations stay
+// in order (one instruction for all lanes' choices would add them in no defined order).  A token's lanes lie in one wave,
+// so no workgroup barrier is needed.
 template <class T, int L>
 __global__ __launch_bounds__(kRouteThreads) void k_route_backward(const T *logits, int64_t n_tokens, int E, int top,
                                                                   int renormalise, const int32_t *experts,
@@ -267,11 +276,16 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_backward(const T *logit
       dot += id[q] >= 0 ? d[q] * w[q] : 0.f;
     }
     dot = group_add(dot, L);
-    __syncthreads();
+    wave_order();
 #pragma unroll
-    for (int q = 0; q < kKept; ++q)
-      if (id[q] >= 0) atomicAdd(&token[id[q]], renormalise ? w[q] * (d[q] - dot) : d[q]);
-    __syncthreads();
+    for (int q = 0; q < kKept; ++q) {
+      const float part = renormalise ? w[q] * (d[q] - dot) : d[q];
+#pragma unroll 1
+      for (int i = 0; i < L && q * L + i < top; ++i) {
+        if (in == i && id[q] >= 0) atomicAdd(&token[id[q]], part);
+        wave_order();   // the compiler may not join two choices' additions
+      }
+    }
     float g[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) g[i] = own[i];

@@ -65,3 +65,26 @@ def test_route_weights_below_the_smallest_normal_float(svt, E, renorm, kind):
         most = np.abs(dw).max(1, keepdims=True).astype(np.float64)
         near(host(d), rd, U * mag * (bs + 51) + HALF[kind] * np.abs(rd) + TINY[kind] + 2.0 ** -149 * (2 * most + 1),
              "d_logits")
+
+
+@pytest.mark.parametrize("E", [8, 16, 64, 512])
+@pytest.mark.parametrize("K", [3, 8])
+def test_route_backward_adds_a_repeated_expert_in_order(svt, E, K):
+    """An expert that a token names several times gets the sum of its parts in the order of the choices, whatever
+    lanes hold them.  Parts of 32 binades, so that the float32 sum depends on the order; weights of 0, so that the
+    parts are dw; equal logits, so that p is the power of two 1 / E: the result is that sum, exactly."""
+    say("repeated", E, K)
+    rng = np.random.default_rng(E + K)
+    T = 300
+    ids = np.stack([rng.choice(rng.choice(E, 2, replace=False), K) for _ in range(T)]).astype(np.int32)
+    dw = rng.choice([1.0, -1.0], (T, K)) * rng.uniform(1, 2, (T, K)) * 2.0 ** rng.integers(-4, 28, (T, K))
+    dw = dw.astype(np.float32)
+    want = np.zeros((T, E), np.float32)
+    for t in range(T):
+        for j in range(K):
+            want[t, ids[t, j]] += dw[t, j]
+    want *= np.float32(1.0 / E)
+    for _ in range(3):
+        got = svt.svt_route_backward(dev(np.zeros((T, E), np.float32)), dev(ids), dev(np.zeros((T, K), np.float32)),
+                                     dev(dw), renormalise=False)
+        assert np.array_equal(host(got).astype(np.float32), want)
