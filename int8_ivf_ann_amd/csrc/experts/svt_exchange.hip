@@ -380,7 +380,10 @@ __global__ __launch_bounds__(kExThreads) void k_combine(ExArgs a, const typename
 }
 
 // d_rows[position[t][j]] = w[t][j] dy[t];  d_weights[t][j] = dy[t] . rows[position[t][j]] (0 for a dropped
-// entry).  The token's lanes sum their products over the row, then with each other.
+// entry).  A lane sums each piece's products, kDotPieces pieces' sums, and those; then the token's lanes add theirs up.
+// So no chain of additions is longer than 512 (one over a lane's whole share of 2^24 values would be 2^18), and a
+// d_weight is off by at most (8 + 512 + 512 + 6) u of sum |dy r|, u = 2^-24.
+constexpr int kDotPieces = 512;
 template <class T, int V, int J>
 __global__ __launch_bounds__(kExThreads) void k_combine_backward(ExArgs a, const typename Bytes<V>::type *dy,
                                                                  const typename Bytes<V>::type *rows,
@@ -401,8 +404,12 @@ __global__ __launch_bounds__(kExThreads) void k_combine_backward(ExArgs a, const
         w[j] = live && j0 + j < a.top ? weights[t * a.top + j0 + j] : 0.f;
         dot[j] = 0.f;
       }
-      if (live)
-        for (int c = in; c < a.chunks; c += 2 * a.lanes) {
+      for (int c0 = in; live && c0 < a.chunks; c0 += kDotPieces * a.lanes) {
+        float part[J];
+#pragma unroll
+        for (int j = 0; j < J; ++j) part[j] = 0.f;
+        const int end = a.chunks - c0 < kDotPieces * a.lanes ? a.chunks : c0 + kDotPieces * a.lanes;
+        for (int c = c0; c < end; c += 2 * a.lanes) {
           const bool two = c + a.lanes < a.chunks;
           const int c2 = two ? c + a.lanes : c;
           const L g0(dy[t * a.chunks + c]), g1(dy[t * a.chunks + c2]);
@@ -422,15 +429,20 @@ __global__ __launch_bounds__(kExThreads) void k_combine_backward(ExArgs a, const
                 const L &g = h ? g1 : g0;
                 const L v(r[j][h]);
                 L d;
+                float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < L::n; ++i) {
-                  dot[j] = fmaf(g.v[i], v.v[i], dot[j]);
+                  sum = fmaf(g.v[i], v.v[i], sum);
                   d.v[i] = w[j] * g.v[i];
                 }
+                part[j] += sum;
                 d_rows[p[j] * a.chunks + (h ? c2 : c)] = d.raw();
               }
             }
         }
+#pragma unroll
+        for (int j = 0; j < J; ++j) dot[j] += part[j];
+      }
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         const float s = group_add(dot[j], a.lanes);

@@ -88,3 +88,31 @@ def test_route_backward_adds_a_repeated_expert_in_order(svt, E, K):
         got = svt.svt_route_backward(dev(np.zeros((T, E), np.float32)), dev(ids), dev(np.zeros((T, K), np.float32)),
                                      dev(dw), renormalise=False)
         assert np.array_equal(host(got).astype(np.float32), want)
+
+
+# ---- exchange ----------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("D", [1 << 22, (1 << 22) + 4, 3000001])
+def test_combine_backward_of_wide_rows(svt, D, kind):
+    """d_weights of wide rows, constant (every addition rounds the same way) and random.  A lane has m = ceil(pieces /
+    64) pieces of n values (16 bytes, or what divides the row): n products in a chain, up to 512 pieces' sums, ceil(m
+    / 512) sums of those, 6 levels across lanes: (n + min(m, 512) + ceil(m / 512) + 6) u of sum |dy r|."""
+    say("wide", D, kind)
+    import torch
+    size = 4 if kind == "f32" else 2
+    v = next(b for b in (16, 8, 4, 2) if D * size % b == 0)
+    n, m = v // size, -(-(D * size // v) // 64)
+    bound = (n + min(m, 512) + -(-m // 512) + 6) * U
+    g = torch.Generator(device="cuda").manual_seed(D)
+    dy = torch.randn((2, D), generator=g, device="cuda").to(ty(kind))
+    rows = torch.randn((4, D), generator=g, device="cuda").to(ty(kind))
+    dy[0], rows[0], rows[1] = 0.7, 1.1, 0.1
+    pos = torch.tensor([[0, 1], [3, 2]], dtype=torch.int32, device="cuda")
+    w = torch.tensor([[0.5, 2.0], [1.0, -1.0]], device="cuda")
+    dr, dw = svt.svt_expert_combine_backward(dy, rows, pos, w)
+    for t in range(2):
+        for j in range(2):
+            a, b = dy[t].double(), rows[int(pos[t, j])].double()
+            near(np.float64(dw[t, j].item()), float(a @ b), bound * float(a.abs() @ b.abs()), f"d_weights {t} {j}")
+            assert torch.equal(dr[int(pos[t, j])], (w[t, j] * dy[t].float()).to(ty(kind)))
