@@ -442,10 +442,11 @@ int svt_quant_pack(const svt_quant_weights *w, const uint8_t *nibbles, const voi
  *   bias        [n_matrices][n_out] float or NULL
  *   activation  SVT_ACT_NONE or SVT_ACT_RELU (NaN stays NaN)
  *   y           [n_rows][n_out] of out_dtype: dtype or SVT_F32
- * No weight or product is rounded: group sums of x q and of x are float32, and 256 times the sum of |x| over a
- * group must stay finite, as must the scales.  A row that holds an infinity or NaN gets NaN outputs.  Of float32
- * rows, digits below 2^-133 are not used.  n_rows == 0 returns
- * SVT_OK without enqueuing.  Errors: SVT_EINVAL, SVT_EUNSUPPORTED (group), SVT_EDEVICE as svt_quant_pack.
+ * No weight or product is rounded; group sums are float32, and 256 times the sum of |x| over a group must stay
+ * finite, as must the scales.  The sums' roundings are in proportion to sum |scale| |x| |q - zero| where y is float32
+ * (a weight of 0 adds exactly 0), and to sum |scale| |x| (q + zero), which y's own rounding covers, where y has two
+ * bytes.  A row that holds an infinity or NaN gets NaN outputs.  Of float32 rows, digits below 2^-133 are not used.
+ * n_rows == 0 returns SVT_OK without enqueuing.  Errors: SVT_EINVAL, SVT_EUNSUPPORTED (group), SVT_EDEVICE as svt_quant_pack.
  */
 int svt_quant_linear(int32_t n_rows, int32_t dtype, const void *x, const svt_quant_weights *w, const int32_t *offsets,
                      const float *bias, int32_t activation, int32_t out_dtype, void *y, void *hip_stream);

@@ -5,11 +5,19 @@
 //   y[r][n] = act(bias[n] + sum_k x[r][k] W[n][k])
 //           = act(bias[n] + sum_g s[n][g] (sum_{k in g} x[r][k] q[n][k] - z[n][g] sum_{k in g} x[r][k]))
 //
-// The inner sums run on the matrix cores (v_mfma_f32_16x16x32, 16 outputs x 16 rows x 32 k) with q as bf16
-// or f16, which hold 0 .. 15 exactly, and float32 accumulation: no weight is rounded, and s and z are
-// applied to float32 group sums.  sum x comes from the same instruction with a matrix of ones, in the
-// lanes that need it; where every zero point is 8, a matrix of -8 gives what the products then start from.
-// (Of float32 rows, products of many rows add x up in float32 while they store the rows.)
+// The inner sums run on the matrix cores (v_mfma_f32_16x16x32, 16 outputs x 16 rows x 32 k) with whole numbers as
+// bf16 or f16, which hold -255 .. 255 exactly, and float32 accumulation: no weight is rounded, and s is applied to
+// float32 group sums.  Two forms:
+//   q - z   (outputs of float32) is formed before the instruction, so that the sums' roundings are in proportion to
+//           sum |x| |q - z|, as those of the product itself: a weight of 0 adds exactly 0.
+//   q       (outputs of two bytes, whose own rounding is 2^7 (float16) or 2^10 (bfloat16) times the 2.5e-6 below), and z
+//           sum x from the group's sum, which the same instruction gives with a matrix of ones; where every zero point is 8, a matrix
+//           of -8 gives what the products then start from.  Its roundings are in proportion to sum |x| (q + z).  Forming
+//           q - z takes 12 more instructions for 8 weights (bf16), 4 (f16).
+// 13 rows, 1024 inputs, groups of 128 with zero points, rows behind a relu: the relative error of float32 rows is 1.2e-7
+// with q - z formed before, 2.5e-6 after (a float32 product 1.9e-7).  In us, before and after: 1 row of 16384 x 4096,
+// float32 16.3 and 14.6, bfloat16 13.4 and 10.7, float16 11.9 and 10.9; 1024 rows of 4096 x 1024, 38.5 and 35.9, 22.6 and
+// 19.8, 20.9 and 20.0.
 // q reaches bf16/f16 two at a time: the byte 0000qqqq read as an 8-bit float with 3 mantissa bits is
 // q * 2^-9 (its subnormals and its first binade share one spacing), and v_cvt_scalef32_pk_* turns two such
 // bytes into two exact numbers with the scale 2^9.
@@ -38,14 +46,15 @@ constexpr int kMaxIn = 1 << 20, kMaxOut = 1 << 19;
 // 128 k and tile of 16 outputs, [block][tile], holding
 //   q       [lane][16]: lane l holds output l % 16, k = 128 block + 32 s + 8 (l / 16) + i for s = 0..3 in dword
 //           s, whose byte i (0..3) holds i in its low and i + 4 in its high half
-//   groups  [h][g]: what lane (., h) of the instruction's result needs, together: the scales of outputs
-//           4 h .. 4 h + 3 for group g of the block, then, where there are any, their zero points (a byte each)
+//   scales  [h][g]: what lane (., h) of the instruction's result needs, together: the scales of outputs
+//           4 h .. 4 h + 3 for group g of the block
+//   zeros   [output][g], where there are zero points: a byte each
 // Outputs and groups past the end have scale 0.  A wave reads whole records, and workgroups that run
 // together read neighbouring ones.
 struct QuantShape {
   int32_t n_out, n_in, group, has_zeros;
   int32_t tiles, blocks;
-  int32_t four, record;   // bytes of one [h][g] entry, of a record
+  int32_t zeros_at, record;   // of a record: where its zero points begin, its bytes
   size_t stride;
 };
 
@@ -57,8 +66,8 @@ inline QuantShape quant_shape(const svt_quant_weights &w) {
   s.has_zeros = w.has_zeros;
   s.tiles = (w.n_out + kTileN - 1) / kTileN;
   s.blocks = (w.n_in + kBlockK - 1) / kBlockK;
-  s.four = 4 * elem_size(w.scale_type) + (w.has_zeros ? 4 : 0);
-  s.record = kGroupsAt + 4 * (kBlockK / w.group) * s.four;
+  s.zeros_at = kGroupsAt + kTileN * (kBlockK / w.group) * elem_size(w.scale_type);
+  s.record = s.zeros_at + (w.has_zeros ? kTileN * (kBlockK / w.group) : 0);
   s.stride = ((size_t)s.tiles * s.blocks * s.record + 255) & ~(size_t)255;
   return s;
 }
@@ -86,10 +95,13 @@ int linear_rows(const char *who, LinearArgs a, int32_t scale_type, void *stream)
 template <class T> struct Mma;
 template <> struct Mma<bf16> {
   typedef bf16x8 frag;
+  typedef bf16x2 two;
+  typedef float zero;   // there is no packed bf16 subtraction
   static constexpr int parts = 1;
   static __device__ __forceinline__ f32x4 mul(frag w, frag x, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x, c, 0, 0, 0);
   }
+  // q of 8 weights
   static __device__ __forceinline__ frag weights(uint32_t d) {
     struct { bf16x2 p[4]; } u;
     const uint32_t a = d & 0x0F0F0F0Fu, b = (d >> 4) & 0x0F0F0F0Fu;
@@ -99,9 +111,26 @@ template <> struct Mma<bf16> {
     u.p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 512.f, true);
     return __builtin_bit_cast(frag, u);
   }
+  // q - z
+  static __device__ __forceinline__ frag weights(uint32_t d, zero z) {
+    struct { bf16x2 p[4]; } u;
+    const uint32_t a = d & 0x0F0F0F0Fu, b = (d >> 4) & 0x0F0F0F0Fu;
+    auto less = [&](auto v) { return bf16x2{(bf16)(v[0] - z), (bf16)(v[1] - z)}; };
+    u.p[0] = less(__builtin_amdgcn_cvt_scalef32_pk_f32_fp8(a, 512.f, false));
+    u.p[1] = less(__builtin_amdgcn_cvt_scalef32_pk_f32_fp8(a, 512.f, true));
+    u.p[2] = less(__builtin_amdgcn_cvt_scalef32_pk_f32_fp8(b, 512.f, false));
+    u.p[3] = less(__builtin_amdgcn_cvt_scalef32_pk_f32_fp8(b, 512.f, true));
+    return __builtin_bit_cast(frag, u);
+  }
+  // c + 0 v: NaN if v holds an infinity or NaN
+  static __device__ __forceinline__ float nothing(two v, float c) {
+    return __builtin_amdgcn_fdot2_f32_bf16(v, two{(bf16)0.f, (bf16)0.f}, c, false);
+  }
 };
 template <> struct Mma<f16> {
   typedef f16x8 frag;
+  typedef f16x2 two;
+  typedef f16 zero;
   static constexpr int parts = 1;
   static __device__ __forceinline__ f32x4 mul(frag w, frag x, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(w, x, c, 0, 0, 0);
@@ -115,18 +144,45 @@ template <> struct Mma<f16> {
     u.p[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 512.f, true);
     return __builtin_bit_cast(frag, u);
   }
+  static __device__ __forceinline__ frag weights(uint32_t d, zero z) {
+    frag w = weights(d);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const two v = two{w[i], w[i + 1]} - two{z, z};
+      w[i] = v[0];
+      w[i + 1] = v[1];
+    }
+    return w;
+  }
+  static __device__ __forceinline__ float nothing(two v, float c) {
+    return __builtin_amdgcn_fdot2(v, two{(f16)0.f, (f16)0.f}, c, false);
+  }
 };
 template <> struct Mma<float> : Mma<bf16> {
   static constexpr int parts = 3;
 };
 
+// how the zero points enter: all are 8 (products start from -8 sum x), after the group's products, or before them
+enum Zeros { kEight, kAfter, kBefore };
+
 template <class T> struct __attribute__((packed, aligned(sizeof(T)))) Eight { T v[8]; };
 
-// the parts of 8 row values, most significant first
-template <class T>
+// The parts of 8 row values, most significant first.
+// An infinity becomes NaN in every form: of float32 rows as inf - inf, of two-byte ones as inf q - inf z or, where z is
+// taken off before (NONFINITE), here (0x7FFF is a NaN of both types).
+template <class T, bool NONFINITE>
 __device__ __forceinline__ void row_parts(const Eight<T> &r, typename Mma<T>::frag (&f)[Mma<T>::parts]) {
   if constexpr (sizeof(T) == 2) {
-    f[0] = __builtin_bit_cast(typename Mma<T>::frag, r);
+    struct Four { uint32_t d[4]; } v = __builtin_bit_cast(Four, r);
+    if constexpr (NONFINITE) {
+      float bad = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) bad = Mma<T>::nothing(__builtin_bit_cast(typename Mma<T>::two, v.d[i]), bad);
+      const uint32_t nan = bad == 0.f ? 0u : 0x7FFF7FFFu;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v.d[i] |= nan;
+    }
+    f[0] = __builtin_bit_cast(typename Mma<T>::frag, v);
   } else {
     struct { uint32_t d[4]; } hi, mid, lo;
     float a[8], b[8], c[8];
@@ -190,13 +246,33 @@ __device__ __forceinline__ bool find_rows(const LinearArgs &a, int64_t unit, int
   return *r0 < *r1;
 }
 
-// the [h][g] entries of a record that one lane needs
-template <class S, int NG, bool Z>
-struct Groups {
-  struct __attribute__((packed, aligned(4))) Four {
-    S s[4];
-    uint32_t z[Z ? 1 : 0];
-  } g[NG];
+// the scales of a record that one lane needs
+template <class S, int NG>
+struct Scales {
+  struct __attribute__((aligned(4 * sizeof(S)))) Four { S s[4]; } g[NG];
+};
+
+// and its zero points: of the four outputs that the lane gets results of (after), of the one whose q it holds (before)
+template <int NG, Zeros Z> struct ZeroPoints {};
+template <int NG> struct ZeroPoints<NG, kAfter> {
+  struct __attribute__((aligned(4 * NG))) Bytes { uint32_t d[NG]; } v;   // [output][g]
+  __device__ __forceinline__ void load(const uint8_t *zeros, int h, int) {
+    v = *reinterpret_cast<const Bytes *>(zeros + (uint32_t)(4 * NG * h));
+  }
+  __device__ __forceinline__ float of(int i, int g) const {
+    const int at = i * NG + g;
+    return (float)((v.d[at / 4] >> (8 * (at % 4))) & 255u);
+  }
+};
+template <int NG> struct ZeroPoints<NG, kBefore> {
+  uint32_t v;
+  __device__ __forceinline__ void load(const uint8_t *zeros, int, int output) {
+    const uint8_t *at = zeros + (uint32_t)(NG * output);
+    if constexpr (NG == 4) v = *reinterpret_cast<const uint32_t *>(at);
+    else if constexpr (NG == 2) v = *reinterpret_cast<const uint16_t *>(at);
+    else v = *at;
+  }
+  __device__ __forceinline__ float of(int g) const { return (float)((v >> (8 * g)) & 255u); }
 };
 
 // the first `left` of four values
@@ -226,32 +302,15 @@ struct Stage {
   static constexpr int kRow = kChunk * 2 + 16;         // bytes of a row of one part: lanes of one h in 64 banks
   static constexpr int kParts = Mma<T>::parts;
   static constexpr size_t bytes(int rows) { return (size_t)kParts * rows * kRow; }
-  // Whether sum x over a group is made once, where the rows are stored, for all waves (else: each wave's own
-  // instructions with a matrix of ones).  For float32 rows those would be three per product of a part: 1024
-  // rows by 32 experts of 2048 x 1024 35 us, else 41.  For two-byte rows they hide better than the sums'
-  // additions: 512 rows, 4096 x 1024: 11.7 us, with sums stored 13.6.
-  template <int MT>
-  static constexpr bool sums = sizeof(T) == 4 && MT >= 2 && WK == 1;
 };
 
-// the row values' sum
-template <class T>
-__device__ __forceinline__ float sum_eight(const Eight<T> &r) {
-  float v[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = (float)r.v[i];
-  return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
-}
-
-template <class T, class S, int G, bool Z, int MT, int NT, int U, int WK, int WN, int OCC>
+template <class T, class S, int G, Zeros Z, int MT, int NT, int U, int WK, int WN, int OCC>
 __global__ __launch_bounds__(64 * WK * WN, OCC) void k_linear(LinearArgs a) {
   using M = Mma<T>;
   using St = Stage<T, WK, U>;
   constexpr int P = M::parts, NG = kBlockK / G, kSteps = G / 32, MN = MT * NT, kThreads = 64 * WK * WN;
   constexpr int kPieces = St::kChunk / 8;                            // 8 values each, of a row of a chunk
   constexpr int kEach = (16 * MT * kPieces + kThreads - 1) / kThreads;   // pieces of a thread at most
-  constexpr bool kSums = St::template sums<MT>;
-  constexpr int kGroups = St::kChunk / G;                            // of a row of a chunk
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int64_t unit = (int64_t)blockIdx.z * gridDim.y + blockIdx.y;
   int matrix = 0;
@@ -277,8 +336,11 @@ __global__ __launch_bounds__(64 * WK * WN, OCC) void k_linear(LinearArgs a) {
     record[n] = base + (size_t)(tile0 + n < s.tiles ? tile0 + n : s.tiles - 1) * s.record;
   struct Weights {
     uint4 d[U][NT];
-    Groups<S, NG, Z> g[U][NT];
+    Scales<S, NG> s[U][NT];
+    ZeroPoints<NG, Z> z[U][NT];
   };
+  // kBefore without zero points: bytes of the scales, which are not used, so that no load is conditional
+  const uint32_t zeros_at = s.has_zeros ? kGroupsAt + kTileN * NG * (uint32_t)sizeof(S) : kGroupsAt;
   auto load_weights = [&](Weights &w, int chunk) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -287,14 +349,15 @@ __global__ __launch_bounds__(64 * WK * WN, OCC) void k_linear(LinearArgs a) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         w.d[u][n] = *reinterpret_cast<const uint4 *>(record[n] + at + (uint32_t)(l * 16));
-        w.g[u][n] = *reinterpret_cast<const Groups<S, NG, Z> *>(record[n] + at + kGroupsAt +
-                                                                (uint32_t)(h * (int)sizeof(Groups<S, NG, Z>)));
+        w.s[u][n] = *reinterpret_cast<const Scales<S, NG> *>(record[n] + at + kGroupsAt +
+                                                             (uint32_t)(h * (int)sizeof(Scales<S, NG>)));
+        if constexpr (Z != kEight) w.z[u][n].load(record[n] + at + zeros_at, h, j);
       }
     }
   };
   typename M::frag fixed;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) fixed[i] = Z ? 1.f : -8.f;
+  for (int i = 0; i < 8; ++i) fixed[i] = Z == kEight ? -8.f : 1.f;
   for (int64_t r0 = first; r0 < last; r0 += 16 * MT) {
     const int n_rows = last - r0 < 16 * MT ? (int)(last - r0) : 16 * MT;
     const T *rows = (const T *)a.x + r0 * K;
@@ -310,26 +373,19 @@ __global__ __launch_bounds__(64 * WK * WN, OCC) void k_linear(LinearArgs a) {
     };
     auto put_piece = [&](int p, int r, const Eight<T> &e) {
       typename M::frag f[P];
-      row_parts<T>(e, f);
+      row_parts<T, Z == kBefore>(e, f);
 #pragma unroll
       for (int q = 0; q < P; ++q)
         *reinterpret_cast<typename M::frag *>(lds + (q * a.lds_rows + r) * St::kRow + 16 * (p % kPieces)) = f[q];
     };
-    float *xsum = reinterpret_cast<float *>(lds + P * a.lds_rows * St::kRow);   // behind the rows
     auto store_rows = [&](const Eight<T> (&x)[kEach], int chunk) {
 #pragma unroll
       for (int e = 0; e < kEach; ++e) {
         if (e * kThreads >= n_rows * kPieces) break;
         const int p = e * kThreads + tid, r = p / kPieces, k = chunk * St::kChunk + 8 * (p % kPieces);
         if (r < n_rows && (k + 8 <= K || k >= K)) put_piece(p, r, k < K ? x[e] : Eight<T>{});
-        if constexpr (kSums) {
-          static_assert(kPieces % (G / 8) == 0 && kThreads % kPieces == 0, "a group's pieces lie in neighbouring lanes");
-          const float sum = group_add(r < n_rows && k + 8 <= K ? sum_eight(x[e]) : 0.f, G / 8);
-          if (r < n_rows && p % (G / 8) == 0) xsum[p / (G / 8)] = Z ? sum : -8.f * sum;   // p / (G / 8) = r kGroups + ..
-        }
       }
       if ((chunk + 1) * St::kChunk > K && K % 8) {   // the piece that K ends inside: a thread per row
-        if constexpr (kSums) __syncthreads();
         for (int r = tid; r < n_rows; r += kThreads) {
           const int k = K / 8 * 8;
           Eight<T> e{};
@@ -338,9 +394,7 @@ __global__ __launch_bounds__(64 * WK * WN, OCC) void k_linear(LinearArgs a) {
             const T v = rows[(int64_t)r * K + (k + i < K ? k + i : k)];
             e.v[i] = k + i < K ? v : T(0.f);
           }
-          const int p = (k - chunk * St::kChunk) / 8;
-          put_piece(p, r, e);
-          if constexpr (kSums) xsum[r * kGroups + p / (G / 8)] += (Z ? 1.f : -8.f) * sum_eight(e);
+          put_piece((k - chunk * St::kChunk) / 8, r, e);
         }
       }
     };
@@ -349,12 +403,11 @@ __global__ __launch_bounds__(64 * WK * WN, OCC) void k_linear(LinearArgs a) {
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int n = 0; n < NT; ++n) acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-    int row_at[MT], sum_at[MT];   // lanes past the last row compute a copy of it, never stored
+    int row_at[MT];   // lanes past the last row compute a copy of it, never stored
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const int r = 16 * m + j;
       row_at[m] = (r < n_rows ? r : n_rows - 1) * St::kRow + ik * (U * kBlockK * 2) + 16 * h;
-      sum_at[m] = (r < n_rows ? r : n_rows - 1) * kGroups;
     }
     auto multiply = [&](const Weights &k) {
 #pragma unroll
@@ -368,11 +421,8 @@ __global__ __launch_bounds__(64 * WK * WN, OCC) void k_linear(LinearArgs a) {
           // xs = sum x over the group (or, without zero points, -8 sum x, which the products start from)
           f32x4 part[MT][NT], xs[MT];
 #pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const float v = kSums ? xsum[sum_at[m] + (ik * U + u) * NG + g] : 0.f;
-            xs[m] = f32x4{v, v, v, v};
-          }
-          if constexpr (!kSums) {
+          for (int m = 0; m < MT; ++m) xs[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+          if constexpr (Z != kBefore) {
 #pragma unroll
             for (int st = g * kSteps; st < (g + 1) * kSteps; ++st)
 #pragma unroll
@@ -380,16 +430,22 @@ __global__ __launch_bounds__(64 * WK * WN, OCC) void k_linear(LinearArgs a) {
 #pragma unroll
                 for (int p = 0; p < P; ++p) xs[m] = M::mul(fixed, row_frag(p, m, st), xs[m]);
           }
+          typename M::zero z[NT];
 #pragma unroll
-          for (int m = 0; m < MT; ++m)
+          for (int n = 0; n < NT; ++n) {
+            if constexpr (Z == kBefore) z[n] = s.has_zeros ? (typename M::zero)k.z[u][n].of(g) : (typename M::zero)8.f;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) part[m][n] = Z ? f32x4{0.f, 0.f, 0.f, 0.f} : xs[m];
+            for (int m = 0; m < MT; ++m) part[m][n] = Z == kEight ? xs[m] : f32x4{0.f, 0.f, 0.f, 0.f};
+          }
 #pragma unroll
           for (int st = g * kSteps; st < (g + 1) * kSteps; ++st) {
             typename M::frag w[NT];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-              w[n] = M::weights(st == 0 ? k.d[u][n].x : st == 1 ? k.d[u][n].y : st == 2 ? k.d[u][n].z : k.d[u][n].w);
+            for (int n = 0; n < NT; ++n) {
+              const uint32_t d = st == 0 ? k.d[u][n].x : st == 1 ? k.d[u][n].y : st == 2 ? k.d[u][n].z : k.d[u][n].w;
+              if constexpr (Z == kBefore) w[n] = M::weights(d, z[n]);
+              else w[n] = M::weights(d);
+            }
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -403,9 +459,9 @@ __global__ __launch_bounds__(64 * WK * WN, OCC) void k_linear(LinearArgs a) {
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float sv = (float)k.g[u][n].g[g].s[i];
-              if constexpr (Z) {
-                const float zv = (float)((k.g[u][n].g[g].z[0] >> (8 * i)) & 255u);
+              const float sv = (float)k.s[u][n].g[g].s[i];
+              if constexpr (Z == kAfter) {
+                const float zv = k.z[u][n].of(i, g);
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
                   acc[m][n][i] = fmaf(sv, fmaf(-zv, xs[m][i], part[m][n][i]), acc[m][n][i]);
@@ -417,7 +473,7 @@ __global__ __launch_bounds__(64 * WK * WN, OCC) void k_linear(LinearArgs a) {
         }
       }
     };
-    if (r0 != first) __syncthreads();   // the sums of the rows before have been read
+    if (r0 != first) __syncthreads();   // the rows before, or their sums, have been read
     f32x4 bias[NT];   // requested here; outputs past the end repeat the last one's, never stored
 #pragma unroll
     for (int n = 0; n < NT; ++n) bias[n] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -482,18 +538,17 @@ __global__ __launch_bounds__(64 * WK * WN, OCC) void k_linear(LinearArgs a) {
   }
 }
 
-template <class T, class S, int G, bool Z, int MT, int NT, int U, int WK, int WN, int OCC>
+template <class T, class S, int G, Zeros Z, int MT, int NT, int U, int WK, int WN, int OCC>
 int launch_linear(const char *who, LinearArgs a, void *stream) {
   using St = Stage<T, WK, U>;
-  constexpr size_t kSumBytes = St::template sums<MT> ? (size_t)16 * MT * (St::kChunk / G) * 4 : 0;
-  static_assert(St::bytes(16 * MT) + kSumBytes <= 160 * 1024, "the rows of a chunk fit a compute unit's LDS");
+  static_assert(St::bytes(16 * MT) <= 160 * 1024, "the rows of a chunk fit a compute unit's LDS");
   const int64_t blocks = (a.n_rows + 16 * MT - 1) / (16 * MT);
   a.direct = a.offsets && blocks <= 4;
   a.n_units = !a.offsets ? blocks : a.direct ? a.n_matrices : blocks + a.n_matrices;
   a.lds_rows = (int32_t)std::min<int64_t>(a.n_rows, 16 * MT);
   const int64_t y = a.n_units < 32768 ? a.n_units : 32768, z = (a.n_units + y - 1) / y;
   const dim3 grid((unsigned)((a.s.tiles + NT * WN - 1) / (NT * WN)), (unsigned)y, (unsigned)z);
-  const size_t lds = std::max(St::bytes(a.lds_rows) + kSumBytes, (size_t)WN * (WK - 1) * MT * NT * 1024);
+  const size_t lds = std::max(St::bytes(a.lds_rows), (size_t)WN * (WK - 1) * MT * NT * 1024);
   return launch(who, k_linear<T, S, G, Z, MT, NT, U, WK, WN, OCC>, grid, 64 * WK * WN, lds, stream, a);
 }
 
@@ -503,12 +558,6 @@ int with_group(int32_t group, F f) {
   if (group == 64) return f(std::integral_constant<int, 64>{});
   return f(std::integral_constant<int, 128>{});
 }
-
-template <class F>
-int with_flag(int32_t on, F f) {
-  return on ? f(std::true_type{}) : f(std::false_type{});
-}
-
 
 // How a product is cut: rows x outputs of a workgroup and how its waves share them, by the number of
 // workgroups that each cut gives.  The largest cut that still gives 512 (two per compute unit, so that one
@@ -521,13 +570,12 @@ int with_flag(int32_t on, F f) {
 //    256 rows, 1024 x 1024:  16 x  32 cut  5.7,  16 x  16  6.0
 //     16 rows, 4096 x 1024:  16 x  16 cut  4.3,  16 x  32  5.1
 // The 32 x 256 cut keeps four tiles' scales and weights: with groups of 64 it loses to 64 x 256 (1024 rows, 4096 x
-// 1024: 23.6 against 22.4; float32 rows, whose sums of x are stored, win: 41.5 against 43.5), with groups of 32
-// for every type (float32 55.5 against 44.6).
+// 1024: 23.6 against 22.4), with groups of 32 too.  Where q - z is formed, 64 x 256 wins by making it for twice the
+// rows (groups of 128, float32 outputs of bfloat16 rows: 22.6 against 26.8, of float32 rows 38.5 against 39.2).
 // Up to 16 rows of a large matrix (a decoding step) are bound by the weights' bytes and want about 8 waves on
 // every compute unit, each with two tiles in flight, of two blocks where they stay in registers: four or eight along
-// k.  1 row, 16384 x 4096: 10.9, as 16 x 16 cut 13.1; float32 rows 14.6, with two blocks more than 16.
-// 17 to 64 rows: 16 x 64 while that gives 512 (64 rows, 8192 x 2048: 9.8, 16 x 32 10.7; float32 rows 16.7, 16 x 32
-// more than 22).  Fewer: 8 waves along k for as many workgroups as compute units, 16 x 32 (64 rows, 2048 x 4096:
+// k.  1 row, 16384 x 4096: 10.9, as 16 x 16 cut 13.1; float32 rows 16.3, with one block 17.7.
+// 17 to 64 rows: 16 x 64 while that gives 512 (64 rows, 8192 x 2048: 9.8, 16 x 32 10.7).  Fewer: 8 waves along k for as many workgroups as compute units, 16 x 32 (64 rows, 2048 x 4096:
 // 8.9, 16 x 16 9.7) or, up to 128 of those, 16 x 16; each wave with two blocks of a long k (1 row, 4096 x 4096:
 // 5.3, one block 5.6; 8 rows, 2048 x 8192: 8.7 against 10.1).
 // Rows by expert: a cut of 32 rows is mostly empty below 8 rows per expert on average (64 rows, 64 experts of
@@ -535,20 +583,20 @@ int with_flag(int32_t on, F f) {
 // rows loses to 32 by the experts' uneven numbers of rows (4096 rows, 8 experts: 32.5 against 25.6).  32 x 256 wins
 // over 32 x 128 for two-byte rows, groups of 128, from 384 workgroups (8192 rows, 8 experts of 4096 x 4096: 445
 // against 474; 1024 rows, 32 experts of 2048 x 1024: 19.6 against 21.2; 8 experts, 288 workgroups: 17.8 against
-// 16.1; float32 rows, 4096 rows, 8 experts: 86 against 83).  Below 8
+// 16.1).  Below 8
 // rows per expert, 16 x 64 wins over 16 x 32 where that still gives every compute unit a workgroup (64 rows,
 // 64 experts of 2048 x 1024: 10.1 against 10.8; 8 experts of 2048 x 512: 6.9 against 6.4).  With groups of 32 two
 // tiles of two blocks do not stay in registers (400 rows, 64 experts: one block 25.3, two 28.3).
 // OCC: more waves than a kind's registers allow spill.  Two-byte
 // rows: 4096 rows by 8 experts, 32 x 128 cut: 3 waves 13.7, 2 waves 16.7; 64 rows by 64 experts, 16 x 32 cut: 4
-// waves 11.5, 2 waves 12.7; but groups of 32, 64 rows, 4096 x 1024: 4 waves 7.4, 2 waves 5.9.  float32 rows, 32 x
-// 128 cut, 4096 rows by 8 experts of 2048 x 1024: groups of 64, 3 waves 86, 2 waves 109; groups of 128 84 and 83.
-template <class T, class S, int G, bool Z>
+// waves 11.5, 2 waves 12.7; but groups of 32, 64 rows, 4096 x 1024: 4 waves 7.4, 2 waves 5.9.
+template <class T, class S, int G, Zeros Z>
 int linear_cut(const char *who, LinearArgs a, void *stream) {
   constexpr bool kShort = sizeof(T) == 2;
   constexpr int kWaves32 = kShort || G <= 64 ? 3 : 2, kWaves16 = kShort && G >= 64 ? 4 : 2;
   constexpr bool kFew = kShort && G >= 64;                   // two tiles of two blocks stay in registers
-  constexpr bool kWide = G == 128 || (!kShort && G == 64);   // 32 x 256 rather than 64 x 256
+  constexpr bool kTwo = G >= 64;                             // and do with 2 waves per SIMD
+  constexpr bool kWide = Z != kBefore && G == 128;           // 32 x 256 rather than 64 x 256
   const int64_t rows = a.n_rows, tiles = a.s.tiles, blocks = a.s.blocks;
   auto groups = [&](int64_t r, int64_t t) { return ((rows + r - 1) / r) * ((tiles + t - 1) / t); };
   auto cut_16_64 = [&] { return launch_linear<T, S, G, Z, 1, 2, kFew || G == 128 ? 2 : 1, 2, 2, kFew ? 3 : 2>(who, a, stream); };
@@ -556,7 +604,7 @@ int linear_cut(const char *who, LinearArgs a, void *stream) {
   if (a.offsets) {
     const int64_t some = std::min<int64_t>(a.n_matrices, rows) / 2;   // half-filled blocks, about
     const bool full = rows >= 8 * (int64_t)a.n_matrices;
-    if constexpr (kShort && G == 128)
+    if constexpr (kWide)
       if (full && (rows / 32 + some) * ((tiles + 15) / 16) >= 384)
         return launch_linear<T, S, G, Z, 2, 4, 1, 1, 4, 2>(who, a, stream);
     if (full && (rows / 32 + some) * ((tiles + 7) / 8) >= 256)
@@ -572,7 +620,7 @@ int linear_cut(const char *who, LinearArgs a, void *stream) {
   if (groups(32, 8) >= 512) return launch_linear<T, S, G, Z, 2, 2, 1, 1, 4, kWaves32>(who, a, stream);
   if (groups(32, 4) >= 512) return launch_linear<T, S, G, Z, 2, 2, 1, 2, 2, 2>(who, a, stream);
   if (rows <= 16 && groups(16, 2) >= 512 && blocks >= 8)
-    return launch_linear<T, S, G, Z, 1, 2, kFew ? 2 : 1, 4, 1, 2>(who, a, stream);
+    return launch_linear<T, S, G, Z, 1, 2, kTwo ? 2 : 1, 4, 1, 2>(who, a, stream);
   if (groups(16, 4) >= 512) return cut_16_64();
   if (blocks < 8 || groups(16, 2) > (rows <= 16 ? 511 : 256)) return cut_16_32();
   if (groups(16, 2) > 128) {
@@ -589,9 +637,12 @@ template <class T>
 int linear_rows(const char *who, LinearArgs a, int32_t scale_type, void *stream) {
   return with_type(scale_type, [&](auto ts) {
     return with_group(a.s.group, [&](auto g) {
-      return with_flag(a.s.has_zeros, [&](auto z) {
-        return linear_cut<T, decltype(ts), decltype(g)::value, decltype(z)::value>(who, a, stream);
-      });
+      using S = decltype(ts);
+      constexpr int G = decltype(g)::value;
+      if constexpr (sizeof(T) == 2)
+        if (!a.out_f32)
+          return a.s.has_zeros ? linear_cut<T, S, G, kAfter>(who, a, stream) : linear_cut<T, S, G, kEight>(who, a, stream);
+      return linear_cut<T, S, G, kBefore>(who, a, stream);
     });
   });
 }

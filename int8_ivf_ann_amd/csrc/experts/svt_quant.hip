@@ -40,19 +40,19 @@ __global__ __launch_bounds__(kPackThreads) void k_pack_q(QuantShape s, int64_t n
   }
 }
 
-template <class T>
-__global__ __launch_bounds__(kPackThreads) void k_pack_groups(QuantShape s, int64_t n_values, int src_groups, int at,
+// scales (at kGroupsAt) or, ZEROS, zero points (at zeros_at)
+template <class T, bool ZEROS>
+__global__ __launch_bounds__(kPackThreads) void k_pack_groups(QuantShape s, int64_t n_values, int src_groups,
                                                               const T *src, uint8_t *packed) {
   const int ng = kBlockK / s.group;
   const int64_t per_matrix = (int64_t)s.tiles * s.blocks * kTileN * ng;
   for (int64_t p = (int64_t)blockIdx.x * kPackThreads + threadIdx.x; p < n_values; p += (int64_t)gridDim.x * kPackThreads) {
     const int64_t m = p / per_matrix, r = p % per_matrix, bt = r / (kTileN * ng);
-    const int in = (int)(r % (kTileN * ng));   // (h * ng + g) * 4 + i
-    const int g = (int)(bt / s.tiles) * ng + in / 4 % ng;
-    const int n = (int)(bt % s.tiles) * kTileN + in / (4 * ng) * 4 + in % 4;
+    const int in = (int)(r % (kTileN * ng));   // zero points: output * ng + g; scales: (h * ng + g) * 4 + i
+    const int gi = ZEROS ? in % ng : in / 4 % ng, o = ZEROS ? in / ng : in / (4 * ng) * 4 + in % 4;
+    const int g = (int)(bt / s.tiles) * ng + gi, n = (int)(bt % s.tiles) * kTileN + o;
     const T v = (n < s.n_out && g < src_groups) ? src[(m * s.n_out + n) * src_groups + g] : T(0);
-    // entry in / 4, value in % 4 of its scales (at 0) or zero points (behind the scales)
-    reinterpret_cast<T *>(packed + m * s.stride + bt * s.record + kGroupsAt + in / 4 * s.four + at)[in % 4] = v;
+    reinterpret_cast<T *>(packed + m * s.stride + bt * s.record + (ZEROS ? s.zeros_at : kGroupsAt))[in] = v;
   }
 }
 
@@ -108,12 +108,14 @@ extern "C" int svt_quant_pack(const svt_quant_weights *w, const uint8_t *nibbles
   const int64_t pieces = (int64_t)w->n_matrices * s.tiles * s.blocks * 64;
   int done = launch(who, k_pack_q, grid(pieces), kPackThreads, 0, hip_stream, s, pieces, nibbles, (uint8_t *)w->packed);
   const int64_t values = (int64_t)w->n_matrices * s.tiles * s.blocks * kTileN * (kBlockK / s.group);
-  auto groups = [&](auto *src, int at) {
-    return launch(who, k_pack_groups<std::remove_const_t<std::remove_pointer_t<decltype(src)>>>, grid(values),
-                  kPackThreads, 0, hip_stream, s, values, src_groups, at, src, (uint8_t *)w->packed);
+  auto groups = [&](auto *src, auto zero_points) {
+    using S = std::remove_const_t<std::remove_pointer_t<decltype(src)>>;
+    return launch(who, k_pack_groups<S, decltype(zero_points)::value>, grid(values), kPackThreads, 0, hip_stream, s,
+                  values, src_groups, src, (uint8_t *)w->packed);
   };
-  if (done == SVT_OK) done = b == 4 ? groups((const uint32_t *)scales, 0) : groups((const uint16_t *)scales, 0);
-  if (done == SVT_OK && w->has_zeros) done = groups(zeros, 4 * b);
+  if (done == SVT_OK)
+    done = b == 4 ? groups((const uint32_t *)scales, std::false_type{}) : groups((const uint16_t *)scales, std::false_type{});
+  if (done == SVT_OK && w->has_zeros) done = groups(zeros, std::true_type{});
   return done;
 }
 

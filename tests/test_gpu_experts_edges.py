@@ -116,3 +116,61 @@ def test_combine_backward_of_wide_rows(svt, D, kind):
             a, b = dy[t].double(), rows[int(pos[t, j])].double()
             near(np.float64(dw[t, j].item()), float(a @ b), bound * float(a.abs() @ b.abs()), f"d_weights {t} {j}")
             assert torch.equal(dr[int(pos[t, j])], (w[t, j] * dy[t].float()).to(ty(kind)))
+
+
+# ---- 4-bit products with float32 outputs ---------------------------------------------------------------
+
+def pack(svt, q, s, z, K, G, scale_kind="f32"):
+    q = np.pad(q, ((0, 0), (0, 0), (0, K % 2)))
+    return svt.svt_quant_pack(dev(q[..., 0::2] | (q[..., 1::2] << 4)), dev(s, ty(scale_kind)), None if z is None else dev(z),
+                              K, G)
+
+
+# rows, outputs, inputs, group; rows of each expert instead of one number: products by expert
+PRECISE = [(1, 300, 1030, 128), (16, 2048, 4096, 64), (16, 16400, 1100, 128), (40, 2100, 1030, 32), (9, 700, 1500, 128),
+           (64, 8200, 260, 64), (520, 4100, 261, 128), (1030, 4100, 260, 64), (1030, 4100, 130, 32),
+           ([200, 90, 33, 0, 250, 1, 140, 61], 4100, 261, 128), ([3] * 30 + [0, 50], 1500, 389, 64), ([1, 0, 2, 5], 40, 1030, 32)]
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("R, N, K, G", PRECISE)
+def test_float32_outputs_lose_nothing_to_zero_points(svt, R, N, K, G, zeros, kind):
+    """Rows behind a relu (no negative value) times weights most of which are 0, that is q at its zero point: errors
+    stay in proportion to sum |s| |x| |q - z|, and outputs whose weights are all 0 are the bias itself.  n = parts G +
+    groups + 12 roundings of independent sign: 4 sqrt(n) u, as for every product; q - z itself is exact."""
+    say("precise", R, N, K, G, zeros, kind)
+    counts = R if isinstance(R, list) else [R]
+    M, off = len(counts), np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    rng = np.random.default_rng(N + K + G)
+    groups = -(-K // G)
+    z = rng.integers(0, 16, (M, N, groups)).astype(np.uint8) if zeros else None
+    zk = np.repeat(np.full((M, N, groups), 8, np.uint8) if z is None else z, G, 2)[:, :, :K]
+    q = np.where(rng.random((M, N, K)) < 1 / 128, rng.integers(0, 16, (M, N, K)), zk).astype(np.uint8)
+    q[:, ::7] = zk[:, ::7]
+    s = rng.normal(size=(M, N, groups)).astype(np.float32)
+    x = dev(np.maximum(rng.normal(size=(off[-1], K)) + 0.5, 0), ty(kind))
+    bias = rng.normal(size=(M, N)).astype(np.float32)
+    y = host(svt.svt_quant_linear(x, pack(svt, q, s, z, K, G), offsets=dev(off) if M > 1 else None, bias=dev(bias),
+                                  out_dtype=ty("f32")))
+    hx, n = host(x), (3 if kind == "f32" else 1) * G + groups + 12
+    for e in range(M):
+        rows, w = hx[off[e]:off[e + 1]], np.repeat(s[e].astype(np.float64), G, 1)[:, :K] * (q[e].astype(np.float64) - zk[e])
+        want, mag = rows @ w.T + bias[e], np.abs(rows) @ np.abs(w).T + np.abs(bias[e])
+        near(y[off[e]:off[e + 1]], want, 4 * np.sqrt(n) * U * mag + U * np.abs(want), f"expert {e}")
+        assert np.all(y[off[e]:off[e + 1], ::7] == bias[e, ::7])
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("G", [32, 64, 128])
+def test_any_zero_point_is_exact(svt, G, kind):
+    """Zero points are whole bytes: rows of the identity return s (q - z), rounded once, up to z = 255."""
+    rng = np.random.default_rng(G + 1)
+    K, N = 260, 48
+    groups = -(-K // G)
+    q = rng.integers(0, 16, (1, N, K)).astype(np.uint8)
+    z = rng.choice([0, 1, 15, 16, 127, 128, 200, 254, 255], (1, N, groups)).astype(np.uint8)
+    s = rng.normal(size=(1, N, groups)).astype(np.float32)
+    y = svt.svt_quant_linear(dev(np.eye(K), ty(kind)), pack(svt, q, s, z, K, G), out_dtype=ty("f32"))
+    want = np.repeat(s[0], G, 1)[:, :K] * (q[0].astype(np.float32) - np.repeat(z[0], G, 1)[:, :K].astype(np.float32))
+    assert np.array_equal(host(y).astype(np.float32), want.T)
