@@ -429,7 +429,9 @@ def svt_rerank(handle, queries, cand_ids, net, k_out: int, query_scales=None, ou
 
 # ------------------------------------------------------------------------------------------------
 # Routed experts: the calls of include/svt.h on torch tensors.  Inputs and outputs are dense tensors on one
-# device; outputs not passed in are allocated on the call's stream.  Gradients are calls of their own.
+# device; outputs not passed in are allocated on the call's stream.  Gradients are calls of their own: no call
+# records history, so a tensor that requires grad is refused where torch would record it (grad mode on).
+# Call under torch.no_grad(), from a torch.autograd.Function, or on detached tensors.
 _TYPES = None
 
 
@@ -484,6 +486,13 @@ class _Run:
             self.ctx.__exit__(*exc)
 
 
+def _check_history(name):
+    import torch
+    if torch.is_grad_enabled():
+        raise ValueError(f"{name}: requires grad, but the call records no history (use torch.no_grad(), an autograd "
+                         "function or detach(); gradients are the _backward calls)")
+
+
 def _rows_of(name, t, dims=2):
     """(shape, element type, device) of a dense float tensor of ``dims`` dimensions on a device."""
     if not hasattr(t, "data_ptr") or t.dim() != dims:
@@ -491,6 +500,8 @@ def _rows_of(name, t, dims=2):
     code = _types().get(t.dtype)
     if code is None:
         raise ValueError(f"{name}: dtype {t.dtype} not in {[str(d) for d in _types()]}")
+    if t.requires_grad:
+        _check_history(name)
     if not t.is_contiguous():
         raise ValueError(f"{name}: not contiguous")
     if not t.is_cuda:
@@ -503,6 +514,8 @@ def _rows_of(name, t, dims=2):
 
 def _check_dense(name, t, dtype, shape, dev):
     """_check_tensor for one dtype, without its formatting on the way to success."""
+    if getattr(t, "requires_grad", False):
+        _check_history(name)
     if t is not None and getattr(t, "dtype", None) is dtype and t.shape == shape and t.is_contiguous() and \
             t.is_cuda and t.device == dev:
         return

@@ -174,3 +174,68 @@ def test_any_zero_point_is_exact(svt, G, kind):
     y = svt.svt_quant_linear(dev(np.eye(K), ty(kind)), pack(svt, q, s, z, K, G), out_dtype=ty("f32"))
     want = np.repeat(s[0], G, 1)[:, :K] * (q[0].astype(np.float32) - np.repeat(z[0], G, 1)[:, :K].astype(np.float32))
     assert np.array_equal(host(y).astype(np.float32), want.T)
+
+
+# ---- tensors that require grad -------------------------------------------------------------------------
+
+def test_history_is_refused_or_not_wanted(svt):
+    """Every floating argument that requires grad is refused in grad mode, outputs too; under no_grad it is not."""
+    import torch
+    rng = np.random.default_rng(0)
+    T, E, K, D = 5, 8, 2, 64
+    x, l, dy = [dev(rng.normal(size=s).astype(np.float32)) for s in ((T, D), (T, E), (T, D))]
+    ids, w = svt.svt_route(l, K)
+    off, order, pos = svt.svt_expert_sort(ids, E)
+    rows = svt.svt_expert_dispatch(x, pos)
+    bias, s = dev(np.zeros((E, 16), np.float32)), dev(np.ones((E, 16, 2), np.float32))
+    nib = dev(rng.integers(0, 256, (E, 16, 32)).astype(np.uint8))
+    packed = svt.svt_quant_pack(nib, s, None, D, 32)
+    calls = [(l, lambda g: svt.svt_route(g, K)), (l, lambda g: svt.svt_route_backward(g, ids, w, w)),
+             (w, lambda g: svt.svt_route(l, K, out_weights=g)),
+             (w, lambda g: svt.svt_route_backward(l, ids, g, w)), (w, lambda g: svt.svt_route_backward(l, ids, w, g)),
+             (x, lambda g: svt.svt_expert_dispatch(g, pos)), (rows, lambda g: svt.svt_expert_dispatch(x, pos, out=g)),
+             (rows, lambda g: svt.svt_expert_dispatch_backward(g, pos)), (rows, lambda g: svt.svt_expert_combine(g, pos, w)),
+             (w, lambda g: svt.svt_expert_combine(rows, pos, g)),
+             (dy, lambda g: svt.svt_expert_combine_backward(g, rows, pos, w)),
+             (rows, lambda g: svt.svt_expert_combine_backward(dy, g, pos, w)),
+             (w, lambda g: svt.svt_expert_combine_backward(dy, rows, pos, g)),
+             (s, lambda g: svt.svt_quant_pack(nib, g, None, D, 32)),
+             (rows, lambda g: svt.svt_quant_linear(g, packed, offsets=off)),
+             (bias, lambda g: svt.svt_quant_linear(rows, packed, offsets=off, bias=g))]
+    for t, call in calls:
+        g = t.clone().requires_grad_()
+        with pytest.raises(ValueError, match="requires grad"):
+            call(g)
+        with torch.no_grad():
+            call(g)
+
+
+def test_combine_in_an_autograd_function(svt):
+    """As a training program uses the calls: inside an autograd function, where torch records nothing."""
+    import torch
+
+    class Combine(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, rows, pos, w):
+            ctx.save_for_backward(rows, pos, w)
+            return svt.svt_expert_combine(rows, pos, w)
+
+        @staticmethod
+        def backward(ctx, dy):
+            rows, pos, w = ctx.saved_tensors
+            dr, dw = svt.svt_expert_combine_backward(dy.contiguous(), rows, pos, w)
+            return dr, None, dw
+
+    rng = np.random.default_rng(1)
+    rows = dev(rng.normal(size=(6, 10)).astype(np.float32)).requires_grad_()
+    w = dev(rng.normal(size=(3, 2)).astype(np.float32)).requires_grad_()
+    pos = dev(np.array([[5, 0], [1, 2], [4, 3]], np.int32))
+    dy = dev(rng.normal(size=(3, 10)).astype(np.float32))
+    Combine.apply(rows, pos, w).backward(dy)
+    want_rows, want_w = torch.zeros(6, 10, device="cuda"), torch.zeros(3, 2, device="cuda")
+    for t in range(3):
+        for j in range(2):
+            want_rows[int(pos[t, j])] = w.detach()[t, j] * dy[t]
+            want_w[t, j] = (dy[t].double() * rows.detach()[int(pos[t, j])].double()).sum()
+    assert torch.equal(rows.grad, want_rows)
+    near(host(w.grad), host(want_w), 17 * U * 10 * 16, "d_weights")   # 10 products of values below 4
