@@ -564,9 +564,10 @@ def svt_route_backward(logits, experts, weights, d_weights, renormalise: bool = 
     the weights' gradient d_weights (float32 [T, top]) -> d_logits [T, E] of the logits' dtype."""
     import torch
     (T, E), code, dev = _rows_of("logits", logits)
-    n, K, _ = _entries("experts", experts, dev)
-    if n != T:
-        raise ValueError(f"experts: shape {tuple(experts.shape)} for {T} tokens")
+    if not hasattr(experts, "data_ptr") or experts.dim() != 2:
+        raise ValueError("experts: expected a 2-D tensor [n_tokens, top]")
+    K = experts.shape[1]
+    _check_dense("experts", experts, torch.int32, (T, K), dev)
     _check_dense("weights", weights, torch.float32, (T, K), dev)
     _check_dense("d_weights", d_weights, torch.float32, (T, K), dev)
     with _Run(dev, stream) as s:
