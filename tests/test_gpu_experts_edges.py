@@ -239,3 +239,66 @@ def test_combine_in_an_autograd_function(svt):
             want_w[t, j] = (dy[t].double() * rows.detach()[int(pos[t, j])].double()).sum()
     assert torch.equal(rows.grad, want_rows)
     near(host(w.grad), host(want_w), 17 * U * 10 * 16, "d_weights")   # 10 products of values below 4
+
+
+# ---- ends of the ranges that nothing else reaches --------------------------------------------------------
+
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+def test_route_backward_of_infinite_logits(svt, renorm, kind):
+    """One and two logits of +inf: the gradient of a finite peak (the oracle's), no NaN."""
+    l = np.zeros((3, 10))
+    l[0, 3], l[1, [2, 7]], l[2, [0, 9]] = np.inf, np.inf, (np.inf, 5.0)
+    l[2, 4] = -np.inf
+    lt = dev(l, ty(kind))
+    ids, w = svt.svt_route(lt, 4, renormalise=renorm)
+    rid, rw, _ = X.route(l, 4, renorm)
+    assert np.array_equal(host(ids), rid) and np.array_equal(host(w), rw)   # 0, 1/2 and 1
+    dw = np.random.default_rng(3).normal(size=(3, 4)).astype(np.float32)
+    d = svt.svt_route_backward(lt, ids, w, dev(dw), renormalise=renorm)
+    rd, mag, _ = X.route_backward(l, rid, rw, dw.astype(np.float64), renorm)
+    near(host(d), rd, U * mag * 51 + HALF[kind] * np.abs(rd) + TINY[kind], "d_logits")
+
+
+def test_exchange_more_tokens_than_one_grid(svt):
+    """4.3 M tokens of 33 bfloat16 (2-byte pieces, a wave per token): workgroups go round a second time from token
+    4194304 on.  One choice per token, so every result but d_weights is one product, rounded once in float32 and
+    once to the type; a d_weight is 33 products in 64 lanes: one product, two sums of one, 6 levels."""
+    import torch
+    T, D = 4300003, 33
+    g = torch.Generator(device="cuda").manual_seed(1)
+    pos = torch.randperm(T, generator=g, device="cuda").to(torch.int32)[:, None].contiguous()
+    at = pos[:, 0].long()
+    x = torch.randn((T, D), generator=g, device="cuda").bfloat16()
+    rows = svt.svt_expert_dispatch(x, pos)
+    assert torch.equal(rows[at], x)
+    assert torch.equal(svt.svt_expert_dispatch_backward(rows, pos), x)
+    w = torch.randn((T, 1), generator=g, device="cuda")
+    assert torch.equal(svt.svt_expert_combine(rows, pos, w), (w * x.float()).bfloat16())
+    dy = torch.randn((T, D), generator=g, device="cuda").bfloat16()
+    dr, dw = svt.svt_expert_combine_backward(dy, rows, pos, w)
+    assert torch.equal(dr[at], (w * dy.float()).bfloat16())
+    want = (dy.double() * x.double()).sum(1, keepdim=True)
+    mag = (dy.double() * x.double()).abs().sum(1, keepdim=True)
+    assert bool(((dw.double() - want).abs() <= 9 * U * mag).all())
+
+
+@pytest.mark.parametrize("kind, least", [("bf16", -133), ("f16", -24), ("f32", -133)])
+@pytest.mark.parametrize("R, N", [(1, 40), (40, 48), (200, 4200)])
+def test_linear_subnormal_rows(svt, R, N, kind, least):
+    """Rows of the types' smallest values, subnormals among them, one value per row: whole multiples of 2^least times q
+    - 8, exactly.  (float32 rows: digits below 2^-133 are not used.)"""
+    rng = np.random.default_rng(R)
+    K = 70
+    q = rng.integers(0, 16, (1, N, K)).astype(np.uint8)
+    x, at = np.zeros((R, K)), rng.integers(0, K, R)
+    whole = rng.integers(1, 2 ** (20 if kind == "f32" else 8), R)
+    x[np.arange(R), at] = rng.choice([-1, 1], R) * whole * 2.0 ** least
+    xt = dev(x, ty(kind))
+    assert np.array_equal(host(xt), x)
+    y = svt.svt_quant_linear(xt, pack(svt, q, np.ones((1, N, 3), np.float32), None, K, 32), out_dtype=ty("f32"))
+    near(host(y), x @ (q[0].astype(np.float64) - 8).T, 0.0, "subnormal")
+    if kind == "f32":   # what lies below the used digits adds less than one of them
+        fine = (x + np.where(x != 0, np.sign(x) * 2.0 ** -134, 0)).astype(np.float32)
+        y = svt.svt_quant_linear(dev(fine), pack(svt, q, np.ones((1, N, 3), np.float32), None, K, 32))
+        near(host(y), fine.astype(np.float64) @ (q[0].astype(np.float64) - 8).T, 8 * 2.0 ** -133, "subnormal")
