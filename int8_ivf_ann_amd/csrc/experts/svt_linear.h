@@ -10,14 +10,14 @@
 // float32 group sums.  Two forms:
 //   q - z   (outputs of float32) is formed before the instruction, so that the sums' roundings are in proportion to
 //           sum |x| |q - z|, as those of the product itself: a weight of 0 adds exactly 0.
-//   q       (outputs of two bytes, whose own rounding is 2^7 (float16) or 2^10 (bfloat16) times the 2.5e-6 below), and z
-//           sum x from the group's sum, which the same instruction gives with a matrix of ones; where every zero point is 8, a matrix
-//           of -8 gives what the products then start from.  Its roundings are in proportion to sum |x| (q + z).  Forming
-//           q - z takes 12 more instructions for 8 weights (bf16), 4 (f16).
+//   q       (outputs of two bytes, whose own rounding is 2^7 (float16) or 2^10 (bfloat16) times the 2.5e-6 below) and
+//           z sum x from the group's sum, which the same instruction gives with a matrix of ones; where every zero
+//           point is 8, a matrix of -8 gives what the products then start from.  Its roundings are in proportion to
+//           sum |x| (q + z).  Forming q - z takes 12 more instructions for 8 weights (bf16), 4 (f16).
 // 13 rows, 1024 inputs, groups of 128 with zero points, rows behind a relu: the relative error of float32 rows is 1.2e-7
 // with q - z formed before, 2.5e-6 after (a float32 product 1.9e-7).  In us, before and after: 1 row of 16384 x 4096,
-// float32 16.3 and 14.6, bfloat16 13.4 and 10.7, float16 11.9 and 10.9; 1024 rows of 4096 x 1024, 38.5 and 35.9, 22.6 and
-// 19.8, 20.9 and 20.0.
+// float32 rows 16.3 and 14.6, bfloat16 rows with float32 outputs 13.4 and 10.7, float16 rows likewise 11.9 and 10.9;
+// 1024 rows of 4096 x 1024, 38.0 and 35.9, 22.6 and 19.8, 20.9 and 20.0.
 // q reaches bf16/f16 two at a time: the byte 0000qqqq read as an 8-bit float with 3 mantissa bits is
 // q * 2^-9 (its subnormals and its first binade share one spacing), and v_cvt_scalef32_pk_* turns two such
 // bytes into two exact numbers with the scale 2^9.
@@ -559,37 +559,45 @@ int with_group(int32_t group, F f) {
   return f(std::integral_constant<int, 128>{});
 }
 
-// How a product is cut: rows x outputs of a workgroup and how its waves share them, by the number of
-// workgroups that each cut gives.  The largest cut that still gives 512 (two per compute unit, so that one
-// loads while the other multiplies; the 8 waves of the 64 x 256 cut do with 256) is taken.  bfloat16, groups
-// of 128, us, the chosen cut against its neighbour:
-//   4096 rows, 4096 x 4096:  32 x 256 cut 213,  64 x 256  266,  32 x 128 241
-//   1024 rows, 4096 x 1024:  32 x 256 cut 18.8, 64 x 256 21.0,  32 x 128 22.8
-//    512 rows, 4096 x 1024:  32 x 128 cut 11.8, 32 x 256 13.8
-//   1024 rows, 1024 x 1024:  32 x  64 cut  9.4,  32 x 128 11.2
-//    256 rows, 1024 x 1024:  16 x  32 cut  5.7,  16 x  16  6.0
-//     16 rows, 4096 x 1024:  16 x  16 cut  4.3,  16 x  32  5.1
-// The 32 x 256 cut keeps four tiles' scales and weights: with groups of 64 it loses to 64 x 256 (1024 rows, 4096 x
-// 1024: 23.6 against 22.4), with groups of 32 too.  Where q - z is formed, 64 x 256 wins by making it for twice the
-// rows (groups of 128, float32 outputs of bfloat16 rows: 22.6 against 26.8, of float32 rows 38.5 against 39.2).
-// Up to 16 rows of a large matrix (a decoding step) are bound by the weights' bytes and want about 8 waves on
-// every compute unit, each with two tiles in flight, of two blocks where they stay in registers: four or eight along
-// k.  1 row, 16384 x 4096: 10.9, as 16 x 16 cut 13.1; float32 rows 16.3, with one block 17.7.
-// 17 to 64 rows: 16 x 64 while that gives 512 (64 rows, 8192 x 2048: 9.8, 16 x 32 10.7).  Fewer: 8 waves along k for as many workgroups as compute units, 16 x 32 (64 rows, 2048 x 4096:
-// 8.9, 16 x 16 9.7) or, up to 128 of those, 16 x 16; each wave with two blocks of a long k (1 row, 4096 x 4096:
-// 5.3, one block 5.6; 8 rows, 2048 x 8192: 8.7 against 10.1).
-// Rows by expert: a cut of 32 rows is mostly empty below 8 rows per expert on average (64 rows, 64 experts of
-// 2048 x 1024: 16 x 32 cut 11.0, 32 x 128 13.0; 1024 rows: 32 x 128 26.2, 16 x 32 more than 32), and one of 64
-// rows loses to 32 by the experts' uneven numbers of rows (4096 rows, 8 experts: 32.5 against 25.6).  32 x 256 wins
-// over 32 x 128 for two-byte rows, groups of 128, from 384 workgroups (8192 rows, 8 experts of 4096 x 4096: 445
-// against 474; 1024 rows, 32 experts of 2048 x 1024: 19.6 against 21.2; 8 experts, 288 workgroups: 17.8 against
-// 16.1).  Below 8
-// rows per expert, 16 x 64 wins over 16 x 32 where that still gives every compute unit a workgroup (64 rows,
-// 64 experts of 2048 x 1024: 10.1 against 10.8; 8 experts of 2048 x 512: 6.9 against 6.4).  With groups of 32 two
-// tiles of two blocks do not stay in registers (400 rows, 64 experts: one block 25.3, two 28.3).
-// OCC: more waves than a kind's registers allow spill.  Two-byte
-// rows: 4096 rows by 8 experts, 32 x 128 cut: 3 waves 13.7, 2 waves 16.7; 64 rows by 64 experts, 16 x 32 cut: 4
-// waves 11.5, 2 waves 12.7; but groups of 32, 64 rows, 4096 x 1024: 4 waves 7.4, 2 waves 5.9.
+// How a product is cut: rows x outputs of a workgroup and how its waves share them, by the number of workgroups that
+// each cut gives.  The largest cut that still gives 512 (two per compute unit, so that one loads while the other
+// multiplies; the 8 waves of the 64 x 256 cut do with 256) is taken.  All figures are us in a replayed graph over
+// rotating inputs; bfloat16 rows, scales and outputs, groups of 128, no zero points, unless stated; the chosen cut
+// first.
+//   4096 rows, 4096 x 4096:  32 x 256 cut 199,  32 x 128 235,   64 x 256 255
+//   1024 rows, 4096 x 1024:  32 x 256 cut 18.0, 64 x 256 19.9,  32 x 128 21.8
+//    512 rows, 4096 x 1024:  32 x 128 cut 11.7, 32 x 256 13.6
+//   1024 rows, 1024 x 1024:  32 x  64 cut  9.4, 32 x 128 11.3
+//    256 rows, 1024 x 1024:  16 x  32 cut  5.8, 32 x  64  8.0,  16 x  16  8.2
+//     16 rows, 4096 x 1024:  16 x  16 cut  4.3, 16 x  32  4.9
+// The 32 x 256 cut keeps four tiles' scales and weights: with groups of 32 64 x 256 is ahead (1024 rows, 4096 x 1024:
+// 21.7 against 22.8), with groups of 64 the two are within 4 % (20.6 and 19.9).  Where q - z is formed, 64 x 256
+// makes it for twice the rows (the same product with float32 outputs: 22.2 against 26.6; of float32 rows 36.7 against
+// 37.9, with groups of 32 39.9 against 48.0).
+// Up to 16 rows of a large matrix (a decoding step) are bound by the weights' bytes and want about 8 waves on every
+// compute unit, each with two tiles in flight, of two blocks where they stay in registers: four or eight along k.
+//   1 row, 16384 x 4096: 16 x 32 cut of two blocks 10.7, of one 12.5, 16 x 64 13.2, 16 x 16 16.1; float32 rows 15.9, of
+//   one block 17.3.
+// 17 to 64 rows: 16 x 64 while that gives 512 (64 rows, 8192 x 2048: 9.9, 16 x 32 11.0).  Fewer: 8 waves along k for
+// as many workgroups as compute units, 16 x 32 (64 rows, 2048 x 4096: 9.0, 16 x 16 12.4; float32 rows 14.7, 22.0) or,
+// up to 128 of those, 16 x 16; each wave with two blocks of a long k (1 row, 4096 x 4096: 5.3, one block 5.6; 8 rows,
+// 2048 x 8192: 8.7, 10.0).
+// Rows by expert: a cut of 32 rows is mostly empty below 8 rows per expert on average (64 rows, 64 experts of 2048 x
+// 1024: 16 x 64 cut 10.2, 32 x 128 12.4; 1024 rows: 32 x 128 26.1, 16 x 64 28.2, 16 x 32 33.6), and one of 64 rows
+// loses to 32 by the experts' uneven numbers of rows (4096 rows, 8 experts: 42.4, 64 x 256 57.2).  32 x 256 wins over
+// 32 x 128 where enough workgroups are left: 8192 rows, 8 experts of 4096 x 4096 434 against 467; 32 experts of 2048
+// x 1024, 1024 rows (384 workgroups) 19.1 against 20.7; 8 experts, 1408 rows (384) 18.7 against 19.9, but 1024 rows
+// (288) 17.3 against 15.9: from 384 (4096 rows, 8 experts of 2048 x 1024, is an exception: 44.4 against 42.4).
+// Below 8 rows per expert 16 x 64 wins over 16 x 32 likewise: 8 experts of 2048 x 512, 64 rows (256 workgroups) 7.2
+// against 6.4, 80 rows (288) 5.5 against 5.6, 64 experts of 2048 x 1024, 64 rows 10.2 against 10.6: from 288.
+// Where two tiles of two blocks do not stay in registers, one block each: groups of 32, 400 rows, 64 experts 20.8
+// against 22.5; float32 rows, 256 rows, 64 experts 21.7 against 25.4.
+// OCC: the waves per SIMD that registers are limited for; 26 of the 612 kinds (mostly float scales with zero points)
+// spill 12 to 72 bytes per lane all the same.  32 x 128: three (4096 rows by 8 experts of 2048 x 1024, float32 rows,
+// groups of 64, 89 against 108 with two; bfloat16 with zero points, groups of 64, 51 against 62), for float32 rows
+// with groups of 128 two (85.1 against 86.8).  16 x 64: three (64 rows by 64 experts of 2048 x 1024, zero points,
+// groups of 64, 11.3 against 12.0), for float32 rows two (15.4 against 16.0).  16 x 32: four (64 rows by 64 experts of
+// 1024 x 1024, zero points, 8.3 against 8.6), with groups of 32 two (9.6 against 10.2).
 template <class T, class S, int G, Zeros Z>
 int linear_cut(const char *who, LinearArgs a, void *stream) {
   constexpr bool kShort = sizeof(T) == 2;
@@ -599,7 +607,7 @@ int linear_cut(const char *who, LinearArgs a, void *stream) {
   constexpr bool kWide = Z != kBefore && G == 128;           // 32 x 256 rather than 64 x 256
   const int64_t rows = a.n_rows, tiles = a.s.tiles, blocks = a.s.blocks;
   auto groups = [&](int64_t r, int64_t t) { return ((rows + r - 1) / r) * ((tiles + t - 1) / t); };
-  auto cut_16_64 = [&] { return launch_linear<T, S, G, Z, 1, 2, kFew || G == 128 ? 2 : 1, 2, 2, kFew ? 3 : 2>(who, a, stream); };
+  auto cut_16_64 = [&] { return launch_linear<T, S, G, Z, 1, 2, kFew ? 2 : 1, 2, 2, kFew ? 3 : 2>(who, a, stream); };
   auto cut_16_32 = [&] { return launch_linear<T, S, G, Z, 1, 1, 2, 2, 2, kWaves16>(who, a, stream); };
   if (a.offsets) {
     const int64_t some = std::min<int64_t>(a.n_matrices, rows) / 2;   // half-filled blocks, about
