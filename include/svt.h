@@ -391,7 +391,8 @@ int svt_expert_sort(int32_t n_tokens, int32_t top, int32_t n_experts, const int3
  *                       d_weights[t][j] = dy[t] . rows[position[t][j]], 0 for a dropped entry
  *   x, y, dx, dy   [n_tokens][width] of dtype, 1 <= width <= 2^24; a token whose entries are all dropped gets a row of zeros
  *   rows, d_rows   [n_tokens * top][width] of dtype; rows that no entry names are neither read nor written
- *   weights, d_weights  [n_tokens][top] float
+ *   weights, d_weights  [n_tokens][top] float; combine_backward takes weights that are not NULL (without weights the
+ *                  gradient in the rows is dispatch of dy)
  * n_tokens == 0 returns SVT_OK without enqueuing.  Errors: SVT_EINVAL, SVT_EDEVICE as svt_route.
  */
 int svt_expert_dispatch(int32_t n_tokens, int32_t top, int32_t width, int32_t dtype, const void *x,

@@ -9,9 +9,12 @@
 //   combine             y[t] = sum_j w[t][j] rows[position[t][j]]
 //   combine backward    d_rows[position[t][j]] = w[t][j] dy[t],  dw[t][j] = dy[t] . rows[position[t][j]]
 //
-// Every exchange kernel walks tokens: a token's own row is read or written once, in order, and its `top`
-// rows on the experts' side are whole rows, so each byte moves once and the only gather is of rows.  Sums
-// run over j in order in float32 and no two threads write one address, so results never vary.
+// Every exchange kernel walks tokens: a token's own row is read or written in order, its `top` rows on the experts'
+// side are whole rows, and the only gather is of rows.  Each byte moves once, but that combine's gradient, which
+// holds 4 rows of the experts at a time, reads dy ceil(top / 4) times (after the first from a cache: 16384 x 1024
+// bfloat16, top 8, 124 us for 570 MB, as fast as top 2's 136 for 671 MB).  Sums run over j in order in float32 and no
+// two threads write one address, so results never vary.  A token belongs to one wave at most, so that few tokens of
+// wide rows leave compute units idle: 1 token of 4096 bfloat16, top 8, 8 us each way and 11 for combine's gradient.
 
 #include <type_traits>
 
@@ -31,8 +34,9 @@ namespace {
 //   two          k_sort_count: a histogram per block; k_sort_place: each block sums the histograms (few blocks
 //                of many entries keep that table small), ranks its entries, orders them in LDS and writes
 //                each expert's run in one piece.
-// Measured: 256 entries 2.3 us, 4096 4.6, 8192 9.0 (two launches 9.2), 1 M entries of 64 experts 13.4 (12.6
-// MB).  All are chains of short steps between barriers; bytes would take 2.5 us at 1 M.
+// Measured: 256 entries of 32 experts 2.6 us, 4096 of 8 experts 5.1, 8192 7.8; 1 M entries of 64 experts 13.7 (12.6
+// MB; all of one expert, whose count is one LDS address: 16.1), of 512 experts 27.7 (half the blocks, so that the
+// table stays small).  All are chains of short steps between barriers; bytes would take 2.5 us at 1 M.
 
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64, kSortSteps = 4;
 constexpr int kTileEntries = kSortThreads * kSortSteps;   // entries of a workgroup at a time
@@ -266,8 +270,8 @@ int with_bits(int E, F f) {
 
 // ---- exchange ------------------------------------------------------------------------------------
 
-// Bound by memory (a copy runs at 5.1 TB/s).  65536 x 1024 bfloat16 rows, top 2: dispatch and combine together
-// 154 us (5.2 TB/s); 32768 tokens, top 4: both gradients 184 us (5.1 TB/s).
+// Bound by memory (a copy runs at 5.1 TB/s).  65536 x 1024 bfloat16 rows, top 2: sort, dispatch and combine together
+// 168 us, 14 of them the sort's (5.2 TB/s); 32768 tokens, top 4: both gradients 184 us (5.1 TB/s).
 
 constexpr int kExThreads = 256;
 constexpr int64_t kExMaxBlocks = 1 << 20;

@@ -11,13 +11,15 @@
 // a wave holds 64 / L tokens and a row of logits is read once into registers.  Each lane sorts its logits
 // (a network of 19 exchanges).  Up to 8 choices, the lanes then merge their lists pairwise: of two descending
 // lists the 8 best are max(a_i, b_{7-i}), put in order by 12 exchanges; log2 L merges, no branch.  Above 8,
-// `top` rounds take the group's best head by DPP moves, and the lane that held it moves up.  Logits become integers of the same order, so ties go to the
-// lowest expert in every type; with 16-bit logits one integer holds the logit and the expert.  Maximum, sums
-// and weights are float32.
+// `top` rounds take the group's best head by DPP moves, and the lane that held it moves up.  Logits become integers
+// of the same order, so ties go to the lowest expert in every type; with 16-bit logits one integer holds the logit
+// and the expert.  Maximum, sums and weights are float32.
 //
-// Measured: 65536 tokens, 64 experts, top 8, bfloat16: 7.6 us (rounds instead of merges 8.0), the gradient 8.7;
-// 12.6 and 23 MB, so 1.7 and 1.4 TB/s.  Both are bound by vector instructions: without the lists' sort and
-// merges the choice takes 5.9 us.
+// Measured, 65536 tokens, 64 experts, top 8, softmax over all experts: the choice 7.8 us for bfloat16, 7.7 for
+// float16, 12.7 for float32 (12.6 and 21 MB, so 1.6 TB/s), the gradient 9.6, 9.5 and 11.6 (23 and 40 MB); one after
+// the other, the logits still in a cache, 16.5 for bfloat16.  A wave loads, computes and stores once, and all waves
+// that fit the card run in step, so that the memory waits while they compute: without the lists' sort and merges the
+// choice still takes 5.9 us.  Rounds instead of merges: 8.0 against 7.6.
 
 #include <type_traits>
 
