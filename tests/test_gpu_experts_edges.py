@@ -176,6 +176,33 @@ def test_any_zero_point_is_exact(svt, G, kind):
     assert np.array_equal(host(y).astype(np.float32), want.T)
 
 
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("R, N, K, G", [(1, 40, 197, 64), (9, 70, 5, 32), (40, 2100, 1030, 128), (600, 4100, 203, 32)])
+def test_float32_outputs_of_rows_with_infinities(svt, R, N, K, G, zeros, kind):
+    """A row that holds an infinity or NaN gets NaN outputs in every form, wherever it lies (in a row's last, short piece
+    too); the largest finite values do not, and other rows keep their bits."""
+    say("infinities", R, N, K, G, zeros, kind)
+    rng = np.random.default_rng(R + K)
+    groups = -(-K // G)
+    q = rng.integers(0, 16, (1, N, K)).astype(np.uint8)
+    z = rng.integers(0, 256, (1, N, groups)).astype(np.uint8) if zeros else None
+    w = pack(svt, q, 0.125 * rng.normal(size=(1, N, groups)).astype(np.float32), z, K, G)
+    most = {"f32": 2.0 ** 100, "f16": 65504.0, "bf16": 2.0 ** 100}[kind]   # sums stay finite
+    x = rng.normal(size=(R, K))
+    x[::3, 0] = most
+    clean = host(svt.svt_quant_linear(dev(x, ty(kind)), w, out_dtype=ty("f32")))
+    assert np.all(np.isfinite(clean))
+    for value in (np.inf, -np.inf, np.nan):
+        for at in {0, K // 2, K - 1}:
+            bad = x.copy()
+            bad[R // 2, at] = value
+            y = host(svt.svt_quant_linear(dev(bad, ty(kind)), w, out_dtype=ty("f32")))
+            assert np.all(np.isnan(y[R // 2]))
+            others = np.arange(R) != R // 2
+            assert np.array_equal(y[others], clean[others])
+
+
 # ---- tensors that require grad -------------------------------------------------------------------------
 
 def test_history_is_refused_or_not_wanted(svt):
