@@ -16,7 +16,7 @@
 //           sum |x| (q + z).  Forming q - z takes 12 more instructions for 8 weights (bf16), 4 (f16).
 // 13 rows, 1024 inputs, groups of 128 with zero points, rows behind a relu: the relative error of float32 rows is 1.2e-7
 // with q - z formed before, 2.5e-6 after (a float32 product 1.9e-7).  In us, before and after: 1 row of 16384 x 4096,
-// float32 rows 16.3 and 14.6, bfloat16 rows with float32 outputs 13.4 and 10.7, float16 rows likewise 11.9 and 10.9;
+// float32 rows 18.1 and 14.8, bfloat16 rows with float32 outputs 13.4 and 10.7, float16 rows likewise 11.9 and 10.9;
 // 1024 rows of 4096 x 1024, 38.0 and 35.9, 22.6 and 19.8, 20.9 and 20.0.
 // q reaches bf16/f16 two at a time: the byte 0000qqqq read as an 8-bit float with 3 mantissa bits is
 // q * 2^-9 (its subnormals and its first binade share one spacing), and v_cvt_scalef32_pk_* turns two such
@@ -576,8 +576,8 @@ int with_group(int32_t group, F f) {
 // 37.9, with groups of 32 39.9 against 48.0).
 // Up to 16 rows of a large matrix (a decoding step) are bound by the weights' bytes and want about 8 waves on every
 // compute unit, each with two tiles in flight, of two blocks where they stay in registers: four or eight along k.
-//   1 row, 16384 x 4096: 16 x 32 cut of two blocks 10.7, of one 12.5, 16 x 64 13.2, 16 x 16 16.1; float32 rows 15.9, of
-//   one block 17.3.
+//   1 row, 16384 x 4096: 16 x 32 cut of two blocks 10.7, of one 12.5, 16 x 64 13.2, 16 x 16 16.1; float32 rows, one
+//   block, 18.1, 16 rows 26.4 (two blocks 16.6 and, as 16 rows' parts then fill most of LDS, 37.5).
 // 17 to 64 rows: 16 x 64 while that gives 512 (64 rows, 8192 x 2048: 9.9, 16 x 32 11.0).  Fewer: 8 waves along k for
 // as many workgroups as compute units, 16 x 32 (64 rows, 2048 x 4096: 9.0, 16 x 16 12.4; float32 rows 14.7, 22.0) or,
 // up to 128 of those, 16 x 16; each wave with two blocks of a long k (1 row, 4096 x 4096: 5.3, one block 5.6; 8 rows,
@@ -592,8 +592,8 @@ int with_group(int32_t group, F f) {
 // against 6.4, 80 rows (288) 5.5 against 5.6, 64 experts of 2048 x 1024, 64 rows 10.2 against 10.6: from 288.
 // Where two tiles of two blocks do not stay in registers, one block each: groups of 32, 400 rows, 64 experts 20.8
 // against 22.5; float32 rows, 256 rows, 64 experts 21.7 against 25.4.
-// OCC: the waves per SIMD that registers are limited for; 26 of the 612 kinds (mostly float scales with zero points)
-// spill 12 to 72 bytes per lane all the same.  32 x 128: three (4096 rows by 8 experts of 2048 x 1024, float32 rows,
+// OCC: the waves per SIMD that registers are limited for; 25 of the 612 kinds (mostly float scales with zero points)
+// spill 12 to 60 bytes per lane all the same.  32 x 128: three (4096 rows by 8 experts of 2048 x 1024, float32 rows,
 // groups of 64, 89 against 108 with two; bfloat16 with zero points, groups of 64, 51 against 62), for float32 rows
 // with groups of 128 two (85.1 against 86.8).  16 x 64: three (64 rows by 64 experts of 2048 x 1024, zero points,
 // groups of 64, 11.3 against 12.0), for float32 rows two (15.4 against 16.0).  16 x 32: four (64 rows by 64 experts of
@@ -603,7 +603,6 @@ int linear_cut(const char *who, LinearArgs a, void *stream) {
   constexpr bool kShort = sizeof(T) == 2;
   constexpr int kWaves32 = kShort || G <= 64 ? 3 : 2, kWaves16 = kShort && G >= 64 ? 4 : 2;
   constexpr bool kFew = kShort && G >= 64;                   // two tiles of two blocks stay in registers
-  constexpr bool kTwo = G >= 64;                             // and do with 2 waves per SIMD
   constexpr bool kWide = Z != kBefore && G == 128;           // 32 x 256 rather than 64 x 256
   const int64_t rows = a.n_rows, tiles = a.s.tiles, blocks = a.s.blocks;
   auto groups = [&](int64_t r, int64_t t) { return ((rows + r - 1) / r) * ((tiles + t - 1) / t); };
@@ -628,7 +627,7 @@ int linear_cut(const char *who, LinearArgs a, void *stream) {
   if (groups(32, 8) >= 512) return launch_linear<T, S, G, Z, 2, 2, 1, 1, 4, kWaves32>(who, a, stream);
   if (groups(32, 4) >= 512) return launch_linear<T, S, G, Z, 2, 2, 1, 2, 2, 2>(who, a, stream);
   if (rows <= 16 && groups(16, 2) >= 512 && blocks >= 8)
-    return launch_linear<T, S, G, Z, 1, 2, kTwo ? 2 : 1, 4, 1, 2>(who, a, stream);
+    return launch_linear<T, S, G, Z, 1, 2, kFew ? 2 : 1, 4, 1, 2>(who, a, stream);
   if (groups(16, 4) >= 512) return cut_16_64();
   if (blocks < 8 || groups(16, 2) > (rows <= 16 ? 511 : 256)) return cut_16_32();
   if (groups(16, 2) > 128) {
