@@ -452,6 +452,81 @@ int svt_quant_pack(const svt_quant_weights *w, const uint8_t *nibbles, const voi
 int svt_quant_linear(int32_t n_rows, int32_t dtype, const void *x, const svt_quant_weights *w, const int32_t *offsets,
                      const float *bias, int32_t activation, int32_t out_dtype, void *y, void *hip_stream);
 
+/*
+ * A scorer in training.  The entry points below are the parts that train such a net on a catalogue: rows of a
+ * table for tokens (items, words), products with a gate (dense, or one pair of matrices per expert over sorted
+ * rows), and the log probabilities of chosen tokens, each with its gradient ["SilverTorch - Index as Model",
+ * evolution section: hand-written modules trained together by back-propagation; recommendation-quality section:
+ * several heads' predictions].  The pages give no formulas; each call states its own.  What is said above of
+ * pointers, element types, sums, streams and overlap holds here too.  Calls that take a workspace do not look at
+ * its contents on entry; calls in flight together, and graphs replayed together, need one each.
+ */
+
+/*
+ * svt_embedding - rows of a table for tokens, scaled: out[i] = scale * table[ids[i]].
+ *   ids    [n_tokens] int64; a token outside [0, n_rows) gets a row of zeros
+ *   table  [n_rows][width] of dtype;  out [n_tokens][width] of dtype
+ *   0 <= n_tokens <= 2^30, 1 <= n_rows <= 2^31 - 2, 1 <= width <= 2^24, scale finite
+ * n_tokens == 0 returns SVT_OK without enqueuing.  Errors: SVT_EINVAL, SVT_EDEVICE as svt_route.
+ */
+int svt_embedding(int64_t n_tokens, int64_t n_rows, int32_t width, int32_t dtype, const void *table,
+                  const int64_t *ids, float scale, void *out, void *hip_stream);
+
+/*
+ * svt_embedding_backward - the gradient in the table: d_table[v] = scale * sum over i with ids[i] = v of d_out[i],
+ * each row's sum in float32 in an order that depends on the tokens alone.
+ *   d_out       [n_tokens][width] of dtype
+ *   accumulate  0: rows that no token names become zeros; 1: the sums are added to d_table, and rows that no token
+ *               names are neither read nor written (for gradients over several calls, and tables far larger than
+ *               a batch)
+ *   d_table     [n_rows][width] of table_type: dtype or SVT_F32
+ *   workspace   svt_embedding_backward_workspace_size(n_tokens, n_rows, width) bytes, 16-byte aligned
+ * Sizes as svt_embedding.  n_tokens == 0 writes the zeros (accumulate: returns without enqueuing).
+ * Errors: SVT_EINVAL, SVT_EDEVICE (a launch failed: d_table is undefined).
+ */
+size_t svt_embedding_backward_workspace_size(int64_t n_tokens, int64_t n_rows, int32_t width);
+int svt_embedding_backward(int64_t n_tokens, int64_t n_rows, int32_t width, int32_t dtype, const void *d_out,
+                           const int64_t *ids, float scale, int32_t accumulate, int32_t table_type, void *d_table,
+                           void *workspace, size_t workspace_bytes, void *hip_stream);
+
+/*
+ * svt_token_logprobs - for each row of logits, with z = scale * logits and p = softmax(z): the log probability of
+ * a given token, the entropy, and the `top` most likely tokens.
+ *   logits         [n_tokens][vocab] of dtype, 1 <= vocab <= 2^30.  -inf or NaN shuts a token (p = 0); +inf counts
+ *                  as the largest finite float32
+ *   tokens         [n_tokens] int64; outside [0, vocab): no token is given
+ *   scale          positive and finite (1 / temperature)
+ *   top            0 <= top <= min(SVT_MAX_TOP, vocab)
+ *   logprobs       [n_tokens] float: log p of the token; 0 where none is given, -inf where it is shut
+ *                  (or below the least float32)
+ *   entropy        [n_tokens] float: -sum p log p; 0 for a row without an open token
+ *   norms          [n_tokens][2] float: what the gradient needs (the largest logit, log2 of the sum relative to it)
+ *   top_tokens     [n_tokens][top] int64, by (logit desc, token asc); -1 where fewer than top are open
+ *   top_logprobs   [n_tokens][top] float: their log p; -inf where the token is -1.  Both may be
+ *                  NULL where top is 0
+ *   workspace      svt_token_logprobs_workspace_size(n_tokens, vocab, top) bytes, 8-byte aligned (NULL where that
+ *                  is 0): few rows of many tokens are split
+ * n_tokens == 0 returns SVT_OK without enqueuing.  Errors: SVT_EINVAL, SVT_EDEVICE as svt_route.
+ */
+size_t svt_token_logprobs_workspace_size(int32_t n_tokens, int32_t vocab, int32_t top);
+int svt_token_logprobs(int32_t n_tokens, int32_t vocab, int32_t top, int32_t dtype, const void *logits,
+                       const int64_t *tokens, float scale, float *logprobs, float *entropy, float *norms,
+                       int64_t *top_tokens, float *top_logprobs, void *workspace, size_t workspace_bytes,
+                       void *hip_stream);
+
+/*
+ * svt_token_logprobs_backward - the gradient in the logits of svt_token_logprobs's log probabilities and entropy:
+ *   d_logits[i] = scale * (d_logprob * ([i is the token] - p_i) - d_entropy * p_i * (log p_i + entropy)),
+ *   0 at shut tokens; d_logprob counts as 0 where no token is given.
+ *   logits, tokens, scale   as given to svt_token_logprobs; norms, entropy: its outputs
+ *   d_logprobs              [n_tokens] float;  d_entropy: [n_tokens] float, or NULL (zeros)
+ *   d_logits                [n_tokens][vocab] of dtype
+ * Errors as svt_route.
+ */
+int svt_token_logprobs_backward(int32_t n_tokens, int32_t vocab, int32_t dtype, const void *logits,
+                                const int64_t *tokens, float scale, const float *norms, const float *entropy,
+                                const float *d_logprobs, const float *d_entropy, void *d_logits, void *hip_stream);
+
 /* svt_last_error - message of the last failed call on this thread ("" if none). */
 const char *svt_last_error(void);
 

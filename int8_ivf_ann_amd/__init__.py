@@ -13,6 +13,8 @@ from .svt import (EXPORTED, SVT_EDEVICE, SVT_EINVAL, SVT_ENOMEM, SVT_ENOSPACE, S
                   svt_rerank, svt_rerank_net,
                   svt_route, svt_route_backward, svt_expert_sort, svt_expert_sort_workspace_size, svt_expert_dispatch,
                   svt_expert_dispatch_backward, svt_expert_combine, svt_expert_combine_backward, svt_quant_pack, svt_quant_linear, svt_quant_weights,
+                  svt_embedding, svt_embedding_backward, svt_embedding_backward_workspace_size, svt_token_logprobs,
+                  svt_token_logprobs_backward, svt_token_logprobs_workspace_size,
                   SVT_F32, SVT_F16, SVT_BF16, SVT_ACT_NONE, SVT_ACT_RELU, SVT_MAX_EXPERTS, SVT_MAX_TOP)
 
 __all__ = ["Index", "SvtError", "svt_bloom_mask", "svt_bloom_sign", "svt_index_free", "svt_index_info",
@@ -23,5 +25,6 @@ __all__ = ["Index", "SvtError", "svt_bloom_mask", "svt_bloom_sign", "svt_index_f
            "SVT_PATH_TILE", "SVT_PATH_EXHAUSTIVE", "SVT_PATH_LARGE_K", "SVT_OPT_MERGE_FROM_SLOTS", "SVT_OPT_FORCE_REDO", "make_options", "svt_search_options",
            "svt_route", "svt_route_backward", "svt_expert_sort", "svt_expert_sort_workspace_size", "svt_expert_dispatch",
            "svt_expert_dispatch_backward", "svt_expert_combine", "svt_expert_combine_backward",
-           "svt_quant_pack", "svt_quant_linear", "svt_quant_weights", "SVT_F32", "SVT_F16", "SVT_BF16",
+           "svt_quant_pack", "svt_quant_linear", "svt_quant_weights", "svt_embedding", "svt_embedding_backward",
+           "svt_embedding_backward_workspace_size", "svt_token_logprobs", "svt_token_logprobs_backward", "svt_token_logprobs_workspace_size", "SVT_F32", "SVT_F16", "SVT_BF16",
            "SVT_ACT_NONE", "SVT_ACT_RELU", "SVT_MAX_EXPERTS", "SVT_MAX_TOP"]

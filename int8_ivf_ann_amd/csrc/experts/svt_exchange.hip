@@ -63,35 +63,6 @@ __device__ __forceinline__ int load_expert(const int32_t *experts, int64_t i, in
   return i < end && (uint32_t)e < (uint32_t)E ? e : -1;
 }
 
-// the lanes of this wave whose expert, below 2^BITS, equals this lane's (0 for a lane without one)
-template <int BITS>
-__device__ __forceinline__ uint64_t same_expert(int e) {
-  uint64_t same = __ballot(e >= 0);
-#pragma unroll
-  for (int b = 0; b < BITS; ++b) {
-    const uint64_t one = __ballot((e >> b) & 1);
-    same &= ((e >> b) & 1) ? one : ~one;
-  }
-  return e >= 0 ? same : 0ull;
-}
-
-// ranks of a wave's entries, step by step: rank[q] = entries of the same expert before it in the wave's
-// piece; count[e] (the wave's own, cleared) becomes the piece's entries of e
-template <int STEPS, int BITS>
-__device__ __forceinline__ void rank_entries(const int (&e)[STEPS], int (&rank)[STEPS], volatile int32_t *count) {
-  const int l = lane_id();
-#pragma unroll
-  for (int q = 0; q < STEPS; ++q) {
-    const uint64_t same = same_expert<BITS>(e[q]);
-    rank[q] = 0;
-    if (e[q] >= 0) {
-      rank[q] = count[e[q]] + mbcnt(same);
-      // the last lane of each expert moves the count on; a wave's LDS operations stay in order
-      if ((same >> l) == 1ull) count[e[q]] = rank[q] + 1;
-    }
-  }
-}
-
 // count[w][e] become exclusive sums over the waves, total[e] their sum
 __device__ __forceinline__ void sum_waves(int32_t (*count)[SVT_MAX_EXPERTS], int32_t *total, int E) {
   for (int e = threadIdx.x; e < E; e += kSortThreads) {

@@ -1,5 +1,5 @@
-// svt_experts.h - shared by the routed-expert operators (svt_route.hip, svt_exchange.hip, svt_quant.hip):
-// element types, conversions, lane-group reductions and host-side argument checks.  Not installed.
+// svt_experts.h - shared by the operators of experts/ and scorer/: element types, conversions, lane-group reductions,
+// ranks by bin and host-side argument checks.  Not installed.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -85,6 +85,35 @@ __device__ __forceinline__ int incl_sums(int v) {
   v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast:15
   v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // row_bcast:31
   return v;
+}
+
+// the lanes of this wave whose bin e, below 2^BITS, equals this lane's (0 for a lane without one, e < 0)
+template <int BITS>
+__device__ __forceinline__ uint64_t same_bin(int e) {
+  uint64_t same = __ballot(e >= 0);
+#pragma unroll
+  for (int b = 0; b < BITS; ++b) {
+    const uint64_t one = __ballot((e >> b) & 1);
+    same &= ((e >> b) & 1) ? one : ~one;
+  }
+  return e >= 0 ? same : 0ull;
+}
+
+// ranks of a wave's entries by bin, step by step: rank[q] = entries of the same bin before it in the wave's piece;
+// count[e] (the wave's own, cleared) becomes the piece's entries of e
+template <int STEPS, int BITS>
+__device__ __forceinline__ void rank_entries(const int (&e)[STEPS], int (&rank)[STEPS], volatile int32_t *count) {
+  const int l = lane_id();
+#pragma unroll
+  for (int q = 0; q < STEPS; ++q) {
+    const uint64_t same = same_bin<BITS>(e[q]);
+    rank[q] = 0;
+    if (e[q] >= 0) {
+      rank[q] = count[e[q]] + mbcnt(same);
+      // the last lane of each bin moves the count on; a wave's LDS operations stay in order
+      if ((same >> l) == 1ull) count[e[q]] = rank[q] + 1;
+    }
+  }
 }
 
 }  // namespace svt

@@ -36,7 +36,8 @@ EXPORTED = ("svt_index_upload", "svt_index_upload_updatable", "svt_index_insert"
             "svt_search", "svt_search_noalloc", "svt_rerank", "svt_route", "svt_route_backward",
             "svt_expert_sort_workspace_size", "svt_expert_sort", "svt_expert_dispatch", "svt_expert_dispatch_backward",
             "svt_expert_combine", "svt_expert_combine_backward", "svt_quant_pack_size", "svt_quant_pack",
-            "svt_quant_linear", "svt_last_error", "svt_bloom_mask", "svt_bloom_sign", "svt_profile_enable", "svt_profile_read")
+            "svt_quant_linear", "svt_embedding", "svt_embedding_backward_workspace_size", "svt_embedding_backward",
+            "svt_token_logprobs_workspace_size", "svt_token_logprobs", "svt_token_logprobs_backward", "svt_last_error", "svt_bloom_mask", "svt_bloom_sign", "svt_profile_enable", "svt_profile_read")
 
 
 class SvtError(RuntimeError):
@@ -142,6 +143,15 @@ def lib():
     L.svt_quant_pack_size.argtypes = [qw]
     L.svt_quant_pack.argtypes = [qw, vp, vp, vp, vp]
     L.svt_quant_linear.argtypes = [i32, i32, vp, qw, vp, vp, i32, i32, vp, vp]
+    f32 = ctypes.c_float
+    L.svt_embedding.argtypes = [i64, i64, i32, i32, vp, vp, f32, vp, vp]
+    L.svt_embedding_backward_workspace_size.argtypes = [i64, i64, i32]
+    L.svt_embedding_backward_workspace_size.restype = sz
+    L.svt_embedding_backward.argtypes = [i64, i64, i32, i32, vp, vp, f32, i32, i32, vp, vp, sz, vp]
+    L.svt_token_logprobs_workspace_size.argtypes = [i32, i32, i32]
+    L.svt_token_logprobs_workspace_size.restype = sz
+    L.svt_token_logprobs.argtypes = [i32, i32, i32, i32, vp, vp, f32, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.svt_token_logprobs_backward.argtypes = [i32, i32, i32, vp, vp, f32, vp, vp, vp, vp, vp, vp]
     L.svt_last_error.restype = ctypes.c_char_p
     L.svt_bloom_mask.argtypes = [vp, i32, i32, i32, vp]
     L.svt_bloom_sign.argtypes = [vp, i64, i32, i32, i32, vp, i32]
@@ -730,6 +740,133 @@ def svt_quant_linear(x, weights: svt_quant_weights, offsets=None, bias=None, act
                                       None if offsets is None else offsets.data_ptr(),
                                       None if bias is None else bias.data_ptr(), _ACTIVATIONS[activation],
                                       _types()[out_dtype], out.data_ptr(), s))
+    return out
+
+
+# ------------------------------------------------------------------------------------------------
+# A scorer in training: rows of a table for tokens, gated products, log probabilities, and their gradients.  As the
+# calls above: dense tensors on one device, no history recorded.
+
+def _token_ids(name, t, dev):
+    """(number, device) of an int64 tensor of tokens."""
+    import torch
+    if not hasattr(t, "data_ptr"):
+        raise ValueError(f"{name}: expected a tensor")
+    _check_dense(name, t, torch.int64, t.shape, dev)
+    return t.numel()
+
+
+def _workspace(given, need, dev, like):
+    """(tensor or None, pointer, bytes) of a workspace: the one given, checked, or a new one of ``need`` bytes."""
+    import torch
+    if given is not None:
+        _check_tensor("workspace", given, (torch.uint8,), (given.numel(),), dev)
+    elif need:
+        given = like.new_empty((need,), dtype=torch.uint8)
+    return (None, None, 0) if given is None else (given, given.data_ptr(), given.numel())
+
+
+def svt_embedding(table, ids, scale: float = 1.0, out=None, stream=None):
+    """Rows of a table for tokens: table [V, D] (float32, float16, bfloat16), ids int64 of any shape -> scale *
+    table[ids], [*ids.shape, D] of the table's dtype; a token outside [0, V) gets a row of zeros."""
+    (V, D), code, dev = _rows_of("table", table)
+    n = _token_ids("ids", ids, dev)
+    with _Run(dev, stream) as s:
+        out = _out("out", out, table.dtype, (*ids.shape, D), dev, table)
+        _check(lib().svt_embedding(n, V, D, code, table.data_ptr(), ids.data_ptr(), scale, out.data_ptr(), s))
+    return out
+
+
+@functools.lru_cache(maxsize=256)
+def svt_embedding_backward_workspace_size(n_tokens: int, n_rows: int, width: int) -> int:
+    """Bytes of workspace that svt_embedding_backward needs for these sizes."""
+    need = lib().svt_embedding_backward_workspace_size(n_tokens, n_rows, width)
+    if need == 0 and svt_last_error():
+        raise SvtError(SVT_EINVAL, svt_last_error())
+    return int(need)
+
+
+def svt_embedding_backward(d_out, ids, n_rows: int, scale: float = 1.0, out=None, accumulate: bool = False,
+                           out_dtype=None, workspace=None, stream=None):
+    """The gradient in a table of ``n_rows`` rows: d_out [*ids.shape, D], ids int64 -> d_table [n_rows, D] of
+    ``out_dtype`` (d_out's, the default, or float32): row v is scale times the sum of the rows of d_out whose token is
+    v.  ``accumulate`` adds them to ``out`` (which has to be given) and touches no other row."""
+    import torch
+    if not hasattr(d_out, "dim") or d_out.dim() < 1:
+        raise ValueError("d_out: expected a tensor [*ids.shape, D]")
+    shape, code, dev = _rows_of("d_out", d_out, d_out.dim())
+    D = shape[-1]
+    n = _token_ids("ids", ids, dev)
+    if d_out.shape[:-1] != ids.shape:
+        raise ValueError(f"ids: shape {tuple(ids.shape)} for d_out of shape {tuple(d_out.shape)}")
+    if accumulate and out is None:
+        raise ValueError("out: to be given where the gradient is added to it")
+    out_dtype = out.dtype if out is not None else d_out.dtype if out_dtype is None else out_dtype
+    if out_dtype is not d_out.dtype and out_dtype is not torch.float32:
+        raise ValueError(f"out: dtype {out_dtype} is neither {d_out.dtype} nor torch.float32")
+    need = svt_embedding_backward_workspace_size(n, n_rows, D)
+    with _Run(dev, stream) as s:
+        out = _out("out", out, out_dtype, (n_rows, D), dev, d_out)
+        workspace, at, size = _workspace(workspace, need, dev, d_out)
+        _check(lib().svt_embedding_backward(n, n_rows, D, code, d_out.data_ptr(), ids.data_ptr(), scale, int(accumulate),
+                                            _types()[out_dtype], out.data_ptr(), at, size, s))
+    return out
+
+
+@functools.lru_cache(maxsize=256)
+def svt_token_logprobs_workspace_size(n_tokens: int, vocab: int, top: int) -> int:
+    """Bytes of workspace that svt_token_logprobs needs for these sizes (0: none)."""
+    need = lib().svt_token_logprobs_workspace_size(n_tokens, vocab, top)
+    if need == 0 and svt_last_error():
+        raise SvtError(SVT_EINVAL, svt_last_error())
+    return int(need)
+
+
+def svt_token_logprobs(logits, tokens, top: int = 0, scale: float = 1.0, out_logprobs=None, out_entropy=None,
+                       out_norms=None, out_top_tokens=None, out_top_logprobs=None, workspace=None, stream=None):
+    """Of p = softmax(scale * logits) for each row: logits [T, V] (float32, float16, bfloat16), tokens int64 [T] ->
+    (logprobs float32 [T], entropy float32 [T], norms float32 [T, 2]), and with ``top`` > 0 also (top_tokens int64
+    [T, top], top_logprobs float32 [T, top]), by (logit desc, token asc).  -inf and NaN shut a token.  logprobs is 0
+    where the token lies outside [0, V); -1 and -inf where fewer than ``top`` are open.  norms is for the gradient."""
+    import torch
+    (T, V), code, dev = _rows_of("logits", logits)
+    _check_dense("tokens", tokens, torch.int64, (T,), dev)
+    if not 0 <= top <= min(SVT_MAX_TOP, V):
+        raise ValueError(f"top: {top} out of [0, min({SVT_MAX_TOP}, {V} tokens)]")
+    need = svt_token_logprobs_workspace_size(T, V, top)
+    with _Run(dev, stream) as s:
+        out_logprobs = _out("out_logprobs", out_logprobs, torch.float32, (T,), dev, logits)
+        out_entropy = _out("out_entropy", out_entropy, torch.float32, (T,), dev, logits)
+        out_norms = _out("out_norms", out_norms, torch.float32, (T, 2), dev, logits)
+        best = ()
+        if top:
+            best = (_out("out_top_tokens", out_top_tokens, torch.int64, (T, top), dev, logits),
+                    _out("out_top_logprobs", out_top_logprobs, torch.float32, (T, top), dev, logits))
+        workspace, at, size = _workspace(workspace, need, dev, logits)
+        _check(lib().svt_token_logprobs(T, V, top, code, logits.data_ptr(), tokens.data_ptr(), scale,
+                                        out_logprobs.data_ptr(), out_entropy.data_ptr(), out_norms.data_ptr(),
+                                        *([t.data_ptr() for t in best] or (None, None)), at, size, s))
+    return (out_logprobs, out_entropy, out_norms, *best)
+
+
+def svt_token_logprobs_backward(logits, tokens, norms, entropy, d_logprobs, d_entropy=None, scale: float = 1.0, out=None,
+                                stream=None):
+    """The gradient in the logits of svt_token_logprobs's log probabilities and entropy: its inputs, its norms and
+    entropy, the gradients d_logprobs and d_entropy (float32 [T]; None: zeros) -> d_logits [T, V] of the logits'
+    dtype."""
+    import torch
+    (T, V), code, dev = _rows_of("logits", logits)
+    _check_dense("tokens", tokens, torch.int64, (T,), dev)
+    _check_dense("norms", norms, torch.float32, (T, 2), dev)
+    _check_dense("entropy", entropy, torch.float32, (T,), dev)
+    _check_dense("d_logprobs", d_logprobs, torch.float32, (T,), dev)
+    if d_entropy is not None:
+        _check_dense("d_entropy", d_entropy, torch.float32, (T,), dev)
+    with _Run(dev, stream) as s:
+        out = _out("out", out, logits.dtype, (T, V), dev, logits)
+        _check(lib().svt_token_logprobs_backward(T, V, code, logits.data_ptr(), tokens.data_ptr(), scale, norms.data_ptr(),
+                                                 entropy.data_ptr(), d_logprobs.data_ptr(),
+                                                 None if d_entropy is None else d_entropy.data_ptr(), out.data_ptr(), s))
     return out
 
 
