@@ -333,7 +333,8 @@ int svt_rerank(const svt_index *ix, int32_t n_queries, const int8_t *queries, co
  *     first that fails ends the call (SVT_EDEVICE), and the outputs of the launches before it are undefined.
  */
 enum { SVT_F32 = 0, SVT_F16 = 1, SVT_BF16 = 2 };   /* element types */
-enum { SVT_ACT_NONE = 0, SVT_ACT_RELU = 1 };       /* activations of svt_quant_linear */
+enum { SVT_ACT_NONE = 0, SVT_ACT_RELU = 1,         /* activations: svt_quant_linear takes these two, */
+       SVT_ACT_SILU = 2, SVT_ACT_GELU = 3 };       /* svt_gated_linear all (GELU with the error function) */
 #define SVT_MAX_EXPERTS 512 /* experts of one net                                                     */
 #define SVT_MAX_TOP 16      /* experts per token                                                      */
 
@@ -488,6 +489,42 @@ size_t svt_embedding_backward_workspace_size(int64_t n_tokens, int64_t n_rows, i
 int svt_embedding_backward(int64_t n_tokens, int64_t n_rows, int32_t width, int32_t dtype, const void *d_out,
                            const int64_t *ids, float scale, int32_t accumulate, int32_t table_type, void *d_table,
                            void *workspace, size_t workspace_bytes, void *hip_stream);
+
+/*
+ * svt_gated_linear - products with a gate: h[r] = act(w_gate x[r]) * (w_up x[r]), elementwise.
+ *   x            [n_rows][n_in] of dtype
+ *   w_gate, w_up [n_matrices][n_out][n_in] of dtype; 1 <= n_matrices <= SVT_MAX_EXPERTS, n_in and n_out 1 .. 2^20
+ *   offsets      NULL: one pair of matrices, which every row uses.  Else [n_matrices + 1] int32, ascending, e.g.
+ *                svt_expert_sort's: rows offsets[e] .. offsets[e + 1] - 1 use pair e (an end is clamped to
+ *                [0, n_rows]); rows that no pair names are neither read nor written
+ *   activation   SVT_ACT_NONE, _RELU, _SILU or _GELU (v times the normal distribution's integral up to v)
+ *   h            [n_rows][n_out] of dtype
+ *   gate, up     [n_rows][n_out] of dtype, or both NULL: w_gate x and w_up x, which the gradient needs
+ * Sums are float32; h, gate and up are rounded once each (h from the unrounded sums).
+ * n_rows == 0 returns SVT_OK without enqueuing.  Errors: SVT_EINVAL, SVT_EDEVICE as svt_route.
+ */
+int svt_gated_linear(int32_t n_rows, int32_t n_in, int32_t n_out, int32_t n_matrices, int32_t dtype, const void *x,
+                     const void *w_gate, const void *w_up, const int32_t *offsets, int32_t activation, void *h,
+                     void *gate, void *up, void *hip_stream);
+
+/*
+ * svt_gated_linear_backward - its gradients: with dg = dh * up * act'(gate) and du = dh * act(gate), both rounded to
+ * dtype as the products take them,
+ *   dx = dg w_gate + du w_up  (per row, with its pair);  dw_gate = sum over a pair's rows of dg x^T;  dw_up of du x^T
+ *   dh, gate, up  [n_rows][n_out] of dtype: the gradient in h, and what svt_gated_linear kept
+ *   dx            [n_rows][n_in] of dtype, or NULL (w_gate and w_up may then be NULL).  Rows that no pair names are left
+ *   dw_gate, dw_up  [n_matrices][n_out][n_in] of dtype, or both NULL (x may then be NULL); zeros for a pair without rows
+ *   workspace     svt_gated_linear_backward_workspace_size(n_rows, n_in, n_out, n_matrices, dtype, offsets != NULL)
+ *                 bytes, 16-byte aligned
+ * act' of SVT_ACT_RELU is 0 at 0.  n_rows == 0 writes the zeros.  Errors: SVT_EINVAL, SVT_EDEVICE (a launch failed: the
+ * outputs are undefined).
+ */
+size_t svt_gated_linear_backward_workspace_size(int32_t n_rows, int32_t n_in, int32_t n_out, int32_t n_matrices,
+                                                int32_t dtype, int32_t by_expert);
+int svt_gated_linear_backward(int32_t n_rows, int32_t n_in, int32_t n_out, int32_t n_matrices, int32_t dtype,
+                              const void *dh, const void *x, const void *w_gate, const void *w_up, const void *gate,
+                              const void *up, const int32_t *offsets, int32_t activation, void *dx, void *dw_gate,
+                              void *dw_up, void *workspace, size_t workspace_bytes, void *hip_stream);
 
 /*
  * svt_token_logprobs - for each row of logits, with z = scale * logits and p = softmax(z): the log probability of

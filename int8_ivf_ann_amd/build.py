@@ -17,7 +17,9 @@ SOURCES = (("svt_kernels.hip", True), ("svt_tile.hip", True), ("svt_noalloc.hip"
            ("svt_largek.hip", True), ("svt_api.cpp", False), ("experts/svt_route.hip", True),
            ("experts/svt_exchange.hip", True), ("experts/svt_quant.hip", True),
            ("experts/svt_linear_f32.hip", True), ("experts/svt_linear_f16.hip", True),
-           ("experts/svt_linear_bf16.hip", True), ("scorer/svt_embedding.hip", True), ("scorer/svt_logprobs.hip", True))
+           ("experts/svt_linear_bf16.hip", True), ("scorer/svt_embedding.hip", True), ("scorer/svt_logprobs.hip", True),
+           ("scorer/svt_gated.hip", True), ("scorer/svt_gated_f32.hip", True), ("scorer/svt_gated_f16.hip", True),
+           ("scorer/svt_gated_bf16.hip", True))
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-result", "-I", os.path.join(ROOT, "include"), "-I", CSRC]
 
 

@@ -1,0 +1,863 @@
+// svt_gated.h - the kernels of products with a gate and of their gradients (svt_gated_*.hip instantiate them, one file
+// per type; svt_gated.hip checks arguments and calls).
+//
+//   g = x Wg^T,  u = x Wu^T,  h = act(g) u                          rows r, inputs k, outputs n
+//   dg = dh u act'(g),  du = dh act(g)
+//   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x
+//
+// All three products run on the matrix cores with float32 accumulation (16 x 16 x 32 instructions for two-byte types,
+// 16 x 16 x 4 for float32).  A workgroup computes a tile of `Q rows x P columns` of the result; per step it brings 128
+// bytes of the reduced index of each side to LDS, straight from memory (two buffers, so that a step's loads are in flight
+// while the step before is multiplied).
+//   side P   the columns of the result, which lie together in memory: the first operand, so that a lane ends up with four
+//            neighbouring columns of one row
+//   side Q   its rows
+// A side is read in one of two forms:
+//   along    the reduced index lies together (x and W forward; dg, du for dx): rows of 128 bytes in LDS, a fragment is
+//            one 16-byte read
+//   across   the other index lies together (W for dx; x, dg, du for dW): rows of the tile's width for each reduced index,
+//            and the transposing read of LDS (float32: single values) collects a fragment
+// In both, the 16-byte pieces of a row are permuted by the row's number, so that the lanes of a read spread over the
+// banks.  Pieces outside the matrix are zeros: their address lies outside the buffer's range.
+#pragma once
+
+#include <type_traits>
+
+#include "../experts/svt_experts.h"
+
+namespace svt {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef f16 f16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) void lds_void;
+
+constexpr int32_t kGatedMax = 1 << 20;   // inputs, outputs
+
+// ---- activations ---------------------------------------------------------------------------------
+
+constexpr float kGateLog2e = 1.44269504088896341f;
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float v) {
+  if constexpr (ACT == SVT_ACT_RELU) return v < 0.f ? 0.f : v;   // NaN stays NaN
+  else if constexpr (ACT == SVT_ACT_SILU) return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kGateLog2e * v));
+  else if constexpr (ACT == SVT_ACT_GELU) return 0.5f * v * erfcf(-0.70710678118654752f * v);
+  else return v;
+}
+
+// value and slope
+template <int ACT>
+__device__ __forceinline__ void act_both(float v, float &value, float &slope) {
+  if constexpr (ACT == SVT_ACT_RELU) {
+    value = v < 0.f ? 0.f : v;
+    slope = v > 0.f ? 1.f : 0.f;
+  } else if constexpr (ACT == SVT_ACT_SILU) {
+    const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kGateLog2e * v));
+    value = v * s;
+    slope = fmaf(value, 1.f - s, s);
+  } else if constexpr (ACT == SVT_ACT_GELU) {
+    const float c = 0.5f * erfcf(-0.70710678118654752f * v);
+    value = v * c;
+    slope = fmaf(v * 0.39894228040143268f, __builtin_amdgcn_exp2f(-0.5f * kGateLog2e * v * v), c);
+  } else {
+    value = v;
+    slope = 1.f;
+  }
+}
+
+// ---- fragments -----------------------------------------------------------------------------------
+
+// 16 bytes of a lane: row lane % 16, reduced indexes (16 / size) (lane / 16) ..
+template <class T> struct Mul;
+template <> struct Mul<bf16> {
+  typedef bf16x8 frag;
+  static __device__ __forceinline__ f32x4 add(frag p, frag q, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(p, q, c, 0, 0, 0);
+  }
+};
+template <> struct Mul<f16> {
+  typedef f16x8 frag;
+  static __device__ __forceinline__ f32x4 add(frag p, frag q, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(p, q, c, 0, 0, 0);
+  }
+};
+template <> struct Mul<float> {
+  typedef f32x4 frag;
+  static __device__ __forceinline__ f32x4 add(frag p, frag q, f32x4 c) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(p[j], q[j], c, 0, 0, 0);
+    return c;
+  }
+};
+
+// ---- tiles ---------------------------------------------------------------------------------------
+
+constexpr int kStepBytes = 128;                    // of the reduced index
+constexpr uint32_t kOutside = 0x80000000u;         // an offset past every buffer's range
+constexpr int kRange = 0x7FFFFFF0;
+
+// Q x P columns of the result, waves WQ x WP
+template <int Q, int P, int WQ_, int WP_>
+struct Cut {
+  static constexpr int q = Q, p = P, WQ = WQ_, WP = WP_;
+  static constexpr int threads = 64 * WQ * WP;
+  static constexpr int nq = Q / WQ / 16, np = P / WP / 16;   // 16 x 16 blocks of a wave
+};
+
+// where a step's pieces begin: the side's first row (of its upper half), at the step's first reduced index
+struct Base { const char *at, *upper; };
+
+// One side of a tile.  ROWS: the tile's size along the side's own index; HALVES: two matrices' rows, half a tile each.
+template <class T, int ROWS, int THREADS, bool ACROSS, bool HALVES = false>
+struct Side {
+  static constexpr int b = sizeof(T), each = 16 / b, step = kStepBytes / b;   // elements of a piece, of a step
+  static constexpr int bytes = ROWS * kStepBytes;
+  static constexpr int pieces = bytes / 16 / THREADS;                         // of a thread
+  static constexpr int row_pieces = ACROSS ? ROWS * b / 16 : kStepBytes / 16;
+  static_assert(pieces >= 1 && bytes % (16 * THREADS) == 0, "whole pieces for every thread");
+  static_assert(!HALVES || (!ACROSS && pieces % 2 == 0), "a thread's pieces change matrix half way");
+
+  // which piece of row `row` lies at its place `at` (an involution)
+  static __device__ __forceinline__ int permuted(int row, int at) {
+    if constexpr (!ACROSS) return at ^ ((row >> 1) & 7);
+    else if constexpr (b == 2) return at ^ ((2 * ((row & 3) | ((row >> 3) & 1) << 2)) & (row_pieces - 1));
+    else return at ^ (4 * ((row >> 2) & 3));
+  }
+
+  uint32_t offset[pieces];   // of the thread's pieces; kOutside: zeros
+  uint32_t gone;             // bit j: piece j is outside in a last step
+  int own, reduced;
+
+  static __device__ __forceinline__ int row_of(int j) { return (j * THREADS + (int)threadIdx.x) / row_pieces; }
+  static __device__ __forceinline__ int piece_of(int j) {
+    return permuted(row_of(j), (j * THREADS + (int)threadIdx.x) % row_pieces);
+  }
+
+  // pitch: bytes of a memory row; own: valid indexes of the side (of each half); reduced: those of a last step
+  __device__ __forceinline__ void init(uint32_t pitch, int own_, int reduced_) {
+    own = own_;
+    reduced = reduced_;
+    gone = 0u;
+#pragma unroll
+    for (int j = 0; j < pieces; ++j) {
+      const int row = row_of(j), piece = piece_of(j), mine = HALVES ? row % (ROWS / 2) : row;
+      const bool out = ACROSS ? piece * each >= own : mine >= own;
+      offset[j] = out ? kOutside : (uint32_t)mine * pitch + (uint32_t)piece * 16u;
+      gone |= (ACROSS ? row >= reduced : piece * each >= reduced) ? 1u << j : 0u;
+    }
+  }
+
+  // A step's pieces to LDS, straight from memory (16-byte aligned rows).  The loads are written out, as the compiler
+  // would have every later read of LDS wait for them; whoever reads waits by loads_done() and a barrier.  (They have no
+  // result in registers.)
+  __device__ __forceinline__ void load(Base from, uint32_t lds, bool final) const {
+    const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)threadIdx.x / 64);
+    auto buffer = [](const char *p) {
+      const uint64_t v = (uint64_t)(uintptr_t)p;
+      return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v),
+                   (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32)) & 0xFFFFu, kRange, 0x00020000u};
+    };
+    const u32x4 lower = buffer(from.at), upper = buffer(HALVES ? from.upper : from.at);
+    const uint32_t out = final ? gone : 0u;
+#pragma unroll
+    for (int j = 0; j < pieces; ++j) {
+      const uint32_t to = lds + (j * THREADS + wave * 64) * 16, at = out >> j & 1u ? kOutside : offset[j];
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(at),
+                   "s"(HALVES && 2 * j >= pieces ? upper : lower)
+                   : "memory");
+    }
+  }
+
+  // the same through registers, for rows of any alignment: a piece may end inside
+  __device__ __forceinline__ void fetch(Base from, u32x4 (&held)[pieces], bool final) const {
+#pragma unroll
+    for (int j = 0; j < pieces; ++j) {
+      const char *p = (HALVES && 2 * j >= pieces ? from.upper : from.at) + offset[j];
+      held[j] = u32x4{0u, 0u, 0u, 0u};
+      if (offset[j] == kOutside || (final && (gone >> j & 1u))) continue;
+      const int left = (ACROSS ? own : reduced) - piece_of(j) * each;
+      if ((ACROSS || final) && left < each) {
+        struct { T t[each]; } v{};
+#pragma unroll
+        for (int i = 0; i < each; ++i)
+          if (i < left) v.t[i] = reinterpret_cast<const T *>(p)[i];
+        held[j] = __builtin_bit_cast(u32x4, v);
+      } else {
+        struct __attribute__((packed, aligned(sizeof(T)))) Raw { uint8_t v[16]; };
+        held[j] = __builtin_bit_cast(u32x4, *reinterpret_cast<const Raw *>(p));
+      }
+    }
+  }
+  __device__ __forceinline__ void put(const u32x4 (&held)[pieces], char *lds) const {
+#pragma unroll
+    for (int j = 0; j < pieces; ++j) *reinterpret_cast<u32x4 *>(lds + (j * THREADS + threadIdx.x) * 16) = held[j];
+  }
+
+  // the fragment of block `block` (16 own indexes), half `h` of the step
+  static __device__ __forceinline__ typename Mul<T>::frag fragment(const char *lds, int block, int h) {
+    const int i = lane_id() % 16, g = lane_id() / 16;
+    if constexpr (!ACROSS) {
+      return *reinterpret_cast<const typename Mul<T>::frag *>(lds + (block * 16 + i) * kStepBytes +
+                                                              ((4 * h + g) ^ (i >> 1)) * 16);
+    } else if constexpr (b == 2) {   // two transposing reads: reduced indexes 8 g .. 8 g + 3 and 8 g + 4 .. 8 g + 7
+      s16x4 v[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int row = 32 * h + 8 * g + 4 * k + i / 4;
+        v[k] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_s16x4 *)(lds + row * (ROWS * b) + permuted(row, 2 * block + i % 4 / 2) * 16 + i % 2 * 8));
+      }
+      struct { s16x4 a, b; } both{v[0], v[1]};
+      return __builtin_bit_cast(typename Mul<T>::frag, both);
+    } else {
+      typename Mul<T>::frag f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int row = 16 * h + 4 * g + k;
+        f[k] = *reinterpret_cast<const float *>(lds + row * (ROWS * b) + permuted(row, 4 * block + i / 4) * 16 + i % 4 * 4);
+      }
+      return f;
+    }
+  }
+};
+
+// all loads of this wave, to registers or to LDS, have arrived
+__device__ __forceinline__ void loads_done() { __builtin_amdgcn_s_waitcnt(0x0F70); }
+
+// acc[b][a] += the product of `steps` steps: lane l holds rows 16 b + l % 16 of its wave's part, columns
+// 16 a + 4 (l / 16) .. + 3.  base(s, p, q): where step s begins; last(s): whether its pieces may end early.
+// With HALVES of side P, the first np / 2 blocks are its lower, the others its upper half's.
+template <class T, class C, bool PA, bool QA, bool HALVES, bool ALIGNED>
+struct Product {
+  using SP = Side<T, C::p, C::threads, PA, HALVES>;
+  using SQ = Side<T, C::q, C::threads, QA>;
+  static constexpr int bytes = SP::bytes + SQ::bytes, lds_bytes = ALIGNED ? 2 * bytes : bytes;
+  SP P;
+  SQ Q;
+
+  static __device__ __forceinline__ void multiply(const char *lds, int wq, int wp, f32x4 (&acc)[C::nq][C::np]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      typename Mul<T>::frag p[C::np];
+#pragma unroll
+      for (int i = 0; i < C::np; ++i) {
+        constexpr int half = C::np / 2;
+        const int block = !HALVES ? wp * C::np + i : i < half ? wp * half + i : C::p / 32 + wp * half + i - half;
+        p[i] = SP::fragment(lds, block, h);
+      }
+#pragma unroll
+      for (int i = 0; i < C::nq; ++i) {
+        const typename Mul<T>::frag q = SQ::fragment(lds + SP::bytes, wq * C::nq + i, h);
+#pragma unroll
+        for (int j = 0; j < C::np; ++j) acc[i][j] = Mul<T>::add(p[j], q, acc[i][j]);
+      }
+    }
+  }
+
+  template <class At, class Last>
+  __device__ __forceinline__ void run(int steps, char *lds, At base, Last last, f32x4 (&acc)[C::nq][C::np]) const {
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64), wq = wave / C::WP, wp = wave % C::WP;
+    if (steps <= 0) return;
+    if constexpr (ALIGNED) {
+      const uint32_t at = (uint32_t)(uintptr_t)(lds_void *)lds;
+      auto load = [&](int s) {
+        Base p, q;
+        base(s, p, q);
+        const bool f = last(s);
+        const uint32_t to = at + (s & 1 ? bytes : 0);
+        P.load(p, to, f);
+        Q.load(q, to + SP::bytes, f);
+      };
+      load(0);
+      for (int s = 0; s < steps; ++s) {
+        loads_done();
+        __syncthreads();   // the step's pieces are there, and the other buffer has been read
+        if (s + 1 < steps) load(s + 1);
+        multiply(lds + (s & 1 ? bytes : 0), wq, wp, acc);
+      }
+    } else {
+      u32x4 hp[SP::pieces], hq[SQ::pieces];
+      auto fetch = [&](int s) {
+        Base p, q;
+        base(s, p, q);
+        const bool f = last(s);
+        P.fetch(p, hp, f);
+        Q.fetch(q, hq, f);
+      };
+      fetch(0);
+      for (int s = 0; s < steps; ++s) {
+        __syncthreads();   // the buffer has been read
+        P.put(hp, lds);
+        Q.put(hq, lds + SP::bytes);
+        __syncthreads();
+        if (s + 1 < steps) fetch(s + 1);
+        multiply(lds, wq, wp, acc);
+      }
+    }
+  }
+};
+
+// ---- rows by expert ------------------------------------------------------------------------------
+
+struct Rows { int matrix; int64_t first, end; };
+
+__device__ __forceinline__ int64_t clamped(int64_t v, int64_t n) { return v < 0 ? 0 : v < n ? v : n; }
+
+// the unit-th block of `per` rows of one matrix; matrix -1: there is none.  The whole wave asks.
+__device__ __forceinline__ Rows rows_of_unit(const int32_t *offsets, int n_matrices, int64_t n_rows, int64_t unit, int per) {
+  if (!offsets) {
+    const int64_t first = unit * per;
+    return {first < n_rows ? 0 : -1, first, first + per < n_rows ? first + per : n_rows};
+  }
+  int64_t before = 0;
+  for (int e0 = 0; e0 < n_matrices; e0 += 64) {
+    const int e = e0 + lane_id();
+    int64_t a = 0, z = 0;
+    if (e < n_matrices) {
+      a = clamped(offsets[e], n_rows);
+      z = clamped(offsets[e + 1], n_rows);
+    }
+    const int blocks = z > a ? (int)((z - a + per - 1) / per) : 0;
+    const int upto = incl_sums(blocks);
+    const uint64_t past = __ballot(before + upto > unit);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      const int skip = (int)(unit - before) - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(blocks, l));
+      const int64_t first = __builtin_amdgcn_readlane((int)a, l) + (int64_t)skip * per;
+      const int64_t end = __builtin_amdgcn_readlane((int)z, l);
+      return {e0 + l, first, first + per < end ? first + per : end};
+    }
+    before += __builtin_amdgcn_readlane(upto, 63);
+  }
+  return {-1, 0, 0};
+}
+
+// The tile of workgroup b: workgroups b, b + 8, .. share an L2, so each eighth takes neighbouring tiles; within them,
+// bands of 8 units go through the columns together.  False: none left.
+__device__ __forceinline__ bool tile_of(int64_t b, int64_t units, int columns, int64_t &unit, int &column) {
+  const int64_t n = units * columns, each = (n + 7) / 8, t = b % 8 * each + b / 8;
+  if (b / 8 >= each || t >= n) return false;
+  const int64_t band = t / (8 * (int64_t)columns), in = t - band * 8 * columns;
+  const int64_t high = units - band * 8 < 8 ? units - band * 8 : 8;
+  unit = band * 8 + in % high;
+  column = (int)(in / high);
+  return true;
+}
+
+struct GatedArgs {
+  int64_t n_rows, units;
+  int32_t ins, outs, n_matrices, columns;   // columns: tiles across
+  int32_t act;
+  int32_t wide;               // the results' rows take four neighbouring values at once
+  const int32_t *offsets;
+  const void *x, *w_gate, *w_up;
+  void *h, *gate, *up;        // gate, up: NULL where they are not kept
+  // gradients
+  const void *dh;
+  void *dx, *dw_gate, *dw_up;
+  char *d_both;               // dg, then du: [n_rows][pitch] each
+  int64_t pitch;              // bytes
+  int32_t splits;             // of the reduced index: partial results in `partial`
+  float *partial;
+};
+
+template <class T>
+__device__ __forceinline__ void store_four(T *at, const float (&v)[4], int left, bool wide) {
+  if (wide && left >= 4) {
+    struct alignas(4 * sizeof(T)) Four { T t[4]; } r{{(T)v[0], (T)v[1], (T)v[2], (T)v[3]}};
+    *reinterpret_cast<Four *>(at) = r;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < left) at[i] = (T)v[i];
+  }
+}
+
+// f of the activation as a constant
+template <class F>
+__device__ __forceinline__ void with_act(int act, F f) {
+  switch (act) {
+    case SVT_ACT_RELU: return f(std::integral_constant<int, SVT_ACT_RELU>{});
+    case SVT_ACT_SILU: return f(std::integral_constant<int, SVT_ACT_SILU>{});
+    case SVT_ACT_GELU: return f(std::integral_constant<int, SVT_ACT_GELU>{});
+    default: return f(std::integral_constant<int, SVT_ACT_NONE>{});
+  }
+}
+
+// ---- forward -------------------------------------------------------------------------------------
+
+// side P: half a tile of Wg's rows and the same outputs' of Wu; side Q: rows of x
+template <class T, class C, bool ALIGNED>
+__global__ __launch_bounds__(C::threads) void k_gated(GatedArgs a) {
+  using Pr = Product<T, C, false, false, true, ALIGNED>;
+  __shared__ __attribute__((aligned(1024))) char lds[Pr::lds_bytes];
+  int64_t unit;
+  int column;
+  if (!tile_of(blockIdx.x, a.units, a.columns, unit, column)) return;
+  const Rows rows = rows_of_unit(a.offsets, a.n_matrices, a.n_rows, unit, C::q);
+  if (rows.matrix < 0) return;
+  constexpr int outs = C::p / 2;   // of a tile
+  const int n0 = column * outs;
+  const int64_t pitch = (int64_t)a.ins * sizeof(T);
+  const int steps = (a.ins + Pr::SP::step - 1) / Pr::SP::step, tail = a.ins - (steps - 1) * Pr::SP::step;
+  Pr product;
+  product.P.init((uint32_t)pitch, a.outs - n0 < outs ? a.outs - n0 : outs, tail);
+  product.Q.init((uint32_t)pitch, (int)(rows.end - rows.first), tail);
+  const int64_t w0 = ((int64_t)rows.matrix * a.outs + n0) * pitch;
+  const char *wg = (const char *)a.w_gate + w0, *wu = (const char *)a.w_up + w0;
+  const char *x = (const char *)a.x + rows.first * pitch;
+  f32x4 acc[C::nq][C::np] = {};
+  product.run(
+      steps, lds,
+      [&](int s, Base &p, Base &q) {
+        const int64_t k = (int64_t)s * kStepBytes;
+        p = {wg + k, wu + k};
+        q = {x + k, x + k};
+      },
+      [&](int s) { return s + 1 == steps; }, acc);
+  const int wave = (int)threadIdx.x / 64, wq = wave / C::WP, wp = wave % C::WP, i = lane_id() % 16, g = lane_id() / 16;
+  with_act(a.act, [&](auto act) {
+#pragma unroll
+    for (int b = 0; b < C::nq; ++b) {
+      const int64_t row = rows.first + (wq * C::nq + b) * 16 + i;
+      if (row >= rows.end) continue;
+#pragma unroll
+      for (int c = 0; c < C::np / 2; ++c) {
+        const int n = n0 + (wp * (C::np / 2) + c) * 16 + 4 * g, left = a.outs - n;
+        if (left <= 0) continue;
+        float h[4], gate[4], up[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          gate[k] = acc[b][c][k];
+          up[k] = acc[b][C::np / 2 + c][k];
+          h[k] = act_value<decltype(act)::value>(gate[k]) * up[k];
+        }
+        const int64_t at = row * a.outs + n;
+        store_four((T *)a.h + at, h, left, a.wide);
+        if (a.gate) {
+          store_four((T *)a.gate + at, gate, left, a.wide);
+          store_four((T *)a.up + at, up, left, a.wide);
+        }
+      }
+    }
+  });
+}
+
+// ---- forward, few rows ---------------------------------------------------------------------------
+//
+// Up to 16 MT rows of one matrix against 16 outputs: the weights' bytes are the cost, so they go straight to registers,
+// each once, 64 bytes of a row at a time and U such pieces in flight.  The waves share the inputs out and their sums meet
+// in LDS.
+
+constexpr int kFewWaves = 8;
+
+// 16 bytes of a row from index k on, zeros past its end
+template <class T>
+__device__ __forceinline__ typename Mul<T>::frag load_sixteen(const T *row, int k, int end) {
+  constexpr int each = 16 / sizeof(T);
+  struct Values { T t[each]; };
+  struct __attribute__((packed, aligned(sizeof(T)))) Raw { uint8_t v[16]; };
+  if (k + each <= end)
+    return __builtin_bit_cast(typename Mul<T>::frag, *reinterpret_cast<const Raw *>(row + k));
+  Values v{};
+#pragma unroll
+  for (int i = 0; i < each; ++i)
+    if (k + i < end) v.t[i] = row[k + i];
+  return __builtin_bit_cast(typename Mul<T>::frag, v);
+}
+
+template <class T, int MT, int U>
+__global__ __launch_bounds__(64 * kFewWaves) void k_gated_few(GatedArgs a) {
+  __shared__ f32x4 sums[kFewWaves][2 * MT][64];
+  const int64_t unit = blockIdx.x / a.columns;
+  const int column = (int)(blockIdx.x - unit * a.columns);
+  const Rows rows = rows_of_unit(a.offsets, a.n_matrices, a.n_rows, unit, 16 * MT);
+  if (rows.matrix < 0) return;
+  const int wave = (int)threadIdx.x / 64, i = lane_id() % 16, g = lane_id() / 16;
+  constexpr int each = 16 / sizeof(T), step = 4 * each;
+  const int n = column * 16 + i < a.outs ? column * 16 + i : a.outs - 1;   // a copy's sums go nowhere
+  const int64_t at = ((int64_t)rows.matrix * a.outs + n) * a.ins;
+  const T *wg = (const T *)a.w_gate + at, *wu = (const T *)a.w_up + at;
+  const T *x[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int64_t r = rows.first + 16 * m + i;
+    x[m] = (const T *)a.x + (r < rows.end ? r : rows.end - 1) * a.ins;
+  }
+  f32x4 acc[2 * MT] = {};
+  for (int k0 = wave * U * step; k0 < a.ins; k0 += kFewWaves * U * step) {
+    typename Mul<T>::frag fg[U], fu[U], fx[MT][U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * step + g * each;
+      fg[u] = load_sixteen(wg, k, a.ins);
+      fu[u] = load_sixteen(wu, k, a.ins);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) fx[m][u] = load_sixteen(x[m], k, a.ins);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        acc[2 * m] = Mul<T>::add(fg[u], fx[m][u], acc[2 * m]);
+        acc[2 * m + 1] = Mul<T>::add(fu[u], fx[m][u], acc[2 * m + 1]);
+      }
+  }
+#pragma unroll
+  for (int m = 0; m < 2 * MT; ++m) sums[wave][m][lane_id()] = acc[m];
+  __syncthreads();
+  if (wave >= MT) return;
+  f32x4 s[2] = {};
+#pragma unroll
+  for (int w = 0; w < kFewWaves; ++w) {
+    s[0] += sums[w][2 * wave][lane_id()];
+    s[1] += sums[w][2 * wave + 1][lane_id()];
+  }
+  const int64_t row = rows.first + 16 * wave + i;
+  const int n0 = column * 16 + 4 * g, left = a.outs - n0;
+  if (row >= rows.end || left <= 0) return;
+  float h[4], gate[4], up[4];
+  with_act(a.act, [&](auto act) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      gate[k] = s[0][k];
+      up[k] = s[1][k];
+      h[k] = act_value<decltype(act)::value>(gate[k]) * up[k];
+    }
+  });
+  const int64_t to = row * a.outs + n0;
+  store_four((T *)a.h + to, h, left, a.wide);
+  if (a.gate) {
+    store_four((T *)a.gate + to, gate, left, a.wide);
+    store_four((T *)a.up + to, up, left, a.wide);
+  }
+}
+
+// ---- gradients -----------------------------------------------------------------------------------
+
+// dg and du of the rows that some matrix names, with zeros up to the pitch.  They are rounded to the rows' type, as the
+// matrix instructions take them: that is the rounding a gradient kept between two layers has.
+constexpr int kBothThreads = 256;
+
+template <class T>
+__global__ __launch_bounds__(kBothThreads) void k_gated_both(GatedArgs a, int lanes) {
+  constexpr int each = 16 / sizeof(T);
+  struct Values { T t[each]; };
+  struct __attribute__((packed, aligned(sizeof(T)))) Raw { uint8_t v[16]; };
+  const int64_t first = a.offsets ? clamped(a.offsets[0], a.n_rows) : 0;
+  const int64_t end = a.offsets ? clamped(a.offsets[a.n_matrices], a.n_rows) : a.n_rows;
+  const int pieces = (int)(a.pitch / 16), in = threadIdx.x % lanes;
+  const int64_t per = kBothThreads / lanes;
+  with_act(a.act, [&](auto act) {
+    for (int64_t r = first + blockIdx.x * per + threadIdx.x / lanes; r < end; r += gridDim.x * per)
+      for (int c = blockIdx.y * lanes + in; c < pieces; c += gridDim.y * lanes) {
+        const int n = c * each;
+        const int64_t at = r * a.outs + n;
+        Values g{}, u{}, d{};
+        if (n + each <= a.outs) {
+          g = __builtin_bit_cast(Values, *reinterpret_cast<const Raw *>((const T *)a.gate + at));
+          u = __builtin_bit_cast(Values, *reinterpret_cast<const Raw *>((const T *)a.up + at));
+          d = __builtin_bit_cast(Values, *reinterpret_cast<const Raw *>((const T *)a.dh + at));
+        } else {
+#pragma unroll
+          for (int i = 0; i < each; ++i)
+            if (n + i < a.outs) {
+              g.t[i] = ((const T *)a.gate)[at + i];
+              u.t[i] = ((const T *)a.up)[at + i];
+              d.t[i] = ((const T *)a.dh)[at + i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < each; ++i) {
+          float value, slope;
+          act_both<decltype(act)::value>((float)g.t[i], value, slope);
+          const float dh = (float)d.t[i];
+          g.t[i] = (T)(dh * (float)u.t[i] * slope);
+          u.t[i] = (T)(dh * value);
+        }
+        char *to = a.d_both + r * a.pitch + c * 16;
+        *reinterpret_cast<u32x4 *>(to) = __builtin_bit_cast(u32x4, g);
+        *reinterpret_cast<u32x4 *>(to + a.n_rows * a.pitch) = __builtin_bit_cast(u32x4, u);
+      }
+  });
+}
+
+// a tile's result: rows `first` .. `end` of width `width`, columns from c0 on, to `out` or, one part of a split, to `part`
+template <class T, class C>
+__device__ __forceinline__ void store_tile(const f32x4 (&acc)[C::nq][C::np], int64_t first, int64_t end, int c0, int width,
+                                           T *out, float *part, bool wide) {
+  const int wave = (int)threadIdx.x / 64, wq = wave / C::WP, wp = wave % C::WP, i = lane_id() % 16, g = lane_id() / 16;
+#pragma unroll
+  for (int b = 0; b < C::nq; ++b) {
+    const int64_t row = first + (wq * C::nq + b) * 16 + i;
+    if (row >= end) continue;
+#pragma unroll
+    for (int c = 0; c < C::np; ++c) {
+      const int k = c0 + (wp * C::np + c) * 16 + 4 * g, left = width - k;
+      if (left <= 0) continue;
+      const float v[4] = {acc[b][c][0], acc[b][c][1], acc[b][c][2], acc[b][c][3]};
+      if (part) store_four(part + row * width + k, v, left, width % 4 == 0);
+      else store_four(out + row * width + k, v, left, wide);
+    }
+  }
+}
+
+// dx: side P: columns of Wg, then of Wu (across); side Q: rows of dg, then of du (along)
+template <class T, class C, bool ALIGNED>
+__global__ __launch_bounds__(C::threads) void k_gated_dx(GatedArgs a) {
+  using Pr = Product<T, C, true, false, false, ALIGNED>;
+  __shared__ __attribute__((aligned(1024))) char lds[Pr::lds_bytes];
+  int64_t unit;
+  int column;
+  if (!tile_of(blockIdx.x, a.units, a.columns, unit, column)) return;
+  const Rows rows = rows_of_unit(a.offsets, a.n_matrices, a.n_rows, unit, C::q);
+  if (rows.matrix < 0) return;
+  const int k0 = column * C::p;
+  const int64_t pitch = (int64_t)a.ins * sizeof(T);
+  const int half = (a.outs + Pr::SP::step - 1) / Pr::SP::step, tail = a.outs - (half - 1) * Pr::SP::step;
+  const int each = (2 * half + a.splits - 1) / a.splits, s0 = blockIdx.y * each;
+  const int steps = 2 * half - s0 < each ? 2 * half - s0 : each;   // none, or fewer, for the last part
+  Pr product;
+  product.P.init((uint32_t)pitch, a.ins - k0 < C::p ? a.ins - k0 : C::p, tail);
+  product.Q.init((uint32_t)a.pitch, (int)(rows.end - rows.first), tail);
+  const int64_t w0 = (int64_t)rows.matrix * a.outs * pitch + (int64_t)k0 * sizeof(T);
+  const char *wg = (const char *)a.w_gate + w0, *wu = (const char *)a.w_up + w0;
+  const char *dg = a.d_both + rows.first * a.pitch, *du = dg + a.n_rows * a.pitch;
+  f32x4 acc[C::nq][C::np] = {};
+  product.run(
+      steps, lds,
+      [&](int t, Base &p, Base &q) {
+        const int s = s0 + t, in = s < half ? s : s - half;
+        const char *w = (s < half ? wg : wu) + (int64_t)in * Pr::SP::step * pitch;
+        const char *d = (s < half ? dg : du) + (int64_t)in * kStepBytes;
+        p = {w, w};
+        q = {d, d};
+      },
+      [&](int t) { return s0 + t + 1 == half || s0 + t + 1 == 2 * half; }, acc);
+  store_tile<T, C>(acc, rows.first, rows.end, k0, a.ins, (T *)a.dx,
+                   a.splits > 1 ? a.partial + (int64_t)blockIdx.y * a.n_rows * a.ins : nullptr, a.wide);
+}
+
+// dWg and dWu: side P: columns of x (across), side Q: columns of dg or du (across); the rows are reduced
+template <class T, class C, bool ALIGNED>
+__global__ __launch_bounds__(C::threads) void k_gated_dw(GatedArgs a) {
+  using Pr = Product<T, C, true, true, false, ALIGNED>;
+  __shared__ __attribute__((aligned(1024))) char lds[Pr::lds_bytes];
+  int64_t unit;
+  int column;
+  if (!tile_of(blockIdx.x, a.units, a.columns, unit, column)) return;
+  const int tiles = (a.outs + C::q - 1) / C::q;
+  const int matrix = (int)(unit / (2 * tiles)), in = (int)(unit - (int64_t)matrix * 2 * tiles);
+  const bool up = in >= tiles;
+  const int n0 = (up ? in - tiles : in) * C::q, k0 = column * C::p;
+  const int64_t first = a.offsets ? clamped(a.offsets[matrix], a.n_rows) : 0;
+  const int64_t end = a.offsets ? clamped(a.offsets[matrix + 1], a.n_rows) : a.n_rows;
+  const int64_t len = end > first ? end - first : 0, all = (len + Pr::SP::step - 1) / Pr::SP::step;
+  const int64_t each = (all + a.splits - 1) / a.splits, s0 = blockIdx.y * each;
+  const int steps = (int)(all - s0 < each ? all - s0 : each);
+  const int64_t pitch = (int64_t)a.ins * sizeof(T);
+  Pr product;
+  const int tail = (int)(len - (all - 1) * Pr::SP::step);
+  product.P.init((uint32_t)pitch, a.ins - k0 < C::p ? a.ins - k0 : C::p, tail);
+  product.Q.init((uint32_t)a.pitch, a.outs - n0 < C::q ? a.outs - n0 : C::q, tail);
+  const char *x = (const char *)a.x + first * pitch + (int64_t)k0 * sizeof(T);
+  const char *d = a.d_both + (up ? a.n_rows * a.pitch : 0) + first * a.pitch + (int64_t)n0 * sizeof(T);
+  f32x4 acc[C::nq][C::np] = {};
+  product.run(
+      steps, lds,
+      [&](int t, Base &p, Base &q) {
+        const int64_t s = (s0 + t) * Pr::SP::step;
+        p = {x + s * pitch, x + s * pitch};
+        q = {d + s * a.pitch, d + s * a.pitch};
+      },
+      [&](int t) { return s0 + t + 1 == all; }, acc);
+  const int64_t size = (int64_t)a.outs * a.ins, of = matrix * size;
+  float *part = a.splits > 1 ? a.partial + (((int64_t)blockIdx.y * 2 + up) * a.n_matrices) * size + of : nullptr;
+  store_tile<T, C>(acc, n0, a.outs, k0, a.ins, (T *)(up ? a.dw_up : a.dw_gate) + of, part, a.wide);
+}
+
+// out[i] = the sum of the parts, in order; of each part `size` values, the last half of them to `upper` (half == size: none).
+// Rows that no matrix names keep their values where `width` is given (dx).
+template <class T>
+__global__ __launch_bounds__(256) void k_gated_parts(const float *partial, int splits, int64_t size, int64_t half, T *out,
+                                                     T *upper, GatedArgs a, int width) {
+  int64_t first = 0, end = size;
+  if (width && a.offsets) {
+    first = clamped(a.offsets[0], a.n_rows) * width;
+    end = clamped(a.offsets[a.n_matrices], a.n_rows) * width;
+  }
+  for (int64_t i = first + blockIdx.x * 256ll + threadIdx.x; i < end; i += gridDim.x * 256ll) {
+    float sum = partial[i];
+    for (int z = 1; z < splits; ++z) sum += partial[z * size + i];
+    if (i < half) out[i] = (T)sum;
+    else upper[i - half] = (T)sum;
+  }
+}
+
+// ---- calls ---------------------------------------------------------------------------------------
+
+// how a call runs; the same for the workspace's size
+struct GatedPlan {
+  int cut;         // 0: 64 x 128, 1: 128 x 128, 2: 256 x 256
+  int splits;
+  int64_t units;
+  int columns;
+};
+
+constexpr int kCutQ[3] = {64, 128, 256}, kCutP[3] = {128, 128, 256};
+
+// blocks of rows at most: every matrix may end inside one
+inline int64_t row_units(int64_t n_rows, int n_matrices, bool by_expert, int per) {
+  return by_expert ? n_rows / per + (n_rows < n_matrices ? n_rows : n_matrices) : (n_rows + per - 1) / per;
+}
+
+// The largest cut whose tiles give most compute units (256) work; the smallest if none does, its reduced index split
+inline GatedPlan plan_cut(int64_t (*units)(const GatedArgs &, int), const GatedArgs &a, int width, int64_t steps) {
+  GatedPlan p{};
+  for (p.cut = 2; p.cut >= 0; --p.cut) {
+    p.units = units(a, kCutQ[p.cut]);
+    p.columns = (width + kCutP[p.cut] - 1) / kCutP[p.cut];
+    if (p.units * p.columns >= 192) break;
+  }
+  if (p.cut < 0) p.cut = 0;
+  p.splits = 1;
+  const int64_t tiles = p.units * p.columns;
+  if (steps > 0 && tiles < 192) {
+    const int64_t want = 512 / (tiles > 0 ? tiles : 1), most = steps / 4;   // at least 4 steps for each part
+    p.splits = (int)(want < most ? want : most);
+    if (p.splits > 32) p.splits = 32;
+    if (p.splits < 1) p.splits = 1;
+  }
+  return p;
+}
+
+inline GatedPlan plan_forward(const GatedArgs &a) {
+  return plan_cut([](const GatedArgs &g, int q) { return row_units(g.n_rows, g.n_matrices, g.offsets != nullptr, q); }, a,
+                  2 * a.outs, 0);
+}
+inline GatedPlan plan_dx(const GatedArgs &a, int elem) {
+  const int step = kStepBytes / elem;
+  return plan_cut([](const GatedArgs &g, int q) { return row_units(g.n_rows, g.n_matrices, g.offsets != nullptr, q); }, a,
+                  a.ins, 2 * ((a.outs + step - 1) / step));
+}
+inline GatedPlan plan_dw(const GatedArgs &a, int elem) {
+  const int step = kStepBytes / elem;
+  return plan_cut([](const GatedArgs &g, int q) { return (int64_t)g.n_matrices * 2 * ((g.outs + q - 1) / q); }, a, a.ins,
+                  a.n_rows / a.n_matrices / step);
+}
+
+// a grid's threads stay below 2^32
+inline bool fits(const GatedPlan &p) { return p.units * p.columns < (1 << 22) / p.splits; }
+
+inline int64_t gated_pitch(int32_t outs, int elem) { return ((int64_t)outs * elem + 15) & ~(int64_t)15; }
+
+// bytes of the partial results, of dx and of dW (one after the other in the same place)
+inline size_t gated_partial(const GatedArgs &a, int elem) {
+  size_t most = 0;
+  if (a.n_rows == 0) return 0;
+  if (a.dx) {
+    const GatedPlan p = plan_dx(a, elem);
+    if (p.splits > 1) most = (size_t)p.splits * a.n_rows * a.ins * 4;
+  }
+  if (a.dw_gate) {
+    const GatedPlan p = plan_dw(a, elem);
+    const size_t n = p.splits > 1 ? (size_t)p.splits * 2 * a.n_matrices * a.outs * a.ins * 4 : 0;
+    if (n > most) most = n;
+  }
+  return most;
+}
+
+// one type's calls
+template <class T> int gated_forward(const char *who, GatedArgs a, bool aligned, void *stream);
+template <class T> int gated_backward(const char *who, GatedArgs a, bool aligned, void *stream);
+
+#ifdef SVT_GATED_INSTANTIATE
+
+template <class F>
+int with_cut(int cut, bool aligned, F f) {
+  auto with = [&](auto c) { return aligned ? f(c, std::true_type{}) : f(c, std::false_type{}); };
+  if (cut == 2) return with(Cut<256, 256, 2, 4>{});
+  if (cut == 1) return with(Cut<128, 128, 2, 2>{});
+  return with(Cut<64, 128, 1, 4>{});
+}
+
+inline int64_t eighths(int64_t tiles) { return (tiles + 7) / 8 * 8; }
+
+template <class T>
+int gated_forward(const char *who, GatedArgs a, bool aligned, void *stream) {
+  // few rows for each matrix: straight from memory
+  const int64_t few = a.offsets ? (a.n_rows + a.n_matrices - 1) / a.n_matrices : a.n_rows;
+  if (few <= (a.offsets ? 24 : 64)) {
+    const int mt = few <= 16 ? 1 : few <= 32 ? 2 : 4;
+    a.units = row_units(a.n_rows, a.n_matrices, a.offsets != nullptr, 16 * mt);
+    a.columns = (a.outs + 15) / 16;
+    if (a.units * a.columns < (1 << 22)) {
+      const unsigned grid = (unsigned)(a.units * a.columns);
+      if (mt == 1) return launch(who, k_gated_few<T, 1, 8>, grid, 64 * kFewWaves, 0, stream, a);
+      if (mt == 2) return launch(who, k_gated_few<T, 2, 4>, grid, 64 * kFewWaves, 0, stream, a);
+      return launch(who, k_gated_few<T, 4, 2>, grid, 64 * kFewWaves, 0, stream, a);
+    }
+  }
+  const GatedPlan p = plan_forward(a);
+  a.units = p.units;
+  a.columns = p.columns;
+  return with_cut(p.cut, aligned, [&](auto cut, auto al) {
+    using C = decltype(cut);
+    return launch(who, k_gated<T, C, decltype(al)::value>, (unsigned)eighths(a.units * a.columns), C::threads, 0, stream, a);
+  });
+}
+
+template <class T>
+int gated_backward(const char *who, GatedArgs a, bool aligned, void *stream) {
+  constexpr int b = sizeof(T);
+  int rc = SVT_OK;
+  if (a.n_rows > 0) {
+    int lanes = 1;
+    while (lanes < kBothThreads && lanes < a.pitch / 16) lanes *= 2;
+    const int64_t per = kBothThreads / lanes, blocks = (a.n_rows + per - 1) / per;
+    const int64_t columns = (a.pitch / 16 + lanes - 1) / lanes;
+    rc = launch(who, k_gated_both<T>, dim3((unsigned)(blocks < 65536 ? blocks : 65536), (unsigned)(columns < 64 ? columns : 64)),
+                kBothThreads, 0, stream, a, lanes);
+    if (rc != SVT_OK) return rc;
+  }
+  auto parts = [&](int64_t size, int64_t half, void *out, void *upper, int width) {
+    const int64_t blocks = (size + 255) / 256;
+    return launch(who, k_gated_parts<T>, (unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, stream, (const float *)a.partial,
+                  a.splits, size, half, (T *)out, (T *)upper, a, width);
+  };
+  if (a.dx && a.n_rows > 0) {
+    const GatedPlan p = plan_dx(a, b);
+    a.units = p.units;
+    a.columns = p.columns;
+    a.splits = p.splits;
+    rc = with_cut(p.cut, aligned, [&](auto cut, auto al) {
+      using C = decltype(cut);
+      return launch(who, k_gated_dx<T, C, decltype(al)::value>, dim3((unsigned)eighths(a.units * a.columns), p.splits),
+                    C::threads, 0, stream, a);
+    });
+    if (rc == SVT_OK && p.splits > 1) rc = parts(a.n_rows * a.ins, a.n_rows * a.ins, a.dx, nullptr, a.ins);
+    if (rc != SVT_OK) return rc;
+  }
+  if (a.dw_gate) {
+    const GatedPlan p = plan_dw(a, b);
+    a.units = p.units;
+    a.columns = p.columns;
+    a.splits = p.splits;
+    rc = with_cut(p.cut, aligned, [&](auto cut, auto al) {
+      using C = decltype(cut);
+      return launch(who, k_gated_dw<T, C, decltype(al)::value>, dim3((unsigned)eighths(a.units * a.columns), p.splits),
+                    C::threads, 0, stream, a);
+    });
+    const int64_t size = (int64_t)a.n_matrices * a.outs * a.ins;
+    if (rc == SVT_OK && p.splits > 1) rc = parts(2 * size, size, a.dw_gate, a.dw_up, 0);
+  }
+  return rc;
+}
+
+#endif   // SVT_GATED_INSTANTIATE
+
+}  // namespace svt

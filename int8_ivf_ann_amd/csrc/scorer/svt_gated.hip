@@ -1,0 +1,149 @@
+// svt_gated.hip - the entry points of products with a gate: arguments checked, the type's kernels called (svt_gated.h).
+#include "svt_gated.h"
+
+namespace svt {
+
+namespace {
+
+int check_gated(const char *who, int32_t n_rows, int32_t n_in, int32_t n_out, int32_t n_matrices, int32_t dtype,
+                int32_t activation, bool by_expert) {
+  if (n_rows < 0) return report(SVT_EINVAL, "%s: n_rows %d < 0", who, n_rows);
+  if (n_in < 1 || n_in > kGatedMax) return report(SVT_EINVAL, "%s: n_in %d out of [1, %d]", who, n_in, kGatedMax);
+  if (n_out < 1 || n_out > kGatedMax) return report(SVT_EINVAL, "%s: n_out %d out of [1, %d]", who, n_out, kGatedMax);
+  if (n_matrices < 1 || n_matrices > SVT_MAX_EXPERTS)
+    return report(SVT_EINVAL, "%s: n_matrices %d out of [1, %d]", who, n_matrices, SVT_MAX_EXPERTS);
+  if (!by_expert && n_matrices != 1)
+    return report(SVT_EINVAL, "%s: %d matrices need offsets", who, n_matrices);
+  if (!elem_size(dtype)) return report(SVT_EINVAL, "%s: unknown element type %d", who, dtype);
+  if (activation < SVT_ACT_NONE || activation > SVT_ACT_GELU)
+    return report(SVT_EINVAL, "%s: unknown activation %d", who, activation);
+  return SVT_OK;
+}
+
+struct Span { const void *at; size_t bytes; };
+
+// whether any of outs overlaps an input or another output
+bool any_overlap(const Span *ins, int n_ins, const Span *outs, int n_outs) {
+  for (int i = 0; i < n_outs; ++i) {
+    for (int j = 0; j < n_ins; ++j)
+      if (overlap(outs[i].at, outs[i].bytes, ins[j].at, ins[j].bytes)) return true;
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i].at, outs[i].bytes, outs[j].at, outs[j].bytes)) return true;
+  }
+  return false;
+}
+
+}  // namespace
+
+}  // namespace svt
+
+using namespace svt;
+
+extern "C" int svt_gated_linear(int32_t n_rows, int32_t n_in, int32_t n_out, int32_t n_matrices, int32_t dtype,
+                                const void *x, const void *w_gate, const void *w_up, const int32_t *offsets,
+                                int32_t activation, void *h, void *gate, void *up, void *hip_stream) {
+  const char *who = "svt_gated_linear";
+  (void)report(SVT_OK, "%s", "");
+  const int rc = check_gated(who, n_rows, n_in, n_out, n_matrices, dtype, activation, offsets != nullptr);
+  if (rc != SVT_OK || n_rows == 0) return rc;
+  if (!x || !w_gate || !w_up || !h) return report(SVT_EINVAL, "%s: NULL input or output", who);
+  if (!gate != !up) return report(SVT_EINVAL, "%s: gate and up are kept both or neither", who);
+  const int b = elem_size(dtype);
+  if (misaligned(x, b) || misaligned(w_gate, b) || misaligned(w_up, b) || misaligned(offsets, 4) || misaligned(h, b) ||
+      misaligned(gate, b) || misaligned(up, b))
+    return report(SVT_EINVAL, "%s: misaligned input or output", who);
+  const size_t nx = (size_t)n_rows * n_in * b, nw = (size_t)n_matrices * n_out * n_in * b, nh = (size_t)n_rows * n_out * b;
+  const Span ins[4] = {{x, nx}, {w_gate, nw}, {w_up, nw}, {offsets, ((size_t)n_matrices + 1) * 4}};
+  const Span outs[3] = {{h, nh}, {gate, nh}, {up, nh}};
+  if (any_overlap(ins, 4, outs, 3)) return report(SVT_EINVAL, "%s: an output overlaps an input or another output", who);
+  GatedArgs a{};
+  a.n_rows = n_rows;
+  a.ins = n_in;
+  a.outs = n_out;
+  a.n_matrices = n_matrices;
+  a.act = activation;
+  a.offsets = offsets;
+  a.x = x;
+  a.w_gate = w_gate;
+  a.w_up = w_up;
+  a.h = h;
+  a.gate = gate;
+  a.up = up;
+  a.splits = 1;
+  a.wide = n_out % 4 == 0 && !misaligned(h, 4 * b) && !misaligned(gate, 4 * b) && !misaligned(up, 4 * b);
+  if (!fits(plan_forward(a))) return report(SVT_EINVAL, "%s: too many rows of too many outputs for one call", who);
+  const bool aligned = (size_t)n_in * b % 16 == 0 && !misaligned(x, 16) && !misaligned(w_gate, 16) && !misaligned(w_up, 16);
+  return with_type(dtype, [&](auto ty) { return gated_forward<decltype(ty)>(who, a, aligned, hip_stream); });
+}
+
+extern "C" size_t svt_gated_linear_backward_workspace_size(int32_t n_rows, int32_t n_in, int32_t n_out, int32_t n_matrices,
+                                                           int32_t dtype, int32_t by_expert) {
+  const char *who = "svt_gated_linear_backward_workspace_size";
+  (void)report(SVT_OK, "%s", "");
+  if (check_gated(who, n_rows, n_in, n_out, n_matrices, dtype, SVT_ACT_NONE, by_expert != 0) != SVT_OK) return 0;
+  GatedArgs a{};
+  a.n_rows = n_rows;
+  a.ins = n_in;
+  a.outs = n_out;
+  a.n_matrices = n_matrices;
+  a.offsets = by_expert ? (const int32_t *)&a : nullptr;   // present or not, never read
+  a.dx = a.dw_gate = &a;
+  const int b = elem_size(dtype);
+  return (size_t)(2 * n_rows * gated_pitch(n_out, b)) + gated_partial(a, b);
+}
+
+extern "C" int svt_gated_linear_backward(int32_t n_rows, int32_t n_in, int32_t n_out, int32_t n_matrices, int32_t dtype,
+                                         const void *dh, const void *x, const void *w_gate, const void *w_up,
+                                         const void *gate, const void *up, const int32_t *offsets, int32_t activation,
+                                         void *dx, void *dw_gate, void *dw_up, void *workspace, size_t workspace_bytes,
+                                         void *hip_stream) {
+  const char *who = "svt_gated_linear_backward";
+  (void)report(SVT_OK, "%s", "");
+  const int rc = check_gated(who, n_rows, n_in, n_out, n_matrices, dtype, activation, offsets != nullptr);
+  if (rc != SVT_OK) return rc;
+  if (!dw_gate != !dw_up) return report(SVT_EINVAL, "%s: dw_gate and dw_up are given both or neither", who);
+  if (!dx && !dw_gate && n_rows > 0) return report(SVT_EINVAL, "%s: NULL outputs", who);
+  if (n_rows == 0 && !dw_gate) return SVT_OK;
+  if (n_rows > 0 && (!dh || !gate || !up || (dw_gate && !x) || (dx && (!w_gate || !w_up))))
+    return report(SVT_EINVAL, "%s: NULL input", who);
+  const int b = elem_size(dtype);
+  const void *elems[9] = {dh, x, w_gate, w_up, gate, up, dx, dw_gate, dw_up};
+  for (const void *p : elems)
+    if (misaligned(p, b)) return report(SVT_EINVAL, "%s: misaligned input or output", who);
+  if (misaligned(offsets, 4) || misaligned(workspace, 16))
+    return report(SVT_EINVAL, "%s: misaligned offsets or workspace", who);
+  GatedArgs a{};
+  a.n_rows = n_rows;
+  a.ins = n_in;
+  a.outs = n_out;
+  a.n_matrices = n_matrices;
+  a.act = activation;
+  a.offsets = offsets;
+  a.x = x;
+  a.w_gate = w_gate;
+  a.w_up = w_up;
+  a.gate = const_cast<void *>(gate);
+  a.up = const_cast<void *>(up);
+  a.dh = dh;
+  a.dx = dx;
+  a.dw_gate = dw_gate;
+  a.dw_up = dw_up;
+  a.splits = 1;
+  a.pitch = gated_pitch(n_out, b);
+  const size_t both = (size_t)(2 * n_rows * a.pitch), need = both + gated_partial(a, b);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return report(SVT_EINVAL, "%s: workspace of %zu bytes, needs %zu", who, workspace ? workspace_bytes : (size_t)0, need);
+  const size_t nx = (size_t)n_rows * n_in * b, nw = (size_t)n_matrices * n_out * n_in * b, nh = (size_t)n_rows * n_out * b;
+  const Span ins[7] = {{dh, nh}, {x, nx}, {w_gate, nw}, {w_up, nw}, {gate, nh}, {up, nh},
+                       {offsets, ((size_t)n_matrices + 1) * 4}};
+  const Span outs[4] = {{dx, nx}, {dw_gate, nw}, {dw_up, nw}, {workspace, need}};
+  if (any_overlap(ins, 7, outs, 4))
+    return report(SVT_EINVAL, "%s: an output or the workspace overlaps an input or another output", who);
+  if ((dx && !fits(plan_dx(a, b))) || (dw_gate && !fits(plan_dw(a, b))))
+    return report(SVT_EINVAL, "%s: too large a product for one call", who);
+  a.d_both = (char *)workspace;
+  a.partial = (float *)(a.d_both + both);
+  a.wide = n_in % 4 == 0 && !misaligned(dx, 4 * b) && !misaligned(dw_gate, 4 * b) && !misaligned(dw_up, 4 * b);
+  const bool aligned = (size_t)n_in * b % 16 == 0 && !misaligned(x, 16) && !misaligned(w_gate, 16) && !misaligned(w_up, 16);
+  return with_type(dtype, [&](auto ty) { return gated_backward<decltype(ty)>(who, a, aligned, hip_stream); });
+}

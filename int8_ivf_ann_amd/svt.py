@@ -26,7 +26,7 @@ SVT_MAX_MASK_GROUPS = 4
 SVT_NOALLOC_SCRATCH_BYTES = 256 << 20
 SVT_RERANK_MAX_EXPERTS, SVT_RERANK_MAX_UNITS, SVT_RERANK_MAX_CAND, SVT_RERANK_MAX_OUT = 8, 64, 4096, 2048
 SVT_F32, SVT_F16, SVT_BF16 = 0, 1, 2
-SVT_ACT_NONE, SVT_ACT_RELU = 0, 1
+SVT_ACT_NONE, SVT_ACT_RELU, SVT_ACT_SILU, SVT_ACT_GELU = 0, 1, 2, 3
 SVT_MAX_EXPERTS, SVT_MAX_TOP = 512, 16
 _PATHS = {"auto": SVT_PATH_AUTO, "query": SVT_PATH_QUERY, "tile": SVT_PATH_TILE, "large_k": SVT_PATH_LARGE_K}
 
@@ -37,6 +37,7 @@ EXPORTED = ("svt_index_upload", "svt_index_upload_updatable", "svt_index_insert"
             "svt_expert_sort_workspace_size", "svt_expert_sort", "svt_expert_dispatch", "svt_expert_dispatch_backward",
             "svt_expert_combine", "svt_expert_combine_backward", "svt_quant_pack_size", "svt_quant_pack",
             "svt_quant_linear", "svt_embedding", "svt_embedding_backward_workspace_size", "svt_embedding_backward",
+            "svt_gated_linear", "svt_gated_linear_backward_workspace_size", "svt_gated_linear_backward",
             "svt_token_logprobs_workspace_size", "svt_token_logprobs", "svt_token_logprobs_backward", "svt_last_error", "svt_bloom_mask", "svt_bloom_sign", "svt_profile_enable", "svt_profile_read")
 
 
@@ -148,6 +149,11 @@ def lib():
     L.svt_embedding_backward_workspace_size.argtypes = [i64, i64, i32]
     L.svt_embedding_backward_workspace_size.restype = sz
     L.svt_embedding_backward.argtypes = [i64, i64, i32, i32, vp, vp, f32, i32, i32, vp, vp, sz, vp]
+    L.svt_gated_linear.argtypes = [i32, i32, i32, i32, i32, vp, vp, vp, vp, i32, vp, vp, vp, vp]
+    L.svt_gated_linear_backward_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32]
+    L.svt_gated_linear_backward_workspace_size.restype = sz
+    L.svt_gated_linear_backward.argtypes = [i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, sz,
+                                            vp]
     L.svt_token_logprobs_workspace_size.argtypes = [i32, i32, i32]
     L.svt_token_logprobs_workspace_size.restype = sz
     L.svt_token_logprobs.argtypes = [i32, i32, i32, i32, vp, vp, f32, vp, vp, vp, vp, vp, vp, sz, vp]
@@ -811,6 +817,77 @@ def svt_embedding_backward(d_out, ids, n_rows: int, scale: float = 1.0, out=None
         _check(lib().svt_embedding_backward(n, n_rows, D, code, d_out.data_ptr(), ids.data_ptr(), scale, int(accumulate),
                                             _types()[out_dtype], out.data_ptr(), at, size, s))
     return out
+
+
+_GATES = {"none": SVT_ACT_NONE, "relu": SVT_ACT_RELU, "silu": SVT_ACT_SILU, "gelu": SVT_ACT_GELU}
+
+
+def _gated_shape(x, w_gate, w_up, offsets, activation):
+    """(rows, inputs, outputs, matrices, element type, device, activation's code) of a gated product."""
+    import torch
+    (R, K), code, dev = _rows_of("x", x)
+    if not hasattr(w_gate, "dim") or w_gate.dim() != (2 if offsets is None else 3):
+        raise ValueError("w_gate: expected a tensor " + ("[N, K]" if offsets is None else "[M, N, K]"))
+    M, N = 1 if offsets is None else w_gate.shape[0], w_gate.shape[-2]
+    shape = (N, K) if offsets is None else (M, N, K)
+    _check_dense("w_gate", w_gate, x.dtype, shape, dev)
+    _check_dense("w_up", w_up, x.dtype, shape, dev)
+    if offsets is not None:
+        _check_dense("offsets", offsets, torch.int32, (M + 1,), dev)
+    if activation not in _GATES:
+        raise ValueError(f"activation: {activation!r} not in {sorted(_GATES)}")
+    return R, K, N, M, code, dev, _GATES[activation]
+
+
+def svt_gated_linear(x, w_gate, w_up, offsets=None, activation: str = "silu", keep: bool = False, out=None, out_gate=None,
+                     out_up=None, stream=None):
+    """h = act(x w_gate^T) * (x w_up^T): x [R, K] (float32, float16, bfloat16), w_gate and w_up [N, K] of its dtype -> h
+    [R, N].  With ``offsets`` int32 [M + 1] (svt_expert_sort's) the weights are [M, N, K], pair e serves rows offsets[e]
+    .. offsets[e + 1] - 1, and rows past the last stay as they were.  activation: "silu", "gelu", "relu" or "none".
+    ``keep`` also returns what the gradient needs: (h, gate, up)."""
+    R, K, N, M, code, dev, act = _gated_shape(x, w_gate, w_up, offsets, activation)
+    with _Run(dev, stream) as s:
+        out = _out("out", out, x.dtype, (R, N), dev, x)
+        if keep:
+            out_gate = _out("out_gate", out_gate, x.dtype, (R, N), dev, x)
+            out_up = _out("out_up", out_up, x.dtype, (R, N), dev, x)
+        _check(lib().svt_gated_linear(R, K, N, M, code, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
+                                      None if offsets is None else offsets.data_ptr(), act, out.data_ptr(),
+                                      out_gate.data_ptr() if keep else None, out_up.data_ptr() if keep else None, s))
+    return (out, out_gate, out_up) if keep else out
+
+
+@functools.lru_cache(maxsize=256)
+def svt_gated_linear_backward_workspace_size(n_rows: int, n_in: int, n_out: int, n_matrices: int, dtype: int,
+                                             by_expert: bool) -> int:
+    """Bytes of workspace that svt_gated_linear_backward needs for these sizes; dtype: SVT_F32, SVT_F16 or SVT_BF16."""
+    need = lib().svt_gated_linear_backward_workspace_size(n_rows, n_in, n_out, n_matrices, dtype, int(by_expert))
+    if need == 0 and svt_last_error():
+        raise SvtError(SVT_EINVAL, svt_last_error())
+    return int(need)
+
+
+def svt_gated_linear_backward(dh, x, w_gate, w_up, gate, up, offsets=None, activation: str = "silu", out_x=None,
+                              out_gate=None, out_up=None, need_x: bool = True, need_weights: bool = True, workspace=None,
+                              stream=None):
+    """The gradients of svt_gated_linear: dh [R, N], its inputs and what it kept -> (dx [R, K], d_gate and d_up like
+    w_gate and w_up).  ``need_x`` and ``need_weights`` leave one part out (None in its place).  Rows that no pair of
+    matrices names stay as they were in dx; a pair without rows gets zeros."""
+    R, K, N, M, code, dev, act = _gated_shape(x, w_gate, w_up, offsets, activation)
+    for name, t in (("dh", dh), ("gate", gate), ("up", up)):
+        _check_dense(name, t, x.dtype, (R, N), dev)
+    need = svt_gated_linear_backward_workspace_size(R, K, N, M, code, offsets is not None)
+    with _Run(dev, stream) as s:
+        out_x = _out("out_x", out_x, x.dtype, (R, K), dev, x) if need_x else None
+        out_gate = _out("out_gate", out_gate, x.dtype, w_gate.shape, dev, x) if need_weights else None
+        out_up = _out("out_up", out_up, x.dtype, w_gate.shape, dev, x) if need_weights else None
+        workspace, at, size = _workspace(workspace, need, dev, x)
+        _check(lib().svt_gated_linear_backward(R, K, N, M, code, dh.data_ptr(), x.data_ptr(), w_gate.data_ptr(),
+                                               w_up.data_ptr(), gate.data_ptr(), up.data_ptr(),
+                                               None if offsets is None else offsets.data_ptr(), act,
+                                               *[None if t is None else t.data_ptr() for t in (out_x, out_gate, out_up)],
+                                               at, size, s))
+    return out_x, out_gate, out_up
 
 
 @functools.lru_cache(maxsize=256)
