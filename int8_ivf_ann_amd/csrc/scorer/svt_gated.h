@@ -100,10 +100,10 @@ constexpr int kStepBytes = 128;                    // of the reduced index
 constexpr uint32_t kOutside = 0x80000000u;         // an offset past every buffer's range
 constexpr int kRange = 0x7FFFFFF0;
 
-// Q x P columns of the result, waves WQ x WP
-template <int Q, int P, int WQ_, int WP_>
+// Q x P columns of the result, waves WQ x WP, buffers
+template <int Q, int P, int WQ_, int WP_, int BUFFERS>
 struct Cut {
-  static constexpr int q = Q, p = P, WQ = WQ_, WP = WP_;
+  static constexpr int q = Q, p = P, WQ = WQ_, WP = WP_, buffers = BUFFERS;
   static constexpr int threads = 64 * WQ * WP;
   static constexpr int nq = Q / WQ / 16, np = P / WP / 16;   // 16 x 16 blocks of a wave
 };
@@ -123,9 +123,10 @@ struct Side {
 
   // which piece of row `row` lies at its place `at` (an involution)
   static __device__ __forceinline__ int permuted(int row, int at) {
+    static_assert((row_pieces & (row_pieces - 1)) == 0, "a place stays inside its row");
     if constexpr (!ACROSS) return at ^ ((row >> 1) & 7);
     else if constexpr (b == 2) return at ^ ((2 * ((row & 3) | ((row >> 3) & 1) << 2)) & (row_pieces - 1));
-    else return at ^ (4 * ((row >> 2) & 3));
+    else return at ^ ((4 * ((row >> 2) & 3)) & (row_pieces - 1));
   }
 
   uint32_t offset[pieces];   // of the thread's pieces; kOutside: zeros
@@ -225,8 +226,12 @@ struct Side {
   }
 };
 
-// all loads of this wave, to registers or to LDS, have arrived
-__device__ __forceinline__ void loads_done() { __builtin_amdgcn_s_waitcnt(0x0F70); }
+// all loads of this wave but the LATER latest, to registers or to LDS, have arrived
+template <int LATER>
+__device__ __forceinline__ void loads_done() {
+  static_assert(LATER < 64, "six bits");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (LATER & 15) | (LATER >> 4) << 14);
+}
 
 // acc[b][a] += the product of `steps` steps: lane l holds rows 16 b + l % 16 of its wave's part, columns
 // 16 a + 4 (l / 16) .. + 3.  base(s, p, q): where step s begins; last(s): whether its pieces may end early.
@@ -235,14 +240,14 @@ template <class T, class C, bool PA, bool QA, bool HALVES, bool ALIGNED>
 struct Product {
   using SP = Side<T, C::p, C::threads, PA, HALVES>;
   using SQ = Side<T, C::q, C::threads, QA>;
-  static constexpr int bytes = SP::bytes + SQ::bytes, lds_bytes = ALIGNED ? 2 * bytes : bytes;
+  static constexpr int bytes = SP::bytes + SQ::bytes, lds_bytes = ALIGNED ? C::buffers * bytes : bytes;
   SP P;
   SQ Q;
 
-  static __device__ __forceinline__ void multiply(const char *lds, int wq, int wp, f32x4 (&acc)[C::nq][C::np]) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      typename Mul<T>::frag p[C::np];
+  // a wave's fragments of half h of a step
+  struct Fragments {
+    typename Mul<T>::frag p[C::np], q[C::nq];
+    __device__ __forceinline__ void read(const char *lds, int wq, int wp, int h) {
 #pragma unroll
       for (int i = 0; i < C::np; ++i) {
         constexpr int half = C::np / 2;
@@ -250,10 +255,35 @@ struct Product {
         p[i] = SP::fragment(lds, block, h);
       }
 #pragma unroll
-      for (int i = 0; i < C::nq; ++i) {
-        const typename Mul<T>::frag q = SQ::fragment(lds + SP::bytes, wq * C::nq + i, h);
+      for (int i = 0; i < C::nq; ++i) q[i] = SQ::fragment(lds + SP::bytes, wq * C::nq + i, h);
+    }
+    __device__ __forceinline__ void multiply(f32x4 (&acc)[C::nq][C::np]) const {
 #pragma unroll
-        for (int j = 0; j < C::np; ++j) acc[i][j] = Mul<T>::add(p[j], q, acc[i][j]);
+      for (int i = 0; i < C::nq; ++i)
+#pragma unroll
+        for (int j = 0; j < C::np; ++j) acc[i][j] = Mul<T>::add(p[j], q[i], acc[i][j]);
+    }
+  };
+
+  // A step, with the loads of a later one.  Large parts with one workgroup a compute unit ask for both halves' fragments at
+  // once, so that their waves wait for LDS once (dx of 16384 rows, 1024 inputs, 2048 outputs, 256 x 256: 119 us half by
+  // half, 111 like this); where workgroups share a compute unit that costs registers for nothing (128 x 128: 122 and 127).
+  template <class Next>
+  static __device__ __forceinline__ void step(const char *lds, int wq, int wp, f32x4 (&acc)[C::nq][C::np], Next next) {
+    Fragments f[2];
+    if constexpr (ALIGNED && C::nq * C::np > 16) {
+      f[0].read(lds, wq, wp, 0);
+      f[1].read(lds, wq, wp, 1);
+      __builtin_amdgcn_sched_barrier(0);
+      next();
+      f[0].multiply(acc);
+      f[1].multiply(acc);
+    } else {
+      next();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        f[h].read(lds, wq, wp, h);
+        f[h].multiply(acc);
       }
     }
   }
@@ -264,20 +294,25 @@ struct Product {
     if (steps <= 0) return;
     if constexpr (ALIGNED) {
       const uint32_t at = (uint32_t)(uintptr_t)(lds_void *)lds;
+      constexpr int ahead = C::buffers - 1;   // steps whose loads are in flight
+      int in = 0, out = 0;                    // buffers, as byte offsets
       auto load = [&](int s) {
         Base p, q;
         base(s, p, q);
         const bool f = last(s);
-        const uint32_t to = at + (s & 1 ? bytes : 0);
-        P.load(p, to, f);
-        Q.load(q, to + SP::bytes, f);
+        P.load(p, at + in, f);
+        Q.load(q, at + in + SP::bytes, f);
+        in = in + bytes == C::buffers * bytes ? 0 : in + bytes;
       };
-      load(0);
+      for (int s = 0; s < ahead && s < steps; ++s) load(s);
       for (int s = 0; s < steps; ++s) {
-        loads_done();
-        __syncthreads();   // the step's pieces are there, and the other buffer has been read
-        if (s + 1 < steps) load(s + 1);
-        multiply(lds + (s & 1 ? bytes : 0), wq, wp, acc);
+        if (s + ahead <= steps) loads_done<(ahead - 1) * (SP::pieces + SQ::pieces)>();   // later steps' are in flight
+        else loads_done<0>();
+        __syncthreads();   // the step's pieces are there, and the buffer before it has been read
+        step(lds + out, wq, wp, acc, [&] {
+          if (s + ahead < steps) load(s + ahead);
+        });
+        out = out + bytes == C::buffers * bytes ? 0 : out + bytes;
       }
     } else {
       u32x4 hp[SP::pieces], hq[SQ::pieces];
@@ -294,8 +329,9 @@ struct Product {
         P.put(hp, lds);
         Q.put(hq, lds + SP::bytes);
         __syncthreads();
-        if (s + 1 < steps) fetch(s + 1);
-        multiply(lds, wq, wp, acc);
+        step(lds, wq, wp, acc, [&] {
+          if (s + 1 < steps) fetch(s + 1);
+        });
       }
     }
   }
@@ -335,6 +371,21 @@ __device__ __forceinline__ Rows rows_of_unit(const int32_t *offsets, int n_matri
   }
   return {-1, 0, 0};
 }
+
+// The matrix whose number of rows is the rank-th largest (ties: the lower one first), of at most 64; the whole wave asks
+__device__ __forceinline__ int by_length(const int32_t *offsets, int n_matrices, int64_t n_rows, int rank) {
+  const int e = lane_id() < n_matrices ? lane_id() : 0;
+  const int64_t a = clamped(offsets[e], n_rows), z = clamped(offsets[e + 1], n_rows);
+  const int len = lane_id() < n_matrices ? (int)(z > a ? z - a : 0) : -1;
+  int before = 0;
+  for (int i = 0; i < n_matrices; ++i) {
+    const int other = __builtin_amdgcn_readlane(len, i);
+    before += other > len || (other == len && i < lane_id()) ? 1 : 0;
+  }
+  return __builtin_ctzll(__ballot(lane_id() < n_matrices && before == rank));
+}
+
+__host__ __device__ inline int64_t eighths(int64_t tiles) { return (tiles + 7) / 8 * 8; }
 
 // The tile of workgroup b: workgroups b, b + 8, .. share an L2, so each eighth takes neighbouring tiles; within them,
 // bands of 8 units go through the columns together.  False: none left.
@@ -388,19 +439,92 @@ __device__ __forceinline__ void with_act(int act, F f) {
   }
 }
 
+// ---- results -------------------------------------------------------------------------------------
+//
+// A wave's registers hold 16 rows of four columns each, 32 bytes of a row per store.  So a tile goes through LDS, where
+// its rows meet, and leaves as pieces of 16 bytes, a whole row of the tile after the other: forward at 8192 rows, 2048
+// inputs and 8192 outputs, kept gate and up, 704 us with direct stores, 457 without any.
+template <class C, class O, int COLUMNS>   // COLUMNS of O
+struct Staged {
+  static constexpr int pitch = COLUMNS * (int)sizeof(O) + 16;   // 16: neighbouring rows on other banks
+  static constexpr int most = (C::q + C::p) * kStepBytes * 2 + 8192;
+  static constexpr int fit() {
+    int n = C::nq;
+    while (C::WQ * 16 * n * pitch > most) n /= 2;
+    return n;
+  }
+  static constexpr int blocks = fit();                           // of a wave at a time
+  static constexpr int rows = C::WQ * 16 * blocks, bytes = rows * pitch;
+  static_assert(blocks >= 1 && C::nq % blocks == 0, "whole passes");
+
+  // value(b, c): a wave's four values of its block b of rows and c of NC blocks of columns.  Rows first .. end - 1 of `out`,
+  // whose rows have `width` values, columns from c0 on.  The whole workgroup calls; lds is free before and after.
+  template <int NC, class Value>
+  static __device__ __forceinline__ void store(char *lds, int64_t first, int64_t end, int c0, int width, O *out, Value value) {
+    const int wave = (int)threadIdx.x / 64, wq = wave / C::WP, wp = wave % C::WP, i = lane_id() % 16, g = lane_id() / 16;
+    struct alignas(4 * sizeof(O) < 16 ? 4 * sizeof(O) : 16) Four { O t[4]; };
+    struct __attribute__((packed, aligned(sizeof(O)))) Raw { uint8_t v[16]; };
+    constexpr int each = 16 / sizeof(O), row_pieces = COLUMNS / each;
+#pragma unroll
+    for (int b0 = 0; b0 < C::nq; b0 += blocks) {
+      __syncthreads();
+#pragma unroll
+      for (int b = 0; b < blocks; ++b)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          float v[4];
+          value(b0 + b, c, v);
+          *reinterpret_cast<Four *>(lds + ((wq * blocks + b) * 16 + i) * pitch +
+                                    ((wp * NC + c) * 16 + 4 * g) * (int)sizeof(O)) = Four{{(O)v[0], (O)v[1], (O)v[2], (O)v[3]}};
+        }
+      __syncthreads();
+      for (int q = (int)threadIdx.x; q < rows * row_pieces; q += C::threads) {
+        const int r = q / row_pieces, piece = q % row_pieces;
+        // row r of this pass is row (r / (16 blocks)) nq 16 + b0 16 + r % (16 blocks) of the tile
+        const int64_t row = first + (r / (16 * blocks) * C::nq + b0) * 16 + r % (16 * blocks);
+        const int col = c0 + piece * each, left = width - col;
+        if (row >= end || left <= 0) continue;
+        const Raw raw = *reinterpret_cast<const Raw *>(lds + r * pitch + piece * 16);
+        O *to = out + row * width + col;
+        if (left >= each) *reinterpret_cast<Raw *>(to) = raw;
+        else {
+          struct Values { O t[each]; } v = __builtin_bit_cast(Values, raw);
+#pragma unroll
+          for (int k = 0; k < each; ++k)
+            if (k < left) to[k] = v.t[k];
+        }
+      }
+    }
+  }
+};
+
+// a tile's result, to `out` or, one part of a split, to `part`
+template <class T, class C>
+__device__ __forceinline__ void store_tile(const f32x4 (&acc)[C::nq][C::np], char *lds, int64_t first, int64_t end, int c0,
+                                           int width, T *out, float *part) {
+  auto value = [&](int b, int c, float (&v)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = acc[b][c][k];
+  };
+  if (part) Staged<C, float, C::p>::template store<C::np>(lds, first, end, c0, width, part, value);
+  else Staged<C, T, C::p>::template store<C::np>(lds, first, end, c0, width, out, value);
+}
+
+constexpr int larger(int a, int b) { return a > b ? a : b; }
+
 // ---- forward -------------------------------------------------------------------------------------
 
 // side P: half a tile of Wg's rows and the same outputs' of Wu; side Q: rows of x
 template <class T, class C, bool ALIGNED>
 __global__ __launch_bounds__(C::threads) void k_gated(GatedArgs a) {
   using Pr = Product<T, C, false, false, true, ALIGNED>;
-  __shared__ __attribute__((aligned(1024))) char lds[Pr::lds_bytes];
+  constexpr int outs = C::p / 2;   // of a tile
+  __shared__ __attribute__((aligned(1024))) char lds[larger(Pr::lds_bytes, Staged<C, T, outs>::bytes)];
   int64_t unit;
   int column;
   if (!tile_of(blockIdx.x, a.units, a.columns, unit, column)) return;
   const Rows rows = rows_of_unit(a.offsets, a.n_matrices, a.n_rows, unit, C::q);
   if (rows.matrix < 0) return;
-  constexpr int outs = C::p / 2;   // of a tile
   const int n0 = column * outs;
   const int64_t pitch = (int64_t)a.ins * sizeof(T);
   const int steps = (a.ins + Pr::SP::step - 1) / Pr::SP::step, tail = a.ins - (steps - 1) * Pr::SP::step;
@@ -419,31 +543,23 @@ __global__ __launch_bounds__(C::threads) void k_gated(GatedArgs a) {
         q = {x + k, x + k};
       },
       [&](int s) { return s + 1 == steps; }, acc);
-  const int wave = (int)threadIdx.x / 64, wq = wave / C::WP, wp = wave % C::WP, i = lane_id() % 16, g = lane_id() / 16;
+  constexpr int half = C::np / 2;
+  using St = Staged<C, T, outs>;
+  if (a.gate) {
+    St::template store<half>(lds, rows.first, rows.end, n0, a.outs, (T *)a.gate, [&](int b, int c, float (&v)[4]) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = acc[b][c][k];
+    });
+    St::template store<half>(lds, rows.first, rows.end, n0, a.outs, (T *)a.up, [&](int b, int c, float (&v)[4]) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = acc[b][half + c][k];
+    });
+  }
   with_act(a.act, [&](auto act) {
+    St::template store<half>(lds, rows.first, rows.end, n0, a.outs, (T *)a.h, [&](int b, int c, float (&v)[4]) {
 #pragma unroll
-    for (int b = 0; b < C::nq; ++b) {
-      const int64_t row = rows.first + (wq * C::nq + b) * 16 + i;
-      if (row >= rows.end) continue;
-#pragma unroll
-      for (int c = 0; c < C::np / 2; ++c) {
-        const int n = n0 + (wp * (C::np / 2) + c) * 16 + 4 * g, left = a.outs - n;
-        if (left <= 0) continue;
-        float h[4], gate[4], up[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          gate[k] = acc[b][c][k];
-          up[k] = acc[b][C::np / 2 + c][k];
-          h[k] = act_value<decltype(act)::value>(gate[k]) * up[k];
-        }
-        const int64_t at = row * a.outs + n;
-        store_four((T *)a.h + at, h, left, a.wide);
-        if (a.gate) {
-          store_four((T *)a.gate + at, gate, left, a.wide);
-          store_four((T *)a.up + at, up, left, a.wide);
-        }
-      }
-    }
+      for (int k = 0; k < 4; ++k) v[k] = act_value<decltype(act)::value>(acc[b][c][k]) * acc[b][half + c][k];
+    });
   });
 }
 
@@ -586,31 +702,12 @@ __global__ __launch_bounds__(kBothThreads) void k_gated_both(GatedArgs a, int la
   });
 }
 
-// a tile's result: rows `first` .. `end` of width `width`, columns from c0 on, to `out` or, one part of a split, to `part`
-template <class T, class C>
-__device__ __forceinline__ void store_tile(const f32x4 (&acc)[C::nq][C::np], int64_t first, int64_t end, int c0, int width,
-                                           T *out, float *part, bool wide) {
-  const int wave = (int)threadIdx.x / 64, wq = wave / C::WP, wp = wave % C::WP, i = lane_id() % 16, g = lane_id() / 16;
-#pragma unroll
-  for (int b = 0; b < C::nq; ++b) {
-    const int64_t row = first + (wq * C::nq + b) * 16 + i;
-    if (row >= end) continue;
-#pragma unroll
-    for (int c = 0; c < C::np; ++c) {
-      const int k = c0 + (wp * C::np + c) * 16 + 4 * g, left = width - k;
-      if (left <= 0) continue;
-      const float v[4] = {acc[b][c][0], acc[b][c][1], acc[b][c][2], acc[b][c][3]};
-      if (part) store_four(part + row * width + k, v, left, width % 4 == 0);
-      else store_four(out + row * width + k, v, left, wide);
-    }
-  }
-}
-
 // dx: side P: columns of Wg, then of Wu (across); side Q: rows of dg, then of du (along)
 template <class T, class C, bool ALIGNED>
 __global__ __launch_bounds__(C::threads) void k_gated_dx(GatedArgs a) {
   using Pr = Product<T, C, true, false, false, ALIGNED>;
-  __shared__ __attribute__((aligned(1024))) char lds[Pr::lds_bytes];
+  __shared__ __attribute__((aligned(1024))) char
+      lds[larger(Pr::lds_bytes, larger(Staged<C, T, C::p>::bytes, Staged<C, float, C::p>::bytes))];
   int64_t unit;
   int column;
   if (!tile_of(blockIdx.x, a.units, a.columns, unit, column)) return;
@@ -638,20 +735,24 @@ __global__ __launch_bounds__(C::threads) void k_gated_dx(GatedArgs a) {
         q = {d, d};
       },
       [&](int t) { return s0 + t + 1 == half || s0 + t + 1 == 2 * half; }, acc);
-  store_tile<T, C>(acc, rows.first, rows.end, k0, a.ins, (T *)a.dx,
-                   a.splits > 1 ? a.partial + (int64_t)blockIdx.y * a.n_rows * a.ins : nullptr, a.wide);
+  store_tile<T, C>(acc, lds, rows.first, rows.end, k0, a.ins, (T *)a.dx,
+                   a.splits > 1 ? a.partial + (int64_t)blockIdx.y * a.n_rows * a.ins : nullptr);
 }
 
 // dWg and dWu: side P: columns of x (across), side Q: columns of dg or du (across); the rows are reduced
 template <class T, class C, bool ALIGNED>
 __global__ __launch_bounds__(C::threads) void k_gated_dw(GatedArgs a) {
   using Pr = Product<T, C, true, true, false, ALIGNED>;
-  __shared__ __attribute__((aligned(1024))) char lds[Pr::lds_bytes];
+  __shared__ __attribute__((aligned(1024))) char
+      lds[larger(Pr::lds_bytes, larger(Staged<C, T, C::p>::bytes, Staged<C, float, C::p>::bytes))];
+  // a matrix's tiles lie together, spread over all L2s; the longest sums come first (8 uneven experts, 16384 rows: @@)
+  const int tiles = (a.outs + C::q - 1) / C::q;
+  const int64_t own = eighths((int64_t)2 * tiles * a.columns);
   int64_t unit;
   int column;
-  if (!tile_of(blockIdx.x, a.units, a.columns, unit, column)) return;
-  const int tiles = (a.outs + C::q - 1) / C::q;
-  const int matrix = (int)(unit / (2 * tiles)), in = (int)(unit - (int64_t)matrix * 2 * tiles);
+  if (!tile_of(blockIdx.x % own, 2 * tiles, a.columns, unit, column)) return;
+  const int rank = (int)(blockIdx.x / own), in = (int)unit;
+  const int matrix = a.offsets && a.n_matrices <= 64 ? by_length(a.offsets, a.n_matrices, a.n_rows, rank) : rank;
   const bool up = in >= tiles;
   const int n0 = (up ? in - tiles : in) * C::q, k0 = column * C::p;
   const int64_t first = a.offsets ? clamped(a.offsets[matrix], a.n_rows) : 0;
@@ -677,81 +778,108 @@ __global__ __launch_bounds__(C::threads) void k_gated_dw(GatedArgs a) {
       [&](int t) { return s0 + t + 1 == all; }, acc);
   const int64_t size = (int64_t)a.outs * a.ins, of = matrix * size;
   float *part = a.splits > 1 ? a.partial + (((int64_t)blockIdx.y * 2 + up) * a.n_matrices) * size + of : nullptr;
-  store_tile<T, C>(acc, n0, a.outs, k0, a.ins, (T *)(up ? a.dw_up : a.dw_gate) + of, part, a.wide);
+  store_tile<T, C>(acc, lds, n0, a.outs, k0, a.ins, (T *)(up ? a.dw_up : a.dw_gate) + of, part);
 }
 
-// out[i] = the sum of the parts, in order; of each part `size` values, the last half of them to `upper` (half == size: none).
-// Rows that no matrix names keep their values where `width` is given (dx).
+// out[i] = the sum of the parts, in order; of each part `size` values, the last size - half of them to `upper`.  Rows that
+// no matrix names keep their values where `width` is given (dx).
 template <class T>
 __global__ __launch_bounds__(256) void k_gated_parts(const float *partial, int splits, int64_t size, int64_t half, T *out,
                                                      T *upper, GatedArgs a, int width) {
+  struct __attribute__((packed, aligned(4))) Raw { float v[4]; };
+  struct __attribute__((packed, aligned(sizeof(T)))) Results { uint8_t v[4 * sizeof(T)]; };
+  struct Values { T t[4]; };
   int64_t first = 0, end = size;
   if (width && a.offsets) {
     first = clamped(a.offsets[0], a.n_rows) * width;
     end = clamped(a.offsets[a.n_matrices], a.n_rows) * width;
   }
-  for (int64_t i = first + blockIdx.x * 256ll + threadIdx.x; i < end; i += gridDim.x * 256ll) {
-    float sum = partial[i];
-    for (int z = 1; z < splits; ++z) sum += partial[z * size + i];
-    if (i < half) out[i] = (T)sum;
-    else upper[i - half] = (T)sum;
+  for (int64_t i = first + (blockIdx.x * 256ll + threadIdx.x) * 4; i < end; i += gridDim.x * 1024ll) {
+    if (i + 4 <= end && (i + 4 <= half || i >= half)) {
+      Raw sum = *reinterpret_cast<const Raw *>(partial + i);
+#pragma unroll 4
+      for (int z = 1; z < splits; ++z) {
+        const Raw v = *reinterpret_cast<const Raw *>(partial + z * size + i);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum.v[k] += v.v[k];
+      }
+      const Values r{{(T)sum.v[0], (T)sum.v[1], (T)sum.v[2], (T)sum.v[3]}};
+      *reinterpret_cast<Results *>(i < half ? out + i : upper + (i - half)) = __builtin_bit_cast(Results, r);
+    } else {
+      for (int64_t k = i; k < end && k < i + 4; ++k) {
+        float sum = partial[k];
+        for (int z = 1; z < splits; ++z) sum += partial[z * size + k];
+        *(k < half ? out + k : upper + (k - half)) = (T)sum;
+      }
+    }
   }
 }
 
 // ---- calls ---------------------------------------------------------------------------------------
 
-// how a call runs; the same for the workspace's size
+// How a product runs; the same for the workspace's size.
 struct GatedPlan {
-  int cut;         // 0: 64 x 128, 1: 128 x 128, 2: 256 x 256
-  int splits;
-  int64_t units;
+  int cut;         // of the four below
+  int splits;      // parts of the reduced index
+  int64_t units;   // tiles along the rows of the result, at most
   int columns;
 };
 
-constexpr int kCutQ[3] = {64, 128, 256}, kCutP[3] = {128, 128, 256};
+// The cuts, and microseconds of a step of 128 bytes: with one workgroup on a compute unit, and for each further one that
+// shares it (the 256 x 256 cut has none beside it: they follow each other).  Measured with 16384 x 1024 x 2048, 4096 x 2048
+// x 4096 and 1024 x 1024 x 1024 products of two-byte and of float32 values.
+struct CutCost { int q, p; float alone[2], shared[2]; };
+constexpr int kCuts = 4;
+constexpr CutCost kCutCost[kCuts] = {{32, 64, {0.28f, 0.46f}, {0.15f, 0.29f}},
+                                     {64, 128, {0.5f, 1.17f}, {0.29f, 1.05f}},
+                                     {128, 128, {0.62f, 2.15f}, {0.45f, 2.0f}},
+                                     {256, 256, {1.65f, 7.5f}, {1.65f, 7.5f}}};
 
 // blocks of rows at most: every matrix may end inside one
 inline int64_t row_units(int64_t n_rows, int n_matrices, bool by_expert, int per) {
   return by_expert ? n_rows / per + (n_rows < n_matrices ? n_rows : n_matrices) : (n_rows + per - 1) / per;
 }
 
-// The largest cut whose tiles give most compute units (256) work; the smallest if none does, its reduced index split
-inline GatedPlan plan_cut(int64_t (*units)(const GatedArgs &, int), const GatedArgs &a, int width, int64_t steps) {
-  GatedPlan p{};
-  for (p.cut = 2; p.cut >= 0; --p.cut) {
-    p.units = units(a, kCutQ[p.cut]);
-    p.columns = (width + kCutP[p.cut] - 1) / kCutP[p.cut];
-    if (p.units * p.columns >= 192) break;
+// The cut and the number of parts with the least time by the table above, 3 us for a launch and 4 + 2.4 us for each million
+// partial values that are written and read again.  units(q): tiles of q along the result's rows; results: its values, 0
+// where its sums cannot be split.
+template <class Units>
+GatedPlan plan_product(int elem, Units units, int width, int64_t steps, double results) {
+  GatedPlan best{};
+  double least = 0;
+  const int type = elem == 4;
+  for (int cut = 0; cut < kCuts; ++cut) {
+    const CutCost &c = kCutCost[cut];
+    GatedPlan p{cut, 1, units(c.q), (width + c.p - 1) / c.p};
+    for (; p.splits <= 32 && (p.splits == 1 || (results > 0 && steps >= 2 * p.splits)); p.splits *= 2) {
+      const int64_t tiles = p.units * p.columns * p.splits, load = (tiles + 255) / 256;
+      const double each = (double)((steps + p.splits - 1) / p.splits);
+      double time = 3 + each * (c.alone[type] + (double)(load - 1) * c.shared[type]);
+      if (p.splits > 1) time += 4 + 2.4e-6 * p.splits * results;
+      if ((cut == 0 && p.splits == 1) || time < least) {
+        least = time;
+        best = p;
+      }
+    }
   }
-  if (p.cut < 0) p.cut = 0;
-  p.splits = 1;
-  const int64_t tiles = p.units * p.columns;
-  if (steps > 0 && tiles < 192) {
-    const int64_t want = 512 / (tiles > 0 ? tiles : 1), most = steps / 4;   // at least 4 steps for each part
-    p.splits = (int)(want < most ? want : most);
-    if (p.splits > 32) p.splits = 32;
-    if (p.splits < 1) p.splits = 1;
-  }
-  return p;
+  return best;
 }
 
-inline GatedPlan plan_forward(const GatedArgs &a) {
-  return plan_cut([](const GatedArgs &g, int q) { return row_units(g.n_rows, g.n_matrices, g.offsets != nullptr, q); }, a,
-                  2 * a.outs, 0);
+inline GatedPlan plan_forward(const GatedArgs &a, int elem) {
+  return plan_product(elem, [&](int q) { return row_units(a.n_rows, a.n_matrices, a.offsets != nullptr, q); }, 2 * a.outs,
+                      (a.ins + kStepBytes / elem - 1) / (kStepBytes / elem), 0);
 }
 inline GatedPlan plan_dx(const GatedArgs &a, int elem) {
-  const int step = kStepBytes / elem;
-  return plan_cut([](const GatedArgs &g, int q) { return row_units(g.n_rows, g.n_matrices, g.offsets != nullptr, q); }, a,
-                  a.ins, 2 * ((a.outs + step - 1) / step));
+  return plan_product(elem, [&](int q) { return row_units(a.n_rows, a.n_matrices, a.offsets != nullptr, q); }, a.ins,
+                      2 * ((a.outs + kStepBytes / elem - 1) / (kStepBytes / elem)), (double)a.n_rows * a.ins);
 }
 inline GatedPlan plan_dw(const GatedArgs &a, int elem) {
-  const int step = kStepBytes / elem;
-  return plan_cut([](const GatedArgs &g, int q) { return (int64_t)g.n_matrices * 2 * ((g.outs + q - 1) / q); }, a, a.ins,
-                  a.n_rows / a.n_matrices / step);
+  return plan_product(elem, [&](int q) { return (int64_t)a.n_matrices * 2 * ((a.outs + q - 1) / q); }, a.ins,
+                      a.n_rows / a.n_matrices / (kStepBytes / elem) + 1, 2.0 * a.n_matrices * a.outs * a.ins);
 }
 
 // a grid's threads stay below 2^32
-inline bool fits(const GatedPlan &p) { return p.units * p.columns < (1 << 22) / p.splits; }
+inline bool fits(const GatedPlan &p) { return (p.units * p.columns + 8 * SVT_MAX_EXPERTS) * p.splits < (1 << 22); }
 
 inline int64_t gated_pitch(int32_t outs, int elem) { return ((int64_t)outs * elem + 15) & ~(int64_t)15; }
 
@@ -780,12 +908,11 @@ template <class T> int gated_backward(const char *who, GatedArgs a, bool aligned
 template <class F>
 int with_cut(int cut, bool aligned, F f) {
   auto with = [&](auto c) { return aligned ? f(c, std::true_type{}) : f(c, std::false_type{}); };
-  if (cut == 2) return with(Cut<256, 256, 2, 4>{});
-  if (cut == 1) return with(Cut<128, 128, 2, 2>{});
-  return with(Cut<64, 128, 1, 4>{});
+  if (cut == 3) return with(Cut<256, 256, 2, 4, 2>{});
+  if (cut == 2) return with(Cut<128, 128, 2, 2, 2>{});
+  if (cut == 1) return with(Cut<64, 128, 1, 4, 2>{});
+  return with(Cut<32, 64, 2, 2, 2>{});
 }
-
-inline int64_t eighths(int64_t tiles) { return (tiles + 7) / 8 * 8; }
 
 template <class T>
 int gated_forward(const char *who, GatedArgs a, bool aligned, void *stream) {
@@ -802,7 +929,7 @@ int gated_forward(const char *who, GatedArgs a, bool aligned, void *stream) {
       return launch(who, k_gated_few<T, 4, 2>, grid, 64 * kFewWaves, 0, stream, a);
     }
   }
-  const GatedPlan p = plan_forward(a);
+  const GatedPlan p = plan_forward(a, sizeof(T));
   a.units = p.units;
   a.columns = p.columns;
   return with_cut(p.cut, aligned, [&](auto cut, auto al) {
@@ -825,7 +952,7 @@ int gated_backward(const char *who, GatedArgs a, bool aligned, void *stream) {
     if (rc != SVT_OK) return rc;
   }
   auto parts = [&](int64_t size, int64_t half, void *out, void *upper, int width) {
-    const int64_t blocks = (size + 255) / 256;
+    const int64_t blocks = (size + 1023) / 1024;
     return launch(who, k_gated_parts<T>, (unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, stream, (const float *)a.partial,
                   a.splits, size, half, (T *)out, (T *)upper, a, width);
   };
@@ -849,7 +976,8 @@ int gated_backward(const char *who, GatedArgs a, bool aligned, void *stream) {
     a.splits = p.splits;
     rc = with_cut(p.cut, aligned, [&](auto cut, auto al) {
       using C = decltype(cut);
-      return launch(who, k_gated_dw<T, C, decltype(al)::value>, dim3((unsigned)eighths(a.units * a.columns), p.splits),
+      const int64_t own = eighths(a.units / a.n_matrices * a.columns);
+      return launch(who, k_gated_dw<T, C, decltype(al)::value>, dim3((unsigned)(own * a.n_matrices), p.splits),
                     C::threads, 0, stream, a);
     });
     const int64_t size = (int64_t)a.n_matrices * a.outs * a.ins;

@@ -71,7 +71,7 @@ extern "C" int svt_gated_linear(int32_t n_rows, int32_t n_in, int32_t n_out, int
   a.up = up;
   a.splits = 1;
   a.wide = n_out % 4 == 0 && !misaligned(h, 4 * b) && !misaligned(gate, 4 * b) && !misaligned(up, 4 * b);
-  if (!fits(plan_forward(a))) return report(SVT_EINVAL, "%s: too many rows of too many outputs for one call", who);
+  if (!fits(plan_forward(a, b))) return report(SVT_EINVAL, "%s: too many rows of too many outputs for one call", who);
   const bool aligned = (size_t)n_in * b % 16 == 0 && !misaligned(x, 16) && !misaligned(w_gate, 16) && !misaligned(w_up, 16);
   return with_type(dtype, [&](auto ty) { return gated_forward<decltype(ty)>(who, a, aligned, hip_stream); });
 }
