@@ -500,12 +500,17 @@ int svt_embedding_backward(int64_t n_tokens, int64_t n_rows, int32_t width, int3
  *   activation   SVT_ACT_NONE, _RELU, _SILU or _GELU (v times the normal distribution's integral up to v)
  *   h            [n_rows][n_out] of dtype
  *   gate, up     [n_rows][n_out] of dtype, or both NULL: w_gate x and w_up x, which the gradient needs
+ *   workspace    svt_gated_linear_workspace_size(n_rows, n_in, n_out, n_matrices, dtype, offsets != NULL, aligned) bytes,
+ *                16-byte aligned; NULL where that is 0.  aligned: 1 if x, w_gate and w_up are 16-byte aligned; where they
+ *                are not, or n_in elements are no multiple of 16 bytes, the call copies them first (but for few rows)
  * Sums are float32; h, gate and up are rounded once each (h from the unrounded sums).
  * n_rows == 0 returns SVT_OK without enqueuing.  Errors: SVT_EINVAL, SVT_EDEVICE as svt_route.
  */
+size_t svt_gated_linear_workspace_size(int32_t n_rows, int32_t n_in, int32_t n_out, int32_t n_matrices, int32_t dtype,
+                                       int32_t by_expert, int32_t aligned);
 int svt_gated_linear(int32_t n_rows, int32_t n_in, int32_t n_out, int32_t n_matrices, int32_t dtype, const void *x,
                      const void *w_gate, const void *w_up, const int32_t *offsets, int32_t activation, void *h,
-                     void *gate, void *up, void *hip_stream);
+                     void *gate, void *up, void *workspace, size_t workspace_bytes, void *hip_stream);
 
 /*
  * svt_gated_linear_backward - its gradients: with dg = dh * up * act'(gate) and du = dh * act(gate), both rounded to
@@ -514,13 +519,13 @@ int svt_gated_linear(int32_t n_rows, int32_t n_in, int32_t n_out, int32_t n_matr
  *   dh, gate, up  [n_rows][n_out] of dtype: the gradient in h, and what svt_gated_linear kept
  *   dx            [n_rows][n_in] of dtype, or NULL (w_gate and w_up may then be NULL).  Rows that no pair names are left
  *   dw_gate, dw_up  [n_matrices][n_out][n_in] of dtype, or both NULL (x may then be NULL); zeros for a pair without rows
- *   workspace     svt_gated_linear_backward_workspace_size(n_rows, n_in, n_out, n_matrices, dtype, offsets != NULL)
- *                 bytes, 16-byte aligned
+ *   workspace     svt_gated_linear_backward_workspace_size(n_rows, n_in, n_out, n_matrices, dtype, offsets != NULL,
+ *                 aligned) bytes, 16-byte aligned; aligned as above
  * act' of SVT_ACT_RELU is 0 at 0.  n_rows == 0 writes the zeros.  Errors: SVT_EINVAL, SVT_EDEVICE (a launch failed: the
  * outputs are undefined).
  */
 size_t svt_gated_linear_backward_workspace_size(int32_t n_rows, int32_t n_in, int32_t n_out, int32_t n_matrices,
-                                                int32_t dtype, int32_t by_expert);
+                                                int32_t dtype, int32_t by_expert, int32_t aligned);
 int svt_gated_linear_backward(int32_t n_rows, int32_t n_in, int32_t n_out, int32_t n_matrices, int32_t dtype,
                               const void *dh, const void *x, const void *w_gate, const void *w_up, const void *gate,
                               const void *up, const int32_t *offsets, int32_t activation, void *dx, void *dw_gate,

@@ -131,7 +131,6 @@ struct Side {
 
   uint32_t offset[pieces];   // of the thread's pieces; kOutside: zeros
   uint32_t gone;             // bit j: piece j is outside in a last step
-  int own, reduced;
 
   static __device__ __forceinline__ int row_of(int j) { return (j * THREADS + (int)threadIdx.x) / row_pieces; }
   static __device__ __forceinline__ int piece_of(int j) {
@@ -139,9 +138,7 @@ struct Side {
   }
 
   // pitch: bytes of a memory row; own: valid indexes of the side (of each half); reduced: those of a last step
-  __device__ __forceinline__ void init(uint32_t pitch, int own_, int reduced_) {
-    own = own_;
-    reduced = reduced_;
+  __device__ __forceinline__ void init(uint32_t pitch, int own, int reduced) {
     gone = 0u;
 #pragma unroll
     for (int j = 0; j < pieces; ++j) {
@@ -152,7 +149,7 @@ struct Side {
     }
   }
 
-  // A step's pieces to LDS, straight from memory (16-byte aligned rows).  The loads are written out, as the compiler
+  // A step's pieces to LDS, straight from memory.  The loads are written out, as the compiler
   // would have every later read of LDS wait for them; whoever reads waits by loads_done() and a barrier.  (They have no
   // result in registers.)
   __device__ __forceinline__ void load(Base from, uint32_t lds, bool final) const {
@@ -171,31 +168,6 @@ struct Side {
                    "s"(HALVES && 2 * j >= pieces ? upper : lower)
                    : "memory");
     }
-  }
-
-  // the same through registers, for rows of any alignment: a piece may end inside
-  __device__ __forceinline__ void fetch(Base from, u32x4 (&held)[pieces], bool final) const {
-#pragma unroll
-    for (int j = 0; j < pieces; ++j) {
-      const char *p = (HALVES && 2 * j >= pieces ? from.upper : from.at) + offset[j];
-      held[j] = u32x4{0u, 0u, 0u, 0u};
-      if (offset[j] == kOutside || (final && (gone >> j & 1u))) continue;
-      const int left = (ACROSS ? own : reduced) - piece_of(j) * each;
-      if ((ACROSS || final) && left < each) {
-        struct { T t[each]; } v{};
-#pragma unroll
-        for (int i = 0; i < each; ++i)
-          if (i < left) v.t[i] = reinterpret_cast<const T *>(p)[i];
-        held[j] = __builtin_bit_cast(u32x4, v);
-      } else {
-        struct __attribute__((packed, aligned(sizeof(T)))) Raw { uint8_t v[16]; };
-        held[j] = __builtin_bit_cast(u32x4, *reinterpret_cast<const Raw *>(p));
-      }
-    }
-  }
-  __device__ __forceinline__ void put(const u32x4 (&held)[pieces], char *lds) const {
-#pragma unroll
-    for (int j = 0; j < pieces; ++j) *reinterpret_cast<u32x4 *>(lds + (j * THREADS + threadIdx.x) * 16) = held[j];
   }
 
   // the fragment of block `block` (16 own indexes), half `h` of the step
@@ -236,11 +208,11 @@ __device__ __forceinline__ void loads_done() {
 // acc[b][a] += the product of `steps` steps: lane l holds rows 16 b + l % 16 of its wave's part, columns
 // 16 a + 4 (l / 16) .. + 3.  base(s, p, q): where step s begins; last(s): whether its pieces may end early.
 // With HALVES of side P, the first np / 2 blocks are its lower, the others its upper half's.
-template <class T, class C, bool PA, bool QA, bool HALVES, bool ALIGNED>
+template <class T, class C, bool PA, bool QA, bool HALVES>
 struct Product {
   using SP = Side<T, C::p, C::threads, PA, HALVES>;
   using SQ = Side<T, C::q, C::threads, QA>;
-  static constexpr int bytes = SP::bytes + SQ::bytes, lds_bytes = ALIGNED ? C::buffers * bytes : bytes;
+  static constexpr int bytes = SP::bytes + SQ::bytes, lds_bytes = C::buffers * bytes;
   SP P;
   SQ Q;
 
@@ -271,7 +243,7 @@ struct Product {
   template <class Next>
   static __device__ __forceinline__ void step(const char *lds, int wq, int wp, f32x4 (&acc)[C::nq][C::np], Next next) {
     Fragments f[2];
-    if constexpr (ALIGNED && C::nq * C::np > 16) {
+    if constexpr (C::nq * C::np > 16) {
       f[0].read(lds, wq, wp, 0);
       f[1].read(lds, wq, wp, 1);
       __builtin_amdgcn_sched_barrier(0);
@@ -292,47 +264,26 @@ struct Product {
   __device__ __forceinline__ void run(int steps, char *lds, At base, Last last, f32x4 (&acc)[C::nq][C::np]) const {
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64), wq = wave / C::WP, wp = wave % C::WP;
     if (steps <= 0) return;
-    if constexpr (ALIGNED) {
-      const uint32_t at = (uint32_t)(uintptr_t)(lds_void *)lds;
-      constexpr int ahead = C::buffers - 1;   // steps whose loads are in flight
-      int in = 0, out = 0;                    // buffers, as byte offsets
-      auto load = [&](int s) {
-        Base p, q;
-        base(s, p, q);
-        const bool f = last(s);
-        P.load(p, at + in, f);
-        Q.load(q, at + in + SP::bytes, f);
-        in = in + bytes == C::buffers * bytes ? 0 : in + bytes;
-      };
-      for (int s = 0; s < ahead && s < steps; ++s) load(s);
-      for (int s = 0; s < steps; ++s) {
-        if (s + ahead <= steps) loads_done<(ahead - 1) * (SP::pieces + SQ::pieces)>();   // later steps' are in flight
-        else loads_done<0>();
-        __syncthreads();   // the step's pieces are there, and the buffer before it has been read
-        step(lds + out, wq, wp, acc, [&] {
-          if (s + ahead < steps) load(s + ahead);
-        });
-        out = out + bytes == C::buffers * bytes ? 0 : out + bytes;
-      }
-    } else {
-      u32x4 hp[SP::pieces], hq[SQ::pieces];
-      auto fetch = [&](int s) {
-        Base p, q;
-        base(s, p, q);
-        const bool f = last(s);
-        P.fetch(p, hp, f);
-        Q.fetch(q, hq, f);
-      };
-      fetch(0);
-      for (int s = 0; s < steps; ++s) {
-        __syncthreads();   // the buffer has been read
-        P.put(hp, lds);
-        Q.put(hq, lds + SP::bytes);
-        __syncthreads();
-        step(lds, wq, wp, acc, [&] {
-          if (s + 1 < steps) fetch(s + 1);
-        });
-      }
+    const uint32_t at = (uint32_t)(uintptr_t)(lds_void *)lds;
+    constexpr int ahead = C::buffers - 1;   // steps whose loads are in flight
+    int in = 0, out = 0;                    // buffers, as byte offsets
+    auto load = [&](int s) {
+      Base p, q;
+      base(s, p, q);
+      const bool f = last(s);
+      P.load(p, at + in, f);
+      Q.load(q, at + in + SP::bytes, f);
+      in = in + bytes == C::buffers * bytes ? 0 : in + bytes;
+    };
+    for (int s = 0; s < ahead && s < steps; ++s) load(s);
+    for (int s = 0; s < steps; ++s) {
+      if (s + ahead <= steps) loads_done<(ahead - 1) * (SP::pieces + SQ::pieces)>();   // later steps' are in flight
+      else loads_done<0>();
+      __syncthreads();   // the step's pieces are there, and the buffer before it has been read
+      step(lds + out, wq, wp, acc, [&] {
+        if (s + ahead < steps) load(s + ahead);
+      });
+      out = out + bytes == C::buffers * bytes ? 0 : out + bytes;
     }
   }
 };
@@ -403,7 +354,6 @@ struct GatedArgs {
   int64_t n_rows, units;
   int32_t ins, outs, n_matrices, columns;   // columns: tiles across
   int32_t act;
-  int32_t wide;               // the results' rows take four neighbouring values at once
   const int32_t *offsets;
   const void *x, *w_gate, *w_up;
   void *h, *gate, *up;        // gate, up: NULL where they are not kept
@@ -412,15 +362,18 @@ struct GatedArgs {
   void *dx, *dw_gate, *dw_up;
   char *d_both;               // dg, then du: [n_rows][pitch] each
   int64_t pitch;              // bytes
+  int64_t in_pitch;           // bytes of a row of x, w_gate and w_up: a multiple of 16, but for few rows
+  char *padded;               // their copies with such rows, where they are not so: x, then w_gate, then w_up
   int32_t splits;             // of the reduced index: partial results in `partial`
   float *partial;
 };
 
 template <class T>
-__device__ __forceinline__ void store_four(T *at, const float (&v)[4], int left, bool wide) {
-  if (wide && left >= 4) {
-    struct alignas(4 * sizeof(T)) Four { T t[4]; } r{{(T)v[0], (T)v[1], (T)v[2], (T)v[3]}};
-    *reinterpret_cast<Four *>(at) = r;
+__device__ __forceinline__ void store_four(T *at, const float (&v)[4], int left) {
+  if (left >= 4) {
+    struct Four { T t[4]; } r{{(T)v[0], (T)v[1], (T)v[2], (T)v[3]}};
+    struct __attribute__((packed, aligned(sizeof(T)))) Raw { uint8_t v[4 * sizeof(T)]; };
+    *reinterpret_cast<Raw *>(at) = __builtin_bit_cast(Raw, r);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -515,9 +468,9 @@ constexpr int larger(int a, int b) { return a > b ? a : b; }
 // ---- forward -------------------------------------------------------------------------------------
 
 // side P: half a tile of Wg's rows and the same outputs' of Wu; side Q: rows of x
-template <class T, class C, bool ALIGNED>
+template <class T, class C>
 __global__ __launch_bounds__(C::threads) void k_gated(GatedArgs a) {
-  using Pr = Product<T, C, false, false, true, ALIGNED>;
+  using Pr = Product<T, C, false, false, true>;
   constexpr int outs = C::p / 2;   // of a tile
   __shared__ __attribute__((aligned(1024))) char lds[larger(Pr::lds_bytes, Staged<C, T, outs>::bytes)];
   int64_t unit;
@@ -526,7 +479,7 @@ __global__ __launch_bounds__(C::threads) void k_gated(GatedArgs a) {
   const Rows rows = rows_of_unit(a.offsets, a.n_matrices, a.n_rows, unit, C::q);
   if (rows.matrix < 0) return;
   const int n0 = column * outs;
-  const int64_t pitch = (int64_t)a.ins * sizeof(T);
+  const int64_t pitch = a.in_pitch;
   const int steps = (a.ins + Pr::SP::step - 1) / Pr::SP::step, tail = a.ins - (steps - 1) * Pr::SP::step;
   Pr product;
   product.P.init((uint32_t)pitch, a.outs - n0 < outs ? a.outs - n0 : outs, tail);
@@ -646,11 +599,36 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_gated_few(GatedArgs a) {
     }
   });
   const int64_t to = row * a.outs + n0;
-  store_four((T *)a.h + to, h, left, a.wide);
+  store_four((T *)a.h + to, h, left);
   if (a.gate) {
-    store_four((T *)a.gate + to, gate, left, a.wide);
-    store_four((T *)a.up + to, up, left, a.wide);
+    store_four((T *)a.gate + to, gate, left);
+    store_four((T *)a.up + to, up, left);
   }
+}
+
+// ---- rows of any alignment -----------------------------------------------------------------------
+//
+// The loads that go straight to LDS want rows that begin at multiples of 16 bytes.  Others are copied first, with zeros
+// behind each row: 2 (x + w) bytes more to move, which is little beside a product of many rows; a path of its own through
+// registers took twice as long as copy and product (1001 x 250 x 999 float32: @@).
+template <class T>
+__global__ __launch_bounds__(256) void k_gated_pad(GatedArgs a, int lanes) {
+  constexpr int each = 16 / sizeof(T);
+  const int64_t w_rows = (int64_t)a.n_matrices * a.outs;
+  const T *from = (const T *)(blockIdx.z == 0 ? a.x : blockIdx.z == 1 ? a.w_gate : a.w_up);
+  if (!from) return;
+  char *to = a.padded + (blockIdx.z == 0 ? 0 : (a.n_rows + (blockIdx.z == 1 ? 0 : w_rows)) * a.in_pitch);
+  int64_t first = 0, end = w_rows;
+  if (blockIdx.z == 0) {   // rows that no matrix names are not read
+    first = a.offsets ? clamped(a.offsets[0], a.n_rows) : 0;
+    end = a.offsets ? clamped(a.offsets[a.n_matrices], a.n_rows) : a.n_rows;
+  }
+  const int pieces = (int)(a.in_pitch / 16), in = threadIdx.x % lanes;
+  const int64_t per = 256 / lanes;
+  for (int64_t r = first + blockIdx.x * per + threadIdx.x / lanes; r < end; r += gridDim.x * per)
+    for (int c = blockIdx.y * lanes + in; c < pieces; c += gridDim.y * lanes)
+      *reinterpret_cast<typename Mul<T>::frag *>(to + r * a.in_pitch + c * 16) =
+          load_sixteen(from + r * a.ins, c * each, a.ins);
 }
 
 // ---- gradients -----------------------------------------------------------------------------------
@@ -703,9 +681,9 @@ __global__ __launch_bounds__(kBothThreads) void k_gated_both(GatedArgs a, int la
 }
 
 // dx: side P: columns of Wg, then of Wu (across); side Q: rows of dg, then of du (along)
-template <class T, class C, bool ALIGNED>
+template <class T, class C>
 __global__ __launch_bounds__(C::threads) void k_gated_dx(GatedArgs a) {
-  using Pr = Product<T, C, true, false, false, ALIGNED>;
+  using Pr = Product<T, C, true, false, false>;
   __shared__ __attribute__((aligned(1024))) char
       lds[larger(Pr::lds_bytes, larger(Staged<C, T, C::p>::bytes, Staged<C, float, C::p>::bytes))];
   int64_t unit;
@@ -714,7 +692,7 @@ __global__ __launch_bounds__(C::threads) void k_gated_dx(GatedArgs a) {
   const Rows rows = rows_of_unit(a.offsets, a.n_matrices, a.n_rows, unit, C::q);
   if (rows.matrix < 0) return;
   const int k0 = column * C::p;
-  const int64_t pitch = (int64_t)a.ins * sizeof(T);
+  const int64_t pitch = a.in_pitch;
   const int half = (a.outs + Pr::SP::step - 1) / Pr::SP::step, tail = a.outs - (half - 1) * Pr::SP::step;
   const int each = (2 * half + a.splits - 1) / a.splits, s0 = blockIdx.y * each;
   const int steps = 2 * half - s0 < each ? 2 * half - s0 : each;   // none, or fewer, for the last part
@@ -740,9 +718,9 @@ __global__ __launch_bounds__(C::threads) void k_gated_dx(GatedArgs a) {
 }
 
 // dWg and dWu: side P: columns of x (across), side Q: columns of dg or du (across); the rows are reduced
-template <class T, class C, bool ALIGNED>
+template <class T, class C>
 __global__ __launch_bounds__(C::threads) void k_gated_dw(GatedArgs a) {
-  using Pr = Product<T, C, true, true, false, ALIGNED>;
+  using Pr = Product<T, C, true, true, false>;
   __shared__ __attribute__((aligned(1024))) char
       lds[larger(Pr::lds_bytes, larger(Staged<C, T, C::p>::bytes, Staged<C, float, C::p>::bytes))];
   // a matrix's tiles lie together, spread over all L2s; the longest sums come first (8 uneven experts, 16384 rows: @@)
@@ -760,7 +738,7 @@ __global__ __launch_bounds__(C::threads) void k_gated_dw(GatedArgs a) {
   const int64_t len = end > first ? end - first : 0, all = (len + Pr::SP::step - 1) / Pr::SP::step;
   const int64_t each = (all + a.splits - 1) / a.splits, s0 = blockIdx.y * each;
   const int steps = (int)(all - s0 < each ? all - s0 : each);
-  const int64_t pitch = (int64_t)a.ins * sizeof(T);
+  const int64_t pitch = a.in_pitch;
   Pr product;
   const int tail = (int)(len - (all - 1) * Pr::SP::step);
   product.P.init((uint32_t)pitch, a.ins - k0 < C::p ? a.ins - k0 : C::p, tail);
@@ -881,7 +859,20 @@ inline GatedPlan plan_dw(const GatedArgs &a, int elem) {
 // a grid's threads stay below 2^32
 inline bool fits(const GatedPlan &p) { return (p.units * p.columns + 8 * SVT_MAX_EXPERTS) * p.splits < (1 << 22); }
 
+// Whether the forward pass takes the kernel for few rows (up to 16, 32 or 64 of a matrix on average: 1, 2 or 4 blocks), or 0
+inline int few_rows(const GatedArgs &a) {
+  const int64_t rows = a.offsets ? (a.n_rows + a.n_matrices - 1) / a.n_matrices : a.n_rows;
+  const int mt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  if (rows > (a.offsets ? 24 : 64)) return 0;
+  return row_units(a.n_rows, a.n_matrices, a.offsets != nullptr, 16 * mt) * ((a.outs + 15) / 16) < (1 << 22) ? mt : 0;
+}
+
+// bytes of a row at a multiple of 16, and of the copies of x and both weights with such rows
 inline int64_t gated_pitch(int32_t outs, int elem) { return ((int64_t)outs * elem + 15) & ~(int64_t)15; }
+
+inline size_t gated_copies(const GatedArgs &a, int elem) {
+  return (size_t)(a.n_rows + 2 * (int64_t)a.n_matrices * a.outs) * gated_pitch(a.ins, elem);
+}
 
 // bytes of the partial results, of dx and of dW (one after the other in the same place)
 inline size_t gated_partial(const GatedArgs &a, int elem) {
@@ -900,55 +891,73 @@ inline size_t gated_partial(const GatedArgs &a, int elem) {
 }
 
 // one type's calls
-template <class T> int gated_forward(const char *who, GatedArgs a, bool aligned, void *stream);
-template <class T> int gated_backward(const char *who, GatedArgs a, bool aligned, void *stream);
+template <class T> int gated_forward(const char *who, GatedArgs a, void *stream);
+template <class T> int gated_backward(const char *who, GatedArgs a, void *stream);
 
 #ifdef SVT_GATED_INSTANTIATE
 
 template <class F>
-int with_cut(int cut, bool aligned, F f) {
-  auto with = [&](auto c) { return aligned ? f(c, std::true_type{}) : f(c, std::false_type{}); };
-  if (cut == 3) return with(Cut<256, 256, 2, 4, 2>{});
-  if (cut == 2) return with(Cut<128, 128, 2, 2, 2>{});
-  if (cut == 1) return with(Cut<64, 128, 1, 4, 2>{});
-  return with(Cut<32, 64, 2, 2, 2>{});
+int with_cut(int cut, F f) {
+  if (cut == 3) return f(Cut<256, 256, 2, 4, 2>{});
+  if (cut == 2) return f(Cut<128, 128, 2, 2, 2>{});
+  if (cut == 1) return f(Cut<64, 128, 1, 4, 2>{});
+  return f(Cut<32, 64, 2, 2, 2>{});
+}
+
+// threads of a workgroup side by side on a row of so many pieces, and the grid for so many rows
+struct RowGrid {
+  int lanes = 1;
+  dim3 grid;
+  RowGrid(int64_t pieces, int64_t rows, int z) {
+    while (lanes < 256 && lanes < pieces) lanes *= 2;
+    const int64_t blocks = (rows + 256 / lanes - 1) / (256 / lanes), columns = (pieces + lanes - 1) / lanes;
+    grid = dim3((unsigned)(blocks < 8192 ? blocks : 8192), (unsigned)(columns < 64 ? columns : 64), z);
+  }
+};
+
+// x, w_gate and w_up (those that a has) at 16-byte rows: the callers' own, or copies
+template <class T>
+int align_rows(const char *who, GatedArgs &a, void *stream) {
+  if (!a.padded) return SVT_OK;
+  const int64_t w_rows = (int64_t)a.n_matrices * a.outs;
+  const RowGrid g(a.in_pitch / 16, a.n_rows > w_rows ? a.n_rows : w_rows, 3);
+  const int rc = launch(who, k_gated_pad<T>, g.grid, 256, 0, stream, a, g.lanes);
+  if (a.x) a.x = a.padded;
+  if (a.w_gate) a.w_gate = a.padded + a.n_rows * a.in_pitch;
+  if (a.w_up) a.w_up = a.padded + (a.n_rows + w_rows) * a.in_pitch;
+  return rc;
 }
 
 template <class T>
-int gated_forward(const char *who, GatedArgs a, bool aligned, void *stream) {
-  // few rows for each matrix: straight from memory
-  const int64_t few = a.offsets ? (a.n_rows + a.n_matrices - 1) / a.n_matrices : a.n_rows;
-  if (few <= (a.offsets ? 24 : 64)) {
-    const int mt = few <= 16 ? 1 : few <= 32 ? 2 : 4;
+int gated_forward(const char *who, GatedArgs a, void *stream) {
+  if (const int mt = few_rows(a)) {
     a.units = row_units(a.n_rows, a.n_matrices, a.offsets != nullptr, 16 * mt);
     a.columns = (a.outs + 15) / 16;
-    if (a.units * a.columns < (1 << 22)) {
-      const unsigned grid = (unsigned)(a.units * a.columns);
-      if (mt == 1) return launch(who, k_gated_few<T, 1, 8>, grid, 64 * kFewWaves, 0, stream, a);
-      if (mt == 2) return launch(who, k_gated_few<T, 2, 4>, grid, 64 * kFewWaves, 0, stream, a);
-      return launch(who, k_gated_few<T, 4, 2>, grid, 64 * kFewWaves, 0, stream, a);
-    }
+    const unsigned grid = (unsigned)(a.units * a.columns);
+    if (mt == 1) return launch(who, k_gated_few<T, 1, 8>, grid, 64 * kFewWaves, 0, stream, a);
+    if (mt == 2) return launch(who, k_gated_few<T, 2, 4>, grid, 64 * kFewWaves, 0, stream, a);
+    return launch(who, k_gated_few<T, 4, 2>, grid, 64 * kFewWaves, 0, stream, a);
   }
+  const int rc = align_rows<T>(who, a, stream);
+  if (rc != SVT_OK) return rc;
   const GatedPlan p = plan_forward(a, sizeof(T));
   a.units = p.units;
   a.columns = p.columns;
-  return with_cut(p.cut, aligned, [&](auto cut, auto al) {
+  return with_cut(p.cut, [&](auto cut) {
     using C = decltype(cut);
-    return launch(who, k_gated<T, C, decltype(al)::value>, (unsigned)eighths(a.units * a.columns), C::threads, 0, stream, a);
+    return launch(who, k_gated<T, C>, (unsigned)eighths(a.units * a.columns), C::threads, 0, stream, a);
   });
 }
 
 template <class T>
-int gated_backward(const char *who, GatedArgs a, bool aligned, void *stream) {
+int gated_backward(const char *who, GatedArgs a, void *stream) {
   constexpr int b = sizeof(T);
   int rc = SVT_OK;
   if (a.n_rows > 0) {
-    int lanes = 1;
-    while (lanes < kBothThreads && lanes < a.pitch / 16) lanes *= 2;
-    const int64_t per = kBothThreads / lanes, blocks = (a.n_rows + per - 1) / per;
-    const int64_t columns = (a.pitch / 16 + lanes - 1) / lanes;
-    rc = launch(who, k_gated_both<T>, dim3((unsigned)(blocks < 65536 ? blocks : 65536), (unsigned)(columns < 64 ? columns : 64)),
-                kBothThreads, 0, stream, a, lanes);
+    rc = align_rows<T>(who, a, stream);
+    if (rc != SVT_OK) return rc;
+    const RowGrid g(a.pitch / 16, a.n_rows, 1);
+    rc = launch(who, k_gated_both<T>, g.grid, kBothThreads, 0, stream, a, g.lanes);
     if (rc != SVT_OK) return rc;
   }
   auto parts = [&](int64_t size, int64_t half, void *out, void *upper, int width) {
@@ -961,10 +970,9 @@ int gated_backward(const char *who, GatedArgs a, bool aligned, void *stream) {
     a.units = p.units;
     a.columns = p.columns;
     a.splits = p.splits;
-    rc = with_cut(p.cut, aligned, [&](auto cut, auto al) {
+    rc = with_cut(p.cut, [&](auto cut) {
       using C = decltype(cut);
-      return launch(who, k_gated_dx<T, C, decltype(al)::value>, dim3((unsigned)eighths(a.units * a.columns), p.splits),
-                    C::threads, 0, stream, a);
+      return launch(who, k_gated_dx<T, C>, dim3((unsigned)eighths(a.units * a.columns), p.splits), C::threads, 0, stream, a);
     });
     if (rc == SVT_OK && p.splits > 1) rc = parts(a.n_rows * a.ins, a.n_rows * a.ins, a.dx, nullptr, a.ins);
     if (rc != SVT_OK) return rc;
@@ -974,11 +982,10 @@ int gated_backward(const char *who, GatedArgs a, bool aligned, void *stream) {
     a.units = p.units;
     a.columns = p.columns;
     a.splits = p.splits;
-    rc = with_cut(p.cut, aligned, [&](auto cut, auto al) {
+    rc = with_cut(p.cut, [&](auto cut) {
       using C = decltype(cut);
       const int64_t own = eighths(a.units / a.n_matrices * a.columns);
-      return launch(who, k_gated_dw<T, C, decltype(al)::value>, dim3((unsigned)(own * a.n_matrices), p.splits),
-                    C::threads, 0, stream, a);
+      return launch(who, k_gated_dw<T, C>, dim3((unsigned)(own * a.n_matrices), p.splits), C::threads, 0, stream, a);
     });
     const int64_t size = (int64_t)a.n_matrices * a.outs * a.ins;
     if (rc == SVT_OK && p.splits > 1) rc = parts(2 * size, size, a.dw_gate, a.dw_up, 0);

@@ -33,15 +33,48 @@ bool any_overlap(const Span *ins, int n_ins, const Span *outs, int n_outs) {
   return false;
 }
 
+GatedArgs gated_args(int32_t n_rows, int32_t n_in, int32_t n_out, int32_t n_matrices, int elem, const int32_t *offsets) {
+  GatedArgs a{};
+  a.n_rows = n_rows;
+  a.ins = n_in;
+  a.outs = n_out;
+  a.n_matrices = n_matrices;
+  a.offsets = offsets;
+  a.splits = 1;
+  a.pitch = gated_pitch(n_out, elem);
+  a.in_pitch = gated_pitch(n_in, elem);
+  return a;
+}
+
+// whether rows of n_in elements begin at multiples of 16 bytes in all of them (NULL: not there)
+bool aligned_rows(int32_t n_in, int elem, const void *x, const void *w_gate, const void *w_up) {
+  return (size_t)n_in * elem % 16 == 0 && !misaligned(x, 16) && !misaligned(w_gate, 16) && !misaligned(w_up, 16);
+}
+
+const int32_t kSome[1] = {0};   // stands for offsets that are given, where only that counts
+
 }  // namespace
 
 }  // namespace svt
 
 using namespace svt;
 
+extern "C" size_t svt_gated_linear_workspace_size(int32_t n_rows, int32_t n_in, int32_t n_out, int32_t n_matrices,
+                                                  int32_t dtype, int32_t by_expert, int32_t aligned) {
+  (void)report(SVT_OK, "%s", "");
+  if (check_gated("svt_gated_linear_workspace_size", n_rows, n_in, n_out, n_matrices, dtype, SVT_ACT_NONE, by_expert != 0) !=
+      SVT_OK)
+    return 0;
+  const int b = elem_size(dtype);
+  const GatedArgs a = gated_args(n_rows, n_in, n_out, n_matrices, b, by_expert ? kSome : nullptr);
+  const bool as_is = n_rows == 0 || few_rows(a) || (aligned && aligned_rows(n_in, b, nullptr, nullptr, nullptr));
+  return as_is ? 0 : gated_copies(a, b);
+}
+
 extern "C" int svt_gated_linear(int32_t n_rows, int32_t n_in, int32_t n_out, int32_t n_matrices, int32_t dtype,
                                 const void *x, const void *w_gate, const void *w_up, const int32_t *offsets,
-                                int32_t activation, void *h, void *gate, void *up, void *hip_stream) {
+                                int32_t activation, void *h, void *gate, void *up, void *workspace,
+                                size_t workspace_bytes, void *hip_stream) {
   const char *who = "svt_gated_linear";
   (void)report(SVT_OK, "%s", "");
   const int rc = check_gated(who, n_rows, n_in, n_out, n_matrices, dtype, activation, offsets != nullptr);
@@ -50,46 +83,40 @@ extern "C" int svt_gated_linear(int32_t n_rows, int32_t n_in, int32_t n_out, int
   if (!gate != !up) return report(SVT_EINVAL, "%s: gate and up are kept both or neither", who);
   const int b = elem_size(dtype);
   if (misaligned(x, b) || misaligned(w_gate, b) || misaligned(w_up, b) || misaligned(offsets, 4) || misaligned(h, b) ||
-      misaligned(gate, b) || misaligned(up, b))
-    return report(SVT_EINVAL, "%s: misaligned input or output", who);
-  const size_t nx = (size_t)n_rows * n_in * b, nw = (size_t)n_matrices * n_out * n_in * b, nh = (size_t)n_rows * n_out * b;
-  const Span ins[4] = {{x, nx}, {w_gate, nw}, {w_up, nw}, {offsets, ((size_t)n_matrices + 1) * 4}};
-  const Span outs[3] = {{h, nh}, {gate, nh}, {up, nh}};
-  if (any_overlap(ins, 4, outs, 3)) return report(SVT_EINVAL, "%s: an output overlaps an input or another output", who);
-  GatedArgs a{};
-  a.n_rows = n_rows;
-  a.ins = n_in;
-  a.outs = n_out;
-  a.n_matrices = n_matrices;
+      misaligned(gate, b) || misaligned(up, b) || misaligned(workspace, 16))
+    return report(SVT_EINVAL, "%s: misaligned input, output or workspace", who);
+  GatedArgs a = gated_args(n_rows, n_in, n_out, n_matrices, b, offsets);
   a.act = activation;
-  a.offsets = offsets;
   a.x = x;
   a.w_gate = w_gate;
   a.w_up = w_up;
   a.h = h;
   a.gate = gate;
   a.up = up;
-  a.splits = 1;
-  a.wide = n_out % 4 == 0 && !misaligned(h, 4 * b) && !misaligned(gate, 4 * b) && !misaligned(up, 4 * b);
+  const size_t need = few_rows(a) || aligned_rows(n_in, b, x, w_gate, w_up) ? 0 : gated_copies(a, b);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return report(SVT_EINVAL, "%s: workspace of %zu bytes, needs %zu", who, workspace ? workspace_bytes : (size_t)0, need);
+  const size_t nx = (size_t)n_rows * n_in * b, nw = (size_t)n_matrices * n_out * n_in * b, nh = (size_t)n_rows * n_out * b;
+  const Span ins[4] = {{x, nx}, {w_gate, nw}, {w_up, nw}, {offsets, ((size_t)n_matrices + 1) * 4}};
+  const Span outs[4] = {{h, nh}, {gate, nh}, {up, nh}, {workspace, need}};
+  if (any_overlap(ins, 4, outs, 4))
+    return report(SVT_EINVAL, "%s: an output or the workspace overlaps an input or another output", who);
   if (!fits(plan_forward(a, b))) return report(SVT_EINVAL, "%s: too many rows of too many outputs for one call", who);
-  const bool aligned = (size_t)n_in * b % 16 == 0 && !misaligned(x, 16) && !misaligned(w_gate, 16) && !misaligned(w_up, 16);
-  return with_type(dtype, [&](auto ty) { return gated_forward<decltype(ty)>(who, a, aligned, hip_stream); });
+  a.padded = need ? (char *)workspace : nullptr;
+  return with_type(dtype, [&](auto ty) { return gated_forward<decltype(ty)>(who, a, hip_stream); });
 }
 
 extern "C" size_t svt_gated_linear_backward_workspace_size(int32_t n_rows, int32_t n_in, int32_t n_out, int32_t n_matrices,
-                                                           int32_t dtype, int32_t by_expert) {
+                                                           int32_t dtype, int32_t by_expert, int32_t aligned) {
   const char *who = "svt_gated_linear_backward_workspace_size";
   (void)report(SVT_OK, "%s", "");
   if (check_gated(who, n_rows, n_in, n_out, n_matrices, dtype, SVT_ACT_NONE, by_expert != 0) != SVT_OK) return 0;
-  GatedArgs a{};
-  a.n_rows = n_rows;
-  a.ins = n_in;
-  a.outs = n_out;
-  a.n_matrices = n_matrices;
-  a.offsets = by_expert ? (const int32_t *)&a : nullptr;   // present or not, never read
-  a.dx = a.dw_gate = &a;
   const int b = elem_size(dtype);
-  return (size_t)(2 * n_rows * gated_pitch(n_out, b)) + gated_partial(a, b);
+  GatedArgs a = gated_args(n_rows, n_in, n_out, n_matrices, b, by_expert ? kSome : nullptr);
+  if (n_rows == 0) return 0;
+  a.dx = a.dw_gate = &a;   // given
+  const bool as_is = aligned && aligned_rows(n_in, b, nullptr, nullptr, nullptr);
+  return (size_t)(2 * n_rows * a.pitch) + (as_is ? 0 : gated_copies(a, b)) + gated_partial(a, b);
 }
 
 extern "C" int svt_gated_linear_backward(int32_t n_rows, int32_t n_in, int32_t n_out, int32_t n_matrices, int32_t dtype,
@@ -112,25 +139,20 @@ extern "C" int svt_gated_linear_backward(int32_t n_rows, int32_t n_in, int32_t n
     if (misaligned(p, b)) return report(SVT_EINVAL, "%s: misaligned input or output", who);
   if (misaligned(offsets, 4) || misaligned(workspace, 16))
     return report(SVT_EINVAL, "%s: misaligned offsets or workspace", who);
-  GatedArgs a{};
-  a.n_rows = n_rows;
-  a.ins = n_in;
-  a.outs = n_out;
-  a.n_matrices = n_matrices;
+  GatedArgs a = gated_args(n_rows, n_in, n_out, n_matrices, b, offsets);
   a.act = activation;
-  a.offsets = offsets;
-  a.x = x;
-  a.w_gate = w_gate;
-  a.w_up = w_up;
+  a.x = dw_gate ? x : nullptr;   // what is not needed is not copied either
+  a.w_gate = dx ? w_gate : nullptr;
+  a.w_up = dx ? w_up : nullptr;
   a.gate = const_cast<void *>(gate);
   a.up = const_cast<void *>(up);
   a.dh = dh;
   a.dx = dx;
   a.dw_gate = dw_gate;
   a.dw_up = dw_up;
-  a.splits = 1;
-  a.pitch = gated_pitch(n_out, b);
-  const size_t both = (size_t)(2 * n_rows * a.pitch), need = both + gated_partial(a, b);
+  const bool as_is = aligned_rows(n_in, b, a.x, a.w_gate, a.w_up);
+  const size_t both = (size_t)(2 * n_rows * a.pitch), copies = as_is || n_rows == 0 ? 0 : gated_copies(a, b);
+  const size_t need = both + copies + gated_partial(a, b);
   if (need > 0 && (!workspace || workspace_bytes < need))
     return report(SVT_EINVAL, "%s: workspace of %zu bytes, needs %zu", who, workspace ? workspace_bytes : (size_t)0, need);
   const size_t nx = (size_t)n_rows * n_in * b, nw = (size_t)n_matrices * n_out * n_in * b, nh = (size_t)n_rows * n_out * b;
@@ -142,8 +164,7 @@ extern "C" int svt_gated_linear_backward(int32_t n_rows, int32_t n_in, int32_t n
   if ((dx && !fits(plan_dx(a, b))) || (dw_gate && !fits(plan_dw(a, b))))
     return report(SVT_EINVAL, "%s: too large a product for one call", who);
   a.d_both = (char *)workspace;
-  a.partial = (float *)(a.d_both + both);
-  a.wide = n_in % 4 == 0 && !misaligned(dx, 4 * b) && !misaligned(dw_gate, 4 * b) && !misaligned(dw_up, 4 * b);
-  const bool aligned = (size_t)n_in * b % 16 == 0 && !misaligned(x, 16) && !misaligned(w_gate, 16) && !misaligned(w_up, 16);
-  return with_type(dtype, [&](auto ty) { return gated_backward<decltype(ty)>(who, a, aligned, hip_stream); });
+  a.padded = copies ? a.d_both + both : nullptr;
+  a.partial = (float *)(a.d_both + both + copies);
+  return with_type(dtype, [&](auto ty) { return gated_backward<decltype(ty)>(who, a, hip_stream); });
 }

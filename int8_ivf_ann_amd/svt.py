@@ -37,7 +37,7 @@ EXPORTED = ("svt_index_upload", "svt_index_upload_updatable", "svt_index_insert"
             "svt_expert_sort_workspace_size", "svt_expert_sort", "svt_expert_dispatch", "svt_expert_dispatch_backward",
             "svt_expert_combine", "svt_expert_combine_backward", "svt_quant_pack_size", "svt_quant_pack",
             "svt_quant_linear", "svt_embedding", "svt_embedding_backward_workspace_size", "svt_embedding_backward",
-            "svt_gated_linear", "svt_gated_linear_backward_workspace_size", "svt_gated_linear_backward",
+            "svt_gated_linear_workspace_size", "svt_gated_linear", "svt_gated_linear_backward_workspace_size", "svt_gated_linear_backward",
             "svt_token_logprobs_workspace_size", "svt_token_logprobs", "svt_token_logprobs_backward", "svt_last_error", "svt_bloom_mask", "svt_bloom_sign", "svt_profile_enable", "svt_profile_read")
 
 
@@ -149,8 +149,10 @@ def lib():
     L.svt_embedding_backward_workspace_size.argtypes = [i64, i64, i32]
     L.svt_embedding_backward_workspace_size.restype = sz
     L.svt_embedding_backward.argtypes = [i64, i64, i32, i32, vp, vp, f32, i32, i32, vp, vp, sz, vp]
-    L.svt_gated_linear.argtypes = [i32, i32, i32, i32, i32, vp, vp, vp, vp, i32, vp, vp, vp, vp]
-    L.svt_gated_linear_backward_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32]
+    L.svt_gated_linear_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32]
+    L.svt_gated_linear_workspace_size.restype = sz
+    L.svt_gated_linear.argtypes = [i32, i32, i32, i32, i32, vp, vp, vp, vp, i32, vp, vp, vp, vp, sz, vp]
+    L.svt_gated_linear_backward_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32]
     L.svt_gated_linear_backward_workspace_size.restype = sz
     L.svt_gated_linear_backward.argtypes = [i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, sz,
                                             vp]
@@ -839,29 +841,44 @@ def _gated_shape(x, w_gate, w_up, offsets, activation):
     return R, K, N, M, code, dev, _GATES[activation]
 
 
+@functools.lru_cache(maxsize=256)
+def svt_gated_linear_workspace_size(n_rows: int, n_in: int, n_out: int, n_matrices: int, dtype: int, by_expert: bool,
+                                    aligned: bool) -> int:
+    """Bytes of workspace that svt_gated_linear needs (0: none); dtype: SVT_F32, SVT_F16 or SVT_BF16, aligned: whether x and
+    the weights are 16-byte aligned."""
+    need = lib().svt_gated_linear_workspace_size(n_rows, n_in, n_out, n_matrices, dtype, int(by_expert), int(aligned))
+    if need == 0 and svt_last_error():
+        raise SvtError(SVT_EINVAL, svt_last_error())
+    return int(need)
+
+
 def svt_gated_linear(x, w_gate, w_up, offsets=None, activation: str = "silu", keep: bool = False, out=None, out_gate=None,
-                     out_up=None, stream=None):
+                     out_up=None, workspace=None, stream=None):
     """h = act(x w_gate^T) * (x w_up^T): x [R, K] (float32, float16, bfloat16), w_gate and w_up [N, K] of its dtype -> h
     [R, N].  With ``offsets`` int32 [M + 1] (svt_expert_sort's) the weights are [M, N, K], pair e serves rows offsets[e]
     .. offsets[e + 1] - 1, and rows past the last stay as they were.  activation: "silu", "gelu", "relu" or "none".
     ``keep`` also returns what the gradient needs: (h, gate, up)."""
     R, K, N, M, code, dev, act = _gated_shape(x, w_gate, w_up, offsets, activation)
+    at_x, at_g, at_u = x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr()
+    need = svt_gated_linear_workspace_size(R, K, N, M, code, offsets is not None, (at_x | at_g | at_u) % 16 == 0)
     with _Run(dev, stream) as s:
         out = _out("out", out, x.dtype, (R, N), dev, x)
         if keep:
             out_gate = _out("out_gate", out_gate, x.dtype, (R, N), dev, x)
             out_up = _out("out_up", out_up, x.dtype, (R, N), dev, x)
-        _check(lib().svt_gated_linear(R, K, N, M, code, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
-                                      None if offsets is None else offsets.data_ptr(), act, out.data_ptr(),
-                                      out_gate.data_ptr() if keep else None, out_up.data_ptr() if keep else None, s))
+        workspace, at, size = _workspace(workspace, need, dev, x)
+        _check(lib().svt_gated_linear(R, K, N, M, code, at_x, at_g, at_u, None if offsets is None else offsets.data_ptr(),
+                                      act, out.data_ptr(), out_gate.data_ptr() if keep else None,
+                                      out_up.data_ptr() if keep else None, at, size, s))
     return (out, out_gate, out_up) if keep else out
 
 
 @functools.lru_cache(maxsize=256)
 def svt_gated_linear_backward_workspace_size(n_rows: int, n_in: int, n_out: int, n_matrices: int, dtype: int,
-                                             by_expert: bool) -> int:
-    """Bytes of workspace that svt_gated_linear_backward needs for these sizes; dtype: SVT_F32, SVT_F16 or SVT_BF16."""
-    need = lib().svt_gated_linear_backward_workspace_size(n_rows, n_in, n_out, n_matrices, dtype, int(by_expert))
+                                             by_expert: bool, aligned: bool) -> int:
+    """Bytes of workspace that svt_gated_linear_backward needs; arguments as svt_gated_linear_workspace_size."""
+    need = lib().svt_gated_linear_backward_workspace_size(n_rows, n_in, n_out, n_matrices, dtype, int(by_expert),
+                                                          int(aligned))
     if need == 0 and svt_last_error():
         raise SvtError(SVT_EINVAL, svt_last_error())
     return int(need)
@@ -876,15 +893,15 @@ def svt_gated_linear_backward(dh, x, w_gate, w_up, gate, up, offsets=None, activ
     R, K, N, M, code, dev, act = _gated_shape(x, w_gate, w_up, offsets, activation)
     for name, t in (("dh", dh), ("gate", gate), ("up", up)):
         _check_dense(name, t, x.dtype, (R, N), dev)
-    need = svt_gated_linear_backward_workspace_size(R, K, N, M, code, offsets is not None)
+    at_x, at_g, at_u = x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr()
+    need = svt_gated_linear_backward_workspace_size(R, K, N, M, code, offsets is not None, (at_x | at_g | at_u) % 16 == 0)
     with _Run(dev, stream) as s:
         out_x = _out("out_x", out_x, x.dtype, (R, K), dev, x) if need_x else None
         out_gate = _out("out_gate", out_gate, x.dtype, w_gate.shape, dev, x) if need_weights else None
         out_up = _out("out_up", out_up, x.dtype, w_gate.shape, dev, x) if need_weights else None
         workspace, at, size = _workspace(workspace, need, dev, x)
-        _check(lib().svt_gated_linear_backward(R, K, N, M, code, dh.data_ptr(), x.data_ptr(), w_gate.data_ptr(),
-                                               w_up.data_ptr(), gate.data_ptr(), up.data_ptr(),
-                                               None if offsets is None else offsets.data_ptr(), act,
+        _check(lib().svt_gated_linear_backward(R, K, N, M, code, dh.data_ptr(), at_x, at_g, at_u, gate.data_ptr(),
+                                               up.data_ptr(), None if offsets is None else offsets.data_ptr(), act,
                                                *[None if t is None else t.data_ptr() for t in (out_x, out_gate, out_up)],
                                                at, size, s))
     return out_x, out_gate, out_up
