@@ -501,8 +501,8 @@ int svt_embedding_backward(int64_t n_tokens, int64_t n_rows, int32_t width, int3
  *   h            [n_rows][n_out] of dtype
  *   gate, up     [n_rows][n_out] of dtype, or both NULL: w_gate x and w_up x, which the gradient needs
  *   workspace    svt_gated_linear_workspace_size(n_rows, n_in, n_out, n_matrices, dtype, offsets != NULL, aligned) bytes,
- *                16-byte aligned; NULL where that is 0.  aligned: 1 if x, w_gate and w_up are 16-byte aligned; where they
- *                are not, or n_in elements are no multiple of 16 bytes, the call copies them first (but for few rows)
+ *                16-byte aligned; NULL where that is 0.  aligned: 1 if x, w_gate and w_up are 4-byte aligned; where they
+ *                are not, or n_in elements are no multiple of 4 bytes, the call copies them first (but for few rows)
  * Sums are float32; h, gate and up are rounded once each (h from the unrounded sums).
  * n_rows == 0 returns SVT_OK without enqueuing.  Errors: SVT_EINVAL, SVT_EDEVICE as svt_route.
  */

@@ -18,7 +18,9 @@
 //   across   the other index lies together (W for dx; x, dg, du for dW): rows of the tile's width for each reduced index,
 //            and the transposing read of LDS (float32: single values) collects a fragment
 // In both, the 16-byte pieces of a row are permuted by the row's number, so that the lanes of a read spread over the
-// banks.  Pieces outside the matrix are zeros: their address lies outside the buffer's range.
+// banks.  Pieces outside the matrix are zeros: their address lies outside the buffer's range.  Rows need only begin at
+// multiples of 4 bytes: the loads ask for no more, the range ends with the array (every 4 bytes are checked by themselves),
+// and a piece that runs on into the next row is cleared in LDS, in the last step alone.
 #pragma once
 
 #include <type_traits>
@@ -109,7 +111,7 @@ struct Cut {
 };
 
 // where a step's pieces begin: the side's first row (of its upper half), at the step's first reduced index
-struct Base { const char *at, *upper; };
+struct Base { const char *at, *upper, *end, *upper_end; };   // end: of the arrays
 
 // One side of a tile.  ROWS: the tile's size along the side's own index; HALVES: two matrices' rows, half a tile each.
 template <class T, int ROWS, int THREADS, bool ACROSS, bool HALVES = false>
@@ -154,12 +156,16 @@ struct Side {
   // result in registers.)
   __device__ __forceinline__ void load(Base from, uint32_t lds, bool final) const {
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)threadIdx.x / 64);
-    auto buffer = [](const char *p) {
+    auto buffer = [](const char *p, const char *end) {
       const uint64_t v = (uint64_t)(uintptr_t)p;
+      const int64_t range = end - p;   // may be negative for an unused upper half
+      const uint32_t bytes = range <= 0 ? 0u : range < kRange ? (uint32_t)range : (uint32_t)kRange;
       return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v),
-                   (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32)) & 0xFFFFu, kRange, 0x00020000u};
+                   (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32)) & 0xFFFFu,
+                   (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00020000u};
     };
-    const u32x4 lower = buffer(from.at), upper = buffer(HALVES ? from.upper : from.at);
+    const u32x4 lower = buffer(from.at, from.end);
+    const u32x4 upper = HALVES ? buffer(from.upper, from.upper_end) : lower;
     const uint32_t out = final ? gone : 0u;
 #pragma unroll
     for (int j = 0; j < pieces; ++j) {
@@ -167,6 +173,15 @@ struct Side {
       asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(at),
                    "s"(HALVES && 2 * j >= pieces ? upper : lower)
                    : "memory");
+    }
+  }
+
+  // clears what lies behind the `reduced` valid elements of a last step in the piece that they end in
+  static __device__ __forceinline__ void clear_tail(char *lds, int reduced) {
+    static_assert(!ACROSS, "across, whole rows lie outside");
+    for (int row = (int)threadIdx.x; row < ROWS; row += THREADS) {
+      T *at = reinterpret_cast<T *>(lds + row * kStepBytes + permuted(row, reduced / each) * 16);
+      for (int i = reduced % each; i < each; ++i) at[i] = (T)0.f;
     }
   }
 
@@ -260,8 +275,10 @@ struct Product {
     }
   }
 
+  // ragged: the valid elements of a last step where its last pieces have to be cleared (both sides along), or 0
   template <class At, class Last>
-  __device__ __forceinline__ void run(int steps, char *lds, At base, Last last, f32x4 (&acc)[C::nq][C::np]) const {
+  __device__ __forceinline__ void run(int steps, int ragged, char *lds, At base, Last last,
+                                      f32x4 (&acc)[C::nq][C::np]) const {
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64), wq = wave / C::WP, wp = wave % C::WP;
     if (steps <= 0) return;
     const uint32_t at = (uint32_t)(uintptr_t)(lds_void *)lds;
@@ -280,6 +297,12 @@ struct Product {
       if (s + ahead <= steps) loads_done<(ahead - 1) * (SP::pieces + SQ::pieces)>();   // later steps' are in flight
       else loads_done<0>();
       __syncthreads();   // the step's pieces are there, and the buffer before it has been read
+      if constexpr (!PA && !QA)
+        if (ragged && last(s)) {
+          SP::clear_tail(lds + out, ragged);
+          SQ::clear_tail(lds + out + SP::bytes, ragged);
+          __syncthreads();
+        }
       step(lds + out, wq, wp, acc, [&] {
         if (s + ahead < steps) load(s + ahead);
       });
@@ -294,7 +317,33 @@ struct Rows { int matrix; int64_t first, end; };
 
 __device__ __forceinline__ int64_t clamped(int64_t v, int64_t n) { return v < 0 ? 0 : v < n ? v : n; }
 
-// the unit-th block of `per` rows of one matrix; matrix -1: there is none.  The whole wave asks.
+// rows of matrix e: [first, end)
+__device__ __forceinline__ Rows rows_of_matrix(const int32_t *offsets, int64_t n_rows, int e) {
+  if (!offsets) return {e, 0, n_rows};
+  const int64_t a = clamped(offsets[e], n_rows), z = clamped(offsets[e + 1], n_rows);
+  return {e, a, z > a ? z : a};
+}
+
+// blocks of `per` rows of matrices e0 .. e0 + 63, one a lane
+__device__ __forceinline__ int blocks_of(const int32_t *offsets, int n_matrices, int64_t n_rows, int e0, int per, Rows &r) {
+  const int e = e0 + lane_id();
+  r = {e, 0, 0};
+  if (e < n_matrices) r = rows_of_matrix(offsets, n_rows, e);
+  return (int)((r.end - r.first + per - 1) / per);
+}
+
+// all blocks of `per` rows; the whole wave asks, as below
+__device__ __forceinline__ int64_t count_units(const int32_t *offsets, int n_matrices, int64_t n_rows, int per) {
+  if (!offsets) return (n_rows + per - 1) / per;
+  int64_t all = 0;
+  for (int e0 = 0; e0 < n_matrices; e0 += 64) {
+    Rows r;
+    all += __builtin_amdgcn_readlane(incl_sums(blocks_of(offsets, n_matrices, n_rows, e0, per, r)), 63);
+  }
+  return all;
+}
+
+// the unit-th of them; matrix -1: there is none
 __device__ __forceinline__ Rows rows_of_unit(const int32_t *offsets, int n_matrices, int64_t n_rows, int64_t unit, int per) {
   if (!offsets) {
     const int64_t first = unit * per;
@@ -302,20 +351,15 @@ __device__ __forceinline__ Rows rows_of_unit(const int32_t *offsets, int n_matri
   }
   int64_t before = 0;
   for (int e0 = 0; e0 < n_matrices; e0 += 64) {
-    const int e = e0 + lane_id();
-    int64_t a = 0, z = 0;
-    if (e < n_matrices) {
-      a = clamped(offsets[e], n_rows);
-      z = clamped(offsets[e + 1], n_rows);
-    }
-    const int blocks = z > a ? (int)((z - a + per - 1) / per) : 0;
+    Rows r;
+    const int blocks = blocks_of(offsets, n_matrices, n_rows, e0, per, r);
     const int upto = incl_sums(blocks);
     const uint64_t past = __ballot(before + upto > unit);
     if (past) {
       const int l = __builtin_ctzll(past);
       const int skip = (int)(unit - before) - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(blocks, l));
-      const int64_t first = __builtin_amdgcn_readlane((int)a, l) + (int64_t)skip * per;
-      const int64_t end = __builtin_amdgcn_readlane((int)z, l);
+      const int64_t first = __builtin_amdgcn_readlane((int)r.first, l) + (int64_t)skip * per;
+      const int64_t end = __builtin_amdgcn_readlane((int)r.end, l);
       return {e0 + l, first, first + per < end ? first + per : end};
     }
     before += __builtin_amdgcn_readlane(upto, 63);
@@ -325,9 +369,8 @@ __device__ __forceinline__ Rows rows_of_unit(const int32_t *offsets, int n_matri
 
 // The matrix whose number of rows is the rank-th largest (ties: the lower one first), of at most 64; the whole wave asks
 __device__ __forceinline__ int by_length(const int32_t *offsets, int n_matrices, int64_t n_rows, int rank) {
-  const int e = lane_id() < n_matrices ? lane_id() : 0;
-  const int64_t a = clamped(offsets[e], n_rows), z = clamped(offsets[e + 1], n_rows);
-  const int len = lane_id() < n_matrices ? (int)(z > a ? z - a : 0) : -1;
+  const Rows r = rows_of_matrix(offsets, n_rows, lane_id() < n_matrices ? lane_id() : 0);
+  const int len = lane_id() < n_matrices ? (int)(r.end - r.first) : -1;
   int before = 0;
   for (int i = 0; i < n_matrices; ++i) {
     const int other = __builtin_amdgcn_readlane(len, i);
@@ -354,6 +397,7 @@ struct GatedArgs {
   int64_t n_rows, units;
   int32_t ins, outs, n_matrices, columns;   // columns: tiles across
   int32_t act;
+  int32_t few;                // forward: blocks of 16 rows for the kernel of few rows, or 0
   const int32_t *offsets;
   const void *x, *w_gate, *w_up;
   void *h, *gate, *up;        // gate, up: NULL where they are not kept
@@ -362,7 +406,7 @@ struct GatedArgs {
   void *dx, *dw_gate, *dw_up;
   char *d_both;               // dg, then du: [n_rows][pitch] each
   int64_t pitch;              // bytes
-  int64_t in_pitch;           // bytes of a row of x, w_gate and w_up: a multiple of 16, but for few rows
+  int64_t in_pitch;           // bytes of a row of x, w_gate and w_up: a multiple of 4, but for few rows
   char *padded;               // their copies with such rows, where they are not so: x, then w_gate, then w_up
   int32_t splits;             // of the reduced index: partial results in `partial`
   float *partial;
@@ -475,7 +519,10 @@ __global__ __launch_bounds__(C::threads) void k_gated(GatedArgs a) {
   __shared__ __attribute__((aligned(1024))) char lds[larger(Pr::lds_bytes, Staged<C, T, outs>::bytes)];
   int64_t unit;
   int column;
-  if (!tile_of(blockIdx.x, a.units, a.columns, unit, column)) return;
+  // the matrices' own blocks, not as many as there may be, are shared out over the L2s: by expert, 1024 tiles in a grid of
+  // 1088, @@
+  const int64_t units = count_units(a.offsets, a.n_matrices, a.n_rows, C::q);
+  if (!tile_of(blockIdx.x, units, a.columns, unit, column)) return;
   const Rows rows = rows_of_unit(a.offsets, a.n_matrices, a.n_rows, unit, C::q);
   if (rows.matrix < 0) return;
   const int n0 = column * outs;
@@ -486,14 +533,16 @@ __global__ __launch_bounds__(C::threads) void k_gated(GatedArgs a) {
   product.Q.init((uint32_t)pitch, (int)(rows.end - rows.first), tail);
   const int64_t w0 = ((int64_t)rows.matrix * a.outs + n0) * pitch;
   const char *wg = (const char *)a.w_gate + w0, *wu = (const char *)a.w_up + w0;
-  const char *x = (const char *)a.x + rows.first * pitch;
+  const char *x = (const char *)a.x + rows.first * pitch, *x_end = (const char *)a.x + a.n_rows * pitch;
+  const int64_t w_bytes = (int64_t)a.n_matrices * a.outs * pitch;
+  const char *wg_end = (const char *)a.w_gate + w_bytes, *wu_end = (const char *)a.w_up + w_bytes;
   f32x4 acc[C::nq][C::np] = {};
   product.run(
-      steps, lds,
+      steps, tail % Pr::SP::each ? tail : 0, lds,
       [&](int s, Base &p, Base &q) {
         const int64_t k = (int64_t)s * kStepBytes;
-        p = {wg + k, wu + k};
-        q = {x + k, x + k};
+        p = {wg + k, wu + k, wg_end, wu_end};
+        q = {x + k, nullptr, x_end, nullptr};
       },
       [&](int s) { return s + 1 == steps; }, acc);
   constexpr int half = C::np / 2;
@@ -520,9 +569,9 @@ __global__ __launch_bounds__(C::threads) void k_gated(GatedArgs a) {
 //
 // Up to 16 MT rows of one matrix against 16 outputs: the weights' bytes are the cost, so they go straight to registers,
 // each once, 64 bytes of a row at a time and U such pieces in flight.  The waves share the inputs out and their sums meet
-// in LDS.
+// in LDS.  Four waves and few pieces each, so that several workgroups share a compute unit: 1 row of 32768 x 4096 bfloat16
+// 97 us (5.5 TB/s), with 8 waves of 8 pieces 104; 64 rows over 128 experts of 1024 x 1024 46 and 64.
 
-constexpr int kFewWaves = 8;
 
 // 16 bytes of a row from index k on, zeros past its end
 template <class T>
@@ -539,9 +588,9 @@ __device__ __forceinline__ typename Mul<T>::frag load_sixteen(const T *row, int 
   return __builtin_bit_cast(typename Mul<T>::frag, v);
 }
 
-template <class T, int MT, int U>
-__global__ __launch_bounds__(64 * kFewWaves) void k_gated_few(GatedArgs a) {
-  __shared__ f32x4 sums[kFewWaves][2 * MT][64];
+template <class T, int MT, int U, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 4) void k_gated_few(GatedArgs a) {
+  __shared__ f32x4 sums[WAVES][2 * MT][64];
   const int64_t unit = blockIdx.x / a.columns;
   const int column = (int)(blockIdx.x - unit * a.columns);
   const Rows rows = rows_of_unit(a.offsets, a.n_matrices, a.n_rows, unit, 16 * MT);
@@ -558,7 +607,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_gated_few(GatedArgs a) {
     x[m] = (const T *)a.x + (r < rows.end ? r : rows.end - 1) * a.ins;
   }
   f32x4 acc[2 * MT] = {};
-  for (int k0 = wave * U * step; k0 < a.ins; k0 += kFewWaves * U * step) {
+  for (int k0 = wave * U * step; k0 < a.ins; k0 += WAVES * U * step) {
     typename Mul<T>::frag fg[U], fu[U], fx[MT][U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -582,7 +631,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_gated_few(GatedArgs a) {
   if (wave >= MT) return;
   f32x4 s[2] = {};
 #pragma unroll
-  for (int w = 0; w < kFewWaves; ++w) {
+  for (int w = 0; w < WAVES; ++w) {
     s[0] += sums[w][2 * wave][lane_id()];
     s[1] += sums[w][2 * wave + 1][lane_id()];
   }
@@ -608,9 +657,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_gated_few(GatedArgs a) {
 
 // ---- rows of any alignment -----------------------------------------------------------------------
 //
-// The loads that go straight to LDS want rows that begin at multiples of 16 bytes.  Others are copied first, with zeros
-// behind each row: 2 (x + w) bytes more to move, which is little beside a product of many rows; a path of its own through
-// registers took twice as long as copy and product (1001 x 250 x 999 float32: @@).
+// The loads that go straight to LDS want rows that begin at multiples of 4 bytes.  Others (two-byte values, an odd number
+// in a row or an odd address) are copied first, to rows of whole pieces with zeros behind: 2 (x + w) bytes more to move.  A
+// path of its own through registers took longer than copy and product together (gradients of 1001 x 250 x 999 float32, when
+// every row that does not begin at 16 bytes went there: 86 us, with the copy 52).
 template <class T>
 __global__ __launch_bounds__(256) void k_gated_pad(GatedArgs a, int lanes) {
   constexpr int each = 16 / sizeof(T);
@@ -688,7 +738,10 @@ __global__ __launch_bounds__(C::threads) void k_gated_dx(GatedArgs a) {
       lds[larger(Pr::lds_bytes, larger(Staged<C, T, C::p>::bytes, Staged<C, float, C::p>::bytes))];
   int64_t unit;
   int column;
-  if (!tile_of(blockIdx.x, a.units, a.columns, unit, column)) return;
+  // the matrices' own blocks, not as many as there may be, are shared out over the L2s: by expert, 1024 tiles in a grid of
+  // 1088, @@
+  const int64_t units = count_units(a.offsets, a.n_matrices, a.n_rows, C::q);
+  if (!tile_of(blockIdx.x, units, a.columns, unit, column)) return;
   const Rows rows = rows_of_unit(a.offsets, a.n_matrices, a.n_rows, unit, C::q);
   if (rows.matrix < 0) return;
   const int k0 = column * C::p;
@@ -701,16 +754,17 @@ __global__ __launch_bounds__(C::threads) void k_gated_dx(GatedArgs a) {
   product.Q.init((uint32_t)a.pitch, (int)(rows.end - rows.first), tail);
   const int64_t w0 = (int64_t)rows.matrix * a.outs * pitch + (int64_t)k0 * sizeof(T);
   const char *wg = (const char *)a.w_gate + w0, *wu = (const char *)a.w_up + w0;
-  const char *dg = a.d_both + rows.first * a.pitch, *du = dg + a.n_rows * a.pitch;
+  const int64_t w_bytes = (int64_t)a.n_matrices * a.outs * pitch;
+  const char *dg = a.d_both + rows.first * a.pitch, *du = dg + a.n_rows * a.pitch, *d_end = a.d_both + 2 * a.n_rows * a.pitch;
   f32x4 acc[C::nq][C::np] = {};
   product.run(
-      steps, lds,
+      steps, 0, lds,
       [&](int t, Base &p, Base &q) {
         const int s = s0 + t, in = s < half ? s : s - half;
         const char *w = (s < half ? wg : wu) + (int64_t)in * Pr::SP::step * pitch;
         const char *d = (s < half ? dg : du) + (int64_t)in * kStepBytes;
-        p = {w, w};
-        q = {d, d};
+        p = {w, nullptr, (const char *)(s < half ? a.w_gate : a.w_up) + w_bytes, nullptr};
+        q = {d, nullptr, d_end, nullptr};
       },
       [&](int t) { return s0 + t + 1 == half || s0 + t + 1 == 2 * half; }, acc);
   store_tile<T, C>(acc, lds, rows.first, rows.end, k0, a.ins, (T *)a.dx,
@@ -733,9 +787,8 @@ __global__ __launch_bounds__(C::threads) void k_gated_dw(GatedArgs a) {
   const int matrix = a.offsets && a.n_matrices <= 64 ? by_length(a.offsets, a.n_matrices, a.n_rows, rank) : rank;
   const bool up = in >= tiles;
   const int n0 = (up ? in - tiles : in) * C::q, k0 = column * C::p;
-  const int64_t first = a.offsets ? clamped(a.offsets[matrix], a.n_rows) : 0;
-  const int64_t end = a.offsets ? clamped(a.offsets[matrix + 1], a.n_rows) : a.n_rows;
-  const int64_t len = end > first ? end - first : 0, all = (len + Pr::SP::step - 1) / Pr::SP::step;
+  const Rows rows = rows_of_matrix(a.offsets, a.n_rows, matrix);
+  const int64_t first = rows.first, len = rows.end - first, all = (len + Pr::SP::step - 1) / Pr::SP::step;
   const int64_t each = (all + a.splits - 1) / a.splits, s0 = blockIdx.y * each;
   const int steps = (int)(all - s0 < each ? all - s0 : each);
   const int64_t pitch = a.in_pitch;
@@ -746,12 +799,13 @@ __global__ __launch_bounds__(C::threads) void k_gated_dw(GatedArgs a) {
   const char *x = (const char *)a.x + first * pitch + (int64_t)k0 * sizeof(T);
   const char *d = a.d_both + (up ? a.n_rows * a.pitch : 0) + first * a.pitch + (int64_t)n0 * sizeof(T);
   f32x4 acc[C::nq][C::np] = {};
+  const char *x_end = (const char *)a.x + a.n_rows * pitch, *d_end = a.d_both + 2 * a.n_rows * a.pitch;
   product.run(
-      steps, lds,
+      steps, 0, lds,
       [&](int t, Base &p, Base &q) {
         const int64_t s = (s0 + t) * Pr::SP::step;
-        p = {x + s * pitch, x + s * pitch};
-        q = {d + s * a.pitch, d + s * a.pitch};
+        p = {x + s * pitch, nullptr, x_end, nullptr};
+        q = {d + s * a.pitch, nullptr, d_end, nullptr};
       },
       [&](int t) { return s0 + t + 1 == all; }, acc);
   const int64_t size = (int64_t)a.outs * a.ins, of = matrix * size;
@@ -859,11 +913,13 @@ inline GatedPlan plan_dw(const GatedArgs &a, int elem) {
 // a grid's threads stay below 2^32
 inline bool fits(const GatedPlan &p) { return (p.units * p.columns + 8 * SVT_MAX_EXPERTS) * p.splits < (1 << 22); }
 
-// Whether the forward pass takes the kernel for few rows (up to 16, 32 or 64 of a matrix on average: 1, 2 or 4 blocks), or 0
-inline int few_rows(const GatedArgs &a) {
+// Whether the forward pass takes the kernel for few rows: 1 or 2 blocks of 16, or 0.  Few: up to 32 (64 x 2048 x 2048 bfloat16
+// 14.3 us there, 10.9 with tiles; 32 x 2048 x 2048 10.1 and 10.7).  By expert up to 4 on average (32 experts of 1024 x 1024,
+// 64 rows 22.2 and 20.9, 256 rows 24.9 and 22.3), or 32 where tiles would need copies.
+inline int few_rows(const GatedArgs &a, bool copies) {
   const int64_t rows = a.offsets ? (a.n_rows + a.n_matrices - 1) / a.n_matrices : a.n_rows;
-  const int mt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  if (rows > (a.offsets ? 24 : 64)) return 0;
+  if (rows > (a.offsets && !copies ? 4 : 32)) return 0;
+  const int mt = rows <= 16 ? 1 : 2;
   return row_units(a.n_rows, a.n_matrices, a.offsets != nullptr, 16 * mt) * ((a.outs + 15) / 16) < (1 << 22) ? mt : 0;
 }
 
@@ -915,7 +971,7 @@ struct RowGrid {
   }
 };
 
-// x, w_gate and w_up (those that a has) at 16-byte rows: the callers' own, or copies
+// x, w_gate and w_up (those that a has) with rows at multiples of 4 bytes: the caller's own, or copies
 template <class T>
 int align_rows(const char *who, GatedArgs &a, void *stream) {
   if (!a.padded) return SVT_OK;
@@ -930,13 +986,12 @@ int align_rows(const char *who, GatedArgs &a, void *stream) {
 
 template <class T>
 int gated_forward(const char *who, GatedArgs a, void *stream) {
-  if (const int mt = few_rows(a)) {
+  if (const int mt = a.few) {
     a.units = row_units(a.n_rows, a.n_matrices, a.offsets != nullptr, 16 * mt);
     a.columns = (a.outs + 15) / 16;
     const unsigned grid = (unsigned)(a.units * a.columns);
-    if (mt == 1) return launch(who, k_gated_few<T, 1, 8>, grid, 64 * kFewWaves, 0, stream, a);
-    if (mt == 2) return launch(who, k_gated_few<T, 2, 4>, grid, 64 * kFewWaves, 0, stream, a);
-    return launch(who, k_gated_few<T, 4, 2>, grid, 64 * kFewWaves, 0, stream, a);
+    if (mt == 1) return launch(who, k_gated_few<T, 1, 4, 4>, grid, 256, 0, stream, a);
+    return launch(who, k_gated_few<T, 2, 2, 4>, grid, 256, 0, stream, a);
   }
   const int rc = align_rows<T>(who, a, stream);
   if (rc != SVT_OK) return rc;

@@ -42,13 +42,13 @@ GatedArgs gated_args(int32_t n_rows, int32_t n_in, int32_t n_out, int32_t n_matr
   a.offsets = offsets;
   a.splits = 1;
   a.pitch = gated_pitch(n_out, elem);
-  a.in_pitch = gated_pitch(n_in, elem);
+  a.in_pitch = (int64_t)n_in * elem;
   return a;
 }
 
-// whether rows of n_in elements begin at multiples of 16 bytes in all of them (NULL: not there)
+// whether rows of n_in elements begin at multiples of 4 bytes in all of them (NULL: not there)
 bool aligned_rows(int32_t n_in, int elem, const void *x, const void *w_gate, const void *w_up) {
-  return (size_t)n_in * elem % 16 == 0 && !misaligned(x, 16) && !misaligned(w_gate, 16) && !misaligned(w_up, 16);
+  return (size_t)n_in * elem % 4 == 0 && !misaligned(x, 4) && !misaligned(w_gate, 4) && !misaligned(w_up, 4);
 }
 
 const int32_t kSome[1] = {0};   // stands for offsets that are given, where only that counts
@@ -67,8 +67,8 @@ extern "C" size_t svt_gated_linear_workspace_size(int32_t n_rows, int32_t n_in, 
     return 0;
   const int b = elem_size(dtype);
   const GatedArgs a = gated_args(n_rows, n_in, n_out, n_matrices, b, by_expert ? kSome : nullptr);
-  const bool as_is = n_rows == 0 || few_rows(a) || (aligned && aligned_rows(n_in, b, nullptr, nullptr, nullptr));
-  return as_is ? 0 : gated_copies(a, b);
+  const bool as_is = n_rows == 0 || (aligned && aligned_rows(n_in, b, nullptr, nullptr, nullptr));
+  return as_is || few_rows(a, true) ? 0 : gated_copies(a, b);
 }
 
 extern "C" int svt_gated_linear(int32_t n_rows, int32_t n_in, int32_t n_out, int32_t n_matrices, int32_t dtype,
@@ -93,7 +93,9 @@ extern "C" int svt_gated_linear(int32_t n_rows, int32_t n_in, int32_t n_out, int
   a.h = h;
   a.gate = gate;
   a.up = up;
-  const size_t need = few_rows(a) || aligned_rows(n_in, b, x, w_gate, w_up) ? 0 : gated_copies(a, b);
+  const bool as_is = aligned_rows(n_in, b, x, w_gate, w_up);
+  a.few = few_rows(a, !as_is);
+  const size_t need = as_is || a.few ? 0 : gated_copies(a, b);
   if (need > 0 && (!workspace || workspace_bytes < need))
     return report(SVT_EINVAL, "%s: workspace of %zu bytes, needs %zu", who, workspace ? workspace_bytes : (size_t)0, need);
   const size_t nx = (size_t)n_rows * n_in * b, nw = (size_t)n_matrices * n_out * n_in * b, nh = (size_t)n_rows * n_out * b;
@@ -102,7 +104,10 @@ extern "C" int svt_gated_linear(int32_t n_rows, int32_t n_in, int32_t n_out, int
   if (any_overlap(ins, 4, outs, 4))
     return report(SVT_EINVAL, "%s: an output or the workspace overlaps an input or another output", who);
   if (!fits(plan_forward(a, b))) return report(SVT_EINVAL, "%s: too many rows of too many outputs for one call", who);
-  a.padded = need ? (char *)workspace : nullptr;
+  if (need) {
+    a.padded = (char *)workspace;
+    a.in_pitch = gated_pitch(n_in, b);
+  }
   return with_type(dtype, [&](auto ty) { return gated_forward<decltype(ty)>(who, a, hip_stream); });
 }
 
@@ -164,7 +169,10 @@ extern "C" int svt_gated_linear_backward(int32_t n_rows, int32_t n_in, int32_t n
   if ((dx && !fits(plan_dx(a, b))) || (dw_gate && !fits(plan_dw(a, b))))
     return report(SVT_EINVAL, "%s: too large a product for one call", who);
   a.d_both = (char *)workspace;
-  a.padded = copies ? a.d_both + both : nullptr;
+  if (copies) {
+    a.padded = a.d_both + both;
+    a.in_pitch = gated_pitch(n_in, b);
+  }
   a.partial = (float *)(a.d_both + both + copies);
   return with_type(dtype, [&](auto ty) { return gated_backward<decltype(ty)>(who, a, hip_stream); });
 }

@@ -845,7 +845,7 @@ def _gated_shape(x, w_gate, w_up, offsets, activation):
 def svt_gated_linear_workspace_size(n_rows: int, n_in: int, n_out: int, n_matrices: int, dtype: int, by_expert: bool,
                                     aligned: bool) -> int:
     """Bytes of workspace that svt_gated_linear needs (0: none); dtype: SVT_F32, SVT_F16 or SVT_BF16, aligned: whether x and
-    the weights are 16-byte aligned."""
+    the weights are 4-byte aligned."""
     need = lib().svt_gated_linear_workspace_size(n_rows, n_in, n_out, n_matrices, dtype, int(by_expert), int(aligned))
     if need == 0 and svt_last_error():
         raise SvtError(SVT_EINVAL, svt_last_error())
@@ -860,7 +860,7 @@ def svt_gated_linear(x, w_gate, w_up, offsets=None, activation: str = "silu", ke
     ``keep`` also returns what the gradient needs: (h, gate, up)."""
     R, K, N, M, code, dev, act = _gated_shape(x, w_gate, w_up, offsets, activation)
     at_x, at_g, at_u = x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr()
-    need = svt_gated_linear_workspace_size(R, K, N, M, code, offsets is not None, (at_x | at_g | at_u) % 16 == 0)
+    need = svt_gated_linear_workspace_size(R, K, N, M, code, offsets is not None, (at_x | at_g | at_u) % 4 == 0)
     with _Run(dev, stream) as s:
         out = _out("out", out, x.dtype, (R, N), dev, x)
         if keep:
@@ -894,7 +894,7 @@ def svt_gated_linear_backward(dh, x, w_gate, w_up, gate, up, offsets=None, activ
     for name, t in (("dh", dh), ("gate", gate), ("up", up)):
         _check_dense(name, t, x.dtype, (R, N), dev)
     at_x, at_g, at_u = x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr()
-    need = svt_gated_linear_backward_workspace_size(R, K, N, M, code, offsets is not None, (at_x | at_g | at_u) % 16 == 0)
+    need = svt_gated_linear_backward_workspace_size(R, K, N, M, code, offsets is not None, (at_x | at_g | at_u) % 4 == 0)
     with _Run(dev, stream) as s:
         out_x = _out("out_x", out_x, x.dtype, (R, K), dev, x) if need_x else None
         out_gate = _out("out_gate", out_gate, x.dtype, w_gate.shape, dev, x) if need_weights else None
