@@ -324,12 +324,15 @@ __device__ __forceinline__ Rows rows_of_matrix(const int32_t *offsets, int64_t n
   return {e, a, z > a ? z : a};
 }
 
-// blocks of `per` rows of matrices e0 .. e0 + 63, one a lane
-__device__ __forceinline__ int blocks_of(const int32_t *offsets, int n_matrices, int64_t n_rows, int e0, int per, Rows &r) {
+// blocks of `per` rows of matrices e0 .. e0 + 63, one a lane; of a matrix without rows `least`
+__device__ __forceinline__ int blocks_of(const int32_t *offsets, int n_matrices, int64_t n_rows, int e0, int64_t per,
+                                         int least, Rows &r) {
   const int e = e0 + lane_id();
   r = {e, 0, 0};
-  if (e < n_matrices) r = rows_of_matrix(offsets, n_rows, e);
-  return (int)((r.end - r.first + per - 1) / per);
+  if (e >= n_matrices) return 0;
+  r = rows_of_matrix(offsets, n_rows, e);
+  const int64_t n = (r.end - r.first + per - 1) / per;
+  return n > least ? (int)n : least;
 }
 
 // all blocks of `per` rows; the whole wave asks, as below
@@ -338,21 +341,23 @@ __device__ __forceinline__ int64_t count_units(const int32_t *offsets, int n_mat
   int64_t all = 0;
   for (int e0 = 0; e0 < n_matrices; e0 += 64) {
     Rows r;
-    all += __builtin_amdgcn_readlane(incl_sums(blocks_of(offsets, n_matrices, n_rows, e0, per, r)), 63);
+    all += __builtin_amdgcn_readlane(incl_sums(blocks_of(offsets, n_matrices, n_rows, e0, per, 0, r)), 63);
   }
   return all;
 }
 
-// the unit-th of them; matrix -1: there is none
-__device__ __forceinline__ Rows rows_of_unit(const int32_t *offsets, int n_matrices, int64_t n_rows, int64_t unit, int per) {
+// the unit-th of them; matrix -1: there is none.  part: its number among the blocks of matrices that have several, or -1
+__device__ __forceinline__ Rows rows_of_unit(const int32_t *offsets, int n_matrices, int64_t n_rows, int64_t unit, int64_t per,
+                                             int least = 0, int64_t *part = nullptr) {
   if (!offsets) {
     const int64_t first = unit * per;
-    return {first < n_rows ? 0 : -1, first, first + per < n_rows ? first + per : n_rows};
+    if (part) *part = n_rows <= per ? -1 : unit;
+    return {first < n_rows || unit < least ? 0 : -1, first, first + per < n_rows ? first + per : n_rows};
   }
-  int64_t before = 0;
+  int64_t before = 0, parts = 0;
   for (int e0 = 0; e0 < n_matrices; e0 += 64) {
     Rows r;
-    const int blocks = blocks_of(offsets, n_matrices, n_rows, e0, per, r);
+    const int blocks = blocks_of(offsets, n_matrices, n_rows, e0, per, least, r);
     const int upto = incl_sums(blocks);
     const uint64_t past = __ballot(before + upto > unit);
     if (past) {
@@ -360,23 +365,18 @@ __device__ __forceinline__ Rows rows_of_unit(const int32_t *offsets, int n_matri
       const int skip = (int)(unit - before) - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(blocks, l));
       const int64_t first = __builtin_amdgcn_readlane((int)r.first, l) + (int64_t)skip * per;
       const int64_t end = __builtin_amdgcn_readlane((int)r.end, l);
+      if (part) {
+        const int several = blocks > 1 ? blocks : 0, upto_several = incl_sums(several);
+        *part = __builtin_amdgcn_readlane(blocks, l) == 1
+                    ? -1
+                    : parts + __builtin_amdgcn_readlane(upto_several, l) - __builtin_amdgcn_readlane(several, l) + skip;
+      }
       return {e0 + l, first, first + per < end ? first + per : end};
     }
     before += __builtin_amdgcn_readlane(upto, 63);
+    if (part) parts += __builtin_amdgcn_readlane(incl_sums(blocks > 1 ? blocks : 0), 63);
   }
   return {-1, 0, 0};
-}
-
-// The matrix whose number of rows is the rank-th largest (ties: the lower one first), of at most 64; the whole wave asks
-__device__ __forceinline__ int by_length(const int32_t *offsets, int n_matrices, int64_t n_rows, int rank) {
-  const Rows r = rows_of_matrix(offsets, n_rows, lane_id() < n_matrices ? lane_id() : 0);
-  const int len = lane_id() < n_matrices ? (int)(r.end - r.first) : -1;
-  int before = 0;
-  for (int i = 0; i < n_matrices; ++i) {
-    const int other = __builtin_amdgcn_readlane(len, i);
-    before += other > len || (other == len && i < lane_id()) ? 1 : 0;
-  }
-  return __builtin_ctzll(__ballot(lane_id() < n_matrices && before == rank));
 }
 
 __host__ __device__ inline int64_t eighths(int64_t tiles) { return (tiles + 7) / 8 * 8; }
@@ -408,7 +408,8 @@ struct GatedArgs {
   int64_t pitch;              // bytes
   int64_t in_pitch;           // bytes of a row of x, w_gate and w_up: a multiple of 4, but for few rows
   char *padded;               // their copies with such rows, where they are not so: x, then w_gate, then w_up
-  int32_t splits;             // of the reduced index: partial results in `partial`
+  int32_t splits;             // dx: parts of the reduced index
+  int64_t per;                // dW: rows of a matrix that are reduced at once
   float *partial;
 };
 
@@ -771,79 +772,104 @@ __global__ __launch_bounds__(C::threads) void k_gated_dx(GatedArgs a) {
                    a.splits > 1 ? a.partial + (int64_t)blockIdx.y * a.n_rows * a.ins : nullptr);
 }
 
-// dWg and dWu: side P: columns of x (across), side Q: columns of dg or du (across); the rows are reduced
+// dWg and dWu: side P: columns of x (across), side Q: columns of dg or du (across); the rows are reduced, a.per of a matrix
+// at a time: the products of a matrix with more rows than that are parts, which k_gated_join adds.  (One expert may have
+// most of the rows: 13018 of 16384 with 7 others, 1024 inputs, 2048 outputs: @@.)
 template <class T, class C>
 __global__ __launch_bounds__(C::threads) void k_gated_dw(GatedArgs a) {
   using Pr = Product<T, C, true, true, false>;
   __shared__ __attribute__((aligned(1024))) char
       lds[larger(Pr::lds_bytes, larger(Staged<C, T, C::p>::bytes, Staged<C, float, C::p>::bytes))];
-  // a matrix's tiles lie together, spread over all L2s; the longest sums come first (8 uneven experts, 16384 rows: @@)
   const int tiles = (a.outs + C::q - 1) / C::q;
-  const int64_t own = eighths((int64_t)2 * tiles * a.columns);
-  int64_t unit;
+  const int64_t own = eighths((int64_t)2 * tiles * a.columns), block = blockIdx.x / own;   // a block's tiles use all L2s
+  int64_t in;
   int column;
-  if (!tile_of(blockIdx.x % own, 2 * tiles, a.columns, unit, column)) return;
-  const int rank = (int)(blockIdx.x / own), in = (int)unit;
-  const int matrix = a.offsets && a.n_matrices <= 64 ? by_length(a.offsets, a.n_matrices, a.n_rows, rank) : rank;
+  if (!tile_of(blockIdx.x % own, 2 * tiles, a.columns, in, column)) return;
+  int64_t part = -1;
+  const Rows rows = rows_of_unit(a.offsets, a.n_matrices, a.n_rows, block, a.per, 1, &part);
+  if (rows.matrix < 0) return;
   const bool up = in >= tiles;
-  const int n0 = (up ? in - tiles : in) * C::q, k0 = column * C::p;
-  const Rows rows = rows_of_matrix(a.offsets, a.n_rows, matrix);
-  const int64_t first = rows.first, len = rows.end - first, all = (len + Pr::SP::step - 1) / Pr::SP::step;
-  const int64_t each = (all + a.splits - 1) / a.splits, s0 = blockIdx.y * each;
-  const int steps = (int)(all - s0 < each ? all - s0 : each);
-  const int64_t pitch = a.in_pitch;
+  const int n0 = (int)(up ? in - tiles : in) * C::q, k0 = column * C::p;
+  const int64_t len = rows.end - rows.first, pitch = a.in_pitch;
+  const int steps = (int)((len + Pr::SP::step - 1) / Pr::SP::step), tail = (int)(len - (int64_t)(steps - 1) * Pr::SP::step);
   Pr product;
-  const int tail = (int)(len - (all - 1) * Pr::SP::step);
   product.P.init((uint32_t)pitch, a.ins - k0 < C::p ? a.ins - k0 : C::p, tail);
   product.Q.init((uint32_t)a.pitch, a.outs - n0 < C::q ? a.outs - n0 : C::q, tail);
-  const char *x = (const char *)a.x + first * pitch + (int64_t)k0 * sizeof(T);
-  const char *d = a.d_both + (up ? a.n_rows * a.pitch : 0) + first * a.pitch + (int64_t)n0 * sizeof(T);
-  f32x4 acc[C::nq][C::np] = {};
+  const char *x = (const char *)a.x + rows.first * pitch + (int64_t)k0 * sizeof(T);
+  const char *d = a.d_both + (up ? a.n_rows * a.pitch : 0) + rows.first * a.pitch + (int64_t)n0 * sizeof(T);
   const char *x_end = (const char *)a.x + a.n_rows * pitch, *d_end = a.d_both + 2 * a.n_rows * a.pitch;
+  f32x4 acc[C::nq][C::np] = {};
   product.run(
       steps, 0, lds,
       [&](int t, Base &p, Base &q) {
-        const int64_t s = (s0 + t) * Pr::SP::step;
+        const int64_t s = (int64_t)t * Pr::SP::step;
         p = {x + s * pitch, nullptr, x_end, nullptr};
         q = {d + s * a.pitch, nullptr, d_end, nullptr};
       },
-      [&](int t) { return s0 + t + 1 == all; }, acc);
-  const int64_t size = (int64_t)a.outs * a.ins, of = matrix * size;
-  float *part = a.splits > 1 ? a.partial + (((int64_t)blockIdx.y * 2 + up) * a.n_matrices) * size + of : nullptr;
-  store_tile<T, C>(acc, lds, n0, a.outs, k0, a.ins, (T *)(up ? a.dw_up : a.dw_gate) + of, part);
+      [&](int t) { return t + 1 == steps; }, acc);
+  const int64_t size = (int64_t)a.outs * a.ins;
+  store_tile<T, C>(acc, lds, n0, a.outs, k0, a.ins, (T *)(up ? a.dw_up : a.dw_gate) + rows.matrix * size,
+                   part < 0 ? nullptr : a.partial + (part * 2 + up) * size);
 }
 
-// out[i] = the sum of the parts, in order; of each part `size` values, the last size - half of them to `upper`.  Rows that
-// no matrix names keep their values where `width` is given (dx).
+struct __attribute__((packed, aligned(4))) FourParts { float v[4]; };
+
+// to[i ..] = the sum of `parts` float32 arrays at from, `stride` apart, in order; up to four values, `left` of them
 template <class T>
-__global__ __launch_bounds__(256) void k_gated_parts(const float *partial, int splits, int64_t size, int64_t half, T *out,
-                                                     T *upper, GatedArgs a, int width) {
-  struct __attribute__((packed, aligned(4))) Raw { float v[4]; };
-  struct __attribute__((packed, aligned(sizeof(T)))) Results { uint8_t v[4 * sizeof(T)]; };
-  struct Values { T t[4]; };
-  int64_t first = 0, end = size;
-  if (width && a.offsets) {
-    first = clamped(a.offsets[0], a.n_rows) * width;
-    end = clamped(a.offsets[a.n_matrices], a.n_rows) * width;
-  }
-  for (int64_t i = first + (blockIdx.x * 256ll + threadIdx.x) * 4; i < end; i += gridDim.x * 1024ll) {
-    if (i + 4 <= end && (i + 4 <= half || i >= half)) {
-      Raw sum = *reinterpret_cast<const Raw *>(partial + i);
+__device__ __forceinline__ void join_four(const float *from, int parts, int64_t stride, int64_t left, T *to) {
+  FourParts sum{};
+  if (left >= 4) {
+    sum = *reinterpret_cast<const FourParts *>(from);
 #pragma unroll 4
-      for (int z = 1; z < splits; ++z) {
-        const Raw v = *reinterpret_cast<const Raw *>(partial + z * size + i);
+    for (int z = 1; z < parts; ++z) {
+      const FourParts v = *reinterpret_cast<const FourParts *>(from + z * stride);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) sum.v[k] += v.v[k];
-      }
-      const Values r{{(T)sum.v[0], (T)sum.v[1], (T)sum.v[2], (T)sum.v[3]}};
-      *reinterpret_cast<Results *>(i < half ? out + i : upper + (i - half)) = __builtin_bit_cast(Results, r);
-    } else {
-      for (int64_t k = i; k < end && k < i + 4; ++k) {
-        float sum = partial[k];
-        for (int z = 1; z < splits; ++z) sum += partial[z * size + k];
-        *(k < half ? out + k : upper + (k - half)) = (T)sum;
-      }
+      for (int k = 0; k < 4; ++k) sum.v[k] += v.v[k];
     }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < left) {
+        sum.v[k] = from[k];
+        for (int z = 1; z < parts; ++z) sum.v[k] += from[z * stride + k];
+      }
+  }
+  store_four(to, sum.v, (int)(left < 4 ? left : 4));
+}
+
+// dx from its parts; rows that no matrix names keep their values
+template <class T>
+__global__ __launch_bounds__(256) void k_gated_join_dx(GatedArgs a) {
+  const int64_t size = a.n_rows * a.ins;
+  const int64_t first = a.offsets ? clamped(a.offsets[0], a.n_rows) * a.ins : 0;
+  const int64_t end = a.offsets ? clamped(a.offsets[a.n_matrices], a.n_rows) * a.ins : size;
+  for (int64_t i = first + (blockIdx.x * 256ll + threadIdx.x) * 4; i < end; i += gridDim.x * 1024ll)
+    join_four(a.partial + i, a.splits, size, end - i, (T *)a.dx + i);
+}
+
+// dWg and dWu of the matrices whose rows were cut into blocks; blockIdx.y: the matrix
+template <class T>
+__global__ __launch_bounds__(256) void k_gated_join_dw(GatedArgs a) {
+  int64_t before = 0;   // parts of the matrices before it
+  const int matrix = blockIdx.y;
+  for (int e0 = 0; a.offsets && e0 < matrix; e0 += 64) {
+    Rows r;
+    const int blocks = blocks_of(a.offsets, matrix, a.n_rows, e0, a.per, 1, r);
+    before += __builtin_amdgcn_readlane(incl_sums(blocks > 1 ? blocks : 0), 63);
+  }
+  const Rows rows = rows_of_matrix(a.offsets, a.n_rows, matrix);
+  const int parts = (int)((rows.end - rows.first + a.per - 1) / a.per);
+  if (parts < 2) return;
+  const int64_t size = (int64_t)a.outs * a.ins;
+  for (int64_t i = (blockIdx.x * 256ll + threadIdx.x) * 4; i < 2 * size; i += gridDim.x * 1024ll) {
+    // four values may lie in both halves
+    const int64_t gate = size - i;
+    const float *from = a.partial + before * 2 * size + i;
+    if (gate > 0) join_four(from, parts, 2 * size, gate, (T *)a.dw_gate + matrix * size + i);
+    const int64_t skip = gate <= 0 ? 0 : gate < 4 ? gate : 4;
+    if (skip < 4 && i + skip < 2 * size)
+      join_four(from + skip, parts, 2 * size, 2 * size - i - skip < 4 - skip ? 2 * size - i - skip : 4 - skip,
+                (T *)a.dw_up + matrix * size + (i + skip - size));
   }
 }
 
@@ -852,8 +878,9 @@ __global__ __launch_bounds__(256) void k_gated_parts(const float *partial, int s
 // How a product runs; the same for the workspace's size.
 struct GatedPlan {
   int cut;         // of the four below
-  int splits;      // parts of the reduced index
-  int64_t units;   // tiles along the rows of the result, at most
+  int splits;      // dx: parts of the reduced index
+  int64_t per;     // dW: rows reduced at once
+  int64_t units;   // tiles along the rows of the result, at most; dW: blocks of rows
   int columns;
 };
 
@@ -882,7 +909,7 @@ GatedPlan plan_product(int elem, Units units, int width, int64_t steps, double r
   const int type = elem == 4;
   for (int cut = 0; cut < kCuts; ++cut) {
     const CutCost &c = kCutCost[cut];
-    GatedPlan p{cut, 1, units(c.q), (width + c.p - 1) / c.p};
+    GatedPlan p{cut, 1, 0, units(c.q), (width + c.p - 1) / c.p};
     for (; p.splits <= 32 && (p.splits == 1 || (results > 0 && steps >= 2 * p.splits)); p.splits *= 2) {
       const int64_t tiles = p.units * p.columns * p.splits, load = (tiles + 255) / 256;
       const double each = (double)((steps + p.splits - 1) / p.splits);
@@ -905,13 +932,44 @@ inline GatedPlan plan_dx(const GatedArgs &a, int elem) {
   return plan_product(elem, [&](int q) { return row_units(a.n_rows, a.n_matrices, a.offsets != nullptr, q); }, a.ins,
                       2 * ((a.outs + kStepBytes / elem - 1) / (kStepBytes / elem)), (double)a.n_rows * a.ins);
 }
+
+// The same for dW, whose rows are cut into blocks of p.per.  By expert, half the rows may be one expert's: blocks that one
+// workgroup walks should not be longer than its share of all steps.
 inline GatedPlan plan_dw(const GatedArgs &a, int elem) {
-  return plan_product(elem, [&](int q) { return (int64_t)a.n_matrices * 2 * ((a.outs + q - 1) / q); }, a.ins,
-                      a.n_rows / a.n_matrices / (kStepBytes / elem) + 1, 2.0 * a.n_matrices * a.outs * a.ins);
+  GatedPlan best{};
+  double least = 0;
+  const int type = elem == 4, step = kStepBytes / elem;
+  const int64_t all = (a.n_rows + step - 1) / step;
+  const int experts = a.offsets ? a.n_matrices : 1;
+  for (int cut = 0; cut < kCuts; ++cut) {
+    const CutCost &c = kCutCost[cut];
+    const int columns = (a.ins + c.p - 1) / c.p;
+    const int64_t tiles = (int64_t)2 * ((a.outs + c.q - 1) / c.q) * columns;
+    for (int parts = 1; parts <= 32 && (parts == 1 || all >= 4 * parts); parts *= 2) {
+      const int64_t steps = (all + parts - 1) / parts;
+      GatedPlan p{cut, 1, steps * step, all / (steps ? steps : 1) + experts, columns};
+      const double longest = (double)(a.offsets && parts == 1 ? (all + 1) / 2 : steps);
+      const double each = longest < 1 ? 1 : longest;                                   // steps of the longest block
+      const double load = ((double)all + 0.5 * experts) * (double)tiles / 256;         // steps of a compute unit
+      double time = 3 + (load <= each ? each * c.alone[type] : load * c.shared[type] + 0.5 * each * c.alone[type]);
+      if (parts > 1) time += 4 + 2.4e-6 * parts * 2.0 * a.outs * a.ins;
+      if ((cut == 0 && parts == 1) || time < least) {
+        least = time;
+        best = p;
+      }
+    }
+  }
+  if (best.per < 1) best.per = 1;
+  if (!a.offsets) best.units = (a.n_rows + best.per - 1) / best.per > 1 ? (a.n_rows + best.per - 1) / best.per : 1;
+  else best.units = a.n_rows / best.per + experts;
+  return best;
 }
 
 // a grid's threads stay below 2^32
-inline bool fits(const GatedPlan &p) { return (p.units * p.columns + 8 * SVT_MAX_EXPERTS) * p.splits < (1 << 22); }
+inline bool fits(const GatedPlan &p) { return (p.units * p.columns + 8) * p.splits < (1 << 22); }
+inline bool fits_dw(const GatedPlan &p, int32_t outs) {
+  return p.units * ((int64_t)2 * ((outs + 31) / 32) * p.columns + 8) < (1 << 23);
+}
 
 // Whether the forward pass takes the kernel for few rows: 1 or 2 blocks of 16, or 0.  Few: up to 32 (64 x 2048 x 2048 bfloat16
 // 14.3 us there, 10.9 with tiles; 32 x 2048 x 2048 10.1 and 10.7).  By expert up to 4 on average (32 experts of 1024 x 1024,
@@ -940,7 +998,8 @@ inline size_t gated_partial(const GatedArgs &a, int elem) {
   }
   if (a.dw_gate) {
     const GatedPlan p = plan_dw(a, elem);
-    const size_t n = p.splits > 1 ? (size_t)p.splits * 2 * a.n_matrices * a.outs * a.ins * 4 : 0;
+    // matrices with several blocks have at most 2 n_rows / per together
+    const size_t n = p.per < a.n_rows ? (size_t)(2 * a.n_rows / p.per) * 2 * a.outs * a.ins * 4 : 0;
     if (n > most) most = n;
   }
   return most;
@@ -1004,6 +1063,8 @@ int gated_forward(const char *who, GatedArgs a, void *stream) {
   });
 }
 
+inline unsigned join_grid(int64_t values) { return (unsigned)((values + 1023) / 1024 < 2048 ? (values + 1023) / 1024 : 2048); }
+
 template <class T>
 int gated_backward(const char *who, GatedArgs a, void *stream) {
   constexpr int b = sizeof(T);
@@ -1015,11 +1076,6 @@ int gated_backward(const char *who, GatedArgs a, void *stream) {
     rc = launch(who, k_gated_both<T>, g.grid, kBothThreads, 0, stream, a, g.lanes);
     if (rc != SVT_OK) return rc;
   }
-  auto parts = [&](int64_t size, int64_t half, void *out, void *upper, int width) {
-    const int64_t blocks = (size + 1023) / 1024;
-    return launch(who, k_gated_parts<T>, (unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, stream, (const float *)a.partial,
-                  a.splits, size, half, (T *)out, (T *)upper, a, width);
-  };
   if (a.dx && a.n_rows > 0) {
     const GatedPlan p = plan_dx(a, b);
     a.units = p.units;
@@ -1029,21 +1085,21 @@ int gated_backward(const char *who, GatedArgs a, void *stream) {
       using C = decltype(cut);
       return launch(who, k_gated_dx<T, C>, dim3((unsigned)eighths(a.units * a.columns), p.splits), C::threads, 0, stream, a);
     });
-    if (rc == SVT_OK && p.splits > 1) rc = parts(a.n_rows * a.ins, a.n_rows * a.ins, a.dx, nullptr, a.ins);
+    if (rc == SVT_OK && p.splits > 1)
+      rc = launch(who, k_gated_join_dx<T>, join_grid(a.n_rows * a.ins), 256, 0, stream, a);
     if (rc != SVT_OK) return rc;
   }
   if (a.dw_gate) {
     const GatedPlan p = plan_dw(a, b);
-    a.units = p.units;
     a.columns = p.columns;
-    a.splits = p.splits;
+    a.per = p.per;
     rc = with_cut(p.cut, [&](auto cut) {
       using C = decltype(cut);
-      const int64_t own = eighths(a.units / a.n_matrices * a.columns);
-      return launch(who, k_gated_dw<T, C>, dim3((unsigned)(own * a.n_matrices), p.splits), C::threads, 0, stream, a);
+      const int64_t own = eighths((int64_t)2 * ((a.outs + C::q - 1) / C::q) * a.columns);
+      return launch(who, k_gated_dw<T, C>, (unsigned)(own * p.units), C::threads, 0, stream, a);
     });
-    const int64_t size = (int64_t)a.n_matrices * a.outs * a.ins;
-    if (rc == SVT_OK && p.splits > 1) rc = parts(2 * size, size, a.dw_gate, a.dw_up, 0);
+    if (rc == SVT_OK && p.per < a.n_rows)
+      rc = launch(who, k_gated_join_dw<T>, dim3(join_grid((int64_t)2 * a.outs * a.ins), a.n_matrices), 256, 0, stream, a);
   }
   return rc;
 }
