@@ -410,6 +410,9 @@ struct GatedArgs {
   char *padded;               // their copies with such rows, where they are not so: x, then w_gate, then w_up
   int32_t splits;             // dx: parts of the reduced index
   int64_t per;                // dW: rows of a matrix that are reduced at once
+  int32_t dx_first;
+  int64_t dx_blocks, dw_blocks;   // workgroups of each, dx's with its parts
+  int64_t dw_partial;         // where dW's parts begin in `partial`, behind dx's
   float *partial;
 };
 
@@ -520,8 +523,7 @@ __global__ __launch_bounds__(C::threads) void k_gated(GatedArgs a) {
   __shared__ __attribute__((aligned(1024))) char lds[larger(Pr::lds_bytes, Staged<C, T, outs>::bytes)];
   int64_t unit;
   int column;
-  // the matrices' own blocks, not as many as there may be, are shared out over the L2s: by expert, 1024 tiles in a grid of
-  // 1088, @@
+  // the matrices' own blocks, not as many as there may be, are shared out over the L2s (dx_tile has the figures)
   const int64_t units = count_units(a.offsets, a.n_matrices, a.n_rows, C::q);
   if (!tile_of(blockIdx.x, units, a.columns, unit, column)) return;
   const Rows rows = rows_of_unit(a.offsets, a.n_matrices, a.n_rows, unit, C::q);
@@ -733,22 +735,20 @@ __global__ __launch_bounds__(kBothThreads) void k_gated_both(GatedArgs a, int la
 
 // dx: side P: columns of Wg, then of Wu (across); side Q: rows of dg, then of du (along)
 template <class T, class C>
-__global__ __launch_bounds__(C::threads) void k_gated_dx(GatedArgs a) {
+__device__ __forceinline__ void dx_tile(const GatedArgs &a, char *lds, int64_t b, int part) {
   using Pr = Product<T, C, true, false, false>;
-  __shared__ __attribute__((aligned(1024))) char
-      lds[larger(Pr::lds_bytes, larger(Staged<C, T, C::p>::bytes, Staged<C, float, C::p>::bytes))];
   int64_t unit;
   int column;
-  // the matrices' own blocks, not as many as there may be, are shared out over the L2s: by expert, 1024 tiles in a grid of
-  // 1088, @@
+  // the matrices' own blocks, not as many as there may be, are shared out over the L2s (8 even experts of 2048 rows, 1024
+  // tiles in a grid for 1088: 179 us by what there may be, 121 like this)
   const int64_t units = count_units(a.offsets, a.n_matrices, a.n_rows, C::q);
-  if (!tile_of(blockIdx.x, units, a.columns, unit, column)) return;
+  if (!tile_of(b, units, a.columns, unit, column)) return;
   const Rows rows = rows_of_unit(a.offsets, a.n_matrices, a.n_rows, unit, C::q);
   if (rows.matrix < 0) return;
   const int k0 = column * C::p;
   const int64_t pitch = a.in_pitch;
   const int half = (a.outs + Pr::SP::step - 1) / Pr::SP::step, tail = a.outs - (half - 1) * Pr::SP::step;
-  const int each = (2 * half + a.splits - 1) / a.splits, s0 = blockIdx.y * each;
+  const int each = (2 * half + a.splits - 1) / a.splits, s0 = part * each;
   const int steps = 2 * half - s0 < each ? 2 * half - s0 : each;   // none, or fewer, for the last part
   Pr product;
   product.P.init((uint32_t)pitch, a.ins - k0 < C::p ? a.ins - k0 : C::p, tail);
@@ -769,22 +769,19 @@ __global__ __launch_bounds__(C::threads) void k_gated_dx(GatedArgs a) {
       },
       [&](int t) { return s0 + t + 1 == half || s0 + t + 1 == 2 * half; }, acc);
   store_tile<T, C>(acc, lds, rows.first, rows.end, k0, a.ins, (T *)a.dx,
-                   a.splits > 1 ? a.partial + (int64_t)blockIdx.y * a.n_rows * a.ins : nullptr);
+                   a.splits > 1 ? a.partial + (int64_t)part * a.n_rows * a.ins : nullptr);
 }
 
 // dWg and dWu: side P: columns of x (across), side Q: columns of dg or du (across); the rows are reduced, a.per of a matrix
-// at a time: the products of a matrix with more rows than that are parts, which k_gated_join adds.  (One expert may have
-// most of the rows: 13018 of 16384 with 7 others, 1024 inputs, 2048 outputs: @@.)
+// at a time: the products of a matrix with more rows than that are parts, which k_gated_join adds
 template <class T, class C>
-__global__ __launch_bounds__(C::threads) void k_gated_dw(GatedArgs a) {
+__device__ __forceinline__ void dw_tile(const GatedArgs &a, char *lds, int64_t b) {
   using Pr = Product<T, C, true, true, false>;
-  __shared__ __attribute__((aligned(1024))) char
-      lds[larger(Pr::lds_bytes, larger(Staged<C, T, C::p>::bytes, Staged<C, float, C::p>::bytes))];
   const int tiles = (a.outs + C::q - 1) / C::q;
-  const int64_t own = eighths((int64_t)2 * tiles * a.columns), block = blockIdx.x / own;   // a block's tiles use all L2s
+  const int64_t own = eighths((int64_t)2 * tiles * a.columns), block = b / own;   // a block's tiles use all L2s
   int64_t in;
   int column;
-  if (!tile_of(blockIdx.x % own, 2 * tiles, a.columns, in, column)) return;
+  if (!tile_of(b % own, 2 * tiles, a.columns, in, column)) return;
   int64_t part = -1;
   const Rows rows = rows_of_unit(a.offsets, a.n_matrices, a.n_rows, block, a.per, 1, &part);
   if (rows.matrix < 0) return;
@@ -809,7 +806,25 @@ __global__ __launch_bounds__(C::threads) void k_gated_dw(GatedArgs a) {
       [&](int t) { return t + 1 == steps; }, acc);
   const int64_t size = (int64_t)a.outs * a.ins;
   store_tile<T, C>(acc, lds, n0, a.outs, k0, a.ins, (T *)(up ? a.dw_up : a.dw_gate) + rows.matrix * size,
-                   part < 0 ? nullptr : a.partial + (part * 2 + up) * size);
+                   part < 0 ? nullptr : a.partial + a.dw_partial + (part * 2 + up) * size);
+}
+
+// dx and dW are tiles of one grid, so that the last of the one leave no compute unit idle beside the other: 16384 rows over 8
+// experts, most of them one's, 1024 inputs, 2048 outputs: 427 us in two launches, 402 in one; 1001 x 250 x 999 float32 51 and 42.  Whichever reduces more at once comes first.
+template <class T, class C>
+__global__ __launch_bounds__(C::threads) void k_gated_gradients(GatedArgs a) {
+  __shared__ __attribute__((aligned(1024))) char lds[larger(Product<T, C, true, false, false>::lds_bytes,
+                                                            larger(Staged<C, T, C::p>::bytes, Staged<C, float, C::p>::bytes))];
+  int64_t b = blockIdx.x;
+  const int64_t first = a.dx_first ? a.dx_blocks : a.dw_blocks;
+  const bool later = b >= first;
+  if (later) b -= first;
+  if (later != (a.dx_first != 0)) {
+    const int64_t own = a.dx_blocks / a.splits;
+    dx_tile<T, C>(a, lds, b % own, (int)(b / own));
+  } else {
+    dw_tile<T, C>(a, lds, b);
+  }
 }
 
 struct __attribute__((packed, aligned(4))) FourParts { float v[4]; };
@@ -837,21 +852,22 @@ __device__ __forceinline__ void join_four(const float *from, int parts, int64_t 
   store_four(to, sum.v, (int)(left < 4 ? left : 4));
 }
 
-// dx from its parts; rows that no matrix names keep their values
+// The parts' sums.  blockIdx.y: dx (0; rows that no matrix names keep their values), then each matrix's dWg and dWu, where
+// its rows were cut into blocks.
 template <class T>
-__global__ __launch_bounds__(256) void k_gated_join_dx(GatedArgs a) {
-  const int64_t size = a.n_rows * a.ins;
-  const int64_t first = a.offsets ? clamped(a.offsets[0], a.n_rows) * a.ins : 0;
-  const int64_t end = a.offsets ? clamped(a.offsets[a.n_matrices], a.n_rows) * a.ins : size;
-  for (int64_t i = first + (blockIdx.x * 256ll + threadIdx.x) * 4; i < end; i += gridDim.x * 1024ll)
-    join_four(a.partial + i, a.splits, size, end - i, (T *)a.dx + i);
-}
-
-// dWg and dWu of the matrices whose rows were cut into blocks; blockIdx.y: the matrix
-template <class T>
-__global__ __launch_bounds__(256) void k_gated_join_dw(GatedArgs a) {
+__global__ __launch_bounds__(256) void k_gated_join(GatedArgs a) {
+  const int64_t at = (blockIdx.x * 256ll + threadIdx.x) * 4, hop = gridDim.x * 1024ll;
+  if (blockIdx.y == 0) {
+    if (!a.dx || a.splits < 2) return;
+    const int64_t size = a.n_rows * a.ins;
+    const int64_t first = a.offsets ? clamped(a.offsets[0], a.n_rows) * a.ins : 0;
+    const int64_t end = a.offsets ? clamped(a.offsets[a.n_matrices], a.n_rows) * a.ins : size;
+    for (int64_t i = first + at; i < end; i += hop) join_four(a.partial + i, a.splits, size, end - i, (T *)a.dx + i);
+    return;
+  }
+  if (!a.dw_gate) return;
   int64_t before = 0;   // parts of the matrices before it
-  const int matrix = blockIdx.y;
+  const int matrix = blockIdx.y - 1;
   for (int e0 = 0; a.offsets && e0 < matrix; e0 += 64) {
     Rows r;
     const int blocks = blocks_of(a.offsets, matrix, a.n_rows, e0, a.per, 1, r);
@@ -861,10 +877,9 @@ __global__ __launch_bounds__(256) void k_gated_join_dw(GatedArgs a) {
   const int parts = (int)((rows.end - rows.first + a.per - 1) / a.per);
   if (parts < 2) return;
   const int64_t size = (int64_t)a.outs * a.ins;
-  for (int64_t i = (blockIdx.x * 256ll + threadIdx.x) * 4; i < 2 * size; i += gridDim.x * 1024ll) {
-    // four values may lie in both halves
-    const int64_t gate = size - i;
-    const float *from = a.partial + before * 2 * size + i;
+  for (int64_t i = at; i < 2 * size; i += hop) {
+    const int64_t gate = size - i;   // four values may lie in both halves
+    const float *from = a.partial + a.dw_partial + before * 2 * size + i;
     if (gate > 0) join_four(from, parts, 2 * size, gate, (T *)a.dw_gate + matrix * size + i);
     const int64_t skip = gate <= 0 ? 0 : gate < 4 ? gate : 4;
     if (skip < 4 && i + skip < 2 * size)
@@ -877,21 +892,24 @@ __global__ __launch_bounds__(256) void k_gated_join_dw(GatedArgs a) {
 
 // How a product runs; the same for the workspace's size.
 struct GatedPlan {
-  int cut;         // of the four below
-  int splits;      // dx: parts of the reduced index
-  int64_t per;     // dW: rows reduced at once
-  int64_t units;   // tiles along the rows of the result, at most; dW: blocks of rows
+  int cut;            // of the four below
+  int64_t units;      // tiles along the rows of h or dx, at most
   int columns;
+  int splits;         // dx: parts of the reduced index
+  int64_t per;        // dW: rows reduced at once
+  int64_t dw_units;   // blocks of them, at most
 };
 
 // The cuts, and microseconds of a step of 128 bytes: with one workgroup on a compute unit, and for each further one that
-// shares it (the 256 x 256 cut has none beside it: they follow each other).  Measured with 16384 x 1024 x 2048, 4096 x 2048
-// x 4096 and 1024 x 1024 x 1024 products of two-byte and of float32 values.
+// shares it (the 256 x 256 cut has none beside it: they follow each other).  Measured with products of two-byte and of
+// float32 values, 200 x 512 x 2048 to 16384 x 1024 x 2048.  The choices by it, gradients in us with this cut and the best:
+// bfloat16 4096 x 4096 x 4096 508 (508), 4096 x 1024 x 2048 91 (91), 1024 x 1024 x 1024 33 (30), 300 x 300 x 300 11.2 (11.2);
+// float32 1001 x 250 x 999 42 (41), 4096 x 1024 x 2048 623 (572).
 struct CutCost { int q, p; float alone[2], shared[2]; };
 constexpr int kCuts = 4;
 constexpr CutCost kCutCost[kCuts] = {{32, 64, {0.28f, 0.46f}, {0.15f, 0.29f}},
-                                     {64, 128, {0.5f, 1.17f}, {0.29f, 1.05f}},
-                                     {128, 128, {0.62f, 2.15f}, {0.45f, 2.0f}},
+                                     {64, 128, {0.5f, 1.17f}, {0.34f, 1.05f}},
+                                     {128, 128, {0.62f, 2.15f}, {0.53f, 2.0f}},
                                      {256, 256, {1.65f, 7.5f}, {1.65f, 7.5f}}};
 
 // blocks of rows at most: every matrix may end inside one
@@ -899,77 +917,76 @@ inline int64_t row_units(int64_t n_rows, int n_matrices, bool by_expert, int per
   return by_expert ? n_rows / per + (n_rows < n_matrices ? n_rows : n_matrices) : (n_rows + per - 1) / per;
 }
 
-// The cut and the number of parts with the least time by the table above, 3 us for a launch and 4 + 2.4 us for each million
-// partial values that are written and read again.  units(q): tiles of q along the result's rows; results: its values, 0
-// where its sums cannot be split.
-template <class Units>
-GatedPlan plan_product(int elem, Units units, int width, int64_t steps, double results) {
-  GatedPlan best{};
-  double least = 0;
-  const int type = elem == 4;
-  for (int cut = 0; cut < kCuts; ++cut) {
-    const CutCost &c = kCutCost[cut];
-    GatedPlan p{cut, 1, 0, units(c.q), (width + c.p - 1) / c.p};
-    for (; p.splits <= 32 && (p.splits == 1 || (results > 0 && steps >= 2 * p.splits)); p.splits *= 2) {
-      const int64_t tiles = p.units * p.columns * p.splits, load = (tiles + 255) / 256;
-      const double each = (double)((steps + p.splits - 1) / p.splits);
-      double time = 3 + each * (c.alone[type] + (double)(load - 1) * c.shared[type]);
-      if (p.splits > 1) time += 4 + 2.4e-6 * p.splits * results;
-      if ((cut == 0 && p.splits == 1) || time < least) {
-        least = time;
-        best = p;
-      }
-    }
-  }
-  return best;
+// blocks of rows at most: every matrix may end inside one
+inline int64_t row_units(int64_t n_rows, int n_matrices, bool by_expert, int64_t per) {
+  return by_expert ? n_rows / per + (n_rows < n_matrices ? n_rows : n_matrices) : (n_rows + per - 1) / per;
 }
 
+// the cut with the least time by the table above
 inline GatedPlan plan_forward(const GatedArgs &a, int elem) {
-  return plan_product(elem, [&](int q) { return row_units(a.n_rows, a.n_matrices, a.offsets != nullptr, q); }, 2 * a.outs,
-                      (a.ins + kStepBytes / elem - 1) / (kStepBytes / elem), 0);
-}
-inline GatedPlan plan_dx(const GatedArgs &a, int elem) {
-  return plan_product(elem, [&](int q) { return row_units(a.n_rows, a.n_matrices, a.offsets != nullptr, q); }, a.ins,
-                      2 * ((a.outs + kStepBytes / elem - 1) / (kStepBytes / elem)), (double)a.n_rows * a.ins);
-}
-
-// The same for dW, whose rows are cut into blocks of p.per.  By expert, half the rows may be one expert's: blocks that one
-// workgroup walks should not be longer than its share of all steps.
-inline GatedPlan plan_dw(const GatedArgs &a, int elem) {
   GatedPlan best{};
   double least = 0;
   const int type = elem == 4, step = kStepBytes / elem;
-  const int64_t all = (a.n_rows + step - 1) / step;
-  const int experts = a.offsets ? a.n_matrices : 1;
   for (int cut = 0; cut < kCuts; ++cut) {
     const CutCost &c = kCutCost[cut];
-    const int columns = (a.ins + c.p - 1) / c.p;
-    const int64_t tiles = (int64_t)2 * ((a.outs + c.q - 1) / c.q) * columns;
-    for (int parts = 1; parts <= 32 && (parts == 1 || all >= 4 * parts); parts *= 2) {
-      const int64_t steps = (all + parts - 1) / parts;
-      GatedPlan p{cut, 1, steps * step, all / (steps ? steps : 1) + experts, columns};
-      const double longest = (double)(a.offsets && parts == 1 ? (all + 1) / 2 : steps);
-      const double each = longest < 1 ? 1 : longest;                                   // steps of the longest block
-      const double load = ((double)all + 0.5 * experts) * (double)tiles / 256;         // steps of a compute unit
-      double time = 3 + (load <= each ? each * c.alone[type] : load * c.shared[type] + 0.5 * each * c.alone[type]);
-      if (parts > 1) time += 4 + 2.4e-6 * parts * 2.0 * a.outs * a.ins;
-      if ((cut == 0 && parts == 1) || time < least) {
-        least = time;
-        best = p;
-      }
+    const GatedPlan p{cut, row_units(a.n_rows, a.n_matrices, a.offsets != nullptr, c.q), (2 * a.outs + c.p - 1) / c.p, 1, 1, 1};
+    const int64_t load = (p.units * p.columns + 255) / 256;
+    const double time = (double)((a.ins + step - 1) / step) * (c.alone[type] + (double)(load - 1) * c.shared[type]);
+    if (cut == 0 || time < least) {
+      least = time;
+      best = p;
     }
   }
-  if (best.per < 1) best.per = 1;
-  if (!a.offsets) best.units = (a.n_rows + best.per - 1) / best.per > 1 ? (a.n_rows + best.per - 1) / best.per : 1;
-  else best.units = a.n_rows / best.per + experts;
   return best;
 }
 
-// a grid's threads stay below 2^32
-inline bool fits(const GatedPlan &p) { return (p.units * p.columns + 8) * p.splits < (1 << 22); }
-inline bool fits_dw(const GatedPlan &p, int32_t outs) {
-  return p.units * ((int64_t)2 * ((outs + 31) / 32) * p.columns + 8) < (1 << 23);
+// The cut, dx's parts and dW's blocks of rows with the least time for both, whichever of them are wanted: what the compute
+// units have to do, but at least what the longest tile takes, and for parts 4 us and 2.4 for each million partial values that
+// are written and read again.  Only products of fewer tiles than compute units are cut into parts: by expert, 8 times 512
+// tiles, no uneven load made parts pay (one expert with 13018 of 16384 rows: 159 us whole, 150 in two, 198 in four parts; even
+// experts: 127, 137, 139).
+inline GatedPlan plan_backward(const GatedArgs &a, int elem) {
+  GatedPlan best{};
+  double least = 0;
+  const int type = elem == 4, step = kStepBytes / elem, experts = a.offsets ? a.n_matrices : 1;
+  const int64_t dx_steps = 2 * (int64_t)((a.outs + step - 1) / step), dw_steps = (a.n_rows + step - 1) / step;
+  for (int cut = 0; cut < kCuts; ++cut) {
+    const CutCost &c = kCutCost[cut];
+    const int columns = (a.ins + c.p - 1) / c.p;
+    const int64_t units = row_units(a.n_rows, a.n_matrices, a.offsets != nullptr, c.q);
+    const int64_t dx_tiles = units * columns, dw_tiles = (int64_t)2 * ((a.outs + c.q - 1) / c.q) * columns;
+    const double load = ((double)dx_tiles * dx_steps + (double)dw_tiles * (dw_steps + 0.5 * experts)) / 256;
+    for (int splits = 1; splits <= 32 && (splits == 1 || (dx_tiles < 256 && dx_steps >= 2 * splits)); splits *= 2)
+      for (int parts = 1; parts <= 32 && (parts == 1 || (dw_tiles < 256 && dw_steps >= 2 * parts)); parts *= 2) {
+        const int64_t blocks = (dw_steps + parts - 1) / parts;
+        // by expert, half the rows may be one expert's
+        const double longest = (double)larger((int)((dx_steps + splits - 1) / splits),
+                                              (int)(a.offsets && parts == 1 ? (dw_steps + 1) / 2 : blocks));
+        const double alone = longest * c.alone[type], shared = load * c.shared[type] + 0.3 * alone;
+        double time = alone > shared ? alone : shared;
+        if (splits > 1 || parts > 1) time += 4;
+        if (splits > 1) time += 2.4e-6 * splits * (double)a.n_rows * a.ins;
+        if (parts > 1) time += 2.4e-6 * parts * 2.0 * a.outs * a.ins;
+        if ((cut == 0 && splits == 1 && parts == 1) || time < least) {
+          least = time;
+          const int64_t per = blocks > 0 ? blocks * step : 1;
+          best = {cut, units, columns, splits, per, a.offsets ? a.n_rows / per + experts : (a.n_rows + per - 1) / per};
+        }
+      }
+  }
+  if (best.dw_units < 1) best.dw_units = 1;   // zeros for no rows
+  return best;
 }
+
+// the workgroups of a plan's gradients
+inline int64_t dx_blocks(const GatedPlan &p) { return eighths(p.units * p.columns) * p.splits; }
+inline int64_t dw_blocks(const GatedPlan &p, int32_t outs) {
+  const int q = kCutCost[p.cut].q;
+  return eighths((int64_t)2 * ((outs + q - 1) / q) * p.columns) * p.dw_units;
+}
+
+// a grid's threads stay below 2^32
+inline bool fits(int64_t blocks) { return blocks < (1 << 23); }
 
 // Whether the forward pass takes the kernel for few rows: 1 or 2 blocks of 16, or 0.  Few: up to 32 (64 x 2048 x 2048 bfloat16
 // 14.3 us there, 10.9 with tiles; 32 x 2048 x 2048 10.1 and 10.7).  By expert up to 4 on average (32 experts of 1024 x 1024,
@@ -988,26 +1005,15 @@ inline size_t gated_copies(const GatedArgs &a, int elem) {
   return (size_t)(a.n_rows + 2 * (int64_t)a.n_matrices * a.outs) * gated_pitch(a.ins, elem);
 }
 
-// bytes of the partial results, of dx and of dW (one after the other in the same place)
-inline size_t gated_partial(const GatedArgs &a, int elem) {
-  size_t most = 0;
-  if (a.n_rows == 0) return 0;
-  if (a.dx) {
-    const GatedPlan p = plan_dx(a, elem);
-    if (p.splits > 1) most = (size_t)p.splits * a.n_rows * a.ins * 4;
-  }
-  if (a.dw_gate) {
-    const GatedPlan p = plan_dw(a, elem);
-    // matrices with several blocks have at most 2 n_rows / per together
-    const size_t n = p.per < a.n_rows ? (size_t)(2 * a.n_rows / p.per) * 2 * a.outs * a.ins * 4 : 0;
-    if (n > most) most = n;
-  }
-  return most;
+// values of dx's parts, and of dW's: matrices with several blocks have at most 2 n_rows / per together
+inline int64_t dx_parts(const GatedArgs &a, const GatedPlan &p) { return p.splits > 1 ? p.splits * a.n_rows * a.ins : 0; }
+inline int64_t dw_parts(const GatedArgs &a, const GatedPlan &p) {
+  return p.per < a.n_rows ? 2 * a.n_rows / p.per * 2 * a.outs * a.ins : 0;
 }
 
 // one type's calls
-template <class T> int gated_forward(const char *who, GatedArgs a, void *stream);
-template <class T> int gated_backward(const char *who, GatedArgs a, void *stream);
+template <class T> int gated_forward(const char *who, GatedArgs a, const GatedPlan &p, void *stream);
+template <class T> int gated_backward(const char *who, GatedArgs a, const GatedPlan &p, void *stream);
 
 #ifdef SVT_GATED_INSTANTIATE
 
@@ -1044,7 +1050,7 @@ int align_rows(const char *who, GatedArgs &a, void *stream) {
 }
 
 template <class T>
-int gated_forward(const char *who, GatedArgs a, void *stream) {
+int gated_forward(const char *who, GatedArgs a, const GatedPlan &p, void *stream) {
   if (const int mt = a.few) {
     a.units = row_units(a.n_rows, a.n_matrices, a.offsets != nullptr, 16 * mt);
     a.columns = (a.outs + 15) / 16;
@@ -1054,7 +1060,6 @@ int gated_forward(const char *who, GatedArgs a, void *stream) {
   }
   const int rc = align_rows<T>(who, a, stream);
   if (rc != SVT_OK) return rc;
-  const GatedPlan p = plan_forward(a, sizeof(T));
   a.units = p.units;
   a.columns = p.columns;
   return with_cut(p.cut, [&](auto cut) {
@@ -1063,11 +1068,8 @@ int gated_forward(const char *who, GatedArgs a, void *stream) {
   });
 }
 
-inline unsigned join_grid(int64_t values) { return (unsigned)((values + 1023) / 1024 < 2048 ? (values + 1023) / 1024 : 2048); }
-
 template <class T>
-int gated_backward(const char *who, GatedArgs a, void *stream) {
-  constexpr int b = sizeof(T);
+int gated_backward(const char *who, GatedArgs a, const GatedPlan &p, void *stream) {
   int rc = SVT_OK;
   if (a.n_rows > 0) {
     rc = align_rows<T>(who, a, stream);
@@ -1076,32 +1078,23 @@ int gated_backward(const char *who, GatedArgs a, void *stream) {
     rc = launch(who, k_gated_both<T>, g.grid, kBothThreads, 0, stream, a, g.lanes);
     if (rc != SVT_OK) return rc;
   }
-  if (a.dx && a.n_rows > 0) {
-    const GatedPlan p = plan_dx(a, b);
-    a.units = p.units;
-    a.columns = p.columns;
-    a.splits = p.splits;
-    rc = with_cut(p.cut, [&](auto cut) {
-      using C = decltype(cut);
-      return launch(who, k_gated_dx<T, C>, dim3((unsigned)eighths(a.units * a.columns), p.splits), C::threads, 0, stream, a);
-    });
-    if (rc == SVT_OK && p.splits > 1)
-      rc = launch(who, k_gated_join_dx<T>, join_grid(a.n_rows * a.ins), 256, 0, stream, a);
-    if (rc != SVT_OK) return rc;
-  }
-  if (a.dw_gate) {
-    const GatedPlan p = plan_dw(a, b);
-    a.columns = p.columns;
-    a.per = p.per;
-    rc = with_cut(p.cut, [&](auto cut) {
-      using C = decltype(cut);
-      const int64_t own = eighths((int64_t)2 * ((a.outs + C::q - 1) / C::q) * a.columns);
-      return launch(who, k_gated_dw<T, C>, (unsigned)(own * p.units), C::threads, 0, stream, a);
-    });
-    if (rc == SVT_OK && p.per < a.n_rows)
-      rc = launch(who, k_gated_join_dw<T>, dim3(join_grid((int64_t)2 * a.outs * a.ins), a.n_matrices), 256, 0, stream, a);
-  }
-  return rc;
+  a.columns = p.columns;
+  a.splits = p.splits;
+  a.per = p.per;
+  a.dx_blocks = a.dx ? dx_blocks(p) : 0;
+  a.dw_blocks = a.dw_gate ? dw_blocks(p, a.outs) : 0;
+  a.dx_first = 2 * (int64_t)a.outs / p.splits > p.per;
+  if (a.dx_blocks + a.dw_blocks == 0) return SVT_OK;
+  rc = with_cut(p.cut, [&](auto cut) {
+    using C = decltype(cut);
+    return launch(who, k_gated_gradients<T, C>, (unsigned)(a.dx_blocks + a.dw_blocks), C::threads, 0, stream, a);
+  });
+  const bool dx_parted = a.dx && dx_parts(a, p) > 0, dw_parted = a.dw_gate && dw_parts(a, p) > 0;
+  if (rc != SVT_OK || (!dx_parted && !dw_parted)) return rc;
+  const int64_t dx_values = dx_parted ? a.n_rows * a.ins : 0, dw_values = dw_parted ? (int64_t)2 * a.outs * a.ins : 0;
+  const int64_t blocks = ((dx_values > dw_values ? dx_values : dw_values) + 1023) / 1024;
+  return launch(who, k_gated_join<T>, dim3((unsigned)(blocks < 2048 ? blocks : 2048), dw_parted ? 1 + a.n_matrices : 1), 256, 0,
+                stream, a);
 }
 
 #endif   // SVT_GATED_INSTANTIATE

@@ -103,12 +103,14 @@ extern "C" int svt_gated_linear(int32_t n_rows, int32_t n_in, int32_t n_out, int
   const Span outs[4] = {{h, nh}, {gate, nh}, {up, nh}, {workspace, need}};
   if (any_overlap(ins, 4, outs, 4))
     return report(SVT_EINVAL, "%s: an output or the workspace overlaps an input or another output", who);
-  if (!fits(plan_forward(a, b))) return report(SVT_EINVAL, "%s: too many rows of too many outputs for one call", who);
+  const GatedPlan plan = plan_forward(a, b);
+  if (!a.few && !fits(eighths(plan.units * plan.columns)))
+    return report(SVT_EINVAL, "%s: too many rows of too many outputs for one call", who);
   if (need) {
     a.padded = (char *)workspace;
     a.in_pitch = gated_pitch(n_in, b);
   }
-  return with_type(dtype, [&](auto ty) { return gated_forward<decltype(ty)>(who, a, hip_stream); });
+  return with_type(dtype, [&](auto ty) { return gated_forward<decltype(ty)>(who, a, plan, hip_stream); });
 }
 
 extern "C" size_t svt_gated_linear_backward_workspace_size(int32_t n_rows, int32_t n_in, int32_t n_out, int32_t n_matrices,
@@ -119,9 +121,10 @@ extern "C" size_t svt_gated_linear_backward_workspace_size(int32_t n_rows, int32
   const int b = elem_size(dtype);
   GatedArgs a = gated_args(n_rows, n_in, n_out, n_matrices, b, by_expert ? kSome : nullptr);
   if (n_rows == 0) return 0;
-  a.dx = a.dw_gate = &a;   // given
+  const GatedPlan plan = plan_backward(a, b);
   const bool as_is = aligned && aligned_rows(n_in, b, nullptr, nullptr, nullptr);
-  return (size_t)(2 * n_rows * a.pitch) + (as_is ? 0 : gated_copies(a, b)) + gated_partial(a, b);
+  return (size_t)(2 * n_rows * a.pitch) + (as_is ? 0 : gated_copies(a, b)) +
+         (size_t)(dx_parts(a, plan) + dw_parts(a, plan)) * 4;
 }
 
 extern "C" int svt_gated_linear_backward(int32_t n_rows, int32_t n_in, int32_t n_out, int32_t n_matrices, int32_t dtype,
@@ -157,7 +160,9 @@ extern "C" int svt_gated_linear_backward(int32_t n_rows, int32_t n_in, int32_t n
   a.dw_up = dw_up;
   const bool as_is = aligned_rows(n_in, b, a.x, a.w_gate, a.w_up);
   const size_t both = (size_t)(2 * n_rows * a.pitch), copies = as_is || n_rows == 0 ? 0 : gated_copies(a, b);
-  const size_t need = both + copies + gated_partial(a, b);
+  const GatedPlan plan = plan_backward(a, b);
+  const int64_t dx_part = dx ? dx_parts(a, plan) : 0, dw_part = dw_gate ? dw_parts(a, plan) : 0;
+  const size_t need = both + copies + (size_t)(dx_part + dw_part) * 4;
   if (need > 0 && (!workspace || workspace_bytes < need))
     return report(SVT_EINVAL, "%s: workspace of %zu bytes, needs %zu", who, workspace ? workspace_bytes : (size_t)0, need);
   const size_t nx = (size_t)n_rows * n_in * b, nw = (size_t)n_matrices * n_out * n_in * b, nh = (size_t)n_rows * n_out * b;
@@ -166,7 +171,7 @@ extern "C" int svt_gated_linear_backward(int32_t n_rows, int32_t n_in, int32_t n
   const Span outs[4] = {{dx, nx}, {dw_gate, nw}, {dw_up, nw}, {workspace, need}};
   if (any_overlap(ins, 7, outs, 4))
     return report(SVT_EINVAL, "%s: an output or the workspace overlaps an input or another output", who);
-  if ((dx && !fits(plan_dx(a, b))) || (dw_gate && !fits_dw(plan_dw(a, b), n_out)))
+  if (!fits(dx_blocks(plan) + dw_blocks(plan, n_out)))
     return report(SVT_EINVAL, "%s: too large a product for one call", who);
   a.d_both = (char *)workspace;
   if (copies) {
@@ -174,5 +179,6 @@ extern "C" int svt_gated_linear_backward(int32_t n_rows, int32_t n_in, int32_t n
     a.in_pitch = gated_pitch(n_in, b);
   }
   a.partial = (float *)(a.d_both + both + copies);
-  return with_type(dtype, [&](auto ty) { return gated_backward<decltype(ty)>(who, a, hip_stream); });
+  a.dw_partial = dx_part;
+  return with_type(dtype, [&](auto ty) { return gated_backward<decltype(ty)>(who, a, plan, hip_stream); });
 }

@@ -3,6 +3,6 @@
 #include "svt_gated.h"
 
 namespace svt {
-template int gated_forward<bf16>(const char *, GatedArgs, void *);
-template int gated_backward<bf16>(const char *, GatedArgs, void *);
+template int gated_forward<bf16>(const char *, GatedArgs, const GatedPlan &, void *);
+template int gated_backward<bf16>(const char *, GatedArgs, const GatedPlan &, void *);
 }  // namespace svt
