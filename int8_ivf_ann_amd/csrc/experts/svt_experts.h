@@ -55,15 +55,21 @@ int launch(const char *who, void (*kernel)(P...), dim3 grid, unsigned threads, s
 
 // Reductions over aligned groups of L lanes (a power of two, at most 64); every lane gets the result.
 // Within 16 lanes: DPP moves (lane ^ 1 and ^ 2 as quad permutations, then mirrors of 8 and of 16 lanes,
-// which pair the already uniform halves); beyond: shuffles.
+// which pair the already uniform halves); beyond: moves that exchange rows of 16 lanes, then halves of the wave.
 template <class Op>
 __device__ __forceinline__ uint32_t group_reduce(uint32_t v, int L, Op op) {
   if (L >= 2) v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true));
   if (L >= 4) v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true));
   if (L >= 8) v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, true));
   if (L >= 16) v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, true));
-  if (L >= 32) v = op(v, (uint32_t)__shfl_xor((int)v, 16));
-  if (L >= 64) v = op(v, (uint32_t)__shfl_xor((int)v, 32));
+  if (L >= 32) {
+    const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);   // (even rows twice, odd rows twice)
+    v = op(p[0], p[1]);
+  }
+  if (L >= 64) {
+    const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = op(p[0], p[1]);
+  }
   return v;
 }
 __device__ __forceinline__ uint32_t group_max(uint32_t v, int L) {

@@ -420,7 +420,7 @@ template <class T>
 __device__ __forceinline__ void store_four(T *at, const float (&v)[4], int left) {
   if (left >= 4) {
     struct Four { T t[4]; } r{{(T)v[0], (T)v[1], (T)v[2], (T)v[3]}};
-    struct __attribute__((packed, aligned(sizeof(T)))) Raw { uint8_t v[4 * sizeof(T)]; };
+    struct __attribute__((packed, aligned(sizeof(T)))) Raw { uint32_t v[sizeof(T)]; };
     *reinterpret_cast<Raw *>(at) = __builtin_bit_cast(Raw, r);
   } else {
 #pragma unroll
@@ -464,7 +464,7 @@ struct Staged {
   static __device__ __forceinline__ void store(char *lds, int64_t first, int64_t end, int c0, int width, O *out, Value value) {
     const int wave = (int)threadIdx.x / 64, wq = wave / C::WP, wp = wave % C::WP, i = lane_id() % 16, g = lane_id() / 16;
     struct alignas(4 * sizeof(O) < 16 ? 4 * sizeof(O) : 16) Four { O t[4]; };
-    struct __attribute__((packed, aligned(sizeof(O)))) Raw { uint8_t v[16]; };
+    struct __attribute__((packed, aligned(sizeof(O)))) Raw { uint32_t v[4]; };
     constexpr int each = 16 / sizeof(O), row_pieces = COLUMNS / each;
 #pragma unroll
     for (int b0 = 0; b0 < C::nq; b0 += blocks) {
@@ -581,7 +581,7 @@ template <class T>
 __device__ __forceinline__ typename Mul<T>::frag load_sixteen(const T *row, int k, int end) {
   constexpr int each = 16 / sizeof(T);
   struct Values { T t[each]; };
-  struct __attribute__((packed, aligned(sizeof(T)))) Raw { uint8_t v[16]; };
+  struct __attribute__((packed, aligned(sizeof(T)))) Raw { uint32_t v[4]; };
   if (k + each <= end)
     return __builtin_bit_cast(typename Mul<T>::frag, *reinterpret_cast<const Raw *>(row + k));
   Values v{};
@@ -694,7 +694,7 @@ template <class T>
 __global__ __launch_bounds__(kBothThreads) void k_gated_both(GatedArgs a, int lanes) {
   constexpr int each = 16 / sizeof(T);
   struct Values { T t[each]; };
-  struct __attribute__((packed, aligned(sizeof(T)))) Raw { uint8_t v[16]; };
+  struct __attribute__((packed, aligned(sizeof(T)))) Raw { uint32_t v[4]; };
   const int64_t first = a.offsets ? clamped(a.offsets[0], a.n_rows) : 0;
   const int64_t end = a.offsets ? clamped(a.offsets[a.n_matrices], a.n_rows) : a.n_rows;
   const int pieces = (int)(a.pitch / 16), in = threadIdx.x % lanes;

@@ -15,6 +15,13 @@
 // Best alternatives: a wave sees its tokens in ascending order, so that a later token only enters above its `top`-th
 // best so far (ties go to the lower token).  Tokens above that bound go to a list in LDS; a full list is cut to its
 // `top` best, which raises the bound.  The first piece's bound is the top-th largest of the lanes' own maxima.
+//
+// Measured: 4096 rows of 49152 bfloat16 74 us (5.4 TB/s; 47 without the loads, 70 without the exponentials: bound by
+// memory), of 50021, whose rows begin at odd addresses, 92; float32 with the 16 best 164 (4.9 TB/s).  Forward and gradient
+// of 4096 x 50021 one after the other 260.  Loads and conversions of a piece stand apart, and the pieces of the next step are
+// asked for before this step's are used: with a branch around each, 124 us for the forward pass of the pair, the row's end
+// element by element 8 us of it.  256 rows of 2048 float32, top 16: 8.7 us, the gradient 4.4.  One row of 131072 bfloat16,
+// top 8: 8.1 us in 32 splits, 4.3 to join them.
 
 #include <type_traits>
 
@@ -67,7 +74,11 @@ __device__ __forceinline__ float wave_max(float v) {
 }
 __device__ __forceinline__ uint64_t wave_best(uint64_t k) {
   const uint32_t hi = group_max((uint32_t)(k >> 32), 64);
-  const uint32_t lo = group_max((uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u, 64);
+  const uint64_t same = __ballot((uint32_t)(k >> 32) == hi);
+  // equal logits, of which the lower token counts, are rare
+  const uint32_t lo = (same & (same - 1)) == 0ull
+                          ? (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)k, __builtin_ctzll(same))
+                          : group_max((uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u, 64);
   return (uint64_t)hi << 32 | lo;
 }
 
@@ -124,6 +135,36 @@ __device__ __forceinline__ uint64_t wave_top(uint64_t (&k)[N], int top) {
   return kept;
 }
 
+// how many of the keys of lanes 0 .. n - 1 are greater than this lane's
+__device__ __forceinline__ int rank_of(uint64_t k, int n) {
+  int rank = 0;
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) {
+    const uint64_t o = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(k >> 32), j) << 32 |
+                       (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)k, j);
+    rank += o > k ? 1 : 0;
+  }
+  return rank;
+}
+// the `top` best of the keys of lanes 0 .. n - 1, no two alike but 0, in order in lanes 0 .. top - 1; through 16 places of LDS
+__device__ __forceinline__ uint64_t in_order(uint64_t k, int n, int top, uint64_t *lds) {
+  const int rank = rank_of(k, n);
+  wave_order();
+  if (lane_id() < SVT_MAX_TOP) lds[lane_id()] = 0ull;
+  wave_order();
+  if (k != 0ull && rank < top) lds[rank] = k;
+  wave_order();
+  return lane_id() < top ? lds[lane_id()] : 0ull;
+}
+
+// The same, by ranks or by rounds that take the best: 256 rows of 2048 float32, top 16, 8.7 us by ranks and 10.1 by rounds; one
+// row of 131072 bfloat16, top 8, 10.6 and 8.1
+__device__ __forceinline__ uint64_t best_of_wave(uint64_t k, int n, int top, uint64_t *lds) {
+  if (top > 8) return in_order(k, n, top, lds);
+  uint64_t one[1] = {k};
+  return wave_top(one, top);
+}
+
 // a wave's candidates
 struct Candidates {
   uint64_t *list;     // LDS [kList]
@@ -131,11 +172,16 @@ struct Candidates {
   float bound;        // a later token enters above it
 
   __device__ __forceinline__ uint64_t cut() {
-    uint64_t k[kList / 64];
+    uint64_t kept;
     wave_order();
+    if (count <= 64) {   // the first piece's, most often
+      kept = best_of_wave(lane_id() < count ? list[lane_id()] : 0ull, count, top, list);
+    } else {
+      uint64_t k[kList / 64];
 #pragma unroll
-    for (int i = 0; i < kList / 64; ++i) k[i] = i * 64 + lane_id() < count ? list[i * 64 + lane_id()] : 0ull;
-    const uint64_t kept = wave_top(k, top);
+      for (int i = 0; i < kList / 64; ++i) k[i] = i * 64 + lane_id() < count ? list[i * 64 + lane_id()] : 0ull;
+      kept = wave_top(k, top);
+    }
     if (lane_id() < top) list[lane_id()] = kept;
     wave_order();
     const uint64_t full = __ballot(lane_id() < top && kept != 0ull);
@@ -176,47 +222,74 @@ struct Candidates {
 };
 
 // aligned to its elements alone: the order of a row's sums does not depend on where the row lies
-template <class T> struct __attribute__((packed, aligned(sizeof(T)))) Piece { uint8_t v[kPiece * sizeof(T)]; };
+template <class T> struct __attribute__((packed, aligned(sizeof(T)))) Piece { uint32_t v[kPiece * sizeof(T) / 4]; };
 template <class T> struct Eight { T v[kPiece]; };
 
-// logits first .. first + 7 of a row (shut past its end)
 template <class T>
-__device__ __forceinline__ void load_piece(const T *row, int first, int vocab, float (&v)[kPiece]) {
-  if (first + kPiece <= vocab) {
-    const Eight<T> p = __builtin_bit_cast(Eight<T>, *reinterpret_cast<const Piece<T> *>(row + first));
+__device__ __forceinline__ Piece<T> raw_piece(const T *row, int first) {
+  return *reinterpret_cast<const Piece<T> *>(row + first);
+}
+template <class T>
+__device__ __forceinline__ void widen(const Piece<T> &raw, float (&v)[kPiece]) {
+  const Eight<T> p = __builtin_bit_cast(Eight<T>, raw);
 #pragma unroll
-    for (int i = 0; i < kPiece; ++i) v[i] = (float)p.v[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < kPiece; ++i) v[i] = first + i < vocab ? (float)row[first + i] : -INFINITY;
-  }
+  for (int i = 0; i < kPiece; ++i) v[i] = (float)p.v[i];
 }
 
-__device__ __forceinline__ void add_piece(Sums &a, const float (&v)[kPiece], float most, float c) {
+// Logits first .. first + 7 of a row, shut past its end: the token of v[0] is returned.  A piece that would run past the end
+// is the row's last 8 logits, of which those before `first` are shut (one load; 8 for rows of fewer).
+template <class T>
+__device__ __forceinline__ int load_piece(const T *row, int first, int vocab, float (&v)[kPiece]) {
+  if (vocab < kPiece) {
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) {
+      const float f = (float)row[i < vocab ? i : vocab - 1];
+      v[i] = first == 0 && i < vocab ? f : -INFINITY;
+    }
+    return 0;
+  }
+  const int at = first + kPiece <= vocab ? first : vocab - kPiece;
+  widen(raw_piece(row, at), v);
+#pragma unroll
+  for (int i = 0; i < kPiece; ++i) v[i] = at + i >= first ? v[i] : -INFINITY;
+  return at;
+}
+
+// the pieces of a thread at a time, in flight together
+template <int U>
+__device__ __forceinline__ void add_pieces(Sums &a, const float (&v)[U][kPiece], float most, float c) {
   most = fminf(most, FLT_MAX);
   if (most > a.m) a.move(most, c);
 #pragma unroll
-  for (int i = 0; i < kPiece; ++i) {
-    const float x = exponent(v[i], a.m, c), e = __builtin_amdgcn_exp2f(x);
-    a.z += e;
-    a.s = fmaf(x, e, a.s);
+  for (int u = 0; u < U; ++u) {
+    float z = 0.f, s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) {
+      const float x = exponent(v[u][i], a.m, c), e = __builtin_amdgcn_exp2f(x);
+      z += e;
+      s = fmaf(x, e, s);
+    }
+    a.z += z;
+    a.s += s;
   }
 }
 
-// logp, H, norms and the alternatives of row t, by one wave: lane j holds the j-th best
+// a row's token and its logit
+struct Given { int64_t token; float logit; };
 template <class T>
-__device__ __forceinline__ void finish(const LogprobArgs &a, const T *row, int64_t t, Sums sum, uint64_t best) {
+__device__ __forceinline__ Given given(const LogprobArgs &a, const T *row, int64_t token) {
+  return {token, (float)row[(uint64_t)token < (uint64_t)a.vocab ? token : 0]};
+}
+
+// logp, H, norms and the alternatives of row t, by one wave: lane j holds the j-th best
+__device__ __forceinline__ void finish(const LogprobArgs &a, Given g, int64_t t, Sums sum, uint64_t best) {
   const bool any = sum.z > 0.f;
   const float log_z = any ? __builtin_amdgcn_logf(sum.z) : 0.f;   // base 2; z >= 1
   const float peak = any ? sum.m : 0.f;
   auto logp = [&](float l) { return (fminf(l, FLT_MAX) - peak) * a.scale - log_z * kLn2; };
   if (lane_id() == 0) {
-    const int64_t token = a.tokens[t];
     float lp = 0.f;
-    if ((uint64_t)token < (uint64_t)a.vocab) {
-      const float l = (float)row[token];
-      lp = l > -INFINITY ? logp(l) : -INFINITY;
-    }
+    if ((uint64_t)g.token < (uint64_t)a.vocab) lp = g.logit > -INFINITY ? logp(g.logit) : -INFINITY;
     a.logprobs[t] = lp;
     a.entropy[t] = any ? (log_z - sum.s / sum.z) * kLn2 : 0.f;
     a.norms[2 * t] = peak;
@@ -228,9 +301,10 @@ __device__ __forceinline__ void finish(const LogprobArgs &a, const T *row, int64
   }
 }
 
-// W waves share a row (or a split of one): 1 or kWaves
+// W waves share a row (or a split of one): 1 or kWaves; a thread takes U pieces at a time
 template <class T, int W, bool TOP, bool SPLIT>
 __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobArgs a, const T *logits) {
+  constexpr int U = 2;
   __shared__ uint64_t lists[TOP ? kWaves : 1][TOP ? kList : 1];
   __shared__ Sums parts[kWaves];
   const int wave = threadIdx.x / 64;
@@ -244,29 +318,53 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobArgs a, const T *l
     const int64_t t = SPLIT ? u / a.splits : u;
     const int part = SPLIT ? (int)(u - t * a.splits) : 0;
     const T *row = logits + t * a.vocab;
+    const int64_t token = SPLIT ? -1 : a.tokens[t];
     const int pieces = (a.vocab + kPiece - 1) / kPiece;
     const int p0 = part * a.pieces, p1 = SPLIT ? (p0 + a.pieces < pieces ? p0 + a.pieces : pieces) : pieces;
     Sums sum = Sums::none();
     Candidates best{TOP ? lists[wave] : nullptr, 0, a.top, -INFINITY};
-    auto take = [&](const float (&v)[kPiece], int p, bool first) {
+    // N pieces of a thread from place q on, 64 W apart; all lanes of a wave act together
+    auto take = [&](int q, auto &v, int token) {   // token: of v[0][0]
+      constexpr int N = sizeof(v) / sizeof(v[0]);
       float most = -INFINITY;   // of a NaN and a number, the number
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i) most = fmaxf(most, v[i]);
-      if (TOP) {
-        if (first) best.start(most);
-        best.offer(v, most, p * kPiece);
+      for (int n = 0; n < N; ++n) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kPiece; ++i) m = fmaxf(m, v[n][i]);
+        if (TOP) {
+          if (n == 0 && q == p0) best.start(m);
+          best.offer(v[n], m, token + n * 64 * W * kPiece);
+        }
+        most = fmaxf(most, m);
       }
-      add_piece(sum, v, most, c);
+      add_pieces<N>(sum, v, most, c);
     };
-    // a piece past the end is shut; the loop's bounds are the wave's, as its lanes act together
-    for (int q = p0; q < p1; q += 2 * 64 * W) {
-      float v[kPiece], w[kPiece];
-      const int p = q + in, p2 = p + 64 * W;
-      const bool two = q + 64 * W < p1;
-      load_piece(row, p < p1 ? p * kPiece : a.vocab, a.vocab, v);
-      if (two) load_piece(row, p2 < p1 ? p2 * kPiece : a.vocab, a.vocab, w);
-      take(v, p, q == p0);
-      if (two) take(w, p2, false);
+    // whole pieces for every thread, the next ones in flight; then what is left, one a thread, shut past the end
+    constexpr int hop = U * 64 * W;
+    const int whole = a.vocab / kPiece, p2 = p1 < whole ? p1 : whole;
+    int q = p0;
+    if (q + hop <= p2) {
+      Piece<T> raw[U];
+      auto ask = [&](int at) {
+#pragma unroll
+        for (int n = 0; n < U; ++n) raw[n] = raw_piece(row, (at + n * 64 * W + in) * kPiece);
+      };
+      ask(q);
+      for (; q + hop <= p2; q += hop) {
+        float v[U][kPiece];
+#pragma unroll
+        for (int n = 0; n < U; ++n) widen(raw[n], v[n]);
+        ask(q + 2 * hop <= p2 ? q + hop : q);   // behind the last, the same again
+        take(q, v, (q + in) * kPiece);
+      }
+    }
+    Given g{};
+    if (!SPLIT) g = given(a, row, token);   // in flight beside the rest
+    for (; q < p1; q += 64 * W) {
+      float v[1][kPiece];
+      const int at = load_piece(row, q + in < p1 ? (q + in) * kPiece : a.vocab, a.vocab, v[0]);
+      take(q, v, at);
     }
     sum = wave_sums(sum, c);
     uint64_t mine = TOP ? best.cut() : 0ull;
@@ -279,8 +377,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobArgs a, const T *l
         if (TOP) {   // kWaves x top <= 64 keys
           const int from = lane_id() / 16, j = lane_id() % 16;
           static_assert(SVT_MAX_TOP == 16 && kWaves == 4, "a lane for every wave's keys");
-          uint64_t k[1] = {j < a.top ? lists[from][j] : 0ull};
-          mine = wave_top(k, a.top);
+          mine = best_of_wave(j < a.top ? lists[from][j] : 0ull, 64, a.top, &lists[0][64]);
         }
       }
     }
@@ -293,7 +390,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobArgs a, const T *l
         }
         if (lane_id() < a.top) a.best[u * a.top + lane_id()] = mine;
       } else {
-        finish(a, row, t, sum, mine);
+        finish(a, g, t, sum, mine);
       }
     }
     if (W > 1) __syncthreads();   // parts and lists are free again
@@ -303,8 +400,10 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobArgs a, const T *l
 // joins the splits of a row, one wave a row
 template <class T, bool TOP>
 __global__ __launch_bounds__(64) void k_logprobs_join(LogprobArgs a, const T *logits) {
+  __shared__ uint64_t ordered[SVT_MAX_TOP];
   const float c = a.scale * kLog2e;
   for (int64_t t = blockIdx.x; t < a.n_tokens; t += gridDim.x) {
+    const Given g = given(a, logits + t * a.vocab, a.tokens[t]);
     Sums sum = Sums::none();
     for (int p = lane_id(); p < a.splits; p += 64) {
       const float *s = a.sums + 3 * (t * a.splits + p);
@@ -314,7 +413,8 @@ __global__ __launch_bounds__(64) void k_logprobs_join(LogprobArgs a, const T *lo
     uint64_t best = 0ull;
     if (TOP) {
       const int n = a.splits * a.top;
-      for (int i0 = 0; i0 < n; i0 += 64 * 7) {
+      if (n <= 64) best = best_of_wave(lane_id() < n ? a.best[t * n + lane_id()] : 0ull, n, a.top, ordered);
+      for (int i0 = 0; n > 64 && i0 < n; i0 += 64 * 7) {
         uint64_t k[8];
 #pragma unroll
         for (int i = 0; i < 7; ++i) k[i] = i0 + 64 * i + lane_id() < n ? a.best[t * n + i0 + 64 * i + lane_id()] : 0ull;
@@ -322,7 +422,7 @@ __global__ __launch_bounds__(64) void k_logprobs_join(LogprobArgs a, const T *lo
         best = wave_top(k, a.top);
       }
     }
-    finish(a, logits + t * a.vocab, t, sum, best);
+    finish(a, g, t, sum, best);
   }
 }
 
@@ -348,26 +448,48 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_backward(LogprobArgs a, c
     const float d = given ? d_logprobs[t] * a.scale : 0.f;
     const float dh = d_entropy ? d_entropy[t] * a.scale : 0.f;
     const float A = -(d + dh * (a.entropy[t] - log_z * kLn2)), B = -dh * kLn2;
-    for (int p = p0 + in; p < p1; p += 64 * W) {
-      const int first = p * kPiece;
-      float v[kPiece];
-      load_piece(row, first, a.vocab, v);
-      const int at = given ? (int)token - first : -1;
+    const int at = given ? (int)token : -kPiece;
+    auto slopes = [&](float (&v)[kPiece], int first) {
 #pragma unroll
       for (int i = 0; i < kPiece; ++i) {
         const float x = exponent(v[i], peak, c);
         const float g = __builtin_amdgcn_exp2f(x - log_z) * fmaf(B, x, A);
-        v[i] = i == at && v[i] > -INFINITY ? g + d : g;
+        v[i] = first + i == at && v[i] > -INFINITY ? g + d : g;
       }
-      if (first + kPiece <= a.vocab) {
-        Eight<T> r;
+    };
+    auto narrow = [&](const float (&v)[kPiece], int first) {
+      Eight<T> r;
 #pragma unroll
-        for (int i = 0; i < kPiece; ++i) r.v[i] = (T)v[i];
-        *reinterpret_cast<Piece<T> *>(out + first) = __builtin_bit_cast(Piece<T>, r);
+      for (int i = 0; i < kPiece; ++i) r.v[i] = (T)v[i];
+      *reinterpret_cast<Piece<T> *>(out + first) = __builtin_bit_cast(Piece<T>, r);
+    };
+    constexpr int U = 2, hop = U * 64 * W;   // pieces of a thread in flight
+    const int whole = a.vocab / kPiece, p2 = p1 < whole ? p1 : whole;
+    int q = p0;
+    for (; q + hop <= p2; q += hop) {
+      Piece<T> raw[U];
+#pragma unroll
+      for (int n = 0; n < U; ++n) raw[n] = raw_piece(row, (q + n * 64 * W + in) * kPiece);
+#pragma unroll
+      for (int n = 0; n < U; ++n) {
+        const int first = (q + n * 64 * W + in) * kPiece;
+        float v[kPiece];
+        widen(raw[n], v);
+        slopes(v, first);
+        narrow(v, first);
+      }
+    }
+    for (int p = q + in; p < p1; p += 64 * W) {
+      const int first = p * kPiece;
+      float v[kPiece];
+      const int from = load_piece(row, first, a.vocab, v);
+      slopes(v, from);
+      if (first + kPiece <= a.vocab) {
+        narrow(v, first);
       } else {
 #pragma unroll
         for (int i = 0; i < kPiece; ++i)
-          if (first + i < a.vocab) out[first + i] = (T)v[i];
+          if (from + i >= first && from + i < a.vocab) out[from + i] = (T)v[i];
       }
     }
   }
