@@ -9,6 +9,10 @@
 // border leave partial sums, which one more launch joins in order; so a token that names half the batch costs no more
 // than any.  Rows that no token names are cleared by workgroups of their own in the launch that adds, which keeps the
 // table's writes beside the gradient's reads.
+//
+// Measured: rows for 65536 tokens of 1024 bfloat16 36 us (176 MB, 4.9 TB/s), for 2048 of 128 float16 2.9.  The gradient in
+// 131072 rows of the former 119: the sort 25 (a chain of four launches), sums and zeros 80 (403 MB, 5 TB/s), the join 9; of
+// 3001 tokens of 250 float32 in 5003 rows 23: 8, 8 and 6, chains of dependent loads all three.
 
 #include <type_traits>
 
@@ -25,6 +29,19 @@ constexpr int32_t kMaxWidth = 1 << 24;
 // M neighbouring elements, moved by one load or store (two where they take 32 bytes)
 template <class T, int M>
 struct alignas(M * sizeof(T) < 16 ? M * sizeof(T) : 16) Vec { T v[M]; };
+
+// the same past the caches, for what is touched once: 16-byte pieces only, others as ever
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+template <class T, int M>
+__device__ __forceinline__ Vec<T, M> load_once(const Vec<T, M> *p) {
+  if constexpr (sizeof(Vec<T, M>) == 16) return __builtin_bit_cast(Vec<T, M>, __builtin_nontemporal_load((const u32x4 *)p));
+  else return *p;
+}
+template <class T, int M>
+__device__ __forceinline__ void clear_once(Vec<T, M> *p) {
+  if constexpr (sizeof(Vec<T, M>) == 16) __builtin_nontemporal_store(u32x4{0u, 0u, 0u, 0u}, (u32x4 *)p);
+  else *p = Vec<T, M>{};
+}
 
 // ---- lookup --------------------------------------------------------------------------------------
 
@@ -72,7 +89,7 @@ __global__ __launch_bounds__(kThreads) void k_lookup(LookupArgs a, const Vec<T, 
 
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 constexpr int kMostBits = 10, kMostBins = 1 << kMostBits;
-constexpr int kSteps = 4, kTile = kSortThreads * kSteps;   // tokens of a block at a time
+constexpr int kSteps = 4;   // tokens of a thread at a time, at most
 constexpr int kOneSteps = 8;
 constexpr int64_t kOneTokens = kOneSteps * kSortThreads;
 constexpr int kMostCounts = 1 << 17;                       // every block reads the whole table of histograms
@@ -82,7 +99,8 @@ struct SortShape {
   int64_t n, n_rows;
   int32_t passes, bits;                // bits a digit
   int32_t blocks;
-  int64_t per_block;                   // a multiple of kTile
+  int32_t steps;                       // tokens of a thread at a time: 1 or kSteps
+  int64_t per_block;                   // a multiple of steps times the threads
 };
 
 __device__ __forceinline__ uint32_t key_of(int64_t id, int64_t n_rows) {
@@ -179,6 +197,7 @@ __device__ __forceinline__ uint32_t load_key(const Digits &d, const SortShape &s
   return d.ids ? key_of(d.ids[i], s.n_rows) : d.keys[i];
 }
 
+template <int STEPS>
 __global__ __launch_bounds__(kSortThreads) void k_sort_count(Digits d, SortShape s, int32_t *counts, int32_t *crossing) {
   __shared__ int32_t hist[kMostBins];
   const int tid = threadIdx.x, bins = 1 << s.bits;
@@ -186,36 +205,36 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_count(Digits d, SortShape
   if (blockIdx.x == 0 && tid == 0) *crossing = 0;
   if (tid < bins) hist[tid] = 0;
   __syncthreads();
-  for (int64_t i0 = b0; i0 < b1; i0 += kTile) {
-    uint32_t k[kSteps];
+  for (int64_t i0 = b0; i0 < b1; i0 += STEPS * kSortThreads) {
+    uint32_t k[STEPS];
 #pragma unroll
-    for (int q = 0; q < kSteps; ++q) {
+    for (int q = 0; q < STEPS; ++q) {
       const int64_t i = i0 + q * kSortThreads + tid;
       k[q] = load_key(d, s, i < b1 ? i : b1 - 1);
     }
 #pragma unroll
-    for (int q = 0; q < kSteps; ++q)
+    for (int q = 0; q < STEPS; ++q)
       if (i0 + q * kSortThreads + tid < b1) atomicAdd(&hist[(k[q] >> d.shift) & (uint32_t)(bins - 1)], 1);
   }
   __syncthreads();
   if (tid < bins) counts[(int64_t)blockIdx.x * bins + tid] = hist[tid];
 }
 
-template <int BITS>
+template <int STEPS, int BITS>
 __global__ __launch_bounds__(kSortThreads) void k_sort_place(Digits d, SortShape s, const int32_t *counts,
                                                              uint32_t *out_keys, int32_t *out_order) {
   __shared__ int32_t count[kSortWaves][kMostBins];
   __shared__ int32_t total[kMostBins], start[kMostBins], next[kMostBins], waves[kSortWaves];
-  __shared__ uint32_t key[kTile];
-  __shared__ int32_t at[kTile];
+  __shared__ uint32_t key[STEPS * kSortThreads];
+  __shared__ int32_t at[STEPS * kSortThreads];
   const int tid = threadIdx.x, wv = tid / 64, b = blockIdx.x, bins = 1 << s.bits;
   const int64_t b0 = b * s.per_block, b1 = b0 + s.per_block < s.n ? b0 + s.per_block : s.n;
-  const int in_tile = wv * (64 * kSteps) + tid % 64;
-  uint32_t k[kSteps];
-  int from[kSteps];
+  const int in_tile = wv * (64 * STEPS) + tid % 64;
+  uint32_t k[STEPS];
+  int from[STEPS];
   auto load = [&](int64_t t0) {
 #pragma unroll
-    for (int q = 0; q < kSteps; ++q) {
+    for (int q = 0; q < STEPS; ++q) {
       const int64_t i = t0 + in_tile + 64 * q, j = i < b1 ? i : b1 - 1;
       k[q] = load_key(d, s, j);
       from[q] = d.ids ? (int)j : d.order[j];
@@ -254,28 +273,28 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_place(Digits d, SortShape
     const int first = scan_bins(tid < bins ? total[tid] : 0, waves);
     if (tid < bins) next[tid] += first;
   }
-  for (int64_t t0 = b0; t0 < b1; t0 += kTile) {
+  for (int64_t t0 = b0; t0 < b1; t0 += STEPS * kSortThreads) {
     if (t0 != b0) load(t0);
-    int e[kSteps], rank[kSteps];
+    int e[STEPS], rank[STEPS];
 #pragma unroll
-    for (int q = 0; q < kSteps; ++q)
+    for (int q = 0; q < STEPS; ++q)
       e[q] = t0 + in_tile + 64 * q < b1 ? (int)((k[q] >> d.shift) & (uint32_t)(bins - 1)) : -1;
     for (int i = tid % 64; i < bins; i += 64) count[wv][i] = 0;
-    rank_entries<kSteps, BITS>(e, rank, count[wv]);
+    rank_entries<STEPS, BITS>(e, rank, count[wv]);
     __syncthreads();   // also: the scan's and the last tile's reads of LDS are done
     const int mine = sum_waves(count, bins);
     const int first = scan_bins(mine, waves);
     if (tid < bins) start[tid] = first;
     __syncthreads();
 #pragma unroll
-    for (int q = 0; q < kSteps; ++q)
+    for (int q = 0; q < STEPS; ++q)
       if (e[q] >= 0) {
         const int to = start[e[q]] + count[wv][e[q]] + rank[q];
         key[to] = k[q];
         at[to] = from[q];
       }
     __syncthreads();
-    const int here = (int)(b1 - t0 < kTile ? b1 - t0 : kTile);
+    const int here = (int)(b1 - t0 < STEPS * kSortThreads ? b1 - t0 : STEPS * kSortThreads);
     for (int p = tid; p < here; p += kSortThreads) {
       const uint32_t v = key[p];
       const int o = (int)((v >> d.shift) & (uint32_t)(bins - 1));
@@ -306,13 +325,15 @@ struct SumArgs {
   int32_t *crossing;           // [0]: their number; then the chunks whose last run starts there and goes on
 };
 
-// first place in [0, n) whose key is at least v
+// First place in [0, n) whose key is at least v, n if there is none; the whole wave asks.  64 places are looked at a time: 3
+// loads one after the other for 65536 tokens, where halving takes 16.
 __device__ __forceinline__ int64_t first_place(const uint32_t *keys, int64_t n, uint64_t v) {
   int64_t lo = 0, hi = n;
   while (lo < hi) {
-    const int64_t mid = (lo + hi) / 2;
-    if (keys[mid] < v) lo = mid + 1;
-    else hi = mid;
+    const int64_t step = (hi - lo + 63) / 64, probe = lo + (lane_id() + 1) * step - 1;   // the last of the lane's piece
+    const bool less = probe < hi && keys[probe < hi ? probe : lo] < v;
+    lo += __builtin_popcountll(__ballot(less)) * step;
+    hi = lo + step - 1 < hi ? lo + step - 1 : hi;
   }
   return lo;
 }
@@ -338,7 +359,7 @@ __device__ __forceinline__ void clear_rows(const SumArgs &a, int64_t first, Vec<
   const int in = threadIdx.x % a.lanes;
   for (int r = threadIdx.x / a.lanes; first + r < end; r += kThreads / a.lanes)
     if (!(named[r / 32] >> (r % 32) & 1u))
-      for (int c = in; c < a.pieces; c += a.lanes) table[(first + r) * a.pieces + c] = Vec<TD, M>{};
+      for (int c = in; c < a.pieces; c += a.lanes) clear_once(&table[(first + r) * a.pieces + c]);
 }
 
 template <class TD, int M, bool ADD>
@@ -350,21 +371,22 @@ __device__ __forceinline__ void put_row(Vec<TD, M> *at, const float (&sum)[M], f
   *at = r;
 }
 
-template <class T, class TD, int M, bool ADD>
+// TWO: rows of more pieces than lanes; J: places in flight
+template <class T, class TD, int M, bool ADD, bool TWO>
 __global__ __launch_bounds__(kThreads) void k_sum_rows(SumArgs a, const Vec<T, M> *d_out, Vec<TD, M> *table) {
   __shared__ uint32_t named[ADD ? 1 : kClearMost / 32];
   if (!ADD && (int)blockIdx.x >= a.sum_blocks) {
     clear_rows<TD, M>(a, (int64_t)(blockIdx.x - a.sum_blocks) * a.clear_rows, table, named);
     return;
   }
-  constexpr int J = 4;   // places in flight
+  constexpr int J = TWO ? 4 : 8;
   const int in = threadIdx.x % a.lanes;
   const int64_t unit = (int64_t)blockIdx.x * (kThreads / a.lanes) + threadIdx.x / a.lanes;
   const int64_t chunk = unit / a.column_blocks;
   if (chunk >= a.chunks) return;
   const int block = (int)(unit - chunk * a.column_blocks);
   const int c = block * 2 * a.lanes + in;
-  const bool one = c < a.pieces, two = c + a.lanes < a.pieces;
+  const bool one = c < a.pieces, two = TWO && c + a.lanes < a.pieces;
   const int c1 = one ? c : 0, c2 = two ? c + a.lanes : c1;
   const int64_t p0 = chunk * a.per, p1 = p0 + a.per < a.n ? p0 + a.per : a.n;
   const uint32_t none = (uint32_t)a.n_rows;
@@ -388,19 +410,28 @@ __global__ __launch_bounds__(kThreads) void k_sum_rows(SumArgs a, const Vec<T, M
       if (whole && block == 0 && in == 0) a.crossing[1 + atomicAdd(a.crossing, 1)] = (int32_t)chunk;
     }
   };
-  for (int64_t p = p0; p < p1; p += J) {
-    uint32_t k[J];
-    Vec<T, M> v[J], w[J];
+  // the places after the next J are looked up while the next J's rows are on their way
+  uint32_t k[J], k_next[J];
+  int32_t o_next[J];
+  Vec<T, M> v[J], w[J];
+  auto look_up = [&](int64_t p) {
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int64_t q = p + j < p1 ? p + j : p1 - 1;
-      k[j] = a.keys[q];
-      const int64_t row = (int64_t)a.order[q] * a.pieces;
-      if (k[j] != none) {
-        v[j] = d_out[row + c1];
-        w[j] = d_out[row + c2];
-      }
+      k_next[j] = a.keys[q];
+      o_next[j] = a.order[q];
     }
+  };
+  look_up(p0);
+  for (int64_t p = p0; p < p1; p += J) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      k[j] = k_next[j];
+      const int64_t row = (int64_t)o_next[j] * a.pieces;
+      v[j] = load_once(&d_out[row + c1]);
+      if (TWO) w[j] = load_once(&d_out[row + c2]);
+    }
+    look_up(p + J);
 #pragma unroll
     for (int j = 0; j < J; ++j)
       if (p + j < p1) {
@@ -411,56 +442,109 @@ __global__ __launch_bounds__(kThreads) void k_sum_rows(SumArgs a, const Vec<T, M
 #pragma unroll
           for (int i = 0; i < M; ++i) s1[i] = s2[i] = 0.f;
         }
-        if (k[j] != none)
 #pragma unroll
-          for (int i = 0; i < M; ++i) {
-            s1[i] += (float)v[j].v[i];
-            s2[i] += (float)w[j].v[i];
-          }
+        for (int i = 0; i < M; ++i) {
+          s1[i] += (float)v[j].v[i];
+          if (TWO) s2[i] += (float)w[j].v[i];
+        }
       }
   }
   leave(p1 == a.n || a.keys[p1] != run);
 }
 
-// Sums of the runs that cross chunks: a workgroup takes 256 columns of one, its four parts a quarter of the chunks
-// each, added in order
-constexpr int kJoinThreads = 1024, kJoinColumns = 256, kJoinParts = kJoinThreads / kJoinColumns;
+// Sums of the runs that cross chunks, 256 columns of one at a time.  Most cross once or twice: a wave each.  Those of more
+// than kJoinAlone chunks are put off until the workgroup's waves share them, each a contiguous part, added in order.
+// (200000 tokens of 300 rows, chunks of 8: 117 us with four waves to every run, 47 like this.)
+constexpr int kJoinColumns = 256, kJoinThreads = 1024, kJoinWaves = kJoinThreads / 64, kJoinAlone = 16;
+
+struct __attribute__((packed, aligned(4))) FourSums { float v[4]; };
+
+// parts i0 .. i1 - 1 of a run that begins in a chunk (row 1 of the first, row 0 of the others), `left` columns from `from` on
+__device__ __forceinline__ FourSums add_parts(const float *from, int64_t i0, int64_t i1, int64_t width, int left) {
+  FourSums sum{};
+  if (left >= 4) {
+    int64_t i = i0;
+    for (; i + 8 <= i1; i += 8) {
+      FourSums v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = *reinterpret_cast<const FourSums *>(from + (i + j ? 2 * (i + j) : 1) * width);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum.v[k] += v[j].v[k];
+    }
+    for (; i < i1; ++i) {
+      const FourSums v = *reinterpret_cast<const FourSums *>(from + (i ? 2 * i : 1) * width);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sum.v[k] += v.v[k];
+    }
+  } else {
+    for (int64_t i = i0; i < i1; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k < left) sum.v[k] += from[(i ? 2 * i : 1) * width + k];
+  }
+  return sum;
+}
 
 template <class TD, bool ADD>
 __global__ __launch_bounds__(kJoinThreads) void k_join_runs(SumArgs a, TD *table) {
-  __shared__ float parts[kJoinParts][kJoinColumns];
-  const int columns = (a.width + kJoinColumns - 1) / kJoinColumns;
+  __shared__ FourSums parts[kJoinWaves][64];
+  __shared__ int64_t put_off[kJoinWaves], length[kJoinWaves];
+  const int columns = (a.width + kJoinColumns - 1) / kJoinColumns, wave = threadIdx.x / 64;
   const int64_t units = (int64_t)a.crossing[0] * columns;
-  const int part = threadIdx.x / kJoinColumns, in = threadIdx.x % kJoinColumns;
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int64_t chunk = a.crossing[1 + u / columns];
-    const int col = (int)(u % columns) * kJoinColumns + in;
-    const uint32_t run = a.keys[(chunk + 1) * a.per - 1];
-    const int64_t last = (first_place(a.keys, a.n, (uint64_t)run + 1) - 1) / a.per;   // the chunk that it ends in
-    const int64_t n = last - chunk + 1, each = (n + kJoinParts - 1) / kJoinParts;
-    const int64_t i0 = part * each, i1 = i0 + each < n ? i0 + each : n;
-    float sum = 0.f;
-    if (col < a.width) {
-      const float *from = a.partial + chunk * 2 * a.width + col;   // row 1 of the first chunk, row 0 of the others
-      int64_t i = i0;
-      for (; i + 8 <= i1; i += 8) {
-        float v[8];
+  auto place = [&](int64_t u, int64_t &chunk, int &col, uint32_t &run) {
+    chunk = a.crossing[1 + u / columns];
+    col = (int)(u % columns) * kJoinColumns + lane_id() * 4;
+    run = a.keys[(chunk + 1) * a.per - 1];
+  };
+  auto put = [&](const FourSums &sum, int col, uint32_t run) {
+    TD *at = table + (int64_t)run * a.width + col;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = from[(i + j ? 2 * (i + j) : 1) * a.width];
+    for (int k = 0; k < 4; ++k)
+      if (col + k < a.width) at[k] = (TD)(ADD ? fmaf(a.scale, sum.v[k], (float)at[k]) : a.scale * sum.v[k]);
+  };
+  // neighbouring runs go to different workgroups: the long ones among a few are spread
+  for (int64_t u0 = blockIdx.x; u0 < units; u0 += (int64_t)gridDim.x * kJoinWaves) {
+    const int64_t u = u0 + (int64_t)wave * gridDim.x;
+    int64_t n = 0;   // chunks that the run lies in: where it begins, and those that begin with it
+    if (u < units) {
+      int64_t chunk;
+      int col;
+      uint32_t run;
+      place(u, chunk, col, run);
+      const int64_t c = chunk + 1 + lane_id();
+      const uint64_t goes_on = __ballot(c < a.chunks && a.keys[(c < a.chunks ? c : chunk) * a.per] == run);
+      n = ~goes_on ? 1 + __builtin_ctzll(~goes_on) : (first_place(a.keys, a.n, (uint64_t)run + 1) - 1) / a.per - chunk + 1;
+      if (n <= kJoinAlone)
+        put(add_parts(a.partial + chunk * 2 * a.width + col, 0, n, a.width, a.width - col), col, run);
+    }
+    if (lane_id() == 0) {
+      put_off[wave] = n > kJoinAlone ? u : -1;
+      length[wave] = n;
+    }
+    __syncthreads();
+    for (int w = 0; w < kJoinWaves; ++w) {
+      if (put_off[w] < 0) continue;   // the same for all
+      int64_t chunk;
+      int col;
+      uint32_t run;
+      place(put_off[w], chunk, col, run);
+      const int64_t each = (length[w] + kJoinWaves - 1) / kJoinWaves, i0 = wave * each;
+      const int64_t i1 = i0 + each < length[w] ? i0 + each : length[w];
+      FourSums sum = add_parts(a.partial + chunk * 2 * a.width + col, i0, i1, a.width, a.width - col);
+      parts[wave][lane_id()] = sum;
+      __syncthreads();
+      if (wave == 0) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum += v[j];
+        for (int j = 1; j < kJoinWaves; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sum.v[k] += parts[j][lane_id()].v[k];
+        put(sum, col, run);
       }
-      for (; i < i1; ++i) sum += from[(i ? 2 * i : 1) * a.width];
+      __syncthreads();
     }
-    parts[part][in] = sum;
-    __syncthreads();
-    if (part == 0 && col < a.width) {
-#pragma unroll
-      for (int j = 1; j < kJoinParts; ++j) sum += parts[j][in];
-      TD *at = table + (int64_t)run * a.width + col;
-      *at = (TD)(ADD ? fmaf(a.scale, sum, (float)*at) : a.scale * sum);
-    }
-    __syncthreads();
+    __syncthreads();   // put_off has been read
   }
 }
 
@@ -486,22 +570,26 @@ int with_elems(int m, F f) {
 }
 
 SortShape sort_shape(int64_t n, int64_t n_rows) {
-  SortShape s{n, n_rows, 0, 0, 1, 0};
+  SortShape s{n, n_rows, 0, 0, 1, 1, 0};
   const int bits = 64 - __builtin_clzll((uint64_t)n_rows);   // of the key n_rows
   s.passes = (bits + kMostBits - 1) / kMostBits;
   s.bits = (bits + s.passes - 1) / s.passes;
-  const int64_t tiles = (n + kTile - 1) / kTile, most = kMostCounts >> s.bits;
+  // up to 128 blocks of one token a thread (65536 tokens: a placing pass 7.9 us, with four tokens a thread 9.3)
+  s.steps = n <= 128 * kSortThreads ? 1 : kSteps;
+  const int64_t tile = s.steps * kSortThreads, tiles = (n + tile - 1) / tile, most = kMostCounts >> s.bits;
   const int64_t each = tiles > most ? (tiles + most - 1) / most : 1;
-  s.per_block = each * kTile;
+  s.per_block = each * tile;
   s.blocks = (int32_t)(n ? (n + s.per_block - 1) / s.per_block : 1);
   return s;
 }
 
-// places of a chunk: few enough for 2048 chunks, 8 to 256 (a sum is a chain of at most that many, then one over the
-// chunks)
-int32_t chunk_places(int64_t n) {
+// Places of a chunk, 8 to 256 (a sum is a chain of at most that many, then one over the chunks): few enough for 4096 waves,
+// of which 512 columns fill one.  65536 tokens x 1024 bfloat16, with half as many waves 126 us, so 121; 200000 x 256 float32
+// of 50000 rows, in chunks of 128 the sums alone 146, of 32 61.
+int32_t chunk_places(int64_t n, int32_t width) {
+  const int64_t want = n * (width < 512 ? width : 512) / (512 * 4096);
   int32_t per = 8;
-  while (per < 256 && n > 2048 * (int64_t)per) per *= 2;
+  while (per < 256 && per < want) per *= 2;
   return per;
 }
 
@@ -525,7 +613,7 @@ Space space(int64_t n, int64_t n_rows, int32_t width) {
       s.order[i] = i < sets ? take((size_t)n * 4) : s.order[0];
     }
     s.counts = n <= kOneTokens ? at : take(((size_t)sh.blocks << sh.bits) * 4);
-    const int32_t per = chunk_places(n);
+    const int32_t per = chunk_places(n, width);
     const size_t chunks = (size_t)((n + per - 1) / per);
     s.partial = take(chunks * 2 * (size_t)width * 4);
     s.crossing = take((chunks + 1) * 4);
@@ -553,6 +641,7 @@ int embedding_backward(const char *who, SumArgs a, const SortShape &sh, const Sp
     auto with_bits = [&](auto f) {
       if (sh.bits <= 6) return f(std::integral_constant<int, 6>{});
       if (sh.bits <= 8) return f(std::integral_constant<int, 8>{});
+      if (sh.bits <= 9) return f(std::integral_constant<int, 9>{});
       return f(std::integral_constant<int, 10>{});
     };
     int32_t *crossing = (int32_t *)(ws + sp.crossing);
@@ -571,10 +660,14 @@ int embedding_backward(const char *who, SumArgs a, const SortShape &sh, const Sp
       for (int p = 0; p < sh.passes; ++p) {
         const Digits d{p ? nullptr : ids, keys(sorted), order(sorted), p * sh.bits};
         if (p) sorted ^= 1;
-        int rc = launch(who, k_sort_count, sh.blocks, kSortThreads, 0, stream, d, sh, counts, crossing);
-        if (rc != SVT_OK) return rc;
-        rc = launch(who, k_sort_place<B>, sh.blocks, kSortThreads, 0, stream, d, sh, (const int32_t *)counts, keys(sorted),
-                    order(sorted));
+        auto pass = [&](auto steps) {
+          constexpr int S = decltype(steps)::value;
+          const int rc = launch(who, k_sort_count<S>, sh.blocks, kSortThreads, 0, stream, d, sh, counts, crossing);
+          if (rc != SVT_OK) return rc;
+          return launch(who, k_sort_place<S, B>, sh.blocks, kSortThreads, 0, stream, d, sh, (const int32_t *)counts,
+                        keys(sorted), order(sorted));
+        };
+        const int rc = sh.steps == 1 ? pass(std::integral_constant<int, 1>{}) : pass(std::integral_constant<int, kSteps>{});
         if (rc != SVT_OK) return rc;
       }
       return (int)SVT_OK;
@@ -584,7 +677,7 @@ int embedding_backward(const char *who, SumArgs a, const SortShape &sh, const Sp
     a.order = order(sorted);
     a.partial = (float *)(ws + sp.partial);
     a.crossing = crossing;
-    a.per = chunk_places(a.n);
+    a.per = chunk_places(a.n, a.width);
     a.chunks = (int32_t)((a.n + a.per - 1) / a.per);
     a.column_blocks = (a.pieces + 2 * a.lanes - 1) / (2 * a.lanes);
     const int64_t units = (int64_t)a.chunks * a.column_blocks, each = kThreads / a.lanes;
@@ -593,17 +686,21 @@ int embedding_backward(const char *who, SumArgs a, const SortShape &sh, const Sp
     a.sum_blocks = (int32_t)blocks;
   }
   int64_t clear_blocks = 0;
-  if (!ADD) {   // about 256 KiB of rows for each
-    const int64_t row = (int64_t)a.width * sizeof(TD);
+  if (!ADD) {   // at most 256 KiB of rows for each, and work for every compute unit
+    const int64_t row = (int64_t)a.width * sizeof(TD), share = (a.n_rows + 1023) / 1024;
     a.clear_rows = (int32_t)(row >= 262144 ? 1 : 262144 / row < kClearMost ? 262144 / row : kClearMost);
+    if (share < a.clear_rows) a.clear_rows = (int32_t)share;
     clear_blocks = (a.n_rows + a.clear_rows - 1) / a.clear_rows;
     if (clear_blocks > INT32_MAX / 4) return report(SVT_EINVAL, "%s: too large a table for one call", who);
   }
   // the grid's threads stay below 2^32
   if ((a.sum_blocks + clear_blocks) * kThreads >= int64_t(1) << 32)
     return report(SVT_EINVAL, "%s: too large a table or batch for one call", who);
-  const int rc = launch(who, k_sum_rows<T, TD, M, ADD>, (unsigned)(a.sum_blocks + clear_blocks), kThreads, 0, stream, a,
-                        (const Vec<T, M> *)d_out, (Vec<TD, M> *)d_table);
+  auto sum = [&](auto two) {
+    return launch(who, k_sum_rows<T, TD, M, ADD, decltype(two)::value>, (unsigned)(a.sum_blocks + clear_blocks), kThreads, 0,
+                  stream, a, (const Vec<T, M> *)d_out, (Vec<TD, M> *)d_table);
+  };
+  const int rc = a.pieces > a.lanes ? sum(std::true_type{}) : sum(std::false_type{});
   if (rc != SVT_OK || a.chunks < 2) return rc;
   const int64_t most = (int64_t)(a.chunks - 1) * ((a.width + kJoinColumns - 1) / kJoinColumns);
   return launch(who, k_join_runs<TD, ADD>, (unsigned)(most < 512 ? most : 512), kJoinThreads, 0, stream, a, (TD *)d_table);
