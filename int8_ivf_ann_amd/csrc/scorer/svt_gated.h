@@ -413,6 +413,7 @@ struct GatedArgs {
   int32_t dx_first;
   int64_t dx_blocks, dw_blocks;   // workgroups of each, dx's with its parts
   int64_t dw_partial;         // where dW's parts begin in `partial`, behind dx's
+  int64_t dw_slots;           // for so many parts there is room: more are not written, offsets that fall would give some
   float *partial;
 };
 
@@ -784,7 +785,7 @@ __device__ __forceinline__ void dw_tile(const GatedArgs &a, char *lds, int64_t b
   if (!tile_of(b % own, 2 * tiles, a.columns, in, column)) return;
   int64_t part = -1;
   const Rows rows = rows_of_unit(a.offsets, a.n_matrices, a.n_rows, block, a.per, 1, &part);
-  if (rows.matrix < 0) return;
+  if (rows.matrix < 0 || part >= a.dw_slots) return;
   const bool up = in >= tiles;
   const int n0 = (int)(up ? in - tiles : in) * C::q, k0 = column * C::p;
   const int64_t len = rows.end - rows.first, pitch = a.in_pitch;
@@ -875,7 +876,7 @@ __global__ __launch_bounds__(256) void k_gated_join(GatedArgs a) {
   }
   const Rows rows = rows_of_matrix(a.offsets, a.n_rows, matrix);
   const int parts = (int)((rows.end - rows.first + a.per - 1) / a.per);
-  if (parts < 2) return;
+  if (parts < 2 || before + parts > a.dw_slots) return;
   const int64_t size = (int64_t)a.outs * a.ins;
   for (int64_t i = at; i < 2 * size; i += hop) {
     const int64_t gate = size - i;   // four values may lie in both halves
@@ -1005,11 +1006,10 @@ inline size_t gated_copies(const GatedArgs &a, int elem) {
   return (size_t)(a.n_rows + 2 * (int64_t)a.n_matrices * a.outs) * gated_pitch(a.ins, elem);
 }
 
-// values of dx's parts, and of dW's: matrices with several blocks have at most 2 n_rows / per together
+// values of dx's parts; dW's parts: matrices with several blocks have at most 2 n_rows / per together; their values
 inline int64_t dx_parts(const GatedArgs &a, const GatedPlan &p) { return p.splits > 1 ? p.splits * a.n_rows * a.ins : 0; }
-inline int64_t dw_parts(const GatedArgs &a, const GatedPlan &p) {
-  return p.per < a.n_rows ? 2 * a.n_rows / p.per * 2 * a.outs * a.ins : 0;
-}
+inline int64_t dw_slots(const GatedArgs &a, const GatedPlan &p) { return p.per < a.n_rows ? 2 * a.n_rows / p.per : 0; }
+inline int64_t dw_parts(const GatedArgs &a, const GatedPlan &p) { return dw_slots(a, p) * 2 * a.outs * a.ins; }
 
 // one type's calls
 template <class T> int gated_forward(const char *who, GatedArgs a, const GatedPlan &p, void *stream);
@@ -1081,6 +1081,7 @@ int gated_backward(const char *who, GatedArgs a, const GatedPlan &p, void *strea
   a.columns = p.columns;
   a.splits = p.splits;
   a.per = p.per;
+  a.dw_slots = dw_slots(a, p);
   a.dx_blocks = a.dx ? dx_blocks(p) : 0;
   a.dw_blocks = a.dw_gate ? dw_blocks(p, a.outs) : 0;
   a.dx_first = 2 * (int64_t)a.outs / p.splits > p.per;

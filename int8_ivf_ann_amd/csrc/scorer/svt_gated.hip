@@ -123,7 +123,7 @@ extern "C" size_t svt_gated_linear_backward_workspace_size(int32_t n_rows, int32
   if (n_rows == 0) return 0;
   const GatedPlan plan = plan_backward(a, b);
   const bool as_is = aligned && aligned_rows(n_in, b, nullptr, nullptr, nullptr);
-  return (size_t)(2 * n_rows * a.pitch) + (as_is ? 0 : gated_copies(a, b)) +
+  return (size_t)(2 * a.n_rows * a.pitch) + (as_is ? 0 : gated_copies(a, b)) +
          (size_t)(dx_parts(a, plan) + dw_parts(a, plan)) * 4;
 }
 
@@ -159,7 +159,7 @@ extern "C" int svt_gated_linear_backward(int32_t n_rows, int32_t n_in, int32_t n
   a.dw_gate = dw_gate;
   a.dw_up = dw_up;
   const bool as_is = aligned_rows(n_in, b, a.x, a.w_gate, a.w_up);
-  const size_t both = (size_t)(2 * n_rows * a.pitch), copies = as_is || n_rows == 0 ? 0 : gated_copies(a, b);
+  const size_t both = (size_t)(2 * a.n_rows * a.pitch), copies = as_is || n_rows == 0 ? 0 : gated_copies(a, b);
   const GatedPlan plan = plan_backward(a, b);
   const int64_t dx_part = dx ? dx_parts(a, plan) : 0, dw_part = dw_gate ? dw_parts(a, plan) : 0;
   const size_t need = both + copies + (size_t)(dx_part + dw_part) * 4;

@@ -147,17 +147,13 @@ def lib():
     f32 = ctypes.c_float
     L.svt_embedding.argtypes = [i64, i64, i32, i32, vp, vp, f32, vp, vp]
     L.svt_embedding_backward_workspace_size.argtypes = [i64, i64, i32]
-    L.svt_embedding_backward_workspace_size.restype = sz
     L.svt_embedding_backward.argtypes = [i64, i64, i32, i32, vp, vp, f32, i32, i32, vp, vp, sz, vp]
     L.svt_gated_linear_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32]
-    L.svt_gated_linear_workspace_size.restype = sz
     L.svt_gated_linear.argtypes = [i32, i32, i32, i32, i32, vp, vp, vp, vp, i32, vp, vp, vp, vp, sz, vp]
     L.svt_gated_linear_backward_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32]
-    L.svt_gated_linear_backward_workspace_size.restype = sz
     L.svt_gated_linear_backward.argtypes = [i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, sz,
                                             vp]
     L.svt_token_logprobs_workspace_size.argtypes = [i32, i32, i32]
-    L.svt_token_logprobs_workspace_size.restype = sz
     L.svt_token_logprobs.argtypes = [i32, i32, i32, i32, vp, vp, f32, vp, vp, vp, vp, vp, vp, sz, vp]
     L.svt_token_logprobs_backward.argtypes = [i32, i32, i32, vp, vp, f32, vp, vp, vp, vp, vp, vp]
     L.svt_last_error.restype = ctypes.c_char_p
@@ -165,7 +161,9 @@ def lib():
     L.svt_bloom_sign.argtypes = [vp, i64, i32, i32, i32, vp, i32]
     L.svt_profile_enable.argtypes = [ctypes.c_int]
     L.svt_profile_read.argtypes = [vp, vp, i32, vp, vp]
-    sizes = ("svt_search_workspace_size", "svt_expert_sort_workspace_size", "svt_quant_pack_size")
+    sizes = ("svt_search_workspace_size", "svt_expert_sort_workspace_size", "svt_quant_pack_size",
+             "svt_embedding_backward_workspace_size", "svt_gated_linear_workspace_size",
+             "svt_gated_linear_backward_workspace_size", "svt_token_logprobs_workspace_size")
     for name in EXPORTED:
         if name in sizes:
             getattr(L, name).restype = sz

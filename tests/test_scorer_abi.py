@@ -56,6 +56,8 @@ def test_embedding_workspace_size(L):
         need = L.svt_embedding_backward_workspace_size(n, V, D)
         # keys and order twice, partial sums of at most one chunk of 8 tokens, histograms
         assert 8 * n < need <= 16 * n + (n // 8 + 1) * (8 * D + 4) + (1 << 20), (n, V, D, need)
+        assert svt.svt_embedding_backward_workspace_size(n, V, D) == need
+    assert svt.svt_embedding_backward_workspace_size(1 << 30, 1 << 30, 64) > 1 << 33
     for bad in ((-1, 10, 8), (1, 0, 8), (1, 10, 0)):
         assert L.svt_embedding_backward_workspace_size(*bad) == 0 and svt.svt_last_error()
         with pytest.raises(svt.SvtError):
@@ -155,6 +157,10 @@ def test_gated_workspace_size(L):
         for bad in ((-1, 8, 8, 1, 0, 0, 1), (1, 0, 8, 1, 0, 0, 1), (1, 8, 8, 2, 0, 0, 1), (1, 8, 8, 513, 0, 1, 1),
                     (1, 8, 8, 1, 5, 0, 1)):
             assert f(*bad) == 0 and svt.svt_last_error()
+    n = 2 ** 31 - 1   # dg and du with rows of 16 bytes, copies of x and both weights
+    assert grad(n, 1, 1, 1, svt.SVT_F16, 0, 1) >= 2 * n * 16 + (n + 2) * 16
+    assert svt.svt_gated_linear_workspace_size(n, 1, 1, 1, svt.SVT_F16, False, True) == (n + 2) * 16
+    assert svt.svt_gated_linear_backward_workspace_size(n, 1, 1, 1, svt.SVT_F16, False, True) == grad(n, 1, 1, 1, svt.SVT_F16, 0, 1)
     with pytest.raises(svt.SvtError):
         svt.svt_gated_linear_workspace_size(1, 0, 8, 1, 0, False, True)
     with pytest.raises(svt.SvtError):
