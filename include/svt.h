@@ -559,7 +559,7 @@ int svt_token_logprobs(int32_t n_tokens, int32_t vocab, int32_t top, int32_t dty
 /*
  * svt_token_logprobs_backward - the gradient in the logits of svt_token_logprobs's log probabilities and entropy:
  *   d_logits[i] = scale * (d_logprob * ([i is the token] - p_i) - d_entropy * p_i * (log p_i + entropy)),
- *   0 at shut tokens; d_logprob counts as 0 where no token is given.
+ *   0 at shut tokens; d_logprob counts as 0 where no token is given, and p as 0 below 2^-126.
  *   logits, tokens, scale   as given to svt_token_logprobs; norms, entropy: its outputs
  *   d_logprobs              [n_tokens] float;  d_entropy: [n_tokens] float, or NULL (zeros)
  *   d_logits                [n_tokens][vocab] of dtype

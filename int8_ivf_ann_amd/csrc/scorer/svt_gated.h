@@ -43,10 +43,22 @@ constexpr int32_t kGatedMax = 1 << 20;   // inputs, outputs
 
 constexpr float kGateLog2e = 1.44269504088896341f;
 
+// 2^x, x <= 0.  The instruction gives 0 below 2^-126, which a factor of 100 would bring back up: its argument is moved.
+__device__ __forceinline__ float exp2_below(float x) {
+  const bool low = x < -126.f;
+  return __builtin_amdgcn_exp2f(low ? x + 64.f : x) * (low ? 0x1p-64f : 1.f);
+}
+
+// 1 / (1 + e^-v), by e^-|v|, which neither overflows nor leaves a reciprocal below 2^-126
+__device__ __forceinline__ float logistic(float v) {
+  const float t = exp2_below(-kGateLog2e * fabsf(v)), r = __builtin_amdgcn_rcpf(1.f + t);
+  return v >= 0.f ? r : t * r;
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_value(float v) {
   if constexpr (ACT == SVT_ACT_RELU) return v < 0.f ? 0.f : v;   // NaN stays NaN
-  else if constexpr (ACT == SVT_ACT_SILU) return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kGateLog2e * v));
+  else if constexpr (ACT == SVT_ACT_SILU) return v * logistic(v);
   else if constexpr (ACT == SVT_ACT_GELU) return 0.5f * v * erfcf(-0.70710678118654752f * v);
   else return v;
 }
@@ -58,13 +70,13 @@ __device__ __forceinline__ void act_both(float v, float &value, float &slope) {
     value = v < 0.f ? 0.f : v;
     slope = v > 0.f ? 1.f : 0.f;
   } else if constexpr (ACT == SVT_ACT_SILU) {
-    const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kGateLog2e * v));
+    const float s = logistic(v);
     value = v * s;
     slope = fmaf(value, 1.f - s, s);
   } else if constexpr (ACT == SVT_ACT_GELU) {
     const float c = 0.5f * erfcf(-0.70710678118654752f * v);
     value = v * c;
-    slope = fmaf(v * 0.39894228040143268f, __builtin_amdgcn_exp2f(-0.5f * kGateLog2e * v * v), c);
+    slope = fmaf(v * 0.39894228040143268f, exp2_below(-0.5f * kGateLog2e * v * v), c);
   } else {
     value = v;
     slope = 1.f;

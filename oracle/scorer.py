@@ -79,7 +79,7 @@ class Row:
         return self.scale * g
 
 
-_erf = np.vectorize(math.erf)
+_erfc = np.vectorize(math.erfc, otypes=[np.float64])
 
 
 def activation(v, act):
@@ -91,7 +91,7 @@ def activation(v, act):
     if act == "silu":
         s = np.where(v >= 0, 1.0 / (1.0 + np.exp(-np.abs(v))), np.exp(-np.abs(v)) / (1.0 + np.exp(-np.abs(v))))
         return v * s, s * (1.0 + v * (1.0 - s))
-    cdf = 0.5 * (1.0 + _erf(v / math.sqrt(2.0))) if v.size else v
+    cdf = 0.5 * _erfc(-v / math.sqrt(2.0))   # 1 + erf would lose the far end
     return v * cdf, cdf + v * np.exp(-0.5 * v * v) / math.sqrt(2.0 * math.pi)
 
 
