@@ -422,8 +422,9 @@ struct GatedArgs {
   char *padded;               // their copies with such rows, where they are not so: x, then w_gate, then w_up
   int32_t splits;             // dx: parts of the reduced index
   int64_t per;                // dW: rows of a matrix that are reduced at once
-  int32_t dx_first;
-  int64_t dx_blocks, dw_blocks;   // workgroups of each, dx's with its parts
+  int64_t dx_blocks;          // workgroups: dx's, with its parts
+  int64_t dw_early, dw_late;  // dW's, before and behind them; where both are there, blocks of more than dw_long rows come early
+  int64_t dw_long;
   int64_t dw_partial;         // where dW's parts begin in `partial`, behind dx's
   int64_t dw_slots;           // for so many parts there is room: more are not written, offsets that fall would give some
   float *partial;
@@ -788,7 +789,7 @@ __device__ __forceinline__ void dx_tile(const GatedArgs &a, char *lds, int64_t b
 // dWg and dWu: side P: columns of x (across), side Q: columns of dg or du (across); the rows are reduced, a.per of a matrix
 // at a time: the products of a matrix with more rows than that are parts, which k_gated_join adds
 template <class T, class C>
-__device__ __forceinline__ void dw_tile(const GatedArgs &a, char *lds, int64_t b) {
+__device__ __forceinline__ void dw_tile(const GatedArgs &a, char *lds, int64_t b, bool early) {
   using Pr = Product<T, C, true, true, false>;
   const int tiles = (a.outs + C::q - 1) / C::q;
   const int64_t own = eighths((int64_t)2 * tiles * a.columns), block = b / own;   // a block's tiles use all L2s
@@ -798,6 +799,7 @@ __device__ __forceinline__ void dw_tile(const GatedArgs &a, char *lds, int64_t b
   int64_t part = -1;
   const Rows rows = rows_of_unit(a.offsets, a.n_matrices, a.n_rows, block, a.per, 1, &part);
   if (rows.matrix < 0 || part >= a.dw_slots) return;
+  if (a.dw_early && a.dw_late && (rows.end - rows.first > a.dw_long) != early) return;
   const bool up = in >= tiles;
   const int n0 = (int)(up ? in - tiles : in) * C::q, k0 = column * C::p;
   const int64_t len = rows.end - rows.first, pitch = a.in_pitch;
@@ -822,21 +824,20 @@ __device__ __forceinline__ void dw_tile(const GatedArgs &a, char *lds, int64_t b
                    part < 0 ? nullptr : a.partial + a.dw_partial + (part * 2 + up) * size);
 }
 
-// dx and dW are tiles of one grid, so that the last of the one leave no compute unit idle beside the other: 16384 rows over 8
-// experts, most of them one's, 1024 inputs, 2048 outputs: 427 us in two launches, 402 in one; 1001 x 250 x 999 float32 51 and 42.  Whichever reduces more at once comes first.
+// dx and dW are tiles of one grid, so that the last of the one leave no compute unit idle beside the other: 1001 x 250 x 999
+// float32 51 us in two launches, 42 in one.  Tiles that reduce more come first: rows of few experts make dW's tiles the longest
+// of all, those of many the shortest (16384 rows over 8 uneven experts, 1024 inputs, 2048 outputs: 427 in two launches; in one
+// with dW first 388, dx first 403, with dW's long blocks before dx and the short ones behind 364; even experts 318, 322, 325).
 template <class T, class C>
 __global__ __launch_bounds__(C::threads) void k_gated_gradients(GatedArgs a) {
   __shared__ __attribute__((aligned(1024))) char lds[larger(Product<T, C, true, false, false>::lds_bytes,
                                                             larger(Staged<C, T, C::p>::bytes, Staged<C, float, C::p>::bytes))];
-  int64_t b = blockIdx.x;
-  const int64_t first = a.dx_first ? a.dx_blocks : a.dw_blocks;
-  const bool later = b >= first;
-  if (later) b -= first;
-  if (later != (a.dx_first != 0)) {
+  const int64_t b = (int64_t)blockIdx.x - a.dw_early;
+  if (b >= 0 && b < a.dx_blocks) {
     const int64_t own = a.dx_blocks / a.splits;
     dx_tile<T, C>(a, lds, b % own, (int)(b / own));
   } else {
-    dw_tile<T, C>(a, lds, b);
+    dw_tile<T, C>(a, lds, b < 0 ? b + a.dw_early : b - a.dx_blocks, b < 0);
   }
 }
 
@@ -865,8 +866,8 @@ __device__ __forceinline__ void join_four(const float *from, int parts, int64_t 
   store_four(to, sum.v, (int)(left < 4 ? left : 4));
 }
 
-// The parts' sums.  blockIdx.y: dx (0; rows that no matrix names keep their values), then each matrix's dWg and dWu, where
-// its rows were cut into blocks.
+// The parts' sums.  blockIdx.y: dx (0; rows that no matrix names keep their values), then dWg and dWu of the matrices whose
+// rows were cut into blocks, one after the other.
 template <class T>
 __global__ __launch_bounds__(256) void k_gated_join(GatedArgs a) {
   const int64_t at = (blockIdx.x * 256ll + threadIdx.x) * 4, hop = gridDim.x * 1024ll;
@@ -880,15 +881,27 @@ __global__ __launch_bounds__(256) void k_gated_join(GatedArgs a) {
   }
   if (!a.dw_gate) return;
   int64_t before = 0;   // parts of the matrices before it
-  const int matrix = blockIdx.y - 1;
-  for (int e0 = 0; a.offsets && e0 < matrix; e0 += 64) {
+  int skip = blockIdx.y - 1, matrix = -1, parts = 0;
+  for (int e0 = 0; e0 < a.n_matrices && matrix < 0; e0 += 64) {
     Rows r;
-    const int blocks = blocks_of(a.offsets, matrix, a.n_rows, e0, a.per, 1, r);
-    before += __builtin_amdgcn_readlane(incl_sums(blocks > 1 ? blocks : 0), 63);
+    int blocks = 0;
+    if (a.offsets) blocks = blocks_of(a.offsets, a.n_matrices, a.n_rows, e0, a.per, 1, r);
+    else if (lane_id() == 0) blocks = (int)((a.n_rows + a.per - 1) / a.per);
+    const int several = blocks > 1 ? blocks : 0, upto = incl_sums(several);
+    uint64_t cut = __ballot(several > 0);
+    const int here = __builtin_popcountll(cut);
+    if (skip < here) {
+      for (; skip > 0; --skip) cut &= cut - 1;
+      const int l = __builtin_ctzll(cut);
+      matrix = e0 + l;
+      parts = __builtin_amdgcn_readlane(several, l);
+      before += __builtin_amdgcn_readlane(upto, l) - parts;
+    } else {
+      skip -= here;
+      before += __builtin_amdgcn_readlane(upto, 63);
+    }
   }
-  const Rows rows = rows_of_matrix(a.offsets, a.n_rows, matrix);
-  const int parts = (int)((rows.end - rows.first + a.per - 1) / a.per);
-  if (parts < 2 || before + parts > a.dw_slots) return;
+  if (matrix < 0 || before + parts > a.dw_slots) return;
   const int64_t size = (int64_t)a.outs * a.ins;
   for (int64_t i = at; i < 2 * size; i += hop) {
     const int64_t gate = size - i;   // four values may lie in both halves
@@ -915,9 +928,9 @@ struct GatedPlan {
 
 // The cuts, and microseconds of a step of 128 bytes: with one workgroup on a compute unit, and for each further one that
 // shares it (the 256 x 256 cut has none beside it: they follow each other).  Measured with products of two-byte and of
-// float32 values, 200 x 512 x 2048 to 16384 x 1024 x 2048.  The choices by it, gradients in us with this cut and the best:
-// bfloat16 4096 x 4096 x 4096 508 (508), 4096 x 1024 x 2048 91 (91), 1024 x 1024 x 1024 33 (30), 300 x 300 x 300 11.2 (11.2);
-// float32 1001 x 250 x 999 42 (41), 4096 x 1024 x 2048 623 (572).
+// float32 values, 200 x 512 x 2048 to 16384 x 1024 x 2048.  Its choices are within 10 % of the best cut's time there; gradients
+// in us: bfloat16 4096 x 4096 x 4096 487, 4096 x 1024 x 2048 88, 1024 x 1024 x 1024 30, 300 x 300 x 300 10.9; float32
+// 1001 x 250 x 999 41, 4096 x 1024 x 2048 581.
 struct CutCost { int q, p; float alone[2], shared[2]; };
 constexpr int kCuts = 4;
 constexpr CutCost kCutCost[kCuts] = {{32, 64, {0.28f, 0.46f}, {0.15f, 0.29f}},
@@ -955,9 +968,11 @@ inline GatedPlan plan_forward(const GatedArgs &a, int elem) {
 
 // The cut, dx's parts and dW's blocks of rows with the least time for both, whichever of them are wanted: what the compute
 // units have to do, but at least what the longest tile takes, and for parts 4 us and 2.4 for each million partial values that
-// are written and read again.  Only products of fewer tiles than compute units are cut into parts: by expert, 8 times 512
-// tiles, no uneven load made parts pay (one expert with 13018 of 16384 rows: 159 us whole, 150 in two, 198 in four parts; even
-// experts: 127, 137, 139).
+// are written and read again.  Only products of fewer tiles than compute units are cut into parts.  By expert one matrix may
+// have all rows, which only the GPU knows: dW's blocks are as long as what each compute unit has to do, so that no tile
+// outlasts the others (16384 rows, 8 uneven experts, 1024 inputs, 2048 outputs: whole 358 us, at most 8192 rows 346, 4096 366;
+// 32 experts, 1024 x 1024: 252, 255, 244; 8192 rows, 8 experts, 2048 x 2048: 338 whole, at most 4096 rows 367).  A tile costs
+// two steps beside its own (100 rows, 16 experts, 1024 x 1024, which small tiles without that count would take: 57 us and 51).
 inline GatedPlan plan_backward(const GatedArgs &a, int elem) {
   GatedPlan best{};
   double least = 0;
@@ -972,15 +987,14 @@ inline GatedPlan plan_backward(const GatedArgs &a, int elem) {
     for (int splits = 1; splits <= 32 && (splits == 1 || (dx_tiles < 256 && dx_steps >= 2 * splits)); splits *= 2)
       for (int parts = 1; parts <= 32 && (parts == 1 || (dw_tiles < 256 && dw_steps >= 2 * parts)); parts *= 2) {
         const int64_t blocks = (dw_steps + parts - 1) / parts;
-        // by expert, half the rows may be one expert's
-        const double longest = (double)larger((int)((dx_steps + splits - 1) / splits),
-                                              (int)(a.offsets && parts == 1 ? (dw_steps + 1) / 2 : blocks));
+        if (a.offsets && (double)blocks > load && parts < 32 && dw_tiles < 256 && dw_steps >= 4 * parts) continue;
+        const double longest = (double)larger((int)((dx_steps + splits - 1) / splits), (int)blocks);
         const double alone = longest * c.alone[type], shared = load * c.shared[type] + 0.3 * alone;
         double time = alone > shared ? alone : shared;
         if (splits > 1 || parts > 1) time += 4;
         if (splits > 1) time += 2.4e-6 * splits * (double)a.n_rows * a.ins;
-        if (parts > 1) time += 2.4e-6 * parts * 2.0 * a.outs * a.ins;
-        if ((cut == 0 && splits == 1 && parts == 1) || time < least) {
+        if (parts > 1) time += (a.offsets ? 3.6e-6 : 2.4e-6) * parts * 2.0 * a.outs * a.ins;
+        if (best.columns == 0 || time < least) {
           least = time;
           const int64_t per = blocks > 0 ? blocks * step : 1;
           best = {cut, units, columns, splits, per, a.offsets ? a.n_rows / per + experts : (a.n_rows + per - 1) / per};
@@ -1095,19 +1109,23 @@ int gated_backward(const char *who, GatedArgs a, const GatedPlan &p, void *strea
   a.per = p.per;
   a.dw_slots = dw_slots(a, p);
   a.dx_blocks = a.dx ? dx_blocks(p) : 0;
-  a.dw_blocks = a.dw_gate ? dw_blocks(p, a.outs) : 0;
-  a.dx_first = 2 * (int64_t)a.outs / p.splits > p.per;
-  if (a.dx_blocks + a.dw_blocks == 0) return SVT_OK;
+  a.dw_long = 2 * (int64_t)a.outs / p.splits;
+  a.dw_early = a.dw_gate && p.per > a.dw_long ? dw_blocks(p, a.outs) : 0;
+  a.dw_late = a.dw_gate && (a.dw_early == 0 || (a.dx && a.offsets)) ? dw_blocks(p, a.outs) : 0;
+  const int64_t tiles = a.dw_early + a.dx_blocks + a.dw_late;
+  if (tiles == 0) return SVT_OK;
   rc = with_cut(p.cut, [&](auto cut) {
     using C = decltype(cut);
-    return launch(who, k_gated_gradients<T, C>, (unsigned)(a.dx_blocks + a.dw_blocks), C::threads, 0, stream, a);
+    return launch(who, k_gated_gradients<T, C>, (unsigned)tiles, C::threads, 0, stream, a);
   });
   const bool dx_parted = a.dx && dx_parts(a, p) > 0, dw_parted = a.dw_gate && dw_parts(a, p) > 0;
   if (rc != SVT_OK || (!dx_parted && !dw_parted)) return rc;
   const int64_t dx_values = dx_parted ? a.n_rows * a.ins : 0, dw_values = dw_parted ? (int64_t)2 * a.outs * a.ins : 0;
   const int64_t blocks = ((dx_values > dw_values ? dx_values : dw_values) + 1023) / 1024;
-  return launch(who, k_gated_join<T>, dim3((unsigned)(blocks < 2048 ? blocks : 2048), dw_parted ? 1 + a.n_matrices : 1), 256, 0,
-                stream, a);
+  int64_t cut = dw_parted ? a.n_rows / (p.per + 1) : 0;   // matrices with more rows than a block
+  if (dw_parted && (cut < 1 || !a.offsets)) cut = 1;
+  if (cut > a.n_matrices) cut = a.n_matrices;
+  return launch(who, k_gated_join<T>, dim3((unsigned)(blocks < 2048 ? blocks : 2048), (unsigned)(1 + cut)), 256, 0, stream, a);
 }
 
 #endif   // SVT_GATED_INSTANTIATE

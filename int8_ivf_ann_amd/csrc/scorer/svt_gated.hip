@@ -171,7 +171,7 @@ extern "C" int svt_gated_linear_backward(int32_t n_rows, int32_t n_in, int32_t n
   const Span outs[4] = {{dx, nx}, {dw_gate, nw}, {dw_up, nw}, {workspace, need}};
   if (any_overlap(ins, 7, outs, 4))
     return report(SVT_EINVAL, "%s: an output or the workspace overlaps an input or another output", who);
-  if (!fits(dx_blocks(plan) + dw_blocks(plan, n_out)))
+  if (!fits(dx_blocks(plan) + 2 * dw_blocks(plan, n_out)))
     return report(SVT_EINVAL, "%s: too large a product for one call", who);
   a.d_both = (char *)workspace;
   if (copies) {

@@ -112,6 +112,17 @@ def test_falling_offsets_stay_in_bounds(svt):
             assert (t[n:] == 7.0).all()
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("how", ["uneven", "one", "even"])
+@pytest.mark.parametrize("R, K, N, M", [(9000, 40, 24, 70), (20000, 24, 20, 3), (6000, 100, 33, 130)])
+def test_long_experts_are_cut(svt, R, K, N, M, how, kind):
+    """Few and many experts of thousands of rows, whose weights' gradients are sums of blocks."""
+    say("cut", R, K, N, M, how, kind)
+    need = svt.svt_gated_linear_backward_workspace_size(R, K, N, M, svt.SVT_F32, True, True)
+    assert need > 2 * R * ((4 * N + 15) // 16 * 16)   # there are parts
+    check(svt, R, K, N, M, "silu", kind, 0, how)
+
+
 @pytest.mark.parametrize("kind, least", [("bf16", -133), ("f16", -24), ("f32", -133)])
 @pytest.mark.parametrize("R", [1, 40, 300])
 def test_gated_subnormal_values(svt, R, kind, least):
