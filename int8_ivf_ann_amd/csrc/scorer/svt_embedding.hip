@@ -12,7 +12,7 @@
 //
 // Measured: rows for 65536 tokens of 1024 bfloat16 36 us (176 MB, 4.9 TB/s), for 2048 of 128 float16 2.9.  The gradient in
 // 131072 rows of the former 119: the sort 25 (a chain of four launches), sums and zeros 80 (403 MB, 5 TB/s), the join 9; of
-// 3001 tokens of 250 float32 in 5003 rows 23: 8, 8 and 6, chains of dependent loads all three.
+// 3001 tokens of 250 float32 in 5003 rows 20.6: 8, 6 and 6, chains of dependent loads all three.
 
 #include <type_traits>
 
@@ -322,8 +322,10 @@ struct SumArgs {
   const uint32_t *keys;        // sorted
   const int32_t *order;
   float *partial;              // [chunk][2][width]: the run that came in, the run that goes on
-  int32_t *crossing;           // [0]: their number; then the chunks whose last run starts there and goes on
+  int32_t *crossing;           // [0]: their number; from [2] on, pairs: a chunk whose last run starts there and goes on, its key
 };
+
+struct Pair { int32_t chunk; uint32_t run; };
 
 // First place in [0, n) whose key is at least v, n if there is none; the whole wave asks.  64 places are looked at a time: 3
 // loads one after the other for 65536 tokens, where halving takes 16.
@@ -407,7 +409,8 @@ __global__ __launch_bounds__(kThreads) void k_sum_rows(SumArgs a, const Vec<T, M
         if (one) to[c1 * M + i] = s1[i];
         if (two) to[c2 * M + i] = s2[i];
       }
-      if (whole && block == 0 && in == 0) a.crossing[1 + atomicAdd(a.crossing, 1)] = (int32_t)chunk;
+      if (whole && block == 0 && in == 0)
+        reinterpret_cast<Pair *>(a.crossing)[1 + atomicAdd(a.crossing, 1)] = Pair{(int32_t)chunk, run};
     }
   };
   // the places after the next J are looked up while the next J's rows are on their way
@@ -454,37 +457,42 @@ __global__ __launch_bounds__(kThreads) void k_sum_rows(SumArgs a, const Vec<T, M
 
 // Sums of the runs that cross chunks, 256 columns of one at a time.  Most cross once or twice: a wave each.  Those of more
 // than kJoinAlone chunks are put off until the workgroup's waves share them, each a contiguous part, added in order.
-// (200000 tokens of 300 rows, chunks of 8: 117 us with four waves to every run, 47 like this.)
+// (200000 tokens of 300 rows, chunks of 8: 117 us with four waves to every run, 47 like this.)  What a run needs is asked for
+// together: the number of runs with its chunk and key, its length with its first two parts (3001 x 250 float32, the whole
+// gradient 23.3 us one after the other, 20.6 like this).
 constexpr int kJoinColumns = 256, kJoinThreads = 1024, kJoinWaves = kJoinThreads / 64, kJoinAlone = 16;
 
 struct __attribute__((packed, aligned(4))) FourSums { float v[4]; };
 
-// parts i0 .. i1 - 1 of a run that begins in a chunk (row 1 of the first, row 0 of the others), `left` columns from `from` on
-__device__ __forceinline__ FourSums add_parts(const float *from, int64_t i0, int64_t i1, int64_t width, int left) {
-  FourSums sum{};
-  if (left >= 4) {
-    int64_t i = i0;
+// part i of a run that begins in a chunk (row 1 of the first, row 0 of the others), `left` columns from `from` on
+__device__ __forceinline__ FourSums part(const float *from, int64_t i, int64_t width, int left) {
+  const float *at = from + (i ? 2 * i : 1) * width;
+  if (left >= 4) return *reinterpret_cast<const FourSums *>(at);
+  FourSums v{};
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (k < left) v.v[k] = at[k];
+  return v;
+}
+
+// parts i0 .. i1 - 1 are added to `sum`, in order
+__device__ __forceinline__ void add_parts(FourSums &sum, const float *from, int64_t i0, int64_t i1, int64_t width, int left) {
+  int64_t i = i0;
+  if (left >= 4)
     for (; i + 8 <= i1; i += 8) {
       FourSums v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = *reinterpret_cast<const FourSums *>(from + (i + j ? 2 * (i + j) : 1) * width);
+      for (int j = 0; j < 8; ++j) v[j] = part(from, i + j, width, left);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
 #pragma unroll
         for (int k = 0; k < 4; ++k) sum.v[k] += v[j].v[k];
     }
-    for (; i < i1; ++i) {
-      const FourSums v = *reinterpret_cast<const FourSums *>(from + (i ? 2 * i : 1) * width);
+  for (; i < i1; ++i) {
+    const FourSums v = part(from, i, width, left);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) sum.v[k] += v.v[k];
-    }
-  } else {
-    for (int64_t i = i0; i < i1; ++i)
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (k < left) sum.v[k] += from[(i ? 2 * i : 1) * width + k];
+    for (int k = 0; k < 4; ++k) sum.v[k] += v.v[k];
   }
-  return sum;
 }
 
 template <class TD, bool ADD>
@@ -493,11 +501,11 @@ __global__ __launch_bounds__(kJoinThreads) void k_join_runs(SumArgs a, TD *table
   __shared__ int64_t put_off[kJoinWaves], length[kJoinWaves];
   const int columns = (a.width + kJoinColumns - 1) / kJoinColumns, wave = threadIdx.x / 64;
   const int64_t units = (int64_t)a.crossing[0] * columns;
-  auto place = [&](int64_t u, int64_t &chunk, int &col, uint32_t &run) {
-    chunk = a.crossing[1 + u / columns];
-    col = (int)(u % columns) * kJoinColumns + lane_id() * 4;
-    run = a.keys[(chunk + 1) * a.per - 1];
+  auto pair_of = [&](int64_t u) {
+    return reinterpret_cast<const Pair *>(a.crossing)[1 + (u / columns < a.chunks ? u / columns : 0)];
   };
+  auto column_of = [&](int64_t u) { return (int)(u % columns) * kJoinColumns + lane_id() * 4; };
+  Pair mine = pair_of(blockIdx.x + (int64_t)wave * gridDim.x);   // beside the number of runs, so perhaps behind the last of them
   auto put = [&](const FourSums &sum, int col, uint32_t run) {
     TD *at = table + (int64_t)run * a.width + col;
 #pragma unroll
@@ -509,15 +517,24 @@ __global__ __launch_bounds__(kJoinThreads) void k_join_runs(SumArgs a, TD *table
     const int64_t u = u0 + (int64_t)wave * gridDim.x;
     int64_t n = 0;   // chunks that the run lies in: where it begins, and those that begin with it
     if (u < units) {
-      int64_t chunk;
-      int col;
-      uint32_t run;
-      place(u, chunk, col, run);
+      const int64_t chunk = mine.chunk;
+      const uint32_t run = mine.run;
+      const int col = column_of(u);
+      const float *from = a.partial + chunk * 2 * a.width + col;
+      const int left = a.width - col;
       const int64_t c = chunk + 1 + lane_id();
-      const uint64_t goes_on = __ballot(c < a.chunks && a.keys[(c < a.chunks ? c : chunk) * a.per] == run);
+      const uint32_t key = a.keys[(c < a.chunks ? c : chunk) * a.per];
+      // two there are in any case: on their way while the run's length is found
+      FourSums sum = part(from, 0, a.width, left);
+      const FourSums next = part(from, 1, a.width, left);
+      const uint64_t goes_on = __ballot(c < a.chunks && key == run);
       n = ~goes_on ? 1 + __builtin_ctzll(~goes_on) : (first_place(a.keys, a.n, (uint64_t)run + 1) - 1) / a.per - chunk + 1;
-      if (n <= kJoinAlone)
-        put(add_parts(a.partial + chunk * 2 * a.width + col, 0, n, a.width, a.width - col), col, run);
+      if (n <= kJoinAlone) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum.v[k] += next.v[k];
+        add_parts(sum, from, 2, n, a.width, left);
+        put(sum, col, run);
+      }
     }
     if (lane_id() == 0) {
       put_off[wave] = n > kJoinAlone ? u : -1;
@@ -526,13 +543,12 @@ __global__ __launch_bounds__(kJoinThreads) void k_join_runs(SumArgs a, TD *table
     __syncthreads();
     for (int w = 0; w < kJoinWaves; ++w) {
       if (put_off[w] < 0) continue;   // the same for all
-      int64_t chunk;
-      int col;
-      uint32_t run;
-      place(put_off[w], chunk, col, run);
+      const Pair p = pair_of(put_off[w]);
+      const int col = column_of(put_off[w]);
       const int64_t each = (length[w] + kJoinWaves - 1) / kJoinWaves, i0 = wave * each;
       const int64_t i1 = i0 + each < length[w] ? i0 + each : length[w];
-      FourSums sum = add_parts(a.partial + chunk * 2 * a.width + col, i0, i1, a.width, a.width - col);
+      FourSums sum{};
+      add_parts(sum, a.partial + (int64_t)p.chunk * 2 * a.width + col, i0, i1, a.width, a.width - col);
       parts[wave][lane_id()] = sum;
       __syncthreads();
       if (wave == 0) {
@@ -540,10 +556,11 @@ __global__ __launch_bounds__(kJoinThreads) void k_join_runs(SumArgs a, TD *table
         for (int j = 1; j < kJoinWaves; ++j)
 #pragma unroll
           for (int k = 0; k < 4; ++k) sum.v[k] += parts[j][lane_id()].v[k];
-        put(sum, col, run);
+        put(sum, col, p.run);
       }
       __syncthreads();
     }
+    mine = pair_of(u + (int64_t)gridDim.x * kJoinWaves);
     __syncthreads();   // put_off has been read
   }
 }
@@ -616,7 +633,7 @@ Space space(int64_t n, int64_t n_rows, int32_t width) {
     const int32_t per = chunk_places(n, width);
     const size_t chunks = (size_t)((n + per - 1) / per);
     s.partial = take(chunks * 2 * (size_t)width * 4);
-    s.crossing = take((chunks + 1) * 4);
+    s.crossing = take((chunks + 1) * sizeof(Pair));
   }
   s.bytes = at;
   return s;
