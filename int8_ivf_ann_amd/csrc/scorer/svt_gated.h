@@ -49,10 +49,11 @@ __device__ __forceinline__ float exp2_below(float x) {
   return __builtin_amdgcn_exp2f(low ? x + 64.f : x) * (low ? 0x1p-64f : 1.f);
 }
 
-// 1 / (1 + e^-v), by e^-|v|, which neither overflows nor leaves a reciprocal below 2^-126
+// 1 / (1 + e^-v), with e^-v as a square: neither it nor the reciprocal's result leaves the normal range where v times the whole
+// is above 2^-126 (8192 x 2048 x 8192 bfloat16: e^-v itself, unscaled, 564 us, e^-|v| with its two cases 577, this 569)
 __device__ __forceinline__ float logistic(float v) {
-  const float t = exp2_below(-kGateLog2e * fabsf(v)), r = __builtin_amdgcn_rcpf(1.f + t);
-  return v >= 0.f ? r : t * r;
+  const float h = __builtin_amdgcn_exp2f(-0.5f * kGateLog2e * v);
+  return __builtin_amdgcn_rcpf(fmaf(h * 0x1p-32f, h, 0x1p-32f)) * 0x1p-32f;
 }
 
 template <int ACT>
