@@ -279,6 +279,55 @@ def test_gated_offsets_past_32_bits(svt):
         assert not dwg[:510].any() and not dwu[:510].any()
 
 
+# ---- the largest sizes of one dimension ----------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_logprobs_of_the_longest_row(svt, kind):
+    """2^30 tokens, equal but for three: log Z is known, and every token's gradient is one of four numbers.  A thread adds
+    the 8 of a piece (8 u), then at most n = 2^30 / 8 / (256 threads) pieces' sums one after the other, each off by u of the sum
+    so far: n u / 2 in all; then joins (16 u)."""
+    import torch
+    say("longest", kind)
+    V = 1 << 30
+    l = torch.zeros((1, V), dtype=ty(kind), device="cuda")
+    places = [3, V // 2 + 1, V - 1]
+    l[0, places] = torch.tensor([21.0, 20.0, 22.0], device="cuda").to(ty(kind))
+    tokens = torch.tensor([V - 1], device="cuda")
+    lp, H, nm, ids, tlp = svt.svt_token_logprobs(l, tokens, top=4)
+    z = V - 3 + np.exp(21.0) + np.exp(20.0) + np.exp(22.0)
+    p = np.exp([21.0, 20.0, 22.0, 0.0]) / z
+    ent = -np.sum(p[:3] * np.log(p[:3])) - (V - 3) * p[3] * np.log(p[3])
+    assert host(ids)[0].tolist() == [V - 1, 3, V // 2 + 1, 0]
+    bound = (2.0 ** 19 / 2 + 24 + 30) * U   # 30: the exponentials and the logarithm
+    near(host(lp)[0], np.log(p[2]), bound, "logp")
+    near(host(H)[0], ent, bound * (1 + 2 * 22), "entropy")
+    near(host(tlp)[0], np.log(p[[2, 0, 1, 3]]), bound, "alternatives")
+    d = svt.svt_token_logprobs_backward(l, tokens, nm, H, torch.ones(1, device="cuda"))
+    for i, w in ((3, -p[0]), (V // 2 + 1, -p[1]), (V - 1, 1 - p[2]), (0, -p[3]), (V - 2, -p[3])):
+        near(np.float64(d[0, i].item()), w, (bound + 64 * U) * abs(p).max() + HALF[kind] * abs(w) + TINY[kind], f"d {i}")
+
+
+@pytest.mark.parametrize("R, K, N", [(1, 1 << 20, 3), (70, 1 << 20, 3), (3, 5, 1 << 20), (70, 6, 1 << 20)])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_gated_longest_sides(svt, R, K, N, kind):
+    say("longest sides", R, K, N, kind)
+    check(svt, R, K, N, None, "silu", kind, 0, "even")
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16"])
+def test_embedding_of_the_widest_rows(svt, kind):
+    import torch
+    say("widest", kind)
+    D = 1 << 24
+    table = torch.randn((2, D), device="cuda").to(ty(kind))
+    ids = torch.tensor([1, 2, 0, 1], device="cuda")
+    out = svt.svt_embedding(table, ids)
+    for i, v in enumerate((1, None, 0, 1)):
+        assert torch.equal(out[i], table[v]) if v is not None else not out[i].any()
+    d = svt.svt_embedding_backward(out, ids, 2)
+    assert torch.equal(d[0], table[0]) and torch.equal(d[1], table[1] + table[1])
+
+
 # ---- captured, on other streams, at once --------------------------------------------------------------
 
 def every_call(svt, torch, kind, T, V, D, N, M):
