@@ -807,6 +807,8 @@ def svt_embedding_backward(d_out, ids, n_rows: int, scale: float = 1.0, out=None
         raise ValueError(f"ids: shape {tuple(ids.shape)} for d_out of shape {tuple(d_out.shape)}")
     if accumulate and out is None:
         raise ValueError("out: to be given where the gradient is added to it")
+    if out is not None and out_dtype is not None and out_dtype is not out.dtype:
+        raise ValueError(f"out: dtype {out.dtype}, expected {out_dtype}")
     out_dtype = out.dtype if out is not None else d_out.dtype if out_dtype is None else out_dtype
     if out_dtype is not d_out.dtype and out_dtype is not torch.float32:
         raise ValueError(f"out: dtype {out_dtype} is neither {d_out.dtype} nor torch.float32")

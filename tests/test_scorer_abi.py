@@ -223,6 +223,7 @@ def test_shapes_and_types_are_checked():
         (lambda: svt.svt_embedding_backward(Stand(bf16, 4, 8), Stand(i64, 5), 10), "ids"),
         (lambda: svt.svt_embedding_backward(Stand(bf16, 4, 8), Stand(i64, 4), 10, accumulate=True), "out"),
         (lambda: svt.svt_embedding_backward(Stand(bf16, 4, 8), Stand(i64, 4), 10, out_dtype=torch.float16), "out"),
+        (lambda: svt.svt_embedding_backward(Stand(bf16, 4, 8), Stand(i64, 4), 10, out=Stand(bf16, 10, 8), out_dtype=f32), "out"),
         (lambda: svt.svt_embedding_backward(3.0, Stand(i64, 4), 10), "d_out"),
         (lambda: svt.svt_token_logprobs(Stand(bf16, 4, 8), Stand(i32, 4)), "tokens"),
         (lambda: svt.svt_token_logprobs(Stand(bf16, 4, 8), Stand(i64, 5)), "tokens"),
