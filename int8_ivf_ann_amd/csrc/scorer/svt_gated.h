@@ -166,7 +166,8 @@ struct Side {
 
   // A step's pieces to LDS, straight from memory.  The loads are written out, as the compiler
   // would have every later read of LDS wait for them; whoever reads waits by loads_done() and a barrier.  (They have no
-  // result in registers.)
+  // result in registers.)  The buffer's words may come from v_readfirstlane right before: a load reads such a register only
+  // five wait states later, which nothing but the asm itself counts (the move of m0 one, the s_nop four).
   __device__ __forceinline__ void load(Base from, uint32_t lds, bool final) const {
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)threadIdx.x / 64);
     auto buffer = [](const char *p, const char *end) {
@@ -183,9 +184,12 @@ struct Side {
 #pragma unroll
     for (int j = 0; j < pieces; ++j) {
       const uint32_t to = lds + (j * THREADS + wave * 64) * 16, at = out >> j & 1u ? kOutside : offset[j];
-      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(at),
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"   // m0 is reserved, but the compiler's own uses of it have to see the write
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(at),
                    "s"(HALVES && 2 * j >= pieces ? upper : lower)
-                   : "memory");
+                   : "memory", "m0");
+#pragma clang diagnostic pop
     }
   }
 
