@@ -504,7 +504,8 @@ int svt_embedding_backward(int64_t n_tokens, int64_t n_rows, int32_t width, int3
  *                16-byte aligned; NULL where that is 0.  aligned: 1 if x, w_gate and w_up are 4-byte aligned; where they
  *                are not, or n_in elements are no multiple of 4 bytes, the call copies them first (but for few rows)
  * Sums are float32; h, gate and up are rounded once each (h from the unrounded sums).
- * n_rows == 0 returns SVT_OK without enqueuing.  Errors: SVT_EINVAL, SVT_EDEVICE as svt_route.
+ * n_rows == 0 returns SVT_OK without enqueuing.  Errors: SVT_EINVAL (also, here, by the size calls and for the gradients, for
+ * products of 2^32 or more tiles, whose arrays lie beyond any memory), SVT_EDEVICE as svt_route.
  */
 size_t svt_gated_linear_workspace_size(int32_t n_rows, int32_t n_in, int32_t n_out, int32_t n_matrices, int32_t dtype,
                                        int32_t by_expert, int32_t aligned);

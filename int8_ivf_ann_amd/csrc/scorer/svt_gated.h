@@ -396,6 +396,9 @@ __device__ __forceinline__ Rows rows_of_unit(const int32_t *offsets, int n_matri
   return {-1, 0, 0};
 }
 
+// the number of a workgroup: a grid's threads along x stay below 2^32, so that many workgroups take several rows of one
+__device__ __forceinline__ int64_t block_number() { return blockIdx.y * (int64_t)gridDim.x + blockIdx.x; }
+
 __host__ __device__ inline int64_t eighths(int64_t tiles) { return (tiles + 7) / 8 * 8; }
 
 // The tile of workgroup b: workgroups b, b + 8, .. share an L2, so each eighth takes neighbouring tiles; within them,
@@ -544,7 +547,7 @@ __global__ __launch_bounds__(C::threads) void k_gated(GatedArgs a) {
   int column;
   // the matrices' own blocks, not as many as there may be, are shared out over the L2s (dx_tile has the figures)
   const int64_t units = count_units(a.offsets, a.n_matrices, a.n_rows, C::q);
-  if (!tile_of(blockIdx.x, units, a.columns, unit, column)) return;
+  if (!tile_of(block_number(), units, a.columns, unit, column)) return;
   const Rows rows = rows_of_unit(a.offsets, a.n_matrices, a.n_rows, unit, C::q);
   if (rows.matrix < 0) return;
   const int n0 = column * outs;
@@ -837,7 +840,8 @@ template <class T, class C>
 __global__ __launch_bounds__(C::threads) void k_gated_gradients(GatedArgs a) {
   __shared__ __attribute__((aligned(1024))) char lds[larger(Product<T, C, true, false, false>::lds_bytes,
                                                             larger(Staged<C, T, C::p>::bytes, Staged<C, float, C::p>::bytes))];
-  const int64_t b = (int64_t)blockIdx.x - a.dw_early;
+  const int64_t b = block_number() - a.dw_early;
+  if (b >= a.dx_blocks + a.dw_late) return;   // the last row of a grid is not full
   if (b >= 0 && b < a.dx_blocks) {
     const int64_t own = a.dx_blocks / a.splits;
     dx_tile<T, C>(a, lds, b % own, (int)(b / own));
@@ -948,11 +952,6 @@ inline int64_t row_units(int64_t n_rows, int n_matrices, bool by_expert, int per
   return by_expert ? n_rows / per + (n_rows < n_matrices ? n_rows : n_matrices) : (n_rows + per - 1) / per;
 }
 
-// blocks of rows at most: every matrix may end inside one
-inline int64_t row_units(int64_t n_rows, int n_matrices, bool by_expert, int64_t per) {
-  return by_expert ? n_rows / per + (n_rows < n_matrices ? n_rows : n_matrices) : (n_rows + per - 1) / per;
-}
-
 // the cut with the least time by the table above
 inline GatedPlan plan_forward(const GatedArgs &a, int elem) {
   GatedPlan best{};
@@ -1010,15 +1009,26 @@ inline GatedPlan plan_backward(const GatedArgs &a, int elem) {
   return best;
 }
 
-// the workgroups of a plan's gradients
-inline int64_t dx_blocks(const GatedPlan &p) { return eighths(p.units * p.columns) * p.splits; }
-inline int64_t dw_blocks(const GatedPlan &p, int32_t outs) {
+// the workgroups of a plan's gradients: dW's before dx's, dx's, dW's behind
+struct GradientBlocks {
+  int64_t early, dx, late;
+  int64_t all() const { return early + dx + late; }
+};
+inline int64_t long_rows(const GatedPlan &p, int32_t outs) { return 2 * (int64_t)outs / p.splits; }
+inline GradientBlocks gradient_blocks(const GatedPlan &p, int32_t outs, bool dx, bool dw, bool by_expert) {
   const int q = kCutCost[p.cut].q;
-  return eighths((int64_t)2 * ((outs + q - 1) / q) * p.columns) * p.dw_units;
+  const int64_t n = dw ? eighths((int64_t)2 * ((outs + q - 1) / q) * p.columns) * p.dw_units : 0;
+  const int64_t early = p.per > long_rows(p, outs) ? n : 0;
+  return {early, dx ? eighths(p.units * p.columns) * p.splits : 0, early == 0 || (dx && by_expert) ? n : 0};
 }
 
-// a grid's threads stay below 2^32
-inline bool fits(int64_t blocks) { return blocks < (1 << 23); }
+// A launch's workgroups: rows of 2^22, so that threads along x stay below 2^32; at most 2^32, which arrays that fit the
+// memory stay far below
+constexpr int64_t kGridRow = 1 << 22;
+inline bool fits(int64_t blocks) { return blocks < int64_t(1) << 32; }
+inline dim3 grid_of(int64_t blocks) {
+  return blocks <= kGridRow ? dim3((unsigned)blocks) : dim3((unsigned)kGridRow, (unsigned)((blocks + kGridRow - 1) / kGridRow));
+}
 
 // Whether the forward pass takes the kernel for few rows: 1 or 2 blocks of 16, or 0.  Few: up to 32 (64 x 2048 x 2048 bfloat16
 // 14.3 us there, 10.9 with tiles; 32 x 2048 x 2048 10.1 and 10.7).  By expert up to 4 on average (32 experts of 1024 x 1024,
@@ -1095,7 +1105,7 @@ int gated_forward(const char *who, GatedArgs a, const GatedPlan &p, void *stream
   a.columns = p.columns;
   return with_cut(p.cut, [&](auto cut) {
     using C = decltype(cut);
-    return launch(who, k_gated<T, C>, (unsigned)eighths(a.units * a.columns), C::threads, 0, stream, a);
+    return launch(who, k_gated<T, C>, grid_of(eighths(a.units * a.columns)), C::threads, 0, stream, a);
   });
 }
 
@@ -1113,24 +1123,24 @@ int gated_backward(const char *who, GatedArgs a, const GatedPlan &p, void *strea
   a.splits = p.splits;
   a.per = p.per;
   a.dw_slots = dw_slots(a, p);
-  a.dx_blocks = a.dx ? dx_blocks(p) : 0;
-  a.dw_long = 2 * (int64_t)a.outs / p.splits;
-  a.dw_early = a.dw_gate && p.per > a.dw_long ? dw_blocks(p, a.outs) : 0;
-  a.dw_late = a.dw_gate && (a.dw_early == 0 || (a.dx && a.offsets)) ? dw_blocks(p, a.outs) : 0;
-  const int64_t tiles = a.dw_early + a.dx_blocks + a.dw_late;
-  if (tiles == 0) return SVT_OK;
+  const GradientBlocks blocks = gradient_blocks(p, a.outs, a.dx != nullptr, a.dw_gate != nullptr, a.offsets != nullptr);
+  a.dx_blocks = blocks.dx;
+  a.dw_long = long_rows(p, a.outs);
+  a.dw_early = blocks.early;
+  a.dw_late = blocks.late;
+  if (blocks.all() == 0) return SVT_OK;
   rc = with_cut(p.cut, [&](auto cut) {
     using C = decltype(cut);
-    return launch(who, k_gated_gradients<T, C>, (unsigned)tiles, C::threads, 0, stream, a);
+    return launch(who, k_gated_gradients<T, C>, grid_of(blocks.all()), C::threads, 0, stream, a);
   });
   const bool dx_parted = a.dx && dx_parts(a, p) > 0, dw_parted = a.dw_gate && dw_parts(a, p) > 0;
   if (rc != SVT_OK || (!dx_parted && !dw_parted)) return rc;
   const int64_t dx_values = dx_parted ? a.n_rows * a.ins : 0, dw_values = dw_parted ? (int64_t)2 * a.outs * a.ins : 0;
-  const int64_t blocks = ((dx_values > dw_values ? dx_values : dw_values) + 1023) / 1024;
+  const int64_t pieces = ((dx_values > dw_values ? dx_values : dw_values) + 1023) / 1024;
   int64_t cut = dw_parted ? a.n_rows / (p.per + 1) : 0;   // matrices with more rows than a block
   if (dw_parted && (cut < 1 || !a.offsets)) cut = 1;
   if (cut > a.n_matrices) cut = a.n_matrices;
-  return launch(who, k_gated_join<T>, dim3((unsigned)(blocks < 2048 ? blocks : 2048), (unsigned)(1 + cut)), 256, 0, stream, a);
+  return launch(who, k_gated_join<T>, dim3((unsigned)(pieces < 2048 ? pieces : 2048), (unsigned)(1 + cut)), 256, 0, stream, a);
 }
 
 #endif   // SVT_GATED_INSTANTIATE

@@ -67,8 +67,14 @@ extern "C" size_t svt_gated_linear_workspace_size(int32_t n_rows, int32_t n_in, 
     return 0;
   const int b = elem_size(dtype);
   const GatedArgs a = gated_args(n_rows, n_in, n_out, n_matrices, b, by_expert ? kSome : nullptr);
-  const bool as_is = n_rows == 0 || (aligned && aligned_rows(n_in, b, nullptr, nullptr, nullptr));
-  return as_is || few_rows(a, true) ? 0 : gated_copies(a, b);
+  const bool as_is = aligned && aligned_rows(n_in, b, nullptr, nullptr, nullptr);
+  if (n_rows == 0 || few_rows(a, !as_is)) return 0;
+  const GatedPlan plan = plan_forward(a, b);
+  if (!fits(eighths(plan.units * plan.columns))) {
+    (void)report(SVT_EINVAL, "svt_gated_linear_workspace_size: too many rows of too many outputs for one call");
+    return 0;
+  }
+  return as_is ? 0 : gated_copies(a, b);
 }
 
 extern "C" int svt_gated_linear(int32_t n_rows, int32_t n_in, int32_t n_out, int32_t n_matrices, int32_t dtype,
@@ -122,6 +128,10 @@ extern "C" size_t svt_gated_linear_backward_workspace_size(int32_t n_rows, int32
   GatedArgs a = gated_args(n_rows, n_in, n_out, n_matrices, b, by_expert ? kSome : nullptr);
   if (n_rows == 0) return 0;
   const GatedPlan plan = plan_backward(a, b);
+  if (!fits(gradient_blocks(plan, n_out, true, true, by_expert != 0).all())) {
+    (void)report(SVT_EINVAL, "%s: too large a product for one call", who);
+    return 0;
+  }
   const bool as_is = aligned && aligned_rows(n_in, b, nullptr, nullptr, nullptr);
   return (size_t)(2 * a.n_rows * a.pitch) + (as_is ? 0 : gated_copies(a, b)) +
          (size_t)(dx_parts(a, plan) + dw_parts(a, plan)) * 4;
@@ -171,7 +181,7 @@ extern "C" int svt_gated_linear_backward(int32_t n_rows, int32_t n_in, int32_t n
   const Span outs[4] = {{dx, nx}, {dw_gate, nw}, {dw_up, nw}, {workspace, need}};
   if (any_overlap(ins, 7, outs, 4))
     return report(SVT_EINVAL, "%s: an output or the workspace overlaps an input or another output", who);
-  if (!fits(dx_blocks(plan) + 2 * dw_blocks(plan, n_out)))
+  if (!fits(gradient_blocks(plan, n_out, dx != nullptr, dw_gate != nullptr, offsets != nullptr).all()))
     return report(SVT_EINVAL, "%s: too large a product for one call", who);
   a.d_both = (char *)workspace;
   if (copies) {
