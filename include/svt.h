@@ -483,7 +483,7 @@ int svt_embedding(int64_t n_tokens, int64_t n_rows, int32_t width, int32_t dtype
  *   d_table     [n_rows][width] of table_type: dtype or SVT_F32
  *   workspace   svt_embedding_backward_workspace_size(n_tokens, n_rows, width) bytes, 16-byte aligned
  * Sizes as svt_embedding.  n_tokens == 0 writes the zeros (accumulate: returns without enqueuing).
- * Errors: SVT_EINVAL, SVT_EDEVICE (a launch failed: d_table is undefined).
+ * Errors: SVT_EINVAL (also where d_out lies beyond any memory), SVT_EDEVICE (a launch failed: d_table is undefined).
  */
 size_t svt_embedding_backward_workspace_size(int64_t n_tokens, int64_t n_rows, int32_t width);
 int svt_embedding_backward(int64_t n_tokens, int64_t n_rows, int32_t width, int32_t dtype, const void *d_out,

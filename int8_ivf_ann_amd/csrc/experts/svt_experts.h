@@ -37,6 +37,14 @@ int with_type(int32_t dtype, F f) {
   }
 }
 
+// The grid of a kernel that numbers its workgroups by block_number(): rows of 2^22, so that the threads along x stay below
+// 2^32; at most 2^32 workgroups, which arrays that fit the memory stay far below.  The last row may not be full.
+constexpr int64_t kGridRow = 1 << 22;
+inline bool fits(int64_t blocks) { return blocks < int64_t(1) << 32; }
+inline dim3 grid_of(int64_t blocks) {
+  return blocks <= kGridRow ? dim3((unsigned)blocks) : dim3((unsigned)kGridRow, (unsigned)((blocks + kGridRow - 1) / kGridRow));
+}
+
 // Launches a kernel: SVT_OK, or its failure reported.  The status is this launch's own (an error that an earlier call
 // left unread is its caller's, and stays), so that a call of several launches can end at the one that failed.
 template <class... P, class... A>
@@ -52,6 +60,8 @@ int launch(const char *who, void (*kernel)(P...), dim3 grid, unsigned threads, s
 }
 
 // ---- device --------------------------------------------------------------------------------------
+
+__device__ __forceinline__ int64_t block_number() { return blockIdx.y * (int64_t)gridDim.x + blockIdx.x; }
 
 // Reductions over aligned groups of L lanes (a power of two, at most 64); every lane gets the result.
 // Within 16 lanes: DPP moves (lane ^ 1 and ^ 2 as quad permutations, then mirrors of 8 and of 16 lanes,

@@ -316,7 +316,7 @@ struct SumArgs {
   int32_t column_blocks;       // of 2 lanes pieces
   int32_t per;                 // places of a chunk
   int32_t chunks;
-  int32_t sum_blocks;          // workgroups that add; the others clear
+  int64_t sum_blocks;          // workgroups that add; the others clear
   int32_t clear_rows;          // rows that one of the others looks after
   float scale;
   const uint32_t *keys;        // sorted
@@ -377,13 +377,14 @@ __device__ __forceinline__ void put_row(Vec<TD, M> *at, const float (&sum)[M], f
 template <class T, class TD, int M, bool ADD, bool TWO>
 __global__ __launch_bounds__(kThreads) void k_sum_rows(SumArgs a, const Vec<T, M> *d_out, Vec<TD, M> *table) {
   __shared__ uint32_t named[ADD ? 1 : kClearMost / 32];
-  if (!ADD && (int)blockIdx.x >= a.sum_blocks) {
-    clear_rows<TD, M>(a, (int64_t)(blockIdx.x - a.sum_blocks) * a.clear_rows, table, named);
+  if (const int64_t cleared = block_number() - a.sum_blocks; cleared >= 0) {
+    const int64_t first = cleared * a.clear_rows;
+    if (!ADD && first < a.n_rows) clear_rows<TD, M>(a, first, table, named);
     return;
   }
   constexpr int J = TWO ? 4 : 8;
   const int in = threadIdx.x % a.lanes;
-  const int64_t unit = (int64_t)blockIdx.x * (kThreads / a.lanes) + threadIdx.x / a.lanes;
+  const int64_t unit = block_number() * (kThreads / a.lanes) + threadIdx.x / a.lanes;
   const int64_t chunk = unit / a.column_blocks;
   if (chunk >= a.chunks) return;
   const int block = (int)(unit - chunk * a.column_blocks);
@@ -699,8 +700,7 @@ int embedding_backward(const char *who, SumArgs a, const SortShape &sh, const Sp
     a.column_blocks = (a.pieces + 2 * a.lanes - 1) / (2 * a.lanes);
     const int64_t units = (int64_t)a.chunks * a.column_blocks, each = kThreads / a.lanes;
     const int64_t blocks = (units + each - 1) / each;
-    if (blocks > INT32_MAX / 4) return report(SVT_EINVAL, "%s: too many tokens of too wide rows for one call", who);
-    a.sum_blocks = (int32_t)blocks;
+    a.sum_blocks = blocks;
   }
   int64_t clear_blocks = 0;
   if (!ADD) {   // at most 256 KiB of rows for each, and work for every compute unit
@@ -708,13 +708,11 @@ int embedding_backward(const char *who, SumArgs a, const SortShape &sh, const Sp
     a.clear_rows = (int32_t)(row >= 262144 ? 1 : 262144 / row < kClearMost ? 262144 / row : kClearMost);
     if (share < a.clear_rows) a.clear_rows = (int32_t)share;
     clear_blocks = (a.n_rows + a.clear_rows - 1) / a.clear_rows;
-    if (clear_blocks > INT32_MAX / 4) return report(SVT_EINVAL, "%s: too large a table for one call", who);
   }
-  // the grid's threads stay below 2^32
-  if ((a.sum_blocks + clear_blocks) * kThreads >= int64_t(1) << 32)
+  if (!fits(a.sum_blocks + clear_blocks))
     return report(SVT_EINVAL, "%s: too large a table or batch for one call", who);
   auto sum = [&](auto two) {
-    return launch(who, k_sum_rows<T, TD, M, ADD, decltype(two)::value>, (unsigned)(a.sum_blocks + clear_blocks), kThreads, 0,
+    return launch(who, k_sum_rows<T, TD, M, ADD, decltype(two)::value>, grid_of(a.sum_blocks + clear_blocks), kThreads, 0,
                   stream, a, (const Vec<T, M> *)d_out, (Vec<TD, M> *)d_table);
   };
   const int rc = a.pieces > a.lanes ? sum(std::true_type{}) : sum(std::false_type{});

@@ -396,9 +396,6 @@ __device__ __forceinline__ Rows rows_of_unit(const int32_t *offsets, int n_matri
   return {-1, 0, 0};
 }
 
-// the number of a workgroup: a grid's threads along x stay below 2^32, so that many workgroups take several rows of one
-__device__ __forceinline__ int64_t block_number() { return blockIdx.y * (int64_t)gridDim.x + blockIdx.x; }
-
 __host__ __device__ inline int64_t eighths(int64_t tiles) { return (tiles + 7) / 8 * 8; }
 
 // The tile of workgroup b: workgroups b, b + 8, .. share an L2, so each eighth takes neighbouring tiles; within them,
@@ -1020,14 +1017,6 @@ inline GradientBlocks gradient_blocks(const GatedPlan &p, int32_t outs, bool dx,
   const int64_t n = dw ? eighths((int64_t)2 * ((outs + q - 1) / q) * p.columns) * p.dw_units : 0;
   const int64_t early = p.per > long_rows(p, outs) ? n : 0;
   return {early, dx ? eighths(p.units * p.columns) * p.splits : 0, early == 0 || (dx && by_expert) ? n : 0};
-}
-
-// A launch's workgroups: rows of 2^22, so that threads along x stay below 2^32; at most 2^32, which arrays that fit the
-// memory stay far below
-constexpr int64_t kGridRow = 1 << 22;
-inline bool fits(int64_t blocks) { return blocks < int64_t(1) << 32; }
-inline dim3 grid_of(int64_t blocks) {
-  return blocks <= kGridRow ? dim3((unsigned)blocks) : dim3((unsigned)kGridRow, (unsigned)((blocks + kGridRow - 1) / kGridRow));
 }
 
 // Whether the forward pass takes the kernel for few rows: 1 or 2 blocks of 16, or 0.  Few: up to 32 (64 x 2048 x 2048 bfloat16

@@ -1,4 +1,4 @@
-"""Gated products of small whole numbers on the GPU: every product and every float32 sum is exact, whatever its order, so
+"""Gated products and embedding gradients of small whole numbers on the GPU: every product and every float32 sum is exact, whatever its order, so
 that the results are the float64 definition's, rounded once.  A part that is lost or counted twice shows."""
 import numpy as np
 import pytest
@@ -95,3 +95,24 @@ def test_the_most_rows(svt, give_back, M):   # noqa: F811
             want = sum((dh[a:b] * other[a:b] * x[a:b]).sum(dtype=torch.float64)
                        for a in range(o[e], o[e + 1], 1 << 27) for b in (min(a + (1 << 27), o[e + 1]),))
             assert dw.view(-1)[e].item() == float(want), e
+
+
+def test_embedding_gradient_of_more_workgroups_than_a_grid_row(svt, give_back):   # noqa: F811
+    """Rows of 2^24 - 1 float16, which begin at 2 bytes: 138 chunks of 8 places and 2^17 pieces of a row's columns each, four to
+    a workgroup."""
+    import torch
+    n, V, D = 1101, 4, 2 ** 24 - 1
+    say("wide rows", n, V, D)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    ids = torch.randint(-1, V, (n,), generator=g, device="cuda")
+    ids[ids == 2] = 3   # a row that no token names, and runs over many chunks
+    d = whole(g, "f16", n, D)
+    out = svt.svt_embedding_backward(d, ids, V)
+    given = whole(g, "f16", V, D)
+    added = svt.svt_embedding_backward(d, ids, V, out=given.clone(), accumulate=True)
+    for v in range(V):
+        want = torch.zeros(D, device="cuda")
+        for i in (ids == v).nonzero()[:, 0].tolist():
+            want += d[i]
+        assert torch.equal(out[v], want.half()), v
+        assert torch.equal(added[v], (want + given[v]).half()), v

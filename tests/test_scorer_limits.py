@@ -1,4 +1,4 @@
-"""Gated products of many experts and long sides on the host: sizes inside the documented ranges are taken, in grids whose
+"""Gated products of many experts and long sides, embedding gradients of wide rows, on the host: sizes inside the documented ranges are taken, in grids whose
 threads along each side stay below 2^32.  The stand-in for the runtime's launch calls (a process of its own) keeps the
 largest grid."""
 import os
@@ -84,3 +84,31 @@ def test_sizes_far_beyond_are_refused_by_the_size_call_too():
     assert "too many rows" in svt.svt_last_error()
     assert L.svt_gated_linear_backward_workspace_size(n, 1 << 20, 1 << 20, 512, svt.SVT_F16, 1, 1) == 0
     assert "too large" in svt.svt_last_error()
+
+
+ROWS = r"""
+import ctypes, sys
+fake = ctypes.CDLL(sys.argv[1], mode=ctypes.RTLD_GLOBAL)
+sys.path.insert(0, sys.argv[2])
+from int8_ivf_ann_amd import svt
+L = svt.lib()
+threads, blocks = [ctypes.c_ulonglong.in_dll(fake, n) for n in ("threads_x", "blocks")]
+n, V, D, kind = eval(sys.argv[3])
+P = [(i + 1) << 42 for i in range(4)]
+size = L.svt_embedding_backward_workspace_size(n, V, D)
+assert size > 0
+for add in (0, 1):
+    for shift in (0, 4):   # rows at 16 bytes where the width has it, and at 4
+        assert L.svt_embedding_backward(n, V, D, kind, P[0] + shift, P[1], 1.0, add, kind, P[2], P[3], size, None) == 0, svt.svt_last_error()
+assert 0 < threads.value < 1 << 32, threads.value
+print("ok", blocks.value)
+"""
+
+
+@pytest.mark.parametrize("size", [(4096, 2, 2 ** 24 - 1, 1), (4096, 2, 2 ** 24 - 1, 0), (1, 1, 1, 0), (2 ** 30, 2 ** 31 - 2, 2, 1),
+                                  (2 ** 30, 1, 33, 1), (2048, 2048, 2 ** 24, 0)])
+def test_embedding_gradients_that_fit_the_memory_are_taken(stand_in, tmp_path, size):
+    child = tmp_path / "rows.py"
+    child.write_text(ROWS)
+    r = subprocess.run([sys.executable, str(child), stand_in[0], ROOT, repr(size)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.startswith("ok"), r.stdout + r.stderr
