@@ -536,9 +536,10 @@ int svt_gated_linear_backward(int32_t n_rows, int32_t n_in, int32_t n_out, int32
  * svt_token_logprobs - for each row of logits, with z = scale * logits and p = softmax(z): the log probability of
  * a given token, the entropy, and the `top` most likely tokens.
  *   logits         [n_tokens][vocab] of dtype, 1 <= vocab <= 2^30.  -inf or NaN shuts a token (p = 0); +inf counts
- *                  as the largest finite float32
+ *                  as the largest finite float32.  Two logits whose difference overflows float32 are infinitely far
+ *                  apart
  *   tokens         [n_tokens] int64; outside [0, vocab): no token is given
- *   scale          positive and finite (1 / temperature)
+ *   scale          in (0, 2^127] (1 / temperature)
  *   top            0 <= top <= min(SVT_MAX_TOP, vocab)
  *   logprobs       [n_tokens] float: log p of the token; 0 where none is given, -inf where it is shut
  *                  (or below the least float32)

@@ -37,6 +37,7 @@ constexpr int kList = 512;                      // a wave's candidates
 constexpr int32_t kMaxVocab = 1 << 30;
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 constexpr float kFar = -1000.f;
+constexpr float kMostScale = 0x1p127f;          // scale log2 e stays finite: 0 times it is 0
 
 struct LogprobArgs {
   int64_t n_tokens;
@@ -546,7 +547,7 @@ extern "C" int svt_token_logprobs(int32_t n_tokens, int32_t vocab, int32_t top, 
   (void)report(SVT_OK, "%s", "");
   int rc = check_logprobs(who, n_tokens, vocab, top, dtype);
   if (rc != SVT_OK) return rc;
-  if (!(scale > 0.f && scale <= FLT_MAX)) return report(SVT_EINVAL, "%s: scale %g is not positive and finite", who, scale);
+  if (!(scale > 0.f && scale <= kMostScale)) return report(SVT_EINVAL, "%s: scale %g out of (0, 2^127]", who, scale);
   if (n_tokens == 0) return SVT_OK;
   if (!logits || !tokens || !logprobs || !entropy || !norms || (top > 0 && (!top_tokens || !top_logprobs)))
     return report(SVT_EINVAL, "%s: NULL input or output", who);
@@ -606,7 +607,7 @@ extern "C" int svt_token_logprobs_backward(int32_t n_tokens, int32_t vocab, int3
   (void)report(SVT_OK, "%s", "");
   int rc = check_logprobs(who, n_tokens, vocab, 0, dtype);
   if (rc != SVT_OK) return rc;
-  if (!(scale > 0.f && scale <= FLT_MAX)) return report(SVT_EINVAL, "%s: scale %g is not positive and finite", who, scale);
+  if (!(scale > 0.f && scale <= kMostScale)) return report(SVT_EINVAL, "%s: scale %g out of (0, 2^127]", who, scale);
   if (n_tokens == 0) return SVT_OK;
   if (!logits || !tokens || !norms || !entropy || !d_logprobs || !d_logits)
     return report(SVT_EINVAL, "%s: NULL input or output", who);

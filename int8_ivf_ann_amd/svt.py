@@ -921,7 +921,8 @@ def svt_token_logprobs(logits, tokens, top: int = 0, scale: float = 1.0, out_log
     """Of p = softmax(scale * logits) for each row: logits [T, V] (float32, float16, bfloat16), tokens int64 [T] ->
     (logprobs float32 [T], entropy float32 [T], norms float32 [T, 2]), and with ``top`` > 0 also (top_tokens int64
     [T, top], top_logprobs float32 [T, top]), by (logit desc, token asc).  -inf and NaN shut a token.  logprobs is 0
-    where the token lies outside [0, V); -1 and -inf where fewer than ``top`` are open.  norms is for the gradient."""
+    where the token lies outside [0, V); -1 and -inf where fewer than ``top`` are open.  norms is for the gradient; scale lies
+    in (0, 2^127]."""
     import torch
     (T, V), code, dev = _rows_of("logits", logits)
     _check_dense("tokens", tokens, torch.int64, (T,), dev)
