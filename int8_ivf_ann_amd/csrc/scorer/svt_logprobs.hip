@@ -83,6 +83,14 @@ __device__ __forceinline__ uint64_t wave_best(uint64_t k) {
   return (uint64_t)hi << 32 | lo;
 }
 
+// f, a signalling NaN quieted: the maximum of one and a number is a NaN, and the next maximum drops that and what was before.
+// (The conversion from float16 quiets by itself; that from bfloat16 is a move of bits.)
+template <class T>
+__device__ __forceinline__ float quiet(float f) {
+  if constexpr (std::is_same<T, f16>::value) return f;
+  else return __builtin_canonicalizef(f);
+}
+
 // (l - m) scale log2 e, in [kFar, 0]; kFar for a NaN (the instruction's median of a NaN is the least of the others)
 __device__ __forceinline__ float exponent(float l, float m, float c) {
   return __builtin_amdgcn_fmed3f((l - m) * c, kFar, 0.f);
@@ -332,7 +340,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobArgs a, const T *l
       for (int n = 0; n < N; ++n) {
         float m = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < kPiece; ++i) m = fmaxf(m, v[n][i]);
+        for (int i = 0; i < kPiece; ++i) m = fmaxf(m, quiet<T>(v[n][i]));
         if (TOP) {
           if (n == 0 && q == p0) best.start(m);
           best.offer(v[n], m, token + n * 64 * W * kPiece);
