@@ -49,35 +49,63 @@ __device__ __forceinline__ float exp2_below(float x) {
   return __builtin_amdgcn_exp2f(low ? x + 64.f : x) * (low ? 0x1p-64f : 1.f);
 }
 
-// 1 / (1 + e^-v), with e^-v as a square: neither it nor the reciprocal's result leaves the normal range where v times the whole
-// is above 2^-126 (8192 x 2048 x 8192 bfloat16: e^-v itself, unscaled, 564 us, e^-|v| with its two cases 577, this 569)
+// 2^32 / (1 + e^-v), with e^-v as a square: neither it nor the reciprocal's result leaves the normal range where v times the
+// whole is above 2^-126 (8192 x 2048 x 8192 bfloat16: e^-v itself, unscaled, 564 us, e^-|v| with its two cases 577, this 569).
+// The exponential instruction's rounded argument is off by |v| 2^-24, which two-byte results do not show; float32's take the
+// library's function.
+template <class T>
 __device__ __forceinline__ float logistic(float v) {
-  const float h = __builtin_amdgcn_exp2f(-0.5f * kGateLog2e * v);
-  return __builtin_amdgcn_rcpf(fmaf(h * 0x1p-32f, h, 0x1p-32f)) * 0x1p-32f;
+  float h;
+  if constexpr (sizeof(T) == 4) h = expf(-0.5f * v);
+  else h = __builtin_amdgcn_exp2f(-0.5f * kGateLog2e * v);
+  return __builtin_amdgcn_rcpf(fmaf(h * 0x1p-32f, h, 0x1p-32f));
 }
 
-template <int ACT>
+// v times the whole, l its 2^32-fold, which alone may leave the normal range (two-byte results do not show that either)
+template <class T>
+__device__ __forceinline__ float silu(float v, float l) {
+  if constexpr (sizeof(T) == 4) return v < 0.f ? v * l * 0x1p-32f : v * (l * 0x1p-32f);
+  else return v * (l * 0x1p-32f);
+}
+
+// the normal distribution's integral up to v and its density at v, times v
+struct Normal { float below, slope; };
+template <class T>
+__device__ __forceinline__ Normal normal(float v) {
+  constexpr float c = 0.39894228040143268f, r = 0.70710678118654752f;
+  if constexpr (sizeof(T) == 4) {   // with what v^2 and the error function's argument were rounded by
+    const float w = __builtin_amdgcn_fmed3f(v, -16.f, 16.f), q = w * w, off = fmaf(w, w, -q);
+    const float t = expf(-0.25f * q);   // a square again, for the range
+    const float a = -r * w, rest = fmaf(-r, w, -a) - (float)(0.70710678118654752440 - (double)r) * w;
+    const float slope = c * w * t * t * fmaf(-0.5f, off, 1.f);
+    return {fmaf(-0.56418958354775629f * rest * t, t, 0.5f * erfcf(a)), v == v ? slope : v};
+  } else {
+    return {0.5f * erfcf(-r * v), c * v * exp2_below(-0.5f * kGateLog2e * v * v)};
+  }
+}
+
+template <int ACT, class T>
 __device__ __forceinline__ float act_value(float v) {
   if constexpr (ACT == SVT_ACT_RELU) return v < 0.f ? 0.f : v;   // NaN stays NaN
-  else if constexpr (ACT == SVT_ACT_SILU) return v * logistic(v);
-  else if constexpr (ACT == SVT_ACT_GELU) return 0.5f * v * erfcf(-0.70710678118654752f * v);
+  else if constexpr (ACT == SVT_ACT_SILU) return silu<T>(v, logistic<T>(v));
+  else if constexpr (ACT == SVT_ACT_GELU) return v * normal<T>(v).below;
   else return v;
 }
 
 // value and slope
-template <int ACT>
+template <int ACT, class T>
 __device__ __forceinline__ void act_both(float v, float &value, float &slope) {
   if constexpr (ACT == SVT_ACT_RELU) {
     value = v < 0.f ? 0.f : v;
     slope = v > 0.f ? 1.f : 0.f;
   } else if constexpr (ACT == SVT_ACT_SILU) {
-    const float s = logistic(v);
-    value = v * s;
+    const float l = logistic<T>(v), s = l * 0x1p-32f;
+    value = silu<T>(v, l);
     slope = fmaf(value, 1.f - s, s);
   } else if constexpr (ACT == SVT_ACT_GELU) {
-    const float c = 0.5f * erfcf(-0.70710678118654752f * v);
-    value = v * c;
-    slope = fmaf(v * 0.39894228040143268f, exp2_below(-0.5f * kGateLog2e * v * v), c);
+    const Normal n = normal<T>(v);
+    value = v * n.below;
+    slope = n.slope + n.below;
   } else {
     value = v;
     slope = 1.f;
@@ -582,7 +610,7 @@ __global__ __launch_bounds__(C::threads) void k_gated(GatedArgs a) {
   with_act(a.act, [&](auto act) {
     St::template store<half>(lds, rows.first, rows.end, n0, a.outs, (T *)a.h, [&](int b, int c, float (&v)[4]) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = act_value<decltype(act)::value>(acc[b][c][k]) * acc[b][half + c][k];
+      for (int k = 0; k < 4; ++k) v[k] = act_value<decltype(act)::value, T>(acc[b][c][k]) * acc[b][half + c][k];
     });
   });
 }
@@ -666,7 +694,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_gated_few(GatedArgs a) {
     for (int k = 0; k < 4; ++k) {
       gate[k] = s[0][k];
       up[k] = s[1][k];
-      h[k] = act_value<decltype(act)::value>(gate[k]) * up[k];
+      h[k] = act_value<decltype(act)::value, T>(gate[k]) * up[k];
     }
   });
   const int64_t to = row * a.outs + n0;
@@ -740,7 +768,7 @@ __global__ __launch_bounds__(kBothThreads) void k_gated_both(GatedArgs a, int la
 #pragma unroll
         for (int i = 0; i < each; ++i) {
           float value, slope;
-          act_both<decltype(act)::value>((float)g.t[i], value, slope);
+          act_both<decltype(act)::value, T>((float)g.t[i], value, slope);
           const float dh = (float)d.t[i];
           g.t[i] = (T)(dh * (float)u.t[i] * slope);
           u.t[i] = (T)(dh * value);
