@@ -515,7 +515,7 @@ int svt_gated_linear(int32_t n_rows, int32_t n_in, int32_t n_out, int32_t n_matr
 
 /*
  * svt_gated_linear_backward - its gradients: with dg = dh * up * act'(gate) and du = dh * act(gate), both rounded to
- * dtype as the products take them,
+ * dtype as the products take them (one rounding more than float32 products have: pass float32 to go without),
  *   dx = dg w_gate + du w_up  (per row, with its pair);  dw_gate = sum over a pair's rows of dg x^T;  dw_up of du x^T
  *   dh, gate, up  [n_rows][n_out] of dtype: the gradient in h, and what svt_gated_linear kept
  *   dx            [n_rows][n_in] of dtype, or NULL (w_gate and w_up may then be NULL).  Rows that no pair names are left

@@ -6,13 +6,15 @@
 // The lookup moves every byte once and is bound by memory.  The gradient sorts the tokens (stable, so that a row's
 // sum has one order), then walks the sorted list: a chunk of consecutive places belongs to a group of lanes, which
 // adds up the runs of equal tokens in registers and writes each finished row once.  Only runs that cross a chunk's
-// border leave partial sums, which one more launch joins in order; so a token that names half the batch costs no more
-// than any.  Rows that no token names are cleared by workgroups of their own in the launch that adds, which keeps the
-// table's writes beside the gradient's reads.
+// border leave partial sums, which one more launch joins in order, 256 columns of a run by one workgroup.  Rows that no
+// token names are cleared by workgroups of their own in the launch that adds, which keeps the table's writes beside the
+// gradient's reads.
 //
-// Measured: rows for 65536 tokens of 1024 bfloat16 36 us (176 MB, 4.9 TB/s), for 2048 of 128 float16 2.9.  The gradient in
-// 131072 rows of the former 119: the sort 25 (a chain of four launches), sums and zeros 80 (403 MB, 5 TB/s), the join 9; of
-// 3001 tokens of 250 float32 in 5003 rows 20.6: 8, 6 and 6, chains of dependent loads all three.
+// Measured, each kernel's average over inputs in turn: rows for 65536 tokens of 1024 bfloat16 41 us (176 MB, 4.3 TB/s; 34 at
+// best), for 2048 of 128 float16 2.6.  The gradient in 131072 rows of the former 118: the sort 25 (a chain of four launches),
+// sums and zeros 80 (403 MB, 5 TB/s), the join 14; of 3001 tokens of 250 float32 in 5003 rows 21: 8, 6 and 7, chains of
+// dependent loads all three.  Tokens that all name one row make the join's run long: the former 149 and the latter 31; 16
+// rows for all 187 and 19.  Added to a float32 table instead of zeros elsewhere, the former takes 111.
 
 #include <type_traits>
 

@@ -734,7 +734,8 @@ __global__ __launch_bounds__(256) void k_gated_pad(GatedArgs a, int lanes) {
 // ---- gradients -----------------------------------------------------------------------------------
 
 // dg and du of the rows that some matrix names, with zeros up to the pitch.  They are rounded to the rows' type, as the
-// matrix instructions take them: that is the rounding a gradient kept between two layers has.
+// matrix instructions take them: that is the rounding a gradient kept between two layers has.  (In two parts each, which would
+// keep 16 bits of bfloat16's, the products would take twice the instructions.)
 constexpr int kBothThreads = 256;
 
 template <class T>
@@ -963,8 +964,9 @@ struct GatedPlan {
 // The cuts, and microseconds of a step of 128 bytes: with one workgroup on a compute unit, and for each further one that
 // shares it (the 256 x 256 cut has none beside it: they follow each other).  Measured with products of two-byte and of
 // float32 values, 200 x 512 x 2048 to 16384 x 1024 x 2048.  Its choices are within 10 % of the best cut's time there; gradients
-// in us: bfloat16 4096 x 4096 x 4096 487, 4096 x 1024 x 2048 88, 1024 x 1024 x 1024 30, 300 x 300 x 300 10.9; float32
-// 1001 x 250 x 999 41, 4096 x 1024 x 2048 581.
+// in us, four sets of inputs in turn: bfloat16 4096 x 4096 x 4096 530, 4096 x 1024 x 2048 100, 1024 x 1024 x 1024 34,
+// 300 x 300 x 300 13; float32 1001 x 250 x 999 45, 4096 x 1024 x 2048 630.  The steps were timed with operands in the caches: few
+// tiles whose weights come from memory wait for each step's loads (64 x 2048 x 2048 bfloat16 14 us in the caches, 26 from memory).
 struct CutCost { int q, p; float alone[2], shared[2]; };
 constexpr int kCuts = 4;
 constexpr CutCost kCutCost[kCuts] = {{32, 64, {0.28f, 0.46f}, {0.15f, 0.29f}},
@@ -999,7 +1001,8 @@ inline GatedPlan plan_forward(const GatedArgs &a, int elem) {
 // units have to do, but at least what the longest tile takes, and for parts 4 us and 2.4 for each million partial values that
 // are written and read again.  Only products of fewer tiles than compute units are cut into parts.  By expert one matrix may
 // have all rows, which only the GPU knows: dW's blocks are as long as what each compute unit has to do, so that no tile
-// outlasts the others (16384 rows, 8 uneven experts, 1024 inputs, 2048 outputs: whole 358 us, at most 8192 rows 346, 4096 366;
+// outlasts the others (16384 rows, 8 uneven experts, 1024 inputs, 2048 outputs: whole 358 us, at most 8192 rows 346, 4096 366,
+// the device's least times, where a call takes 365 to 385;
 // 32 experts, 1024 x 1024: 252, 255, 244; 8192 rows, 8 experts, 2048 x 2048: 338 whole, at most 4096 rows 367).  A tile costs
 // two steps beside its own (100 rows, 16 experts, 1024 x 1024, which small tiles without that count would take: 57 us and 51).
 inline GatedPlan plan_backward(const GatedArgs &a, int elem) {
@@ -1047,9 +1050,11 @@ inline GradientBlocks gradient_blocks(const GatedPlan &p, int32_t outs, bool dx,
   return {early, dx ? eighths(p.units * p.columns) * p.splits : 0, early == 0 || (dx && by_expert) ? n : 0};
 }
 
-// Whether the forward pass takes the kernel for few rows: 1 or 2 blocks of 16, or 0.  Few: up to 32 (64 x 2048 x 2048 bfloat16
-// 14.3 us there, 10.9 with tiles; 32 x 2048 x 2048 10.1 and 10.7).  By expert up to 4 on average (32 experts of 1024 x 1024,
-// 64 rows 22.2 and 20.9, 256 rows 24.9 and 22.3), or 32 where tiles would need copies.
+// Whether the forward pass takes the kernel for few rows: 1 or 2 blocks of 16, or 0.  Few: up to 32 (32 rows of bfloat16, weights
+// from memory: 2048 x 2048 12.8 us there, 26 with tiles; 4096 x 8192 43 and 55).  Above that it reads the weights once for every 32
+// rows, and which is faster depends on the outputs: 64 x 2048 x 2048 13 and 26, 64 x 4096 x 8192 70 and 57, 128 x 4096 x 8192 127
+// and 65.  By expert up to 4 on average (32 experts of 1024 x 1024, 128 rows 32 and 30, 512 rows 38 and 30), or 32 where tiles
+// would need copies.
 inline int few_rows(const GatedArgs &a, bool copies) {
   const int64_t rows = a.offsets ? (a.n_rows + a.n_matrices - 1) / a.n_matrices : a.n_rows;
   if (rows > (a.offsets && !copies ? 4 : 32)) return 0;

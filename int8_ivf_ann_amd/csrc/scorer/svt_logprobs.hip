@@ -16,12 +16,12 @@
 // best so far (ties go to the lower token).  Tokens above that bound go to a list in LDS; a full list is cut to its
 // `top` best, which raises the bound.  The first piece's bound is the top-th largest of the lanes' own maxima.
 //
-// Measured: 4096 rows of 49152 bfloat16 74 us (5.4 TB/s; 47 without the loads, 70 without the exponentials: bound by
-// memory), of 50021, whose rows begin at odd addresses, 92; float32 with the 16 best 164 (4.9 TB/s).  Forward and gradient
-// of 4096 x 50021 one after the other 260.  Loads and conversions of a piece stand apart, and the pieces of the next step are
-// asked for before this step's are used: with a branch around each, 124 us for the forward pass of the pair, the row's end
-// element by element 8 us of it.  256 rows of 2048 float32, top 16: 8.7 us, the gradient 4.4.  One row of 131072 bfloat16,
-// top 8: 8.1 us in 32 splits, 4.3 to join them.
+// Measured, the forward pass alone over inputs in turn: 4096 rows of 49152 bfloat16 81 us (5.0 TB/s: bound by memory), of
+// 50021, whose rows begin at odd addresses, 108 (3.8 TB/s); 49152 float32 with the 16 best 191 (4.2 TB/s).  The gradient of
+// the first two 146 and 161, of forward and gradient one after the other 246 and 280: behind the gradient's writes the
+// forward pass of 50021 takes 125.  Loads and conversions of a piece stand apart, and the pieces of the next step are asked
+// for before this step's are used.  256 rows of 2048 float32, top 16: 8.0 us, the gradient 4.6.  One row of 131072 bfloat16,
+// top 8: 7.7 us in 32 splits, 4.5 to join them.
 
 #include <type_traits>
 
@@ -166,8 +166,9 @@ __device__ __forceinline__ uint64_t in_order(uint64_t k, int n, int top, uint64_
   return lane_id() < top ? lds[lane_id()] : 0ull;
 }
 
-// The same, by ranks or by rounds that take the best: 256 rows of 2048 float32, top 16, 8.7 us by ranks and 10.1 by rounds; one
-// row of 131072 bfloat16, top 8, 10.6 and 8.1
+// The same, by ranks or by rounds that take the best.  The whole forward pass by ranks and by rounds in us, top 4, 8 and 16:
+// 256 rows of 2048 float32 6.3 and 5.9, 6.9 and 7.3, 8.0 and 10.0; 4096 of them 26 and 24, 30 and 31, 35 and 44; one row of 131072
+// bfloat16 10.1 and 8.9, 12.3 and 11.6, 20.6 and 20.9; 16384 rows of 900 24 and 24, 28 and 30, 36 and 40
 __device__ __forceinline__ uint64_t best_of_wave(uint64_t k, int n, int top, uint64_t *lds) {
   if (top > 8) return in_order(k, n, top, lds);
   uint64_t one[1] = {k};

@@ -888,8 +888,9 @@ def svt_gated_linear_backward(dh, x, w_gate, w_up, gate, up, offsets=None, activ
                               out_gate=None, out_up=None, need_x: bool = True, need_weights: bool = True, workspace=None,
                               stream=None):
     """The gradients of svt_gated_linear: dh [R, N], its inputs and what it kept -> (dx [R, K], d_gate and d_up like
-    w_gate and w_up).  ``need_x`` and ``need_weights`` leave one part out (None in its place).  Rows that no pair of
-    matrices names stay as they were in dx; a pair without rows gets zeros."""
+    w_gate and w_up).  The gradients of gate and up are rounded to x's dtype before the products.  ``need_x`` and
+    ``need_weights`` leave one part out (None in its place).  Rows that no pair of matrices names stay as they were in dx;
+    a pair without rows gets zeros."""
     R, K, N, M, code, dev, act = _gated_shape(x, w_gate, w_up, offsets, activation)
     for name, t in (("dh", dh), ("gate", gate), ("up", up)):
         _check_dense(name, t, x.dtype, (R, N), dev)
